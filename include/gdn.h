@@ -1,5 +1,6 @@
 /*
- * gdn.h -- C ABI of the Gated DeltaNet prefill scan (part of the same library as moe.h).
+ * gdn.h -- C ABI of the Gated DeltaNet prefill scan and decode step (part of the same library
+ * as moe.h).
  *
  * "Optimizing on-device inference for Apple Silicon", section "Prefill > Keep recurrent
  * state on chip": during prefill a Gated DeltaNet layer scans the prompt in order and
@@ -49,6 +50,28 @@ extern "C" {
 moe_status moe_gdn_scan(int32_t T, int32_t n_kheads, int32_t n_vheads, int32_t d_k, int32_t d_v,
                         const void *q, const void *k, const void *v, const float *alpha,
                         const float *beta, float *state, void *out, hipStream_t stream);
+
+/* One token each of R rows, for serving: row r brings one token of the sequence whose state is
+ * slot[r] of a pool of states, which is read and written in place (the update of
+ * moe_gdn_scan).  Rows of one slot are applied in row order, so a few tokens of one sequence
+ * (a draft to verify) may follow each other as rows; different slots are independent.
+ *   R          rows, >= 0 (0: nothing is enqueued); R * n_vheads <= 2^20 (MOE_ERR_TOKENS)
+ *   n_kheads   key/query heads >= 1; n_vheads value heads, a multiple of n_kheads, <= 4096
+ *   d_k, d_v   head widths; both must be 128
+ *   q, k       bf16 [R][n_kheads][128], 16-byte aligned
+ *   v          bf16 [R][n_vheads][128], 16-byte aligned
+ *   alpha      float32 [R][n_vheads], beta float32 [R][n_vheads], 4-byte aligned
+ *   state      float32 [n_slots][n_vheads][128][128] (row j = value channel j), 16-byte aligned
+ *   slot       int32 [R], 4-byte aligned: a row whose slot lies outside [0, n_slots) is
+ *              padding: it touches no state, and its output is zeros
+ *   out        bf16 [R][n_vheads][128], o_t rounded to nearest even, 2-byte aligned
+ * out and state may overlap neither an input nor each other (MOE_ERR_ALIAS).  Status codes as
+ * moe_gdn_scan (MOE_ERR_SHAPE also for n_slots < 1).  May be captured in a graph: slot is
+ * read when the kernel runs. */
+moe_status moe_gdn_step(int32_t R, int32_t n_kheads, int32_t n_vheads, int32_t d_k, int32_t d_v,
+                        const void *q, const void *k, const void *v, const float *alpha,
+                        const float *beta, float *state, int32_t n_slots, const int32_t *slot, void *out,
+                        hipStream_t stream);
 
 #ifdef __cplusplus
 }

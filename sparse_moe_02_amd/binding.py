@@ -46,7 +46,13 @@ MOE_F_HOST_ROUTING = 1 << 6
 EXPORTED = ("moe_plan_create", "moe_plan_destroy", "moe_workspace_init", "moe_workspace_check",
             "moe_forward_prefill", "moe_forward_decode", "moe_forward_decode_batch", "moe_forward_decode_static",
             "moe_pack_qparams",
-            "moe_pack_codes", "moe_status_string", "moe_version", "moe_gdn_scan")
+            "moe_pack_codes", "moe_status_string", "moe_version", "moe_gdn_scan", "moe_gdn_step", "moe_rope_freqs",
+            "moe_rope_append", "moe_paged_attn_workspace", "moe_paged_attn")
+
+# include/attn.h
+MOE_ROPE_NONE, MOE_ROPE_LINEAR, MOE_ROPE_NTK, MOE_ROPE_YARN = range(4)
+MOE_ROPE_INTERLEAVED = 1
+MOE_ATTN_FULL = 1
 
 
 class moe_config(ctypes.Structure):
@@ -70,6 +76,23 @@ class moe_debug_out(ctypes.Structure):
     _fields_ = [("topk_ids", ctypes.c_void_p), ("gates", ctypes.c_void_p), ("counts", ctypes.c_void_p),
                 ("offsets", ctypes.c_void_p), ("row_token", ctypes.c_void_p), ("n_refined", ctypes.c_void_p),
                 ("events", ctypes.c_void_p), ("logits32", ctypes.c_void_p), ("radii32", ctypes.c_void_p)]
+
+
+class moe_heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class moe_paged_kv(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int)]
+
+
+class moe_batch(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("row", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("n_rows", ctypes.c_int32),
+                ("table_cols", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -115,6 +138,20 @@ def lib() -> ctypes.CDLL:
             L.moe_pack_codes.argtypes = [P, P, I64, ctypes.c_int32, P]
             L.moe_gdn_scan.restype = ctypes.c_int
             L.moe_gdn_scan.argtypes = [ctypes.c_int32] * 5 + [P] * 7 + [P]
+            L.moe_gdn_step.restype = ctypes.c_int
+            L.moe_gdn_step.argtypes = [ctypes.c_int32] * 5 + [P] * 6 + [ctypes.c_int32, P, P, P]
+            KV, BA, HD = ctypes.POINTER(moe_paged_kv), ctypes.POINTER(moe_batch), ctypes.POINTER(moe_heads)
+            L.moe_rope_freqs.restype = ctypes.c_int
+            L.moe_rope_freqs.argtypes = [ctypes.c_int32, ctypes.c_double, ctypes.c_int, ctypes.c_double, I64, P, P]
+            L.moe_rope_append.restype = ctypes.c_int
+            L.moe_rope_append.argtypes = [KV, BA, I64, HD, HD, ctypes.c_int32, HD, HD, P, P, ctypes.c_int32,
+                                          ctypes.c_float, ctypes.c_uint32, P]
+            L.moe_paged_attn_workspace.restype = ctypes.c_int
+            L.moe_paged_attn_workspace.argtypes = [KV, I64, ctypes.c_int32, I64, I64, ctypes.c_int32,
+                                                   ctypes.POINTER(SZ)]
+            L.moe_paged_attn.restype = ctypes.c_int
+            L.moe_paged_attn.argtypes = [KV, BA, I64, I64, I64, HD, ctypes.c_int32, HD, P, ctypes.c_float,
+                                         ctypes.c_int32, ctypes.c_uint32, P, SZ, P]
             L.moe_status_string.restype = ctypes.c_char_p
             L.moe_status_string.argtypes = [ctypes.c_int]
             L.moe_version.restype = ctypes.c_char_p
@@ -196,6 +233,41 @@ def moe_gdn_scan(T: int, n_kheads: int, n_vheads: int, d_k: int, d_v: int, q_ptr
                  alpha_ptr: int, beta_ptr: int, state_ptr: int, out_ptr: int, stream: int) -> None:
     _check("moe_gdn_scan", lib().moe_gdn_scan(T, n_kheads, n_vheads, d_k, d_v, q_ptr, k_ptr, v_ptr, alpha_ptr,
                                               beta_ptr, state_ptr, out_ptr, stream))
+
+
+def moe_gdn_step(R: int, n_kheads: int, n_vheads: int, d_k: int, d_v: int, q_ptr: int, k_ptr: int, v_ptr: int,
+                 alpha_ptr: int, beta_ptr: int, state_ptr: int, n_slots: int, slot_ptr: int, out_ptr: int,
+                 stream: int) -> None:
+    _check("moe_gdn_step", lib().moe_gdn_step(R, n_kheads, n_vheads, d_k, d_v, q_ptr, k_ptr, v_ptr, alpha_ptr,
+                                              beta_ptr, state_ptr, n_slots, slot_ptr, out_ptr, stream))
+
+
+def moe_rope_freqs(rot_dim: int, base: float, scaling: int = MOE_ROPE_NONE, factor: float = 1.0, trained: int = 1):
+    """Returns (list of rot_dim / 2 frequencies, mscale)."""
+    out = (ctypes.c_double * max(1, rot_dim // 2))()
+    mscale = ctypes.c_float()
+    _check("moe_rope_freqs", lib().moe_rope_freqs(rot_dim, base, scaling, factor, trained, out, ctypes.byref(mscale)))
+    return list(out), mscale.value
+
+
+def moe_rope_append(kv: moe_paged_kv, batch: moe_batch, T: int, q: moe_heads, q_out: moe_heads, n_heads: int,
+                    k: moe_heads, v: moe_heads, pos_ptr: int | None, inv_freq_ptr: int | None, rot_dim: int,
+                    mscale: float, flags: int, stream: int) -> None:
+    _check("moe_rope_append", lib().moe_rope_append(kv, batch, T, q, q_out, n_heads, k, v, pos_ptr, inv_freq_ptr,
+                                                    rot_dim, mscale, flags, stream))
+
+
+def moe_paged_attn_workspace(kv: moe_paged_kv, T: int, n_seqs: int, max_q: int, max_kv: int, n_heads: int) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_paged_attn_workspace", lib().moe_paged_attn_workspace(kv, T, n_seqs, max_q, max_kv, n_heads, n))
+    return n.value
+
+
+def moe_paged_attn(kv: moe_paged_kv, batch: moe_batch, T: int, max_q: int, max_kv: int, q: moe_heads, n_heads: int,
+                   out: moe_heads, lse_ptr: int | None, scale: float, window: int, flags: int, ws_ptr: int | None,
+                   ws_bytes: int, stream: int) -> None:
+    _check("moe_paged_attn", lib().moe_paged_attn(kv, batch, T, max_q, max_kv, q, n_heads, out, lse_ptr, scale, window,
+                                                  flags, ws_ptr, ws_bytes, stream))
 
 
 def moe_pack_qparams(src_ptr: int, dst_ptr: int, rows: int, k: int, stream: int) -> None:

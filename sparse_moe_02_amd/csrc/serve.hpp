@@ -1,0 +1,74 @@
+// Launch interfaces of the serving operators: rotary append, paged attention, gated delta
+// steps (host side calls these from serve_api.cpp).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+struct Heads {  // [token][head][head_dim] with strides in elements
+  uint16_t *p;
+  int64_t ts, hs;
+};
+
+struct PagedKv {
+  uint16_t *k, *v;
+  int64_t ps, ts, hs;  // page, token and head strides in elements
+  int n_pages, page_shift, n_kv, dim;
+  bool fp16;
+};
+
+struct Batch {
+  const int32_t *q_start, *kv_len, *table, *row;
+  int n_seqs, n_rows, cols;
+};
+
+struct RopeArgs {
+  PagedKv kv;
+  Batch b;
+  Heads q, qo, k, v;  // k.p null: nothing is appended
+  const int32_t *pos;
+  const double *freq;
+  int T, H, R;
+  float mscale;
+  bool interleaved;
+};
+hipError_t launch_rope_append(const RopeArgs &a, hipStream_t s);
+
+constexpr int kAttnRows = 16;   // query rows (token x head of a group) of a small tile
+constexpr int kAttnKeys = 32;   // keys of one block
+
+struct AttnArgs {
+  PagedKv kv;
+  Batch b;
+  Heads q, out;
+  float *lse;      // [T][H] or null
+  float *part;     // [T * H][splits][dim] unnormalised partial outputs (splits > 1)
+  float *part_ml;  // [T * H][splits][2] running maximum (base-2 exponent) and sum
+  int T, H, G;     // G: query heads of one key/value head
+  int tiles;       // bound on the number of row tiles
+  int splits;
+  int window;
+  bool full;
+  float scale_log2;
+};
+// What the launch is shaped by, from host-known sizes alone.
+struct AttnShape {
+  int tiles, splits;
+  size_t ws_bytes, off_ml;
+};
+AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int H, int n_kv, int dim);
+hipError_t launch_paged_attn(const AttnArgs &a, hipStream_t s);
+
+struct GdnStepArgs {
+  const uint16_t *q, *k, *v;
+  const float *alpha, *beta;
+  float *state;
+  const int32_t *slot;
+  uint16_t *out;
+  int R, hk, hv, n_slots;
+};
+hipError_t launch_gdn_step(const GdnStepArgs &a, hipStream_t s);
+
+}  // namespace moe

@@ -1,5 +1,5 @@
-"""Gated DeltaNet prefill scan on device tensors (argument marshalling for
-``moe_gdn_scan`` of ``include/gdn.h``; every step runs in the HIP kernel)."""
+"""Gated DeltaNet prefill scan and decode step on device tensors (argument marshalling for
+``moe_gdn_scan`` and ``moe_gdn_step`` of ``include/gdn.h``; every step runs in the HIP kernels)."""
 
 from __future__ import annotations
 
@@ -35,4 +35,33 @@ def gdn_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Ten
     s = stream if stream is not None else torch.cuda.current_stream(v.device).cuda_stream
     B.moe_gdn_scan(T, hk, hv, dk, dv, _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(state), _ptr(out),
                    s)
+    return out
+
+
+def gdn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Tensor, beta: torch.Tensor,
+             state: torch.Tensor, slot: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """One token each of R rows; row r updates state slot[r] in place, rows of one slot in row
+    order (see ``moe_gdn_step``).  q, k: bf16 [R][n_kheads][128]; v: bf16 [R][n_vheads][128];
+    alpha, beta: float32 [R][n_vheads]; state: float32 [n_slots][n_vheads][128][128]; slot: int32
+    [R] (outside the pool: padding, zeros out).  Returns out (bf16 [R][n_vheads][128]); enqueued on
+    torch's current stream of the tensors' device."""
+    if k.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+        raise ValueError("q, k, v must be [R][heads][128] and state [n_slots][n_vheads][128][128]")
+    R, hk, dk = k.shape
+    hv, dv = v.shape[1], v.shape[2]
+    if out is None:
+        out = torch.empty_like(v)
+    dev = v.device
+    for name, t, dt in (("q", q, torch.bfloat16), ("k", k, torch.bfloat16), ("v", v, torch.bfloat16),
+                        ("alpha", alpha, torch.float32), ("beta", beta, torch.float32),
+                        ("state", state, torch.float32), ("slot", slot, torch.int32), ("out", out, torch.bfloat16)):
+        if t.dtype != dt or not t.is_cuda or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous {dt} tensor on {dev} required")
+    if q.shape != k.shape or v.shape[0] != R or alpha.shape != (R, hv) or beta.shape != (R, hv) or slot.shape != (R,):
+        raise ValueError("shape mismatch")
+    if state.shape[1:] != (hv, dv, dk) or out.shape != v.shape:
+        raise ValueError("state must be [n_slots][n_vheads][d_v][d_k], out as v")
+    with torch.cuda.device(dev):
+        B.moe_gdn_step(R, hk, hv, dk, dv, _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(state),
+                       state.shape[0], _ptr(slot), _ptr(out), torch.cuda.current_stream(dev).cuda_stream)
     return out

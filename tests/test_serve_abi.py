@@ -1,0 +1,228 @@
+"""The serving operators' C ABI on the CPU: host checks return the documented statuses before a
+device is touched (made-up pointers that are never read), and the rotary frequencies."""
+
+import ctypes
+import math
+import os
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+M = 1 << 30  # made-up arrays lie this far apart
+
+
+@pytest.fixture(scope="module")
+def B():
+    from sparse_moe_02_amd import binding
+
+    if not os.path.exists(binding.LIB_PATH):
+        import __graft_entry__
+
+        __graft_entry__.build()
+    return binding
+
+
+NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, TOKENS, DEVICE, ALIAS = 1, 2, 3, 4, 5, 6, 7, 9
+
+
+def _kv(B, **kw):
+    d = dict(k=M, v=2 * M, page_stride=32 * 2 * 128, token_stride=2 * 128, head_stride=128, n_pages=10, page_size=32,
+             n_kv_heads=2, head_dim=128, dtype=B.MOE_BF16)
+    d.update(kw)
+    return B.moe_paged_kv(**d)
+
+
+def _batch(B, **kw):
+    d = dict(q_start=3 * M, kv_len=3 * M + 4096, table=3 * M + 8192, row=None, n_seqs=4, n_rows=4, table_cols=5)
+    d.update(kw)
+    return B.moe_batch(**d)
+
+
+def _status(B, fn, *args):
+    """The status of a call, whatever it is; a valid call stops at the missing GPU."""
+    try:
+        fn(*args)
+    except B.MoeError as e:
+        return e.status
+    return 0
+
+
+def _attn(B, kv=None, batch=None, T=6, max_q=3, max_kv=100, q=None, H=8, out=None, lse=None, scale=0.1, window=0, flags=0,
+          ws=6 * M, wsn=1 << 28):
+    q = q or B.moe_heads(4 * M, 8 * 128, 128)
+    out = out or B.moe_heads(5 * M, 8 * 128, 128)
+    return _status(B, B.moe_paged_attn, kv or _kv(B), batch or _batch(B), T, max_q, max_kv, q, H, out, lse, scale, window,
+                   flags, ws, wsn, 0)
+
+
+def _rope(B, kv=None, batch=None, T=6, q=None, qo=None, H=8, k=None, v=None, pos=None, freq=8 * M, rot=64, flags=0):
+    q = q or B.moe_heads(4 * M, 8 * 128, 128)
+    qo = qo or B.moe_heads(5 * M, 8 * 128, 128)
+    k = k or B.moe_heads(6 * M, 2 * 128, 128)
+    v = v or B.moe_heads(7 * M, 2 * 128, 128)
+    return _status(B, B.moe_rope_append, kv or _kv(B), batch or _batch(B), T, q, qo, H, k, v, pos, freq, rot, 1.0, flags, 0)
+
+
+@pytest.fixture()
+def no_gpu():
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+
+
+def test_valid_calls_reach_the_device_check(B, no_gpu):
+    assert _attn(B) == DEVICE and _rope(B) == DEVICE
+    # slices of one projection's rows, q rotated in place
+    rows = 12 * 128
+    q, k, v = (B.moe_heads(4 * M + 2 * 128 * i, rows, 128) for i in (0, 8, 10))
+    assert _rope(B, q=q, qo=q, k=k, v=v) == DEVICE
+    # keys and values page by page in one allocation; head-major pages
+    assert _attn(B, kv=_kv(B, v=M + 2 * 8192, page_stride=2 * 8192)) == DEVICE
+    assert _attn(B, kv=_kv(B, token_stride=128, head_stride=32 * 128)) == DEVICE
+    # only queries; nothing rotated
+    none = B.moe_heads(None, 0, 0)
+    assert _rope(B, kv=_kv(B, k=None, v=None), k=none, v=none) == DEVICE
+    assert _rope(B, freq=None, rot=0) == DEVICE
+    assert _rope(B, q=none, qo=none, H=0) == DEVICE
+
+
+def test_no_tokens_is_no_work(B):
+    assert _attn(B, T=0) == 0 and _rope(B, T=0) == 0
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(k=None), NULL), (dict(v=None), NULL), (dict(k=M + 8), ALIGN), (dict(dtype=2), DTYPE), (dict(dtype=9), DTYPE),
+    (dict(head_dim=96), SHAPE), (dict(head_dim=0), SHAPE), (dict(n_kv_heads=0), SHAPE), (dict(n_pages=0), SHAPE),
+    (dict(page_size=8), SHAPE), (dict(page_size=48), SHAPE), (dict(page_size=0), SHAPE), (dict(page_size=1 << 17), SHAPE),
+    (dict(page_stride=100), ALIGN), (dict(token_stride=-8), SHAPE), (dict(head_stride=0), SHAPE),
+    (dict(token_stride=128), SHAPE),             # tokens share places
+    (dict(page_stride=32 * 2 * 128 - 8), SHAPE),  # pages overlap
+    (dict(token_stride=1 << 30), SHAPE),          # a page spans too much
+])
+def test_bad_caches(B, kw, status):
+    assert _attn(B, kv=_kv(B, **kw)) == status
+    assert _rope(B, kv=_kv(B, **kw)) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q_start=None), NULL), (dict(kv_len=None), NULL), (dict(table=None), NULL), (dict(n_seqs=0), SHAPE),
+    (dict(n_seqs=65536, n_rows=65536), SHAPE), (dict(n_rows=3), SHAPE), (dict(table_cols=0), SHAPE),
+    (dict(table_cols=1 << 26), SHAPE), (dict(q_start=3 * M + 2), ALIGN), (dict(row=3 * M + 1), ALIGN),
+])
+def test_bad_batches(B, kw, status):
+    assert _attn(B, batch=_batch(B, **kw)) == status
+    assert _rope(B, batch=_batch(B, **kw)) == status
+
+
+def test_bad_attention_arguments(B):
+    H = B.moe_heads
+    assert _attn(B, T=-1) == TOKENS and _attn(B, T=(1 << 20) + 1) == TOKENS
+    assert _attn(B, H=0) == SHAPE and _attn(B, H=7) == SHAPE and _attn(B, H=8192) == SHAPE
+    assert _attn(B, kv=_kv(B, n_kv_heads=1, token_stride=128), T=1 << 20, H=256, wsn=1 << 60) == TOKENS
+    assert _attn(B, max_q=-1) == SHAPE and _attn(B, max_kv=-1) == SHAPE
+    assert _attn(B, window=-1) == SHAPE and _attn(B, window=5, flags=1) == SHAPE and _attn(B, flags=2) == SHAPE
+    assert _attn(B, scale=math.nan) == SHAPE and _attn(B, scale=math.inf) == SHAPE
+    assert _attn(B, q=H(None, 1024, 128)) == NULL and _attn(B, out=H(None, 1024, 128)) == NULL
+    assert _attn(B, q=H(4 * M + 4, 1024, 128)) == ALIGN and _attn(B, q=H(4 * M, 1028, 128)) == ALIGN
+    assert _attn(B, q=H(4 * M, -1024, 128)) == SHAPE
+    assert _attn(B, out=H(5 * M, 512, 128)) == SHAPE and _attn(B, out=H(5 * M, 1024, 64)) == SHAPE
+    assert _attn(B, lse=9 * M + 2) == ALIGN
+    assert _attn(B, ws=None, max_kv=5000) == WORKSPACE and _attn(B, wsn=100, max_kv=5000) == WORKSPACE
+    assert _attn(B, ws=6 * M + 128, max_kv=5000) == ALIGN
+    q = H(4 * M, 1024, 128)
+    assert _attn(B, q=q, out=q) == ALIAS
+    assert _attn(B, out=H(M + 256, 1024, 128)) == ALIAS       # in the cache
+    assert _attn(B, out=H(3 * M + 4096, 1024, 128)) == ALIAS  # over the lengths
+    assert _attn(B, lse=5 * M + 64) == ALIAS and _attn(B, lse=4 * M) == ALIAS
+    assert _attn(B, ws=5 * M, max_kv=5000) == ALIAS
+
+
+def test_workspace_size(B):
+    kv = _kv(B)
+    one = B.moe_paged_attn_workspace(kv, 1, 1, 1, 4096, 8)
+    assert one >= 2 * 8 * (128 + 2) * 4
+    assert B.moe_paged_attn_workspace(kv, 100000, 1, 100000, 100000, 8) == 0
+    assert B.moe_paged_attn_workspace(kv, 0, 1, 1, 4096, 8) == 0
+    assert _status(B, B.moe_paged_attn_workspace, kv, 1, 0, 1, 1, 8) == SHAPE
+    assert _status(B, B.moe_paged_attn_workspace, _kv(B, dtype=2), 1, 1, 1, 1, 8) == DTYPE
+
+
+def test_bad_rope_arguments(B):
+    H = B.moe_heads
+    assert _rope(B, T=-1) == TOKENS and _rope(B, T=(1 << 20) + 1) == TOKENS
+    assert _rope(B, H=-1) == SHAPE and _rope(B, H=5000) == SHAPE
+    assert _rope(B, rot=63) == SHAPE and _rope(B, rot=130) == SHAPE and _rope(B, rot=-2) == SHAPE
+    assert _rope(B, flags=2) == SHAPE
+    assert _rope(B, freq=None) == NULL and _rope(B, freq=8 * M + 4) == ALIGN and _rope(B, pos=9 * M + 2) == ALIGN
+    assert _rope(B, k=H(None, 256, 128)) == NULL and _rope(B, v=H(None, 256, 128)) == NULL
+    assert _rope(B, k=H(6 * M + 8, 256, 128)) == ALIGN
+    assert _rope(B, qo=H(5 * M, 512, 128)) == SHAPE
+    assert _rope(B, qo=H(4 * M + 1024 * 2, 1024, 128)) == ALIAS  # q, one token on
+    assert _rope(B, qo=H(6 * M, 1024, 128)) == ALIAS             # over k
+    assert _rope(B, qo=H(M, 1024, 128)) == ALIAS                 # in the cache
+    assert _rope(B, k=H(M, 256, 128)) == ALIAS
+    assert _rope(B, kv=_kv(B, v=M + 8192)) == ALIAS              # planes overlap
+    assert _rope(B, qo=H(8 * M, 1024, 128)) == ALIAS             # over the frequencies
+    assert _rope(B, pos=5 * M) == ALIAS
+    assert _rope(B, batch=_batch(B, kv_len=5 * M)) == ALIAS
+
+
+def test_bad_steps(B):
+    def step(R=3, hk=2, hv=4, dk=128, dv=128, q=M, k=2 * M, v=3 * M, a=4 * M, b=5 * M, state=6 * M, n=8, slot=7 * M,
+             out=8 * M):
+        return _status(B, B.moe_gdn_step, R, hk, hv, dk, dv, q, k, v, a, b, state, n, slot, out, 0)
+
+    assert step(R=-1) == TOKENS and step(R=1 << 20) == TOKENS
+    assert step(dk=64) == SHAPE and step(hv=3) == SHAPE and step(hk=0) == SHAPE and step(n=0) == SHAPE
+    assert step(hv=8192) == SHAPE
+    for name in ("q", "k", "v", "a", "b", "state", "slot", "out"):
+        assert step(**{name: None}) == NULL, name
+    assert step(q=M + 8) == ALIGN and step(slot=7 * M + 2) == ALIGN and step(state=6 * M + 4) == ALIGN
+    assert step(out=6 * M) == ALIAS and step(out=3 * M) == ALIAS and step(slot=6 * M + 64) == ALIAS
+    assert step(R=0) == 0
+
+
+def test_rope_frequencies(B):
+    f, m = B.moe_rope_freqs(64, 1e4)
+    assert m == 1.0 and all(abs(x - 1e4 ** (-2 * i / 64)) <= 1e-15 for i, x in enumerate(f))
+    g, _ = B.moe_rope_freqs(64, 1e4, B.MOE_ROPE_LINEAR, 4.0)
+    assert all(abs(a - b / 4) <= 1e-16 for a, b in zip(g, f))
+    n, _ = B.moe_rope_freqs(64, 1e4, B.MOE_ROPE_NTK, 4.0)
+    assert n[0] == 1.0 and abs(n[31] * 4 / f[31] - 1) < 1e-12  # the slowest pair is stretched by the factor
+    y, m = B.moe_rope_freqs(64, 1e4, B.MOE_ROPE_YARN, 4.0, 4096)
+    assert abs(m - (0.1 * math.log(4) + 1)) < 1e-7
+    for a, b in zip(y, f):
+        turns = 4096 * b / (2 * math.pi)
+        keep = min(1.0, max(0.0, (turns - 1) / 31))
+        assert abs(a - (b * keep + b / 4 * (1 - keep))) <= 1e-15
+    assert y[0] == f[0] and y[31] == f[31] / 4
+
+
+@pytest.mark.parametrize("args", [(63, 1e4), (0, 1e4), (258, 1e4), (64, 1.0), (64, math.nan), (64, math.inf),
+                                  (64, 1e4, 4, 2.0), (64, 1e4, 1, 0.5), (64, 1e4, 1, math.nan), (64, 1e4, 3, 2.0, 0),
+                                  (2, 1e4, 2, 2.0)])
+def test_bad_frequencies(B, args):
+    assert _status(B, B.moe_rope_freqs, *args) == SHAPE
+
+
+def test_struct_layouts(B):
+    assert ctypes.sizeof(B.moe_heads) == 24 and ctypes.sizeof(B.moe_paged_kv) == 64 and ctypes.sizeof(B.moe_batch) == 48
+
+
+def test_python_wrappers_refuse():
+    torch = pytest.importorskip("torch")
+    from sparse_moe_02_amd.attn import paged_attn, rope_append, rope_freqs
+    from sparse_moe_02_amd.gdn import gdn_step
+
+    z = torch.zeros
+    i32 = dict(dtype=torch.int32)
+    q = z((2, 4, 64), dtype=torch.bfloat16)
+    kc = z((3, 16, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):  # host tensors
+        paged_attn(q, kc, kc, z((1, 2), **i32), z(2, **i32), z(1, **i32), 2, 2)
+    with pytest.raises(ValueError):
+        rope_append(q, q, q, kc, kc, z((1, 2), **i32), z(2, **i32), z(1, **i32), None)
+    with pytest.raises(ValueError):
+        gdn_step(z((1, 1, 128)), z((1, 1, 128)), z((1, 1, 128)), z((1, 1)), z((1, 1)), z((1, 1, 128, 128)), z(1, **i32))
+    with pytest.raises(ValueError):
+        rope_freqs(64, scaling="other")
