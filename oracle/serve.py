@@ -115,3 +115,92 @@ def gdn_step(q, k, v, alpha, beta, state, slot):
             S[slot[r], h] = A
             out[r, h] = A @ qq
     return out, S
+
+
+class Pool:
+    """The paged cache's bookkeeping by its definition in ``include/pages.h``.  cache: an array
+    [plane][page] of page contents.  A call with an error changes nothing and returns its name."""
+
+    def __init__(self, table, lens, refs, page_size, cache=None):
+        self.table, self.lens, self.refs = (np.array(x, np.int64) for x in (table, lens, refs))
+        self.page, self.cache = page_size, None if cache is None else np.array(cache)
+
+    def _count(self, n):
+        return -(-int(n) // self.page)
+
+    def _fresh(self, n):
+        return [p for p in range(len(self.refs)) if self.refs[p] <= 0][:n]
+
+    def _known(self, seqs):
+        cap = self.table.shape[1] * self.page
+        return all(0 <= s < len(self.lens) and 0 <= self.lens[s] <= cap for s in seqs)
+
+    def _held(self, s):
+        return self.table[s, :self._count(self.lens[s])]
+
+    def _sound(self, seqs):
+        return all(((self._held(s) >= 0) & (self._held(s) < len(self.refs))).all() for s in seqs)
+
+    def grow(self, seqs, tokens):
+        if len(set(seqs)) != len(seqs) or not self._known(seqs):
+            return "shape"
+        cap = self.table.shape[1] * self.page
+        if any(t < 0 or self.lens[s] + t > cap for s, t in zip(seqs, tokens)):
+            return "shape"
+        need = [self._count(self.lens[s] + t) - self._count(self.lens[s]) for s, t in zip(seqs, tokens)]
+        fresh = self._fresh(sum(need))
+        if len(fresh) < sum(need):
+            return "alloc"
+        for s, t, n in zip(seqs, tokens, need):
+            at = self._count(self.lens[s])
+            for c in range(n):
+                p = fresh.pop(0)
+                self.table[s, at + c], self.refs[p] = p, 1
+            self.lens[s] += t
+        return ""
+
+    def fork(self, src, dst):
+        if not self._known(src) or not self._known(dst) or len(set(dst)) != len(dst) or set(src) & set(dst):
+            return "shape"
+        if any(self.lens[d] != 0 for d in dst) or not self._sound(src):
+            return "shape"
+        part = [s for s in src if self.lens[s] % self.page]
+        fresh = self._fresh(len(part))
+        if len(fresh) < len(part):
+            return "alloc"
+        for s, d in zip(src, dst):
+            full = int(self.lens[s]) // self.page
+            for c in range(full):
+                self.table[d, c] = self.table[s, c]
+                self.refs[self.table[s, c]] += 1
+            if self.lens[s] % self.page:
+                p = fresh.pop(0)
+                self.cache[:, p] = self.cache[:, self.table[s, full]]
+                self.table[d, full], self.refs[p] = p, 1
+            self.lens[d] = self.lens[s]
+        return ""
+
+    def free(self, seqs):
+        if len(set(seqs)) != len(seqs) or not self._known(seqs) or not self._sound(seqs):
+            return "shape"
+        for s in seqs:
+            for p in self._held(s):
+                self.refs[p] -= 1
+            self.lens[s] = 0
+        return ""
+
+    def compact(self):
+        every = range(len(self.lens))
+        if not self._known(every) or not self._sound(every):
+            return "shape"
+        used = [p for p in range(len(self.refs)) if self.refs[p] > 0]
+        move = [p for p in used if p >= len(used)]
+        hole = [p for p in range(len(used)) if self.refs[p] <= 0]
+        to = dict(zip(move, hole))
+        for a, b in to.items():
+            self.cache[:, b] = self.cache[:, a]
+            self.refs[b], self.refs[a] = self.refs[a], 0
+        for s in every:
+            for c in range(self._count(self.lens[s])):
+                self.table[s, c] = to.get(int(self.table[s, c]), self.table[s, c])
+        return ""

@@ -47,7 +47,8 @@ EXPORTED = ("moe_plan_create", "moe_plan_destroy", "moe_workspace_init", "moe_wo
             "moe_forward_prefill", "moe_forward_decode", "moe_forward_decode_batch", "moe_forward_decode_static",
             "moe_pack_qparams",
             "moe_pack_codes", "moe_status_string", "moe_version", "moe_gdn_scan", "moe_gdn_step", "moe_rope_freqs",
-            "moe_rope_append", "moe_paged_attn_workspace", "moe_paged_attn")
+            "moe_rope_append", "moe_paged_attn_workspace", "moe_paged_attn", "moe_pages_workspace", "moe_pages_grow",
+            "moe_pages_fork", "moe_pages_free", "moe_pages_compact", "moe_pages_copy", "moe_pages_check")
 
 # include/attn.h
 MOE_ROPE_NONE, MOE_ROPE_LINEAR, MOE_ROPE_NTK, MOE_ROPE_YARN = range(4)
@@ -93,6 +94,17 @@ class moe_batch(ctypes.Structure):
     _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p),
                 ("row", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("n_rows", ctypes.c_int32),
                 ("table_cols", ctypes.c_int32)]
+
+
+class moe_pages(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("table_cols", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
+class moe_page_memory(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("plane_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("page_bytes", ctypes.c_int64), ("n_planes", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -152,6 +164,21 @@ def lib() -> ctypes.CDLL:
             L.moe_paged_attn.restype = ctypes.c_int
             L.moe_paged_attn.argtypes = [KV, BA, I64, I64, I64, HD, ctypes.c_int32, HD, P, ctypes.c_float,
                                          ctypes.c_int32, ctypes.c_uint32, P, SZ, P]
+            PG, PM, I32 = ctypes.POINTER(moe_pages), ctypes.POINTER(moe_page_memory), ctypes.c_int32
+            L.moe_pages_workspace.restype = ctypes.c_int
+            L.moe_pages_workspace.argtypes = [PG, I32, ctypes.POINTER(SZ)]
+            L.moe_pages_grow.restype = ctypes.c_int
+            L.moe_pages_grow.argtypes = [PG, PG, I32, P, P, P, P, SZ, P]
+            L.moe_pages_fork.restype = ctypes.c_int
+            L.moe_pages_fork.argtypes = [PG, PG, PM, I32, P, P, P, P, SZ, P]
+            L.moe_pages_free.restype = ctypes.c_int
+            L.moe_pages_free.argtypes = [PG, PG, I32, P, P, P, SZ, P]
+            L.moe_pages_compact.restype = ctypes.c_int
+            L.moe_pages_compact.argtypes = [PG, PG, PM, P, P, SZ, P]
+            L.moe_pages_copy.restype = ctypes.c_int
+            L.moe_pages_copy.argtypes = [PM, I32, I32, P, P, P]
+            L.moe_pages_check.restype = ctypes.c_int
+            L.moe_pages_check.argtypes = [P, P]
             L.moe_status_string.restype = ctypes.c_char_p
             L.moe_status_string.argtypes = [ctypes.c_int]
             L.moe_version.restype = ctypes.c_char_p
@@ -268,6 +295,47 @@ def moe_paged_attn(kv: moe_paged_kv, batch: moe_batch, T: int, max_q: int, max_k
                    ws_bytes: int, stream: int) -> None:
     _check("moe_paged_attn", lib().moe_paged_attn(kv, batch, T, max_q, max_kv, q, n_heads, out, lse_ptr, scale, window,
                                                   flags, ws_ptr, ws_bytes, stream))
+
+
+def moe_pages_workspace(pages: moe_pages, n: int) -> int:
+    size = ctypes.c_size_t()
+    _check("moe_pages_workspace", lib().moe_pages_workspace(pages, n, size))
+    return size.value
+
+
+def moe_pages_grow(src: moe_pages, dst: moe_pages, n: int, seqs_ptr: int | None, tokens_ptr: int | None,
+                   error_ptr: int, ws_ptr: int, ws_bytes: int, stream: int) -> None:
+    _check("moe_pages_grow", lib().moe_pages_grow(src, dst, n, seqs_ptr, tokens_ptr, error_ptr, ws_ptr, ws_bytes, stream))
+
+
+def moe_pages_fork(src: moe_pages, dst: moe_pages, mem: moe_page_memory, n: int, src_ptr: int | None,
+                   dst_ptr: int | None, error_ptr: int, ws_ptr: int, ws_bytes: int, stream: int) -> None:
+    _check("moe_pages_fork", lib().moe_pages_fork(src, dst, mem, n, src_ptr, dst_ptr, error_ptr, ws_ptr, ws_bytes,
+                                                  stream))
+
+
+def moe_pages_free(src: moe_pages, dst: moe_pages, n: int, seqs_ptr: int | None, error_ptr: int, ws_ptr: int,
+                   ws_bytes: int, stream: int) -> None:
+    _check("moe_pages_free", lib().moe_pages_free(src, dst, n, seqs_ptr, error_ptr, ws_ptr, ws_bytes, stream))
+
+
+def moe_pages_compact(src: moe_pages, dst: moe_pages, mem: moe_page_memory, error_ptr: int, ws_ptr: int,
+                      ws_bytes: int, stream: int) -> None:
+    _check("moe_pages_compact", lib().moe_pages_compact(src, dst, mem, error_ptr, ws_ptr, ws_bytes, stream))
+
+
+def moe_pages_copy(mem: moe_page_memory, n_pages: int, n: int, src_ptr: int | None, dst_ptr: int | None,
+                   stream: int) -> None:
+    _check("moe_pages_copy", lib().moe_pages_copy(mem, n_pages, n, src_ptr, dst_ptr, stream))
+
+
+def moe_pages_check(error_ptr: int, stream: int) -> int:
+    """The first error that the pool's calls left (MOE_OK, MOE_ERR_SHAPE or MOE_ERR_ALLOC: returned,
+    not raised); raises on other statuses."""
+    st = lib().moe_pages_check(error_ptr, stream)
+    if st not in (MOE_OK, MOE_ERR_SHAPE, MOE_ERR_ALLOC):
+        raise MoeError("moe_pages_check", st)
+    return st
 
 
 def moe_pack_qparams(src_ptr: int, dst_ptr: int, rows: int, k: int, stream: int) -> None:

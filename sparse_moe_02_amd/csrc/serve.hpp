@@ -71,4 +71,40 @@ struct GdnStepArgs {
 };
 hipError_t launch_gdn_step(const GdnStepArgs &a, hipStream_t s);
 
+// Paged cache bookkeeping (pages.hip).
+struct Pages {
+  int32_t *table, *len, *refs;
+};
+struct PageMem {
+  uint8_t *base;
+  int64_t plane, page, bytes;  // strides and size in bytes
+  int n_planes;
+};
+constexpr int kPageGroup = 4096;  // pages whose free ones are counted by one workgroup
+
+enum class PageOp { Grow, Fork, Free, Compact };
+
+struct PageArgs {
+  Pages in, out;
+  PageMem mem;
+  int n_seqs, cols, n_pages, page_shift;
+  int n;               // requests
+  const int32_t *a, *b;  // grow: sequences, tokens; fork: sources, destinations; free: sequences
+  int32_t *error;
+  // workspace
+  int32_t *hdr;        // [0] status of the requests, [1] fresh pages needed, [2] pages that move
+  int32_t *free_n;     // [groups] free pages of the group
+  int32_t *bad;        // [requests, or sequences (compact)] a table entry lies outside the pool
+  int32_t *base;       // [n + 1] fresh pages needed before the request
+  int32_t *col, *longer;  // [n] grow: pages held before, length after
+  int32_t *fresh;      // [n] fork: the request's fresh page; compact: [n_pages] free page by rank
+  int32_t *moved;      // compact: [n_pages] page that moves, by rank from the pool's end
+};
+struct PageWs {
+  size_t free_n, bad, base, col, longer, fresh, moved, total;
+};
+PageWs page_ws(int n_seqs, int n_pages, int n);
+hipError_t launch_pages(PageOp op, const PageArgs &a, hipStream_t s);
+hipError_t launch_pages_copy(const PageMem &m, int n_pages, int n, const int32_t *src, const int32_t *dst, hipStream_t s);
+
 }  // namespace moe

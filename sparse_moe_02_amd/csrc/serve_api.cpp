@@ -1,4 +1,5 @@
-// Host side of the C ABI declared in include/attn.h and of moe_gdn_step (include/gdn.h):
+// Host side of the C ABI declared in include/attn.h and include/pages.h and of moe_gdn_step
+// (include/gdn.h):
 // argument checks and launches.  Every check precedes every launch.
 #include <hip/hip_runtime.h>
 
@@ -10,6 +11,7 @@
 
 #include "../../include/attn.h"
 #include "../../include/gdn.h"
+#include "../../include/pages.h"
 #include "kernels.hpp"
 #include "serve.hpp"
 
@@ -181,6 +183,87 @@ AttnShape shape_of(int64_t T, int32_t n_seqs, int64_t max_q, int64_t max_kv, int
                    const moe_paged_kv &kv) {
   return attn_shape(T, n_seqs, std::min<int64_t>(max_q, kMaxTokens), std::min<int64_t>(max_kv, int64_t(1) << 30), n_heads,
                     kv.n_kv_heads, kv.head_dim);
+}
+
+// ------------------------------------------------------------------------ pages
+
+moe_status check_pages(const moe_pages *p) {
+  if (!p || !p->table || !p->len || !p->refs) return MOE_ERR_NULL;
+  if (p->n_seqs < 1 || p->n_seqs > 65535 || p->table_cols < 1 || p->n_pages < 1 || p->n_pages > 1 << 26)
+    return MOE_ERR_SHAPE;
+  if (p->page_size < 1 || p->page_size > 65536 || (p->page_size & (p->page_size - 1))) return MOE_ERR_SHAPE;
+  if ((int64_t)p->table_cols * p->page_size > int64_t(1) << 30 || (int64_t)p->n_seqs * p->table_cols >= int64_t(1) << 31)
+    return MOE_ERR_SHAPE;
+  if (!aligned(p->table, 4) || !aligned(p->len, 4) || !aligned(p->refs, 4)) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+moe_status check_memory(const moe_page_memory *m, int32_t n_pages) {
+  if (!m || !m->base) return MOE_ERR_NULL;
+  if (m->n_planes < 1 || m->n_planes > 65535 || m->page_bytes < 16 || m->page_bytes > int64_t(1) << 30) return MOE_ERR_SHAPE;
+  if (m->plane_stride < 0 || m->page_stride < 0) return MOE_ERR_SHAPE;
+  if (!aligned(m->base, 16) || m->plane_stride % 16 || m->page_stride % 16 || m->page_bytes % 16) return MOE_ERR_ALIGN;
+  Dim d[2] = {{m->plane_stride, m->n_planes}, {m->page_stride, n_pages}};
+  return distinct(d, 2, m->page_bytes) ? MOE_OK : MOE_ERR_SHAPE;
+}
+Span memory_span(const moe_page_memory &m, int32_t n_pages) {
+  return Span{m.base, (uint64_t)((m.n_planes - 1) * m.plane_stride + (n_pages - 1) * m.page_stride + m.page_bytes)};
+}
+PageMem dev_memory(const moe_page_memory &m) {
+  return PageMem{static_cast<uint8_t *>(m.base), m.plane_stride, m.page_stride, m.page_bytes, m.n_planes};
+}
+
+// The checks that every call on a pool shares, and its launch.  x, y: the requests' arrays.
+moe_status pages_call(PageOp op, const moe_pages *in, const moe_pages *out, const moe_page_memory *mem, int32_t n,
+                      const int32_t *x, const int32_t *y, int32_t *error, void *ws, size_t ws_bytes, hipStream_t stream) {
+  const bool has_mem = op == PageOp::Fork || op == PageOp::Compact;
+  const bool has_y = op == PageOp::Grow || op == PageOp::Fork;
+  moe_status st = check_pages(in);
+  if (st != MOE_OK || (st = check_pages(out)) != MOE_OK) return st;
+  if (in->n_seqs != out->n_seqs || in->table_cols != out->table_cols || in->n_pages != out->n_pages ||
+      in->page_size != out->page_size)
+    return MOE_ERR_SHAPE;
+  if (has_mem && (st = check_memory(mem, in->n_pages)) != MOE_OK) return st;
+  if (n < 0 || n > in->n_seqs) return MOE_ERR_SHAPE;
+  if (!error || (n > 0 && (!x || (has_y && !y)))) return MOE_ERR_NULL;
+  if (!aligned(error, 4) || !aligned(x, 4) || !aligned(y, 4)) return MOE_ERR_ALIGN;
+  const PageWs w = page_ws(in->n_seqs, in->n_pages, n);
+  if (!ws || ws_bytes < w.total) return MOE_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return MOE_ERR_ALIGN;
+  const uint64_t nt = 4 * (uint64_t)in->n_seqs * in->table_cols, nl = 4 * (uint64_t)in->n_seqs, nr = 4 * (uint64_t)in->n_pages;
+  const Span ti{in->table, nt}, li{in->len, nl}, ri{in->refs, nr}, to{out->table, nt}, lo{out->len, nl}, ro{out->refs, nr};
+  const bool same = in->table == out->table && in->len == out->len && in->refs == out->refs;
+  const Span sx{n ? x : nullptr, 4 * (uint64_t)n}, sy{n && has_y ? y : nullptr, 4 * (uint64_t)n}, se{error, 4}, sw{ws, w.total};
+  const Span sm = has_mem ? memory_span(*mem, in->n_pages) : Span{nullptr, 0};
+  // everything apart from each other, but the pools where they are one
+  const Span all[] = {to, lo, ro, se, sw, sm, sx, sy, ti, li, ri};
+  const int n_all = same ? 8 : 11, writes = 6;
+  for (int i = 0; i < writes; ++i)
+    for (int j = i + 1; j < n_all; ++j)
+      if (overlap(all[i], all[j])) return MOE_ERR_ALIAS;
+  if ((st = device_ok()) != MOE_OK) return st;
+  if (same && n == 0 && op != PageOp::Compact) return MOE_OK;
+  PageArgs a{};
+  a.in = Pages{in->table, in->len, in->refs};
+  a.out = Pages{out->table, out->len, out->refs};
+  if (has_mem) a.mem = dev_memory(*mem);
+  a.n_seqs = in->n_seqs;
+  a.cols = in->table_cols;
+  a.n_pages = in->n_pages;
+  a.page_shift = __builtin_ctz((unsigned)in->page_size);
+  a.n = n;
+  a.a = x;
+  a.b = y;
+  a.error = error;
+  auto at = [&](size_t o) { return reinterpret_cast<int32_t *>(static_cast<char *>(ws) + o); };
+  a.hdr = at(0);
+  a.free_n = at(w.free_n);
+  a.bad = at(w.bad);
+  a.base = at(w.base);
+  a.col = at(w.col);
+  a.longer = at(w.longer);
+  a.fresh = at(w.fresh);
+  a.moved = at(w.moved);
+  return launch_pages(op, a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 }  // namespace
@@ -366,6 +449,58 @@ moe_status moe_gdn_step(int32_t R, int32_t n_kheads, int32_t n_vheads, int32_t d
   a.hv = n_vheads;
   a.n_slots = n_slots;
   return launch_gdn_step(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_pages_workspace(const moe_pages *pages, int32_t n, size_t *bytes) {
+  if (!pages || !bytes) return MOE_ERR_NULL;
+  if (pages->n_seqs < 1 || pages->n_seqs > 65535 || pages->n_pages < 1 || pages->n_pages > 1 << 26) return MOE_ERR_SHAPE;
+  if (n < 0 || n > pages->n_seqs) return MOE_ERR_SHAPE;
+  *bytes = page_ws(pages->n_seqs, pages->n_pages, n).total;
+  return MOE_OK;
+}
+
+moe_status moe_pages_grow(const moe_pages *in, const moe_pages *out, int32_t n, const int32_t *seqs,
+                          const int32_t *tokens, int32_t *error, void *workspace, size_t workspace_bytes,
+                          hipStream_t stream) {
+  return pages_call(PageOp::Grow, in, out, nullptr, n, seqs, tokens, error, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_pages_fork(const moe_pages *in, const moe_pages *out, const moe_page_memory *mem, int32_t n,
+                          const int32_t *src, const int32_t *dst, int32_t *error, void *workspace,
+                          size_t workspace_bytes, hipStream_t stream) {
+  return pages_call(PageOp::Fork, in, out, mem, n, src, dst, error, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_pages_free(const moe_pages *in, const moe_pages *out, int32_t n, const int32_t *seqs, int32_t *error,
+                          void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  return pages_call(PageOp::Free, in, out, nullptr, n, seqs, nullptr, error, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_pages_compact(const moe_pages *in, const moe_pages *out, const moe_page_memory *mem, int32_t *error,
+                             void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  return pages_call(PageOp::Compact, in, out, mem, 0, nullptr, nullptr, error, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_pages_copy(const moe_page_memory *mem, int32_t n_pages, int32_t n, const int32_t *src,
+                          const int32_t *dst, hipStream_t stream) {
+  if (n_pages < 1 || n_pages > 1 << 26 || n < 0 || n > 1 << 20) return MOE_ERR_SHAPE;
+  moe_status st = check_memory(mem, n_pages);
+  if (st != MOE_OK) return st;
+  if (n == 0) return MOE_OK;
+  if (!src || !dst) return MOE_ERR_NULL;
+  if (!aligned(src, 4) || !aligned(dst, 4)) return MOE_ERR_ALIGN;
+  const Span sm = memory_span(*mem, n_pages);
+  if (overlap(sm, {src, 4 * (uint64_t)n}) || overlap(sm, {dst, 4 * (uint64_t)n})) return MOE_ERR_ALIAS;
+  if ((st = device_ok()) != MOE_OK) return st;
+  return launch_pages_copy(dev_memory(*mem), n_pages, n, src, dst, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_pages_check(const int32_t *error, hipStream_t stream) {
+  if (!error) return MOE_ERR_NULL;
+  int32_t e = 0;
+  if (hipMemcpyAsync(&e, error, 4, hipMemcpyDeviceToHost, stream) != hipSuccess || hipStreamSynchronize(stream) != hipSuccess)
+    return MOE_ERR_HIP;
+  return (moe_status)e;
 }
 
 }  // extern "C"

@@ -226,3 +226,105 @@ def test_python_wrappers_refuse():
         gdn_step(z((1, 1, 128)), z((1, 1, 128)), z((1, 1, 128)), z((1, 1)), z((1, 1)), z((1, 1, 128, 128)), z(1, **i32))
     with pytest.raises(ValueError):
         rope_freqs(64, scaling="other")
+
+
+def _pool(B, base=M, **kw):
+    d = dict(table=base, len=base + (1 << 20), refs=base + (2 << 20), n_seqs=8, table_cols=10, n_pages=100, page_size=16)
+    d.update(kw)
+    return B.moe_pages(**d)
+
+
+def _mem(B, **kw):
+    d = dict(base=5 * M, plane_stride=100 * 512, page_stride=512, page_bytes=512, n_planes=4)
+    d.update(kw)
+    return B.moe_page_memory(**d)
+
+
+def _calls(B, pin=None, pout=None, mem=None, n=3, x=8 * M, y=9 * M, err=10 * M, ws=11 * M, wsn=1 << 20):
+    pin = pin or _pool(B)
+    pout = pout or pin
+    mem = mem or _mem(B)
+    return {"grow": _status(B, B.moe_pages_grow, pin, pout, n, x, y, err, ws, wsn, 0),
+            "fork": _status(B, B.moe_pages_fork, pin, pout, mem, n, x, y, err, ws, wsn, 0),
+            "free": _status(B, B.moe_pages_free, pin, pout, n, x, err, ws, wsn, 0),
+            "compact": _status(B, B.moe_pages_compact, pin, pout, mem, err, ws, wsn, 0)}
+
+
+ALL = ("grow", "fork", "free", "compact")
+
+
+def test_valid_pool_calls_reach_the_device_check(B, no_gpu):
+    assert set(_calls(B).values()) == {DEVICE}
+    assert set(_calls(B, pout=_pool(B, 3 * M)).values()) == {DEVICE}
+    assert set(_calls(B, mem=_mem(B, plane_stride=512, page_stride=4 * 512)).values()) == {DEVICE}
+    assert _status(B, B.moe_pages_copy, _mem(B), 100, 5, M, 2 * M, 0) == DEVICE
+    assert _status(B, B.moe_pages_copy, _mem(B), 100, 0, None, None, 0) == 0
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(table=None), NULL), (dict(len=None), NULL), (dict(refs=None), NULL), (dict(n_seqs=0), SHAPE),
+    (dict(n_seqs=65536), SHAPE), (dict(table_cols=0), SHAPE), (dict(table_cols=1 << 27), SHAPE), (dict(n_pages=0), SHAPE),
+    (dict(n_pages=(1 << 26) + 1), SHAPE), (dict(page_size=24), SHAPE), (dict(page_size=0), SHAPE), (dict(len=M + 2), ALIGN),
+])
+def test_bad_pools(B, kw, status):
+    assert set(_calls(B, pin=_pool(B, **kw)).values()) == {status}
+    assert set(_calls(B, pout=_pool(B, 3 * M, **kw)).values()) == {status}
+
+
+def test_pools_of_other_sizes(B):
+    for kw in (dict(n_seqs=7), dict(table_cols=9), dict(n_pages=99), dict(page_size=32)):
+        assert set(_calls(B, pout=_pool(B, 3 * M, **kw)).values()) == {SHAPE}
+
+
+def test_bad_pool_arguments(B):
+    def only(names, status, **kw):
+        got = _calls(B, **kw)
+        for name in names:
+            assert got[name] == status, (name, kw, got)
+
+    req = ("grow", "fork", "free")
+    only(req, SHAPE, n=-1)
+    only(req, SHAPE, n=9)
+    only(req, NULL, x=None)
+    only(("grow", "fork"), NULL, y=None)
+    only(ALL, NULL, err=None)
+    only(req, ALIGN, x=8 * M + 2)
+    only(ALL, ALIGN, err=10 * M + 2)
+    only(ALL, WORKSPACE, ws=None)
+    only(ALL, WORKSPACE, wsn=100)
+    only(ALL, ALIGN, ws=11 * M + 16)
+    only(ALL, ALIAS, pout=_pool(B, M + 64))
+    only(ALL, ALIAS, pout=_pool(B, 3 * M, len=M))
+    only(ALL, ALIAS, err=M + 8)
+    only(ALL, ALIAS, ws=M)
+    only(req, ALIAS, x=M)
+    only(("fork", "compact"), ALIAS, mem=_mem(B, base=M))
+    only(("fork", "compact"), NULL, mem=_mem(B, base=None))
+    only(("fork", "compact"), ALIGN, mem=_mem(B, base=5 * M + 8))
+    for kw in (dict(n_planes=0), dict(page_bytes=0), dict(page_bytes=1 << 31), dict(page_stride=256), dict(plane_stride=512),
+               dict(page_stride=-512)):
+        only(("fork", "compact"), SHAPE, mem=_mem(B, **kw))
+    for kw in (dict(page_bytes=504), dict(page_stride=520), dict(plane_stride=100 * 512 + 8)):
+        only(("fork", "compact"), ALIGN, mem=_mem(B, **kw))
+    copy = B.moe_pages_copy
+    assert _status(B, copy, _mem(B), 0, 1, M, M, 0) == SHAPE and _status(B, copy, _mem(B), 100, -1, M, M, 0) == SHAPE
+    assert _status(B, copy, _mem(B), 100, 1, None, M, 0) == NULL and _status(B, copy, _mem(B), 100, 1, M + 1, M, 0) == ALIGN
+    assert _status(B, copy, _mem(B), 100, 1, 5 * M + 64, M, 0) == ALIAS
+    assert _status(B, B.moe_pages_check, None, 0) == NULL
+
+
+def test_pool_workspace(B):
+    a = B.moe_pages_workspace(_pool(B), 0)
+    assert a < B.moe_pages_workspace(_pool(B, n_pages=1 << 20), 8)
+    assert _status(B, B.moe_pages_workspace, _pool(B), 9) == SHAPE
+    assert ctypes.sizeof(B.moe_pages) == 40 and ctypes.sizeof(B.moe_page_memory) == 40
+
+
+def test_pool_wrapper_refuses():
+    torch = pytest.importorskip("torch")
+    from sparse_moe_02_amd.pages import PagePool, copy_pages
+
+    with pytest.raises(ValueError):
+        PagePool(10, 16, 2, 2, device="cpu")
+    with pytest.raises(ValueError):
+        copy_pages(torch.zeros(2, 3, 8), torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
