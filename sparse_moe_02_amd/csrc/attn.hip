@@ -62,6 +62,12 @@ __device__ __forceinline__ bool nonfinite(uint32_t w) {
   return (w & m) == m || ((w >> 16) & m) == m;
 }
 
+template <bool F16>
+__device__ __forceinline__ bool nonfinite16(uint32_t w) {
+  const uint32_t m = F16 ? 0x7c00u : 0x7f80u;
+  return (w & m) == m;
+}
+
 __device__ __forceinline__ uint64_t tr_read(uint32_t lds) {
   return __builtin_bit_cast(uint64_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                           (__attribute__((address_space(3))) s16x4 *)(uintptr_t)lds));
@@ -375,6 +381,292 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(AttnArgs a) {
   }
 }
 
+// ---------------------------------------------------------------- tiles of many rows
+
+__device__ __forceinline__ float halves_max(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float halves_sum(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+template <bool F16>
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+constexpr int kStages = 3;  // K and V blocks in LDS: one in use, two in flight
+
+template <int D, bool F16, int NW>
+__global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
+  constexpr int kBuf = kAttnKeys * D * 2;      // one K or V block, bytes
+  constexpr int kInstr = kBuf / 1024 / NW;     // load instructions a wave issues for one block
+  constexpr int kRowsPer = 512 / D;            // LDS rows of one instruction
+  static_assert(kInstr >= 1, "every wave loads");
+  extern __shared__ __align__(16) uint8_t lds_raw[];
+  Tile t;
+  if (!find_tile(a, a.tiles - 1 - blockIdx.x, 32 * NW, t)) return;  // the longest tiles first
+  // Behind the buffers, so that these start at LDS address 0 (addresses are combined by
+  // exclusive or): whether some value that not all rows see is an infinity or NaN.
+  int &odd = *(int *)(lds_raw + kStages * 2 * kBuf);
+  const int kvh = blockIdx.y, split = blockIdx.z;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  if (tid == 0) odd = 0;
+  __syncthreads();
+  const int n = lane & 31, half = lane >> 5;
+  const uint32_t lds0 = lds_addr(lds_raw);
+
+  // this lane's query row, and its wave's
+  const int w0 = t.r0 + wave * 32;                               // first row of the wave
+  const int wn = max(0, min(32, t.r0 + t.nr - w0));              // rows of the wave
+  const int rr = w0 + n;
+  const bool live = n < wn;
+  const int tok = t.t0 + rr / a.G, head = kvh * a.G + rr % a.G;
+  const int64_t pos = live ? t.first + rr / a.G : -1;
+  const int last_key = (int)(a.full ? (live ? (int64_t)t.len - 1 : -1) : min(pos, (int64_t)t.len - 1));
+  const int first_key = a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
+  const int64_t pf = t.first + w0 / a.G, pl = t.first + (w0 + max(wn, 1) - 1) / a.G;
+  // all rows of the wave see the keys of [all_lo, all_hi); some row sees those of [any_lo, any_hi)
+  const int all_hi = (int)(a.full ? (int64_t)t.len : min(pf + 1, (int64_t)t.len));
+  const int all_lo = a.window ? (int)max(pl - a.window + 1, (int64_t)0) : 0;
+  const int any_hi = wn == 0 ? 0 : (int)(a.full ? (int64_t)t.len : min(pl + 1, (int64_t)t.len));
+  const int any_lo = a.window ? (int)max(pf - a.window + 1, (int64_t)0) : 0;
+
+  // keys below all_lo_t and from all_hi_t on are hidden from some row of the tile
+  const int64_t tf = t.first + t.r0 / a.G, tl = t.first + (t.r0 + t.nr - 1) / a.G;
+  const int all_hi_t = (int)(a.full ? (int64_t)t.len : max(min(tf + 1, (int64_t)t.len), (int64_t)0));
+  const int all_lo_t = a.window ? (int)max(tl - a.window + 1, (int64_t)0) : 0;
+
+  // a negative scale is taken as a positive one on negated queries, so that the largest score
+  // is the largest product
+  const float scale = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);  // 0: of queries of zeros
+  const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+  u32x4 qf[D / 16];
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    qf[c] = u32x4{0, 0, 0, 0};
+    if (live && a.scale_log2 != 0.0f)
+      qf[c] = *(const u32x4 *)(a.q.p + (int64_t)tok * a.q.ts + (int64_t)head * a.q.hs + 16 * c + 8 * half);
+    qf[c] ^= flip;
+  }
+
+  const int blk0 = t.lo / kAttnKeys, nblk = (t.hi + kAttnKeys - 1) / kAttnKeys - blk0;
+  const int b0 = blk0 + (int)((int64_t)nblk * split / a.splits), b1 = blk0 + (int)((int64_t)nblk * (split + 1) / a.splits);
+
+  const int32_t *trow = a.b.table + (int64_t)max(t.row, 0) * a.b.cols;
+  const int pmask = (1 << a.kv.page_shift) - 1;
+  // the rows that this wave loads lie in one 16-key half of a block
+  const int my_r0 = wave * kInstr * kRowsPer;
+  auto page_of = [&](int blk) {
+    const int col = (blk * kAttnKeys + (my_r0 & 16)) >> a.kv.page_shift;
+    const int page = blk < b1 && col < a.b.cols ? trow[col] : -1;
+    return __builtin_amdgcn_readfirstlane((unsigned)page < (unsigned)a.kv.n_pages ? page : -1);
+  };
+  uint32_t voff[kInstr];
+#pragma unroll
+  for (int i = 0; i < kInstr; ++i) {
+    const int r = my_r0 + i * kRowsPer + lane / (D / 8);
+    voff[i] = (uint32_t)(((r & 15) * (int)a.kv.ts + (((lane % (D / 8)) ^ swz<D>(r)) * 8)) * 2);
+  }
+  auto load = [&](int blk, int page, int stage) {
+    const int64_t o = (int64_t)max(page, 0) * a.kv.ps + (int64_t)((blk * kAttnKeys + (my_r0 & 16)) & pmask) * a.kv.ts +
+                      (int64_t)kvh * a.kv.hs;
+    const uint32_t at = lds0 + stage * 2 * kBuf + wave * kInstr * 1024;
+#pragma unroll
+    for (int i = 0; i < kInstr; ++i) dma16(a.kv.k + o, voff[i], at + i * 1024);
+#pragma unroll
+    for (int i = 0; i < kInstr; ++i) dma16(a.kv.v + o, voff[i], at + kBuf + i * 1024);
+  };
+
+  f32x16 acc[D / 32];
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+  float m = -INFINITY, l = 0.0f;  // m: of the unscaled products
+
+  // pages of the block in use, the next, and the one after (for this wave's loads)
+  int pg = page_of(b0), pg1 = page_of(b0 + 1), pg2 = page_of(b0 + 2);
+  if (b0 < b1) load(b0, pg, 0);
+  if (b0 + 1 < b1) load(b0 + 1, pg1, 1);
+  int stage = 0;
+  for (int blk = b0; blk < b1; ++blk) {
+    const int key0 = blk * kAttnKeys;
+    const uint32_t kbuf = lds0 + stage * 2 * kBuf, vbuf = kbuf + kBuf;
+    if (blk + 1 < b1) wait_vm<2 * kInstr>(); else wait_vm<0>();
+    // where some key is hidden from some row, its weight there is 0 and its value must be
+    // finite: absent keys' values (behind the end, in a bad page) become zeros, and so do
+    // infinities and NaN, which are put back at the end where they are seen
+    if (pg < 0 || key0 + kAttnKeys > all_hi_t || key0 < all_lo_t) {
+#pragma unroll
+      for (int i = 0; i < kInstr; ++i) {
+        const int r = my_r0 + i * kRowsPer + lane / (D / 8);
+        auto *w = (__attribute__((address_space(3))) u32x4 *)(uintptr_t)(vbuf + (wave * kInstr + i) * 1024 + lane * 16);
+        u32x4 v = *w;
+        const bool absent = pg < 0 || key0 + r >= t.len;
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (nonfinite16<F16>(v[j])) v[j] &= 0xffff0000u, bad = true;
+          if (nonfinite16<F16>(v[j] >> 16)) v[j] &= 0xffffu, bad = true;
+        }
+        if (absent) v = u32x4{0, 0, 0, 0};
+        if (absent || bad) *w = v;
+        if (bad && !absent) odd = 1;
+      }
+    }
+    wait_lds();
+    lds_barrier();
+    const int pg3 = page_of(blk + 3);
+    if (blk + 2 < b1) load(blk + 2, pg2, stage == 0 ? 2 : stage - 1);
+    pg = pg1;
+    pg1 = pg2;
+    pg2 = pg3;
+    stage = stage == 2 ? 0 : stage + 1;
+    if (key0 >= any_hi || key0 + kAttnKeys <= any_lo) continue;
+
+    // the chunk's number enters the swizzled address by exclusive or: one register and one
+    // operation a read, instead of a register for every chunk
+    const uint32_t ka = kbuf + n * D * 2 + (half ^ swz<D>(n)) * 16;
+    f32x16 s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      const u32x4 kf = *(const __attribute__((address_space(3))) u32x4 *)(uintptr_t)(ka ^ (c * 32));
+      s = mfma32<F16>(kf, qf[c], s);
+    }
+    // pages of the block's halves: bad ones are rare, so looked up again where masks are made
+    bool whole = key0 + kAttnKeys <= all_hi && key0 >= all_lo && wn == 32;
+    const int c0 = key0 >> a.kv.page_shift, c1 = (key0 + 16) >> a.kv.page_shift;
+    const int have0 = c0 < a.b.cols && (unsigned)trow[c0] < (unsigned)a.kv.n_pages ? max(0, min(16, t.len - key0)) : 0;
+    const int have1 = c1 < a.b.cols && (unsigned)trow[c1] < (unsigned)a.kv.n_pages ? max(0, min(16, t.len - key0 - 16)) : 0;
+    whole = whole && have0 + have1 == kAttnKeys;
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int k = 8 * (i / 4) + 4 * half + i % 4, key = key0 + k;
+        if ((k & 15) >= (i < 8 ? have0 : have1) || key > last_key || key < first_key) s[i] = -INFINITY;
+      }
+    }
+    float mx = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
+    const float mn = fmaxf(m, halves_max(mx));
+    const float mu = mn == -INFINITY ? 0.0f : mn;
+    const float f = __builtin_amdgcn_exp2f((m - mu) * scale);
+    m = mn;
+    const float off = -mu * scale;
+    float ps = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale, off));
+      ps += s[i];
+    }
+    l = l * f + ps;
+    if (__ballot(f != 1.0f)) {
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) acc[d] *= f;
+    }
+    u32x4 pf4[2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pf4[i / 4][i % 4] = pack2<F16>(s[2 * i], s[2 * i + 1]);
+
+    {
+      // rows kr, kr + 8, kr + 16, kr + 24; swz(kr + 8) = swz(kr) ^ swz(8), and 16 changes nothing
+      const int l16 = lane & 15, kr = 4 * half + (l16 >> 2);
+      const uint32_t va = vbuf + kr * D * 2 + (((2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ swz<D>(kr)) * 16 + (l16 & 1) * 8);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) {
+        const uint32_t a0 = va ^ (d * 64), a1 = va ^ (d * 64) ^ (swz<D>(8) * 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t v0 = tr_read(a0 + 16 * h * D * 2), v1 = tr_read(a1 + (16 * h + 8) * D * 2);
+          const u32x4 vf = {(uint32_t)v0, (uint32_t)(v0 >> 32), (uint32_t)v1, (uint32_t)(v1 >> 32)};
+          acc[d] = mfma32<F16>(vf, pf4[h], acc[d]);
+        }
+      }
+    }
+  }
+
+  l = halves_sum(l);
+  __syncthreads();
+  const bool fix = odd != 0;
+  if (!live && !fix) return;
+  const int64_t row = (int64_t)tok * a.H + head;
+  if (!live) {
+  } else if (a.splits == 1) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t *o = a.out.p + (int64_t)tok * a.out.ts + (int64_t)head * a.out.hs + 4 * half;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint2 w = {pack2<F16>(acc[d][4 * i] * inv, acc[d][4 * i + 1] * inv),
+                         pack2<F16>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv)};
+        *(uint2 *)(o + 32 * d + 8 * i) = w;
+      }
+    if (a.lse && half == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m * scale + __log2f(l)) * kLn2;
+  } else {
+    const int64_t at = row * a.splits + split;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(f32x4 *)(a.part + at * D + 32 * d + 8 * i + 4 * half) =
+            f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+    if (half == 0) {
+      a.part_ml[2 * at] = m == -INFINITY ? m : m * scale;
+      a.part_ml[2 * at + 1] = l;
+    }
+  }
+  if (!fix) return;
+  // rare: add the infinities and NaN that were taken out to the rows that see them
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "agent");
+  constexpr int kE = D / 64;
+  for (int key = max(t.lo, b0 * kAttnKeys); key < min(t.hi, b1 * kAttnKeys); ++key) {
+    const int k0 = key & ~(kAttnKeys - 1), col = key >> a.kv.page_shift;
+    const int page = trow[col];
+    if ((k0 + kAttnKeys <= all_hi_t && k0 >= all_lo_t) || (unsigned)page >= (unsigned)a.kv.n_pages) continue;
+    const uint16_t *v = a.kv.v + (int64_t)page * a.kv.ps + (int64_t)(key & pmask) * a.kv.ts + (int64_t)kvh * a.kv.hs;
+    float x[kE];
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      const uint16_t w = v[lane * kE + e];
+      x[e] = nonfinite16<F16>(w) ? unpack<F16>(w, false) : 0.0f;
+      any |= nonfinite16<F16>(w);
+    }
+    if (!__ballot(any)) continue;
+    for (int r = 0; r < wn; ++r) {
+      const int64_t p = t.first + (w0 + r) / a.G;
+      if ((!a.full && key > p) || (a.window && key <= p - a.window)) continue;
+      const int64_t tk = t.t0 + (w0 + r) / a.G, hd = kvh * a.G + (w0 + r) % a.G;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        if (x[e] == 0.0f) continue;
+        if (a.splits == 1) {
+          uint16_t *o = a.out.p + tk * a.out.ts + hd * a.out.hs + lane * kE + e;
+          *o = (uint16_t)pack2<F16>(unpack<F16>(*o, false) + x[e], 0.0f);
+        } else {
+          a.part[((tk * a.H + hd) * a.splits + split) * D + lane * kE + e] += x[e];
+        }
+      }
+    }
+  }
+}
+
 // Join the splits' partial results: one wave per (token, head), D / 64 elements a lane.
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads) k_attn_join(AttnArgs a) {
@@ -403,25 +695,35 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(AttnArgs a) {
   if (a.lse && lane == 0) a.lse[r] = sum == 0.0f ? -INFINITY : (mw + __log2f(sum)) * kLn2;
 }
 
-template <int D, bool F16>
-hipError_t launch(const AttnArgs &a, hipStream_t s) {
-  auto k = k_attn_rows<D, F16>;
-  constexpr int lds = Rows<D>::kLds;
-  // the attribute belongs to the function on one device: set once for each
-  static std::atomic<uint64_t> done{0};
+// Sets the LDS limit of a kernel, once for each device (the attribute belongs to the device).
+template <class K>
+hipError_t allow_lds(K k, int lds, std::atomic<uint64_t> &done) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
-  if (dev > 63 || !(done.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (dev <= 63 && done.load(std::memory_order_relaxed) >> dev & 1) return hipSuccess;
+  e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e == hipSuccess && dev <= 63) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  return e;
+}
+
+template <int D, bool F16>
+hipError_t launch(const AttnArgs &a, hipStream_t s) {
+  const dim3 grid(a.tiles, a.kv.n_kv, a.splits);
+  if (a.rows == kAttnRows) {
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = allow_lds(k_attn_rows<D, F16>, Rows<D>::kLds, done);
     if (e != hipSuccess) return e;
-    if (dev <= 63) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    hipLaunchKernelGGL((k_attn_rows<D, F16>), grid, dim3(kThreads), Rows<D>::kLds, s, a);
+  } else {
+    static std::atomic<uint64_t> done{0};
+    constexpr int lds = kStages * 2 * kAttnKeys * D * 2 + 16, nw = attn_tile(D) / 32;
+    const hipError_t e = allow_lds(k_attn_tile<D, F16, nw>, lds, done);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_attn_tile<D, F16, nw>), grid, dim3(64 * nw), lds, s, a);
   }
-  hipLaunchKernelGGL(k, dim3(a.tiles, a.kv.n_kv, a.splits), dim3(kThreads), lds, s, a);
-  if (a.splits > 1) {
-    auto j = k_attn_join<D, F16>;
-    hipLaunchKernelGGL(j, dim3(((int64_t)a.T * a.H + kWaves - 1) / kWaves), dim3(kThreads), 0, s, a);
-  }
+  if (a.splits > 1)
+    hipLaunchKernelGGL((k_attn_join<D, F16>), dim3(((int64_t)a.T * a.H + kWaves - 1) / kWaves), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -430,11 +732,14 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
 AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int H, int n_kv, int dim) {
   AttnShape s{};
   const int64_t G = H / n_kv;
-  s.tiles = (int)(T * G / kAttnRows + n_seqs);
+  s.rows = max_q * G > 2 * kAttnRows ? attn_tile(dim) : kAttnRows;
+  s.tiles = (int)(T * G / s.rows + n_seqs);
   // tiles that can hold rows, and splits that fill the chip with them
-  const int64_t per_seq = (max_q * G + kAttnRows - 1) / kAttnRows;
-  const int64_t busy = (per_seq < 1 ? 1 : per_seq) * n_seqs < s.tiles ? (per_seq < 1 ? 1 : per_seq) * n_seqs : s.tiles;
-  const int64_t want = 512 / (busy * n_kv < 1 ? 1 : busy * n_kv);
+  int64_t busy = (max_q * G + s.rows - 1) / s.rows;
+  busy = (busy < 1 ? 1 : busy) * n_seqs;
+  if (busy > s.tiles) busy = s.tiles;
+  busy *= n_kv;
+  const int64_t want = (s.rows == kAttnRows ? 512 : 256) / (busy < 1 ? 1 : busy);
   const int64_t most = (max_kv + kAttnKeys * kWaves - 1) / (kAttnKeys * kWaves);
   int64_t n = want < most ? want : most;
   s.splits = (int)(n < 1 || T * H > 1 << 22 ? 1 : n > 64 ? 64 : n);

@@ -37,6 +37,9 @@ struct RopeArgs {
 hipError_t launch_rope_append(const RopeArgs &a, hipStream_t s);
 
 constexpr int kAttnRows = 16;   // query rows (token x head of a group) of a small tile
+// Query rows of a large tile: eight waves of 32, or four where a block of keys has too few bytes
+// for eight to load.
+constexpr int attn_tile(int dim) { return dim == 64 ? 128 : 256; }
 constexpr int kAttnKeys = 32;   // keys of one block
 
 struct AttnArgs {
@@ -47,6 +50,7 @@ struct AttnArgs {
   float *part;     // [T * H][splits][dim] unnormalised partial outputs (splits > 1)
   float *part_ml;  // [T * H][splits][2] running maximum (base-2 exponent) and sum
   int T, H, G;     // G: query heads of one key/value head
+  int rows;        // rows of a tile: kAttnRows or attn_tile(dim)
   int tiles;       // bound on the number of row tiles
   int splits;
   int window;
@@ -55,7 +59,7 @@ struct AttnArgs {
 };
 // What the launch is shaped by, from host-known sizes alone.
 struct AttnShape {
-  int tiles, splits;
+  int rows, tiles, splits;
   size_t ws_bytes, off_ml;
 };
 AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int H, int n_kv, int dim);

@@ -403,6 +403,7 @@ moe_status moe_paged_attn(const moe_paged_kv *kv, const moe_batch *batch, int64_
   a.T = (int)T;
   a.H = n_heads;
   a.G = n_heads / kv->n_kv_heads;
+  a.rows = sh.rows;
   a.tiles = sh.tiles;
   a.splits = sh.splits;
   a.window = window;
