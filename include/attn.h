@@ -132,7 +132,7 @@ moe_status moe_rope_append(const moe_paged_kv *kv, const moe_batch *batch, int64
  * (MOE_ERR_TOKENS). */
 #define MOE_ATTN_FULL 1u
 moe_status moe_paged_attn_workspace(const moe_paged_kv *kv, int64_t T, int32_t n_seqs, int64_t max_q,
-                                    int64_t max_kv, int32_t n_heads, size_t *bytes);
+                                    int64_t max_kv, int32_t n_heads, int32_t window, size_t *bytes);
 moe_status moe_paged_attn(const moe_paged_kv *kv, const moe_batch *batch, int64_t T, int64_t max_q,
                           int64_t max_kv, const moe_heads *q, int32_t n_heads, const moe_heads *out,
                           float *lse, float scale, int32_t window, uint32_t flags, void *workspace,

@@ -143,7 +143,7 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, ta
         if lse.shape != (T, H) or not lse.is_contiguous():
             raise ValueError("lse: contiguous float32 [T][n_heads] required")
         lp = lse.data_ptr()
-    n = B.moe_paged_attn_workspace(kv, T, b.n_seqs, max_q, max_kv, H)
+    n = B.moe_paged_attn_workspace(kv, T, b.n_seqs, max_q, max_kv, H, window)
     if workspace is None:
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=dev)
@@ -160,7 +160,7 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, ta
 
 
 def paged_attn_workspace(T: int, n_seqs: int, max_q: int, max_kv: int, n_heads: int, n_kv_heads: int, head_dim: int,
-                         dtype: torch.dtype = torch.bfloat16) -> int:
+                         dtype: torch.dtype = torch.bfloat16, window: int = 0) -> int:
     """Bytes of workspace that ``paged_attn`` needs for these sizes."""
     kv = B.moe_paged_kv(None, None, 0, 0, 0, 1, 16, n_kv_heads, head_dim, _DTYPES[dtype])
-    return B.moe_paged_attn_workspace(kv, T, n_seqs, max_q, max_kv, n_heads)
+    return B.moe_paged_attn_workspace(kv, T, n_seqs, max_q, max_kv, n_heads, window)

@@ -159,7 +159,7 @@ def lib() -> ctypes.CDLL:
             L.moe_rope_append.argtypes = [KV, BA, I64, HD, HD, ctypes.c_int32, HD, HD, P, P, ctypes.c_int32,
                                           ctypes.c_float, ctypes.c_uint32, P]
             L.moe_paged_attn_workspace.restype = ctypes.c_int
-            L.moe_paged_attn_workspace.argtypes = [KV, I64, ctypes.c_int32, I64, I64, ctypes.c_int32,
+            L.moe_paged_attn_workspace.argtypes = [KV, I64, ctypes.c_int32, I64, I64, ctypes.c_int32, ctypes.c_int32,
                                                    ctypes.POINTER(SZ)]
             L.moe_paged_attn.restype = ctypes.c_int
             L.moe_paged_attn.argtypes = [KV, BA, I64, I64, I64, HD, ctypes.c_int32, HD, P, ctypes.c_float,
@@ -284,9 +284,11 @@ def moe_rope_append(kv: moe_paged_kv, batch: moe_batch, T: int, q: moe_heads, q_
                                                     rot_dim, mscale, flags, stream))
 
 
-def moe_paged_attn_workspace(kv: moe_paged_kv, T: int, n_seqs: int, max_q: int, max_kv: int, n_heads: int) -> int:
+def moe_paged_attn_workspace(kv: moe_paged_kv, T: int, n_seqs: int, max_q: int, max_kv: int, n_heads: int,
+                             window: int = 0) -> int:
     n = ctypes.c_size_t()
-    _check("moe_paged_attn_workspace", lib().moe_paged_attn_workspace(kv, T, n_seqs, max_q, max_kv, n_heads, n))
+    _check("moe_paged_attn_workspace", lib().moe_paged_attn_workspace(kv, T, n_seqs, max_q, max_kv, n_heads,
+                                                                              window, n))
     return n.value
 
 

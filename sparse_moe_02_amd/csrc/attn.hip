@@ -32,6 +32,10 @@ typedef __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16 f16x8;
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 
 constexpr int kThreads = 256, kWaves = 4;
+constexpr int kMaxSplits = 256;
+constexpr int kMaxRuns = 1024;  // workgroups of k_attn_rows at most
+// workgroups of k_attn_rows that fill the chip (registers allow 1, 2 or 3 on a compute unit)
+constexpr int runs_of(int dim) { return dim == 256 ? 256 : dim == 128 ? 512 : 768; }
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <bool F16>
@@ -55,13 +59,7 @@ __device__ __forceinline__ float unpack(uint32_t w, bool hi) {
   const uint16_t v = (uint16_t)(hi ? w >> 16 : w & 0xffff);
   return F16 ? fp16_to_f32(v) : bf16_to_f32(v);
 }
-// whether a word of two values holds an infinity or NaN
-template <bool F16>
-__device__ __forceinline__ bool nonfinite(uint32_t w) {
-  const uint32_t m = F16 ? 0x7c00u : 0x7f80u;
-  return (w & m) == m || ((w >> 16) & m) == m;
-}
-
+// whether a value is an infinity or NaN
 template <bool F16>
 __device__ __forceinline__ bool nonfinite16(uint32_t w) {
   const uint32_t m = F16 ? 0x7c00u : 0x7f80u;
@@ -100,6 +98,20 @@ __device__ __forceinline__ int swz(int r) {
   return D == 64 ? (r >> 1) & 7 : r & 15;
 }
 
+// Page table entries are read as constants: by the scalar unit, whose loads have a counter of
+// their own -- a vector load's wait would drain the direct-to-LDS loads in flight.
+typedef const __attribute__((address_space(4))) int32_t *TableRow;
+
+// The page of the 16 keys from `key` on, or -1.
+__device__ __forceinline__ int page_at(const AttnArgs &a, TableRow row, int key) {
+  const int col = __builtin_amdgcn_readfirstlane(key >> a.kv.page_shift);
+  const int page = row[min(col, a.b.cols - 1)];
+  return __builtin_amdgcn_readfirstlane(col < a.b.cols && (unsigned)page < (unsigned)a.kv.n_pages ? page : -1);
+}
+__device__ __forceinline__ TableRow table_row(const AttnArgs &a, int row) {
+  return (TableRow)(uintptr_t)uniform_ptr(a.b.table + (int64_t)max(row, 0) * a.b.cols);
+}
+
 // A tile's place in the batch: which sequence, its query rows and the keys they see.
 struct Tile {
   int seq, row;       // row: of the table, -1: none
@@ -110,16 +122,13 @@ struct Tile {
   int lo, hi;         // keys that any row of the tile sees lie in [lo, hi)
 };
 
-// Tile x of `rows`-row tiles: sequence b's tiles start at floor(q_start[b] G / rows) + b,
-// which leaves room for ceil(n_b G / rows) of them, so no list of tiles is needed.
-__device__ __forceinline__ bool find_tile(const AttnArgs &a, int x, int rows, Tile &t) {
+// The tile of `rows` rows from r0 of sequence t.seq on.  Returns whether there are any.
+__device__ __forceinline__ bool set_tile(const AttnArgs &a, int64_t r0, int rows, Tile &t) {
   const Batch &b = a.b;
-  t.seq = wave_find(b.n_seqs, x, [&](int i) { return (int64_t)b.q_start[i] * a.G / rows + i; });
   t.t0 = b.q_start[t.seq];
   const int t1 = b.q_start[t.seq + 1];
   t.n = t1 - t.t0;
-  if (t.t0 < 0 || t1 > a.T) return false;  // not a batch: touch nothing
-  const int64_t r0 = ((int64_t)x - ((int64_t)t.t0 * a.G / rows + t.seq)) * rows;
+  if (t.t0 < 0 || t1 > a.T || t.n <= 0) return false;  // (not a batch: touch nothing)
   if (r0 < 0 || r0 >= (int64_t)t.n * a.G) return false;
   t.r0 = (int)r0;
   t.nr = min(rows, t.n * a.G - t.r0);
@@ -136,41 +145,200 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &a, int x, int rows, Ti
   return true;
 }
 
-template <int D>
-struct Rows {
-  static constexpr int kBuf = kAttnKeys * D * 2;         // one K or V buffer, bytes
-  static constexpr int kWaveLds = 2 * kBuf;
-  static constexpr int kOStride = D + 4;                 // floats; padded against bank conflicts
-  static constexpr int kLds = kWaves * kWaveLds;
-  static_assert(kAttnRows * kOStride * 4 <= kWaveLds, "a wave's partial output fits its buffers");
-};
+// Tile x of `rows`-row tiles: sequence b's tiles start at floor(q_start[b] G / rows) + b,
+// which leaves room for ceil(n_b G / rows) of them, so no list of tiles is needed.
+__device__ __forceinline__ bool find_tile(const AttnArgs &a, int x, int rows, Tile &t) {
+  const Batch &b = a.b;
+  t.seq = wave_find(b.n_seqs, x, [&](int i) { return (int64_t)b.q_start[i] * a.G / rows + i; });
+  return set_tile(a, ((int64_t)x - ((int64_t)b.q_start[t.seq] * a.G / rows + t.seq)) * rows, rows, t);
+}
 
-// 32 rows of one cache plane into LDS: keys key0 .. key0+31 lie in two 16-key halves of one
-// page each.  The halves' bases are wave-uniform.
-template <int D>
-__device__ __forceinline__ void load_block(const uint16_t *h0, const uint16_t *h1, int64_t ts, uint32_t lds) {
-  constexpr int kChunks = D / 8, kRowsPer = 64 / kChunks, kN = kAttnKeys / kRowsPer;
-  const int lane = threadIdx.x & 63;
+// Values that not all rows of a tile see must be finite, for a hidden key's weight is 0: absent
+// keys' values become zeros, and so do infinities and NaN.  Returns whether there were any.
+template <bool F16>
+__device__ __forceinline__ uint32_t make_finite(u32x4 &v, bool absent) {
+  constexpr uint32_t m = F16 ? 0x7c007c00u : 0x7f807f80u;
+  uint32_t bad = 0;
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    const int r = i * kRowsPer + lane / kChunks;  // rows of one instruction lie in one half
-    const int c = (lane % kChunks) ^ swz<D>(r);
-    const uint32_t off = (uint32_t)(((r & 15) * (int)ts + c * 8) * 2);
-    dma16(i < kN / 2 ? h0 : h1, off, lds + i * 1024);
+  for (int j = 0; j < 4; ++j) {
+    // a half of t is 0 where its exponent is all ones, and otherwise at least 0x80, so taking 1
+    // from it turns its top bit on in the first case only
+    const uint32_t t = (v[j] & m) ^ m, z = ((t - 0x00010001u) & ~t & 0x80008000u) >> 15;
+    v[j] &= absent ? 0u : ~(z * 0xffffu);
+    bad |= z;
+  }
+  return absent ? 0u : bad;
+}
+
+// Adds the infinities and NaN that make_finite took out of blocks [b0, b1) to the results,
+// already written, of the rows that see them: rows r0, r0 + step, ... below r1 (relative to the
+// sequence).  part(r, token, head): where the row's partial results lie, or null: in out.
+// Rare.  By a whole wave, for rows that no other wave writes.
+template <int D, bool F16, class F>
+__device__ void put_back(const AttnArgs &a, const Tile &t, int kvh, int b0, int b1, int all_lo, int all_hi, int r0,
+                         int r1, int step, F part) {
+  const int lane = threadIdx.x & 63;
+  const TableRow trow = table_row(a, t.row);
+  constexpr int kE = D / 64;
+  for (int key = max(t.lo, b0 * kAttnKeys); key < min(t.hi, b1 * kAttnKeys); ++key) {
+    const int k0 = key & ~(kAttnKeys - 1), page = page_at(a, trow, key);
+    if ((k0 + kAttnKeys <= all_hi && k0 >= all_lo) || page < 0) continue;
+    const uint16_t *v = a.kv.v + (int64_t)page * a.kv.ps + (int64_t)(key & ((1 << a.kv.page_shift) - 1)) * a.kv.ts +
+                        (int64_t)kvh * a.kv.hs;
+    float x[kE];
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      const uint16_t w = v[lane * kE + e];
+      x[e] = nonfinite16<F16>(w) ? unpack<F16>(w, false) : 0.0f;
+      any |= nonfinite16<F16>(w);
+    }
+    if (!__ballot(any)) continue;
+    for (int r = r0; r < r1; r += step) {
+      const int64_t p = t.first + r / a.G;
+      if ((!a.full && key > p) || (a.window && key <= p - a.window)) continue;
+      const int64_t tk = t.t0 + r / a.G, hd = kvh * a.G + r % a.G;
+      float *d = part(r, tk, hd);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        if (x[e] == 0.0f) continue;
+        if (!d) {
+          uint16_t *o = a.out.p + tk * a.out.ts + hd * a.out.hs + lane * kE + e;
+          *o = (uint16_t)pack2<F16>(unpack<F16>(*o, false) + x[e], 0.0f);
+        } else {
+          d[lane * kE + e] += x[e];
+        }
+      }
+    }
   }
 }
 
+template <int D>
+struct Rows {
+  static constexpr int kBuf = kAttnKeys * D * 2;         // V buffer of a wave, bytes
+  static constexpr int kOStride = D + 4;                 // floats; padded against bank conflicts
+  static constexpr int kOut = kAttnRows * kOStride * 4;  // a wave's partial output, over its buffer
+  static constexpr int kWaveLds = kBuf > kOut ? kBuf : kOut;
+  static constexpr int kLds = kWaves * kWaveLds;
+};
+
+// How k_attn_rows divides its work.  A segment is one (tile, key/value head); a sequence's
+// segments have as many blocks of keys each as the longest of them, at least 1.  The blocks of
+// all segments, one after the other, are cut into equal runs, one for each workgroup, so
+// the lengths of the sequences do not matter.
+struct SeqSize {
+  int tiles, blocks;
+};
+__device__ __forceinline__ SeqSize seq_size(const AttnArgs &a, int s) {
+  const int t0 = a.b.q_start[s], t1 = a.b.q_start[s + 1], n = t1 - t0;
+  SeqSize z{0, 1};
+  if (n <= 0 || t0 < 0 || t1 > a.T) return z;
+  z.tiles = (int)(((int64_t)n * a.G + kAttnRows - 1) / kAttnRows);
+  const int row = batch_row(a.b, s), total = row < 0 ? 0 : a.b.kv_len[row];
+  const int len = min(max(total, 0), a.b.cols << a.kv.page_shift);
+  const int64_t lo = a.window ? max((int64_t)total - n - a.window + 1, (int64_t)0) : 0;
+  z.blocks = max(1, (int)((len + kAttnKeys - 1) / kAttnKeys - min(lo, (int64_t)len) / kAttnKeys));
+  return z;
+}
+__device__ __forceinline__ int64_t total_blocks(const AttnArgs &a, const SeqSize &z) {
+  return (int64_t)z.tiles * a.kv.n_kv * z.blocks;
+}
+
+__device__ __forceinline__ uint64_t div_u64(uint64_t x, uint64_t y) {
+  return (x | y) >> 32 ? x / y : (uint32_t)x / (uint32_t)y;
+}
+
+// Runs of `total` blocks over `n` workgroups: the first `more` take one more than `each`.
+struct Runs {
+  int64_t each, more;
+  int n;
+  __device__ __forceinline__ Runs(int64_t total, int wgs) {
+    const int64_t least = (total + kWaves - 1) / kWaves;  // a block for every wave
+    n = (int)max(min((int64_t)wgs, least), (int64_t)1);
+    each = (int64_t)div_u64((uint64_t)total, (uint64_t)n);
+    more = total - each * n;
+  }
+  __device__ __forceinline__ int64_t start(int64_t w) const { return each * w + min(w, more); }
+  __device__ __forceinline__ int holder(int64_t x) const {  // of block x
+    const int64_t edge = more * (each + 1);
+    return (int)(x < edge ? div_u64((uint64_t)x, (uint64_t)(each + 1)) : more + div_u64((uint64_t)(x - edge), (uint64_t)each));
+  }
+};
+
+__device__ __forceinline__ int64_t wave_incl_scan64(int64_t v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t y = __shfl_up((long long)v, d, 64);
+    if (lane >= d) v += y;
+  }
+  return v;
+}
+
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_rows(AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) k_attn_rows(AttnArgs a) {
   using L = Rows<D>;
   extern __shared__ __align__(16) uint8_t lds_raw[];
   __shared__ float ml[kWaves][2][kAttnRows];
-  Tile t;
-  if (!find_tile(a, blockIdx.x, kAttnRows, t)) return;
-  const int kvh = blockIdx.y, split = blockIdx.z;
+  __shared__ int odd;  // some value that not all rows see is an infinity or NaN
+  __shared__ int64_t sums[kWaves], found_cum;
+  __shared__ int found;
+  const int wg = blockIdx.x;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+
+  // this workgroup's run, and the sequence where it starts
+  int64_t mine = 0;
+  for (int s = tid; s < a.b.n_seqs; s += kThreads) mine += total_blocks(a, seq_size(a, s));
+  {
+    const int64_t w = wave_incl_scan64(mine);
+    if (lane == 63) sums[wave] = w;
+  }
+  if (tid == 0) odd = 0;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) total += sums[i];
+  const Runs runs(total, a.wgs);
+  if (tid == 0) a.rec[wg].n = 0;  // results to be joined from this workgroup on: none so far
+  if (total == 0 || wg >= runs.n) return;
+  int64_t cur = runs.start(wg);
+  const int64_t end = runs.start(wg + 1);
+  {
+    int64_t before = 0;
+    for (int s0 = 0; s0 < a.b.n_seqs; s0 += kThreads) {
+      const int s = s0 + tid;
+      const int64_t v = s < a.b.n_seqs ? (a.b.n_seqs <= kThreads ? mine : total_blocks(a, seq_size(a, s))) : 0;
+      const int64_t inc = wave_incl_scan64(v);
+      __syncthreads();
+      if (lane == 63) sums[wave] = inc;
+      __syncthreads();
+      int64_t at = before + inc - v;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) {
+        if (i < wave) at += sums[i];
+        before += sums[i];
+      }
+      if (at <= cur && cur < at + v) {
+        found = s;
+        found_cum = at;
+      }
+      if (cur < before) break;
+    }
+    __syncthreads();
+  }
+  int seq = __builtin_amdgcn_readfirstlane(found);
+  int64_t cum = found_cum;  // blocks before the sequence
+
   const int n = lane & 15, g = lane >> 4;  // query row of the lane, lane group
-  const uint32_t kbuf = lds_addr(lds_raw) + wave * L::kWaveLds, vbuf = kbuf + L::kBuf;
+  const uint32_t vbuf = lds_addr(lds_raw) + wave * L::kWaveLds;
+  while (true) {
+  const SeqSize z = seq_size(a, seq);
+  const int seg = (int)div_u64((uint64_t)(cur - cum), (uint64_t)z.blocks), o0 = (int)(cur - cum - (int64_t)seg * z.blocks);
+  const int o1 = (int)min((int64_t)z.blocks, o0 + (end - cur));
+  const int kvh = __builtin_amdgcn_readfirstlane(seg % a.kv.n_kv);
+  Tile t;
+  t.seq = seq;
+  set_tile(a, (int64_t)(seg / a.kv.n_kv) * kAttnRows, kAttnRows, t);
 
   // this lane's query row
   const int rr = t.r0 + n;
@@ -180,77 +348,102 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(AttnArgs a) {
   // visible keys: first_key .. last_key
   const int last_key = (int)(a.full ? (live ? (int64_t)t.len - 1 : -1) : min(pos, (int64_t)t.len - 1));
   const int first_key = a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
-  // every live row of the tile sees all keys of [all_lo, all_hi)
+  // every row of the tile sees all keys of [all_lo, all_hi); lanes without a row (queries of
+  // zeros) go along, and nothing of theirs is stored
   const int64_t pf = t.first + t.r0 / a.G, pl = t.first + (t.r0 + t.nr - 1) / a.G;
   const int all_hi = (int)(a.full ? (int64_t)t.len : min(pf + 1, (int64_t)t.len));
   const int64_t all_lo = a.window ? pl - a.window + 1 : 0;
 
+  // (lanes without a row read the tile's first one, and take zeros)
+  const uint16_t *qp = a.q.p + (int64_t)(live ? tok : t.t0 + t.r0 / a.G) * a.q.ts +
+                       (int64_t)(live ? head : kvh * a.G + t.r0 % a.G) * a.q.hs;
   u32x4 qf[D / 32];
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    qf[c] = u32x4{0, 0, 0, 0};
-    if (live) qf[c] = *(const u32x4 *)(a.q.p + (int64_t)tok * a.q.ts + (int64_t)head * a.q.hs + 32 * c + 8 * g);
-  }
+  for (int c = 0; c < D / 32; ++c) qf[c] = *(const u32x4 *)(qp + 32 * c + 8 * g);
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c)
+    if (!live) qf[c] = u32x4{0, 0, 0, 0};
 
-  // this split's blocks of 32 keys
+  // this run's blocks of the segment
   const int blk0 = t.lo / kAttnKeys, nblk = (t.hi + kAttnKeys - 1) / kAttnKeys - blk0;
-  const int b0 = blk0 + (int)((int64_t)nblk * split / a.splits), b1 = blk0 + (int)((int64_t)nblk * (split + 1) / a.splits);
+  const int b0 = blk0 + min(nblk, o0), b1 = blk0 + min(nblk, o1);
+  const bool alone = o0 == 0 && o1 == z.blocks;
+  // partial results: of a segment that goes on in the next run, and of one from the run before
+  const int64_t slot = (2 * (int64_t)wg + (o0 == 0)) * kAttnRows;
 
   f32x4 acc[D / 16];
 #pragma unroll
   for (int d = 0; d < D / 16; ++d) acc[d] = f32x4{0, 0, 0, 0};
   float m = -INFINITY, l = 0.0f;
 
-  // The page of the 16 keys from `key`, or -1; and its rows' base in one plane.
-  const int32_t *trow = a.b.table + (int64_t)max(t.row, 0) * a.b.cols;
+  const TableRow trow = table_row(a, t.row);
   const int pmask = (1 << a.kv.page_shift) - 1;
-  auto page_of = [&](int key) {
-    const int col = key >> a.kv.page_shift;
-    const int page = col < a.b.cols ? trow[col] : -1;
-    return __builtin_amdgcn_readfirstlane((unsigned)page < (unsigned)a.kv.n_pages ? page : -1);
-  };
+  auto page_of = [&](int key) { return page_at(a, trow, key); };
   auto base = [&](const uint16_t *plane, int page, int key) {
-    return plane + (int64_t)max(page, 0) * a.kv.ps + (int64_t)(key & pmask) * a.kv.ts + (int64_t)kvh * a.kv.hs;
+    return (const char *)uniform_ptr(plane + (int64_t)max(page, 0) * a.kv.ps + (int64_t)(key & pmask) * a.kv.ts +
+                                     (int64_t)kvh * a.kv.hs);
   };
-  constexpr int kLoads = D / 16;  // load instructions of one block
+  // K comes in the layout of the matrix operand (lane: key n of a half, 8 elements from 8 g of
+  // each 32), V in rows of whole cache lines
+  constexpr int kChunks = D / 8, kRowsPer = 64 / kChunks, kVLoads = kAttnKeys / kRowsPer;
+  const int ts2 = (int)a.kv.ts * 2;
+  const int koff = n * ts2 + 16 * g, vrow = lane / kChunks;
+  const int voff = vrow * ts2 + lane % kChunks * 16;
+  u32x4 kr[2][D / 32], vr[kVLoads];
+  auto load = [&](int key0, int pg0, int pg1) {
+    const char *k0 = base(a.kv.k, pg0, key0), *k1 = base(a.kv.k, pg1, key0 + 16);
+    const char *v0 = base(a.kv.v, pg0, key0), *v1 = base(a.kv.v, pg1, key0 + 16);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) kr[0][c] = *(const u32x4 *)(k0 + koff + 64 * c);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) kr[1][c] = *(const u32x4 *)(k1 + koff + 64 * c);
+#pragma unroll
+    for (int i = 0; i < kVLoads; ++i)
+      vr[i] = *(const u32x4 *)((i < kVLoads / 2 ? v0 : v1) + (voff + i % (kVLoads / 2) * kRowsPer * ts2));
+  };
 
   int blk = b0 + wave;
   int pg0 = -1, pg1 = -1;
   if (blk < b1) {
     pg0 = page_of(blk * kAttnKeys);
     pg1 = page_of(blk * kAttnKeys + 16);
-    load_block<D>(base(a.kv.k, pg0, blk * kAttnKeys), base(a.kv.k, pg1, blk * kAttnKeys + 16), a.kv.ts, kbuf);
-    load_block<D>(base(a.kv.v, pg0, blk * kAttnKeys), base(a.kv.v, pg1, blk * kAttnKeys + 16), a.kv.ts, vbuf);
+    load(blk * kAttnKeys, pg0, pg1);
   }
   for (; blk < b1; blk += kWaves) {
     const int key0 = blk * kAttnKeys;
-    const bool more = blk + kWaves < b1;
-    int npg0 = -1, npg1 = -1;
-    if (more) {
-      npg0 = page_of(key0 + kWaves * kAttnKeys);
-      npg1 = page_of(key0 + kWaves * kAttnKeys + 16);
-    }
+    // (a block behind the last one is not loaded: its numbers are those of this one)
+    const int next = blk + kWaves < b1 ? key0 + kWaves * kAttnKeys : key0;
+    const int npg0 = page_of(next), npg1 = page_of(next + 16);
     // keys present in the halves (behind the sequence's end, or in a bad page: absent)
     const int have0 = pg0 < 0 ? 0 : max(0, min(16, t.len - key0));
     const int have1 = pg1 < 0 ? 0 : max(0, min(16, t.len - key0 - 16));
 
-    wait_vm<kLoads>();
     f32x4 s[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
     for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 16 * h + n;
-        const u32x4 kf = *(const __attribute__((address_space(3))) u32x4 *)(uintptr_t)(kbuf + r * D * 2 +
-                                                                                 (((4 * c + g) ^ swz<D>(r)) * 16));
-        s[h] = mfma16<F16>(kf, qf[c], s[h]);
-      }
-    wait_lds();
-    if (more)
-      load_block<D>(base(a.kv.k, npg0, key0 + kWaves * kAttnKeys), base(a.kv.k, npg1, key0 + kWaves * kAttnKeys + 16),
-                    a.kv.ts, kbuf);
+      for (int h = 0; h < 2; ++h) s[h] = mfma16<F16>(kr[h][c], qf[c], s[h]);
 
-    const bool whole = have0 + have1 == kAttnKeys && key0 + kAttnKeys <= all_hi && key0 >= all_lo && t.nr == kAttnRows;
+    const bool edge = key0 + kAttnKeys > all_hi || key0 < all_lo;
+    const bool whole = have0 + have1 == kAttnKeys && !edge;
+    if (!whole) {
+      uint32_t bad = 0;
+#pragma unroll
+      for (int i = 0; i < kVLoads; ++i) {
+        const int r = i * kRowsPer + vrow;
+        const bool absent = (r & 15) >= (r < 16 ? have0 : have1);
+        if (edge) bad |= make_finite<F16>(vr[i], absent);
+        else if (absent) vr[i] = u32x4{0, 0, 0, 0};
+      }
+      if (bad) odd = 1;
+    }
+#pragma unroll
+    for (int i = 0; i < kVLoads; ++i) {
+      const int r = i * kRowsPer + vrow;
+      *(__attribute__((address_space(3))) u32x4 *)(uintptr_t)(vbuf + r * D * 2 + (((lane % kChunks) ^ swz<D>(r)) * 16)) = vr[i];
+    }
+    if (blk + kWaves < b1) load(next, npg0, npg1);
+
     float p[8];
     float mx = -INFINITY;
 #pragma unroll
@@ -280,60 +473,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(AttnArgs a) {
     }
     const u32x4 pf4 = {pack2<F16>(p[0], p[1]), pack2<F16>(p[2], p[3]), pack2<F16>(p[4], p[5]), pack2<F16>(p[6], p[7])};
 
-    if (more) wait_vm<kLoads>(); else wait_vm<0>();
-    bool odd = false;  // the block holds values that must not meet a zero weight
-    if (!whole) {
-      // absent keys' values become zeros; then look for infinities and NaN among the rest
-      constexpr int kChunks = D / 8;
-#pragma unroll
-      for (int i = 0; i < kAttnKeys * kChunks / 64; ++i) {
-        const int r = (i * 64 + lane) / kChunks;
-        auto *w = (__attribute__((address_space(3))) u32x4 *)(uintptr_t)(vbuf + (i * 64 + lane) * 16);
-        if ((r & 15) >= (r < 16 ? have0 : have1)) {
-          *w = u32x4{0, 0, 0, 0};
-        } else {
-          const u32x4 v = *w;
-          odd |= nonfinite<F16>(v[0]) || nonfinite<F16>(v[1]) || nonfinite<F16>(v[2]) || nonfinite<F16>(v[3]);
-        }
-      }
-      odd = __ballot(odd) != 0;
-      wait_lds();
-    }
-    if (!odd) {
-      const int kr = 4 * g + (n >> 2);  // LDS row this lane addresses for the transposing reads
+    {
+      const int vk = 4 * g + (n >> 2);  // LDS row this lane addresses for the transposing reads
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
         const int c = 2 * d + ((n & 3) >> 1);
-        const uint32_t o = (uint32_t)((c ^ swz<D>(kr)) * 16 + (n & 1) * 8 + kr * D * 2);
-        const uint32_t o2 = (uint32_t)((c ^ swz<D>(kr + 16)) * 16 + (n & 1) * 8 + (kr + 16) * D * 2);
+        const uint32_t o = (uint32_t)((c ^ swz<D>(vk)) * 16 + (n & 1) * 8 + vk * D * 2);
+        const uint32_t o2 = (uint32_t)((c ^ swz<D>(vk + 16)) * 16 + (n & 1) * 8 + (vk + 16) * D * 2);
         const uint64_t v0 = tr_read(vbuf + o), v1 = tr_read(vbuf + o2);
         const u32x4 vf = {(uint32_t)v0, (uint32_t)(v0 >> 32), (uint32_t)v1, (uint32_t)(v1 >> 32)};
         acc[d] = mfma16<F16>(vf, pf4, acc[d]);
       }
-    } else {
-      // rare: values are summed key by key, for the rows that see the key only
-      for (int k = 0; k < kAttnKeys; ++k) {
-        const uint32_t w01 = (k & 2) ? pf4[k / 16 * 2 + 1] : pf4[k / 16 * 2];
-        const float pk = unpack<F16>(__shfl(w01, n + 16 * ((k & 15) >> 2), 64), k & 1);
-        const int key = key0 + k;
-        const bool sees = (k & 15) < (k < 16 ? have0 : have1) && key <= last_key && key >= first_key;
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-          const int e = 16 * d + 4 * g;
-          const uint64_t w = *(const __attribute__((address_space(3))) uint64_t *)(uintptr_t)(
-              vbuf + k * D * 2 + (((e / 8) ^ swz<D>(k)) * 16 + (e & 4) * 2));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v = unpack<F16>((uint32_t)(i < 2 ? w : w >> 32), i & 1);
-            acc[d][i] = sees ? __builtin_fmaf(pk, v, acc[d][i]) : acc[d][i];
-          }
-        }
-      }
     }
-    wait_lds();
-    if (more)
-      load_block<D>(base(a.kv.v, npg0, key0 + kWaves * kAttnKeys), base(a.kv.v, npg1, key0 + kWaves * kAttnKeys + 16),
-                    a.kv.ts, vbuf);
     pg0 = npg0;
     pg1 = npg1;
   }
@@ -365,19 +516,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(AttnArgs a) {
     }
     const int q = t.r0 + r;
     const int64_t tk = t.t0 + q / a.G, hd = kvh * a.G + q % a.G;
-    if (a.splits == 1) {
+    if (alone) {
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       const uint2 w = {pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv)};
       *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + c) = w;
       if (a.lse && c == 0) a.lse[tk * a.H + hd] = sum == 0.0f ? -INFINITY : (mw + __log2f(sum)) * kLn2;
     } else {
-      const int64_t at = (tk * a.H + hd) * a.splits + split;
+      const int64_t at = slot + r;
       *(f32x4 *)(a.part + at * D + c) = v;
       if (c == 0) {
         a.part_ml[2 * at] = mw;
         a.part_ml[2 * at + 1] = sum;
       }
     }
+  }
+  if (odd) {  // (a barrier lies behind its last write)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "agent");
+    __syncthreads();
+    put_back<D, F16>(a, t, kvh, b0, b1, (int)min(all_lo, (int64_t)INT32_MAX), all_hi, t.r0 + wave, t.r0 + t.nr, kWaves,
+                     [&](int r, int64_t, int64_t) { return alone ? nullptr : a.part + (slot + r - t.r0) * D; });
+  }
+  if (o0 == 0 && o1 < z.blocks) {  // the first of the workgroups that share the segment
+    if (tid == 0) a.rec[wg] = AttnRec{runs.holder(cum + (int64_t)(seg + 1) * z.blocks - 1) - wg + 1, t.t0, t.r0, t.nr, kvh};
+    return;
+  }
+  cur += o1 - o0;
+  if (cur == end) return;
+  __syncthreads();  // buffers, sums and the flag are free again
+  if (tid == 0) odd = 0;
+  if (cur == cum + total_blocks(a, z)) {  // the next sequence that has new tokens
+    cum = cur;
+    for (int s0 = seq + 1;; s0 += 64) {
+      const uint64_t some = __ballot(s0 + lane < a.b.n_seqs && seq_size(a, s0 + lane).tiles > 0);
+      if (some) {
+        seq = s0 + __builtin_ctzll(some);
+        break;
+      }
+      if (s0 + 64 >= a.b.n_seqs) return;  // (never: blocks are left)
+    }
+  }
+  __syncthreads();
   }
 }
 
@@ -452,27 +630,26 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   // is the largest product
   const float scale = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);  // 0: of queries of zeros
   const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+  // (lanes without a row read the tile's first one, and take zeros)
+  const uint16_t *qp = a.q.p + (int64_t)(live ? tok : t.t0 + t.r0 / a.G) * a.q.ts +
+                       (int64_t)(live ? head : kvh * a.G + t.r0 % a.G) * a.q.hs;
   u32x4 qf[D / 16];
 #pragma unroll
+  for (int c = 0; c < D / 16; ++c) qf[c] = *(const u32x4 *)(qp + 16 * c + 8 * half);
+#pragma unroll
   for (int c = 0; c < D / 16; ++c) {
-    qf[c] = u32x4{0, 0, 0, 0};
-    if (live && a.scale_log2 != 0.0f)
-      qf[c] = *(const u32x4 *)(a.q.p + (int64_t)tok * a.q.ts + (int64_t)head * a.q.hs + 16 * c + 8 * half);
+    if (!live || a.scale_log2 == 0.0f) qf[c] = u32x4{0, 0, 0, 0};
     qf[c] ^= flip;
   }
 
   const int blk0 = t.lo / kAttnKeys, nblk = (t.hi + kAttnKeys - 1) / kAttnKeys - blk0;
-  const int b0 = blk0 + (int)((int64_t)nblk * split / a.splits), b1 = blk0 + (int)((int64_t)nblk * (split + 1) / a.splits);
+  const int b0 = blk0 + min(nblk, split * a.split_blocks), b1 = blk0 + (split + 1 == a.splits ? nblk : min(nblk, (split + 1) * a.split_blocks));
 
-  const int32_t *trow = a.b.table + (int64_t)max(t.row, 0) * a.b.cols;
+  const TableRow trow = table_row(a, t.row);
   const int pmask = (1 << a.kv.page_shift) - 1;
   // the rows that this wave loads lie in one 16-key half of a block
   const int my_r0 = wave * kInstr * kRowsPer;
-  auto page_of = [&](int blk) {
-    const int col = (blk * kAttnKeys + (my_r0 & 16)) >> a.kv.page_shift;
-    const int page = blk < b1 && col < a.b.cols ? trow[col] : -1;
-    return __builtin_amdgcn_readfirstlane((unsigned)page < (unsigned)a.kv.n_pages ? page : -1);
-  };
+  auto page_of = [&](int blk) { return page_at(a, trow, blk * kAttnKeys + (my_r0 & 16)); };
   uint32_t voff[kInstr];
 #pragma unroll
   for (int i = 0; i < kInstr; ++i) {
@@ -514,16 +691,8 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
         const int r = my_r0 + i * kRowsPer + lane / (D / 8);
         auto *w = (__attribute__((address_space(3))) u32x4 *)(uintptr_t)(vbuf + (wave * kInstr + i) * 1024 + lane * 16);
         u32x4 v = *w;
-        const bool absent = pg < 0 || key0 + r >= t.len;
-        bool bad = false;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (nonfinite16<F16>(v[j])) v[j] &= 0xffff0000u, bad = true;
-          if (nonfinite16<F16>(v[j] >> 16)) v[j] &= 0xffffu, bad = true;
-        }
-        if (absent) v = u32x4{0, 0, 0, 0};
-        if (absent || bad) *w = v;
-        if (bad && !absent) odd = 1;
+        if (make_finite<F16>(v, pg < 0 || key0 + r >= t.len)) odd = 1;
+        *w = v;
       }
     }
     wait_lds();
@@ -547,11 +716,9 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
       const u32x4 kf = *(const __attribute__((address_space(3))) u32x4 *)(uintptr_t)(ka ^ (c * 32));
       s = mfma32<F16>(kf, qf[c], s);
     }
-    // pages of the block's halves: bad ones are rare, so looked up again where masks are made
-    bool whole = key0 + kAttnKeys <= all_hi && key0 >= all_lo && wn == 32;
-    const int c0 = key0 >> a.kv.page_shift, c1 = (key0 + 16) >> a.kv.page_shift;
-    const int have0 = c0 < a.b.cols && (unsigned)trow[c0] < (unsigned)a.kv.n_pages ? max(0, min(16, t.len - key0)) : 0;
-    const int have1 = c1 < a.b.cols && (unsigned)trow[c1] < (unsigned)a.kv.n_pages ? max(0, min(16, t.len - key0 - 16)) : 0;
+    bool whole = key0 + kAttnKeys <= all_hi && key0 >= all_lo;
+    const int have0 = page_at(a, trow, key0) < 0 ? 0 : max(0, min(16, t.len - key0));
+    const int have1 = page_at(a, trow, key0 + 16) < 0 ? 0 : max(0, min(16, t.len - key0 - 16));
     whole = whole && have0 + have1 == kAttnKeys;
     if (!whole) {
 #pragma unroll
@@ -620,6 +787,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
     if (a.lse && half == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m * scale + __log2f(l)) * kLn2;
   } else {
     const int64_t at = row * a.splits + split;
+    if (b0 < b1)
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -632,67 +800,132 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
     }
   }
   if (!fix) return;
-  // rare: add the infinities and NaN that were taken out to the rows that see them
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "agent");
-  constexpr int kE = D / 64;
-  for (int key = max(t.lo, b0 * kAttnKeys); key < min(t.hi, b1 * kAttnKeys); ++key) {
-    const int k0 = key & ~(kAttnKeys - 1), col = key >> a.kv.page_shift;
-    const int page = trow[col];
-    if ((k0 + kAttnKeys <= all_hi_t && k0 >= all_lo_t) || (unsigned)page >= (unsigned)a.kv.n_pages) continue;
-    const uint16_t *v = a.kv.v + (int64_t)page * a.kv.ps + (int64_t)(key & pmask) * a.kv.ts + (int64_t)kvh * a.kv.hs;
-    float x[kE];
-    bool any = false;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const uint16_t w = v[lane * kE + e];
-      x[e] = nonfinite16<F16>(w) ? unpack<F16>(w, false) : 0.0f;
-      any |= nonfinite16<F16>(w);
-    }
-    if (!__ballot(any)) continue;
-    for (int r = 0; r < wn; ++r) {
-      const int64_t p = t.first + (w0 + r) / a.G;
-      if ((!a.full && key > p) || (a.window && key <= p - a.window)) continue;
-      const int64_t tk = t.t0 + (w0 + r) / a.G, hd = kvh * a.G + (w0 + r) % a.G;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        if (x[e] == 0.0f) continue;
-        if (a.splits == 1) {
-          uint16_t *o = a.out.p + tk * a.out.ts + hd * a.out.hs + lane * kE + e;
-          *o = (uint16_t)pack2<F16>(unpack<F16>(*o, false) + x[e], 0.0f);
-        } else {
-          a.part[((tk * a.H + hd) * a.splits + split) * D + lane * kE + e] += x[e];
-        }
-      }
-    }
-  }
+  put_back<D, F16>(a, t, kvh, b0, b1, all_lo_t, all_hi_t, t.r0 + wave * 32, t.r0 + wave * 32 + wn, 1,
+                   [&](int, int64_t tk, int64_t hd) {
+                     return a.splits == 1 ? nullptr : a.part + ((tk * a.H + hd) * a.splits + split) * D;
+                   });
 }
 
-// Join the splits' partial results: one wave per (token, head), D / 64 elements a lane.
+// Join the splits' partial results: one workgroup per (token, head).  Every wave holds the
+// splits' weights, split s in lane s % 64; D / 4 threads take the splits of their group in
+// turn, four loads in flight, and the groups' sums are added in LDS.  Splits without keys have
+// weight 0 and their outputs are not read (they are not written either).
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads) k_attn_join(AttnArgs a) {
-  const int64_t r = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
+  constexpr int kVecs = D / 4, kGroups = kThreads / kVecs, kRegs = kMaxSplits / 64;
+  __shared__ f32x4 sums[kGroups][kVecs];
+  __shared__ float weight[kMaxSplits];
+  const int64_t r = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63;
   const int64_t tk = r / a.H, hd = r % a.H;
-  if (tk >= a.T || tk >= a.b.q_start[a.b.n_seqs]) return;
-  const float *ml = a.part_ml + r * a.splits * 2;
-  float mw = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) mw = fmaxf(mw, ml[2 * s]);
-  const float mu = mw == -INFINITY ? 0.0f : mw;
-  constexpr int kE = D / 64;
-  float v[kE] = {};
-  float sum = 0.0f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float f = __builtin_amdgcn_exp2f(ml[2 * s] - mu);
-    sum += f * ml[2 * s + 1];
-    const float *p = a.part + (r * a.splits + s) * D + lane * kE;
+  if (tk >= a.b.q_start[a.b.n_seqs]) return;
+  float ms[kRegs], ls[kRegs], mw = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) v[e] += f * p[e];
+  for (int i = 0; i < kRegs; ++i) {
+    ms[i] = -INFINITY;
+    ls[i] = 0.0f;
+    if (64 * i + lane < a.splits) {
+      const float *ml = a.part_ml + (r * a.splits + 64 * i + lane) * 2;
+      ms[i] = ml[0];
+      ls[i] = ml[1];
+    }
+    mw = fmaxf(mw, ms[i]);
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint16_t *o = a.out.p + tk * a.out.ts + hd * a.out.hs + lane * kE;
+  mw = wave_max(mw);
+  const float mu = mw == -INFINITY ? 0.0f : mw;
+  float sum = 0.0f;
 #pragma unroll
-  for (int e = 0; e < kE; ++e) o[e] = (uint16_t)pack2<F16>(v[e] * inv, 0.0f);
-  if (a.lse && lane == 0) a.lse[r] = sum == 0.0f ? -INFINITY : (mw + __log2f(sum)) * kLn2;
+  for (int i = 0; i < kRegs; ++i) {
+    const float f = ls[i] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ms[i] - mu);
+    sum += f * ls[i];
+    if (tid < 64) weight[64 * i + lane] = f;
+  }
+  sum = wave_sum(sum);
+  __syncthreads();
+  const int c = tid % kVecs, g = tid / kVecs;
+  const f32x4 *p = (const f32x4 *)(a.part + r * a.splits * D) + c;
+  f32x4 v = {0, 0, 0, 0};
+  for (int s0 = g; s0 < a.splits; s0 += 4 * kGroups) {
+    f32x4 x[4];
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = s0 + i * kGroups;
+      w[i] = s < a.splits ? weight[s] : 0.0f;
+      x[i] = f32x4{0, 0, 0, 0};
+      if (w[i] != 0.0f) x[i] = p[(int64_t)s * kVecs];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v += w[i] * x[i];
+  }
+  sums[g][c] = v;
+  __syncthreads();
+  if (g > 0) return;
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i) v += sums[i][c];
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + 4 * c) =
+      make_uint2(pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv));
+  if (a.lse && tid == 0) a.lse[r] = sum == 0.0f ? -INFINITY : (mw + __log2f(sum)) * kLn2;
+}
+
+// Join the runs' partial results of segments that several workgroups share: workgroup x takes
+// the segment, if any, that starts in run x, rows in turn.  Run x's results lie in its second
+// slot, the following runs' in their first ones.
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads) k_attn_join_runs(AttnArgs a) {
+  constexpr int kVecs = D / 4, kGroups = kThreads / kVecs;
+  __shared__ f32x4 sums[kGroups][kVecs];
+  __shared__ float weight[kMaxRuns], red[2][kWaves];
+  const int wg = blockIdx.x;
+  const AttnRec rec = a.rec[wg];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int c = tid % kVecs, g = tid / kVecs;
+  for (int r = blockIdx.y; rec.n > 0 && r < rec.nr; r += gridDim.y) {
+    auto at = [&](int s) { return (2 * (int64_t)(wg + s) + (s == 0)) * kAttnRows + r; };
+    float mw = -INFINITY;
+    for (int s = tid; s < rec.n; s += kThreads) mw = fmaxf(mw, a.part_ml[2 * at(s)]);
+    mw = wave_max(mw);
+    if (lane == 0) red[0][tid >> 6] = mw;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) mw = fmaxf(mw, red[0][i]);
+    const float mu = mw == -INFINITY ? 0.0f : mw;
+    float sum = 0.0f;
+    for (int s = tid; s < rec.n; s += kThreads) {
+      const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at(s)] - mu);
+      sum += f * a.part_ml[2 * at(s) + 1];
+      weight[s] = f;
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) red[1][tid >> 6] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) sum += red[1][i];
+    f32x4 v = {0, 0, 0, 0};
+    for (int s0 = g; s0 < rec.n; s0 += 4 * kGroups) {
+      f32x4 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = *(const f32x4 *)(a.part + at(min(s0 + i * kGroups, rec.n - 1)) * D + 4 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (s0 + i * kGroups < rec.n) v += weight[s0 + i * kGroups] * x[i];
+    }
+    sums[g][c] = v;
+    __syncthreads();
+    if (g == 0) {
+#pragma unroll
+      for (int i = 1; i < kGroups; ++i) v += sums[i][c];
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const int64_t tk = rec.t0 + (rec.r0 + r) / a.G, hd = rec.kvh * a.G + (rec.r0 + r) % a.G;
+      *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + 4 * c) =
+          make_uint2(pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv));
+      if (a.lse && tid == 0) a.lse[tk * a.H + hd] = sum == 0.0f ? -INFINITY : (mw + __log2f(sum)) * kLn2;
+    }
+    __syncthreads();
+  }
 }
 
 // Sets the LDS limit of a kernel, once for each device (the attribute belongs to the device).
@@ -709,40 +942,55 @@ hipError_t allow_lds(K k, int lds, std::atomic<uint64_t> &done) {
 
 template <int D, bool F16>
 hipError_t launch(const AttnArgs &a, hipStream_t s) {
-  const dim3 grid(a.tiles, a.kv.n_kv, a.splits);
   if (a.rows == kAttnRows) {
     static std::atomic<uint64_t> done{0};
     const hipError_t e = allow_lds(k_attn_rows<D, F16>, Rows<D>::kLds, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn_rows<D, F16>), grid, dim3(kThreads), Rows<D>::kLds, s, a);
+    hipLaunchKernelGGL((k_attn_rows<D, F16>), dim3(a.wgs), dim3(kThreads), Rows<D>::kLds, s, a);
+    hipLaunchKernelGGL((k_attn_join_runs<D, F16>), dim3(a.wgs, a.join_rows), dim3(kThreads), 0, s, a);
   } else {
     static std::atomic<uint64_t> done{0};
     constexpr int lds = kStages * 2 * kAttnKeys * D * 2 + 16, nw = attn_tile(D) / 32;
     const hipError_t e = allow_lds(k_attn_tile<D, F16, nw>, lds, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn_tile<D, F16, nw>), grid, dim3(64 * nw), lds, s, a);
+    hipLaunchKernelGGL((k_attn_tile<D, F16, nw>), dim3(a.tiles, a.kv.n_kv, a.splits), dim3(64 * nw), lds, s, a);
+    if (a.splits > 1)
+      hipLaunchKernelGGL((k_attn_join<D, F16>), dim3(a.T * a.H), dim3(kThreads), 0, s, a);
   }
-  if (a.splits > 1)
-    hipLaunchKernelGGL((k_attn_join<D, F16>), dim3(((int64_t)a.T * a.H + kWaves - 1) / kWaves), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int H, int n_kv, int dim) {
+AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int window, int H, int n_kv, int dim) {
   AttnShape s{};
   const int64_t G = H / n_kv;
   s.rows = max_q * G > 2 * kAttnRows ? attn_tile(dim) : kAttnRows;
   s.tiles = (int)(T * G / s.rows + n_seqs);
+  if (T == 0) return s;
+  if (s.rows == kAttnRows) {
+    s.splits = 1;
+    s.wgs = runs_of(dim);
+    s.join_rows = (int)(max_q * G < 1 ? 1 : max_q * G < kAttnRows ? max_q * G : kAttnRows);
+    const size_t slots = (size_t)2 * s.wgs * kAttnRows;
+    s.off_ml = slots * dim * 4;
+    s.off_rec = s.off_ml + slots * 8;
+    s.ws_bytes = s.off_rec + s.wgs * sizeof(AttnRec);
+    return s;
+  }
   // tiles that can hold rows, and splits that fill the chip with them
   int64_t busy = (max_q * G + s.rows - 1) / s.rows;
   busy = (busy < 1 ? 1 : busy) * n_seqs;
   if (busy > s.tiles) busy = s.tiles;
   busy *= n_kv;
-  const int64_t want = (s.rows == kAttnRows ? 512 : 256) / (busy < 1 ? 1 : busy);
-  const int64_t most = (max_kv + kAttnKeys * kWaves - 1) / (kAttnKeys * kWaves);
-  int64_t n = want < most ? want : most;
-  s.splits = (int)(n < 1 || T * H > 1 << 22 ? 1 : n > 64 ? 64 : n);
+  const int64_t want = 256 / (busy < 1 ? 1 : busy);
+  if (window > 0 && max_kv > window + max_q) max_kv = window + max_q;
+  const int64_t blocks = (max_kv + kAttnKeys - 1) / kAttnKeys + 1;
+  int64_t per = (blocks + (want < 1 ? 1 : want) - 1) / (want < 1 ? 1 : want);  // blocks of a split
+  if (per < kWaves) per = kWaves;
+  if (per * kMaxSplits < blocks) per = (blocks + kMaxSplits - 1) / kMaxSplits;
+  s.splits = T * H > 1 << 22 ? 1 : (int)((blocks + per - 1) / per);
+  s.split_blocks = (int)per;
   if (s.splits > 1) {
     const size_t rows = (size_t)T * H * s.splits;
     s.off_ml = (rows * dim * 4 + 255) & ~(size_t)255;

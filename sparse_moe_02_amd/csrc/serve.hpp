@@ -42,27 +42,34 @@ constexpr int kAttnRows = 16;   // query rows (token x head of a group) of a sma
 constexpr int attn_tile(int dim) { return dim == 64 ? 128 : 256; }
 constexpr int kAttnKeys = 32;   // keys of one block
 
+// A segment (row tile and key/value head) whose keys n consecutive workgroups share.
+struct AttnRec {
+  int n, t0, r0, nr, kvh;
+};
+
 struct AttnArgs {
   PagedKv kv;
   Batch b;
   Heads q, out;
   float *lse;      // [T][H] or null
-  float *part;     // [T * H][splits][dim] unnormalised partial outputs (splits > 1)
-  float *part_ml;  // [T * H][splits][2] running maximum (base-2 exponent) and sum
+  float *part;     // unnormalised partial outputs: [T * H][splits][dim], small tiles [wgs][2][16][dim]
+  float *part_ml;  // [..][2] of each: running maximum (base-2 exponent) and sum
   int T, H, G;     // G: query heads of one key/value head
   int rows;        // rows of a tile: kAttnRows or attn_tile(dim)
   int tiles;       // bound on the number of row tiles
-  int splits;
+  int splits, split_blocks;
+  int wgs, join_rows;  // small tiles: workgroups, and rows that the join takes at once
+  AttnRec *rec;        // [wgs]
   int window;
   bool full;
   float scale_log2;
 };
 // What the launch is shaped by, from host-known sizes alone.
 struct AttnShape {
-  int rows, tiles, splits;
-  size_t ws_bytes, off_ml;
+  int rows, tiles, splits, split_blocks, wgs, join_rows;
+  size_t ws_bytes, off_ml, off_rec;
 };
-AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int H, int n_kv, int dim);
+AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int window, int H, int n_kv, int dim);
 hipError_t launch_paged_attn(const AttnArgs &a, hipStream_t s);
 
 struct GdnStepArgs {

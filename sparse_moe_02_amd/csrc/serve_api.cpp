@@ -179,9 +179,9 @@ moe_status check_attn_sizes(int64_t T, int32_t n_seqs, int64_t max_q, int64_t ma
   return MOE_OK;
 }
 
-AttnShape shape_of(int64_t T, int32_t n_seqs, int64_t max_q, int64_t max_kv, int32_t n_heads,
+AttnShape shape_of(int64_t T, int32_t n_seqs, int64_t max_q, int64_t max_kv, int32_t window, int32_t n_heads,
                    const moe_paged_kv &kv) {
-  return attn_shape(T, n_seqs, std::min<int64_t>(max_q, kMaxTokens), std::min<int64_t>(max_kv, int64_t(1) << 30), n_heads,
+  return attn_shape(T, n_seqs, std::min<int64_t>(max_q, kMaxTokens), std::min<int64_t>(max_kv, int64_t(1) << 30), window, n_heads,
                     kv.n_kv_heads, kv.head_dim);
 }
 
@@ -359,12 +359,13 @@ moe_status moe_rope_append(const moe_paged_kv *kv, const moe_batch *batch, int64
 }
 
 moe_status moe_paged_attn_workspace(const moe_paged_kv *kv, int64_t T, int32_t n_seqs, int64_t max_q, int64_t max_kv,
-                                    int32_t n_heads, size_t *bytes) {
+                                    int32_t n_heads, int32_t window, size_t *bytes) {
   if (!bytes) return MOE_ERR_NULL;
   moe_status st = check_kv(kv, false);
   if (st != MOE_OK) return st;
   if ((st = check_attn_sizes(T, n_seqs, max_q, max_kv, n_heads, *kv)) != MOE_OK) return st;
-  *bytes = shape_of(T, n_seqs, max_q, max_kv, n_heads, *kv).ws_bytes;
+  if (window < 0) return MOE_ERR_SHAPE;
+  *bytes = shape_of(T, n_seqs, max_q, max_kv, window, n_heads, *kv).ws_bytes;
   return MOE_OK;
 }
 
@@ -382,7 +383,7 @@ moe_status moe_paged_attn(const moe_paged_kv *kv, const moe_batch *batch, int64_
   if (!aligned(lse, 4)) return MOE_ERR_ALIGN;
   const int64_t D = kv->head_dim;
   if (!heads_distinct(*out, T, n_heads, D)) return MOE_ERR_SHAPE;
-  const AttnShape sh = shape_of(T, batch->n_seqs, max_q, max_kv, n_heads, *kv);
+  const AttnShape sh = shape_of(T, batch->n_seqs, max_q, max_kv, window, n_heads, *kv);
   if (sh.ws_bytes > 0 && (!workspace || workspace_bytes < sh.ws_bytes)) return MOE_ERR_WORKSPACE;
   if (sh.ws_bytes > 0 && !aligned(workspace, 256)) return MOE_ERR_ALIGN;
   const Span sq = span(*q, T, n_heads, D), ck = kv_span(*kv, kv->k), cv = kv_span(*kv, kv->v);
@@ -406,6 +407,10 @@ moe_status moe_paged_attn(const moe_paged_kv *kv, const moe_batch *batch, int64_
   a.rows = sh.rows;
   a.tiles = sh.tiles;
   a.splits = sh.splits;
+  a.split_blocks = sh.split_blocks;
+  a.wgs = sh.wgs;
+  a.join_rows = sh.join_rows;
+  a.rec = reinterpret_cast<AttnRec *>(static_cast<char *>(workspace) + sh.off_rec);
   a.window = window;
   a.full = flags & MOE_ATTN_FULL;
   a.scale_log2 = scale * 1.44269504088896341f;  // scores are kept as base-2 exponents
