@@ -112,9 +112,9 @@ __device__ __forceinline__ TableRow table_row(const AttnArgs &a, int row) {
   return (TableRow)(uintptr_t)uniform_ptr(a.b.table + (int64_t)max(row, 0) * a.b.cols);
 }
 
-// A tile's place in the batch: which sequence, its query rows and the keys they see.
+// A tile's place in its sequence: its query rows and the keys they see.
 struct Tile {
-  int seq, row;       // row: of the table, -1: none
+  int row;            // of the table, -1: none
   int t0, n;          // first token, number of new tokens
   int r0, nr;         // first row (token * G + head) and rows of the tile
   int64_t first;      // position of the sequence's first new token
@@ -122,20 +122,33 @@ struct Tile {
   int lo, hi;         // keys that any row of the tile sees lie in [lo, hi)
 };
 
-// The tile of `rows` rows from r0 of sequence t.seq on.  Returns whether there are any.
-__device__ __forceinline__ bool set_tile(const AttnArgs &a, int64_t r0, int rows, Tile &t) {
+// A sequence of the batch: first token, new tokens (0 where the numbers are no batch: nothing is
+// touched then), table row (or -1) and length.
+struct Seq {
+  int t0, n, row, total;
+};
+__device__ __forceinline__ Seq read_seq(const AttnArgs &a, int s) {
   const Batch &b = a.b;
-  t.t0 = b.q_start[t.seq];
-  const int t1 = b.q_start[t.seq + 1];
-  t.n = t1 - t.t0;
-  if (t.t0 < 0 || t1 > a.T || t.n <= 0) return false;  // (not a batch: touch nothing)
+  Seq q;
+  q.t0 = b.q_start[s];
+  const int t1 = b.q_start[s + 1];
+  q.row = batch_row(b, s);
+  const int len = b.kv_len[max(q.row, 0)];
+  q.total = q.row < 0 ? 0 : len;
+  q.n = q.t0 < 0 || t1 > a.T ? 0 : max(t1 - q.t0, 0);
+  return q;
+}
+
+// The tile of `rows` rows from r0 of a sequence on.  Returns whether there are any.
+__device__ __forceinline__ bool set_tile(const AttnArgs &a, const Seq &q, int64_t r0, int rows, Tile &t) {
+  t.t0 = q.t0;
+  t.n = q.n;
   if (r0 < 0 || r0 >= (int64_t)t.n * a.G) return false;
   t.r0 = (int)r0;
   t.nr = min(rows, t.n * a.G - t.r0);
-  t.row = batch_row(b, t.seq);
-  const int total = t.row < 0 ? 0 : b.kv_len[t.row];
-  t.first = (int64_t)total - t.n;
-  t.len = min(max(total, 0), b.cols << a.kv.page_shift);
+  t.row = q.row;
+  t.first = (int64_t)q.total - t.n;
+  t.len = min(max(q.total, 0), a.b.cols << a.kv.page_shift);
   const int64_t p0 = t.first + t.r0 / a.G, p1 = t.first + (t.r0 + t.nr - 1) / a.G;
   int64_t lo = 0, hi = t.len;
   if (!a.full && p1 + 1 < hi) hi = p1 + 1;
@@ -149,8 +162,9 @@ __device__ __forceinline__ bool set_tile(const AttnArgs &a, int64_t r0, int rows
 // which leaves room for ceil(n_b G / rows) of them, so no list of tiles is needed.
 __device__ __forceinline__ bool find_tile(const AttnArgs &a, int x, int rows, Tile &t) {
   const Batch &b = a.b;
-  t.seq = wave_find(b.n_seqs, x, [&](int i) { return (int64_t)b.q_start[i] * a.G / rows + i; });
-  return set_tile(a, ((int64_t)x - ((int64_t)b.q_start[t.seq] * a.G / rows + t.seq)) * rows, rows, t);
+  const int s = wave_find(b.n_seqs, x, [&](int i) { return (int64_t)b.q_start[i] * a.G / rows + i; });
+  const Seq q = read_seq(a, s);
+  return set_tile(a, q, ((int64_t)x - ((int64_t)q.t0 * a.G / rows + s)) * rows, rows, t);
 }
 
 // Values that not all rows of a tile see must be finite, for a hidden key's weight is 0: absent
@@ -229,14 +243,11 @@ struct Rows {
 struct SeqSize {
   int tiles, blocks;
 };
-__device__ __forceinline__ SeqSize seq_size(const AttnArgs &a, int s) {
-  const int t0 = a.b.q_start[s], t1 = a.b.q_start[s + 1], n = t1 - t0;
-  SeqSize z{0, 1};
-  if (n <= 0 || t0 < 0 || t1 > a.T) return z;
-  z.tiles = (int)(((int64_t)n * a.G + kAttnRows - 1) / kAttnRows);
-  const int row = batch_row(a.b, s), total = row < 0 ? 0 : a.b.kv_len[row];
-  const int len = min(max(total, 0), a.b.cols << a.kv.page_shift);
-  const int64_t lo = a.window ? max((int64_t)total - n - a.window + 1, (int64_t)0) : 0;
+__device__ __forceinline__ SeqSize seq_size(const AttnArgs &a, const Seq &q) {
+  SeqSize z;
+  z.tiles = (int)(((int64_t)q.n * a.G + kAttnRows - 1) / kAttnRows);
+  const int len = min(max(q.total, 0), a.b.cols << a.kv.page_shift);
+  const int64_t lo = a.window ? max((int64_t)q.total - q.n - a.window + 1, (int64_t)0) : 0;
   z.blocks = max(1, (int)((len + kAttnKeys - 1) / kAttnKeys - min(lo, (int64_t)len) / kAttnKeys));
   return z;
 }
@@ -265,15 +276,78 @@ struct Runs {
   }
 };
 
-__device__ __forceinline__ int64_t wave_incl_scan64(int64_t v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t y = __shfl_up((long long)v, d, 64);
-    if (lane >= d) v += y;
-  }
-  return v;
+// Inclusive prefix sums over the wave's lanes, of numbers below 2^53: as binary64, whose DPP
+// steps need no LDS.
+__device__ __forceinline__ int64_t wave_incl_scan64(int64_t x) {
+  double v = (double)x;
+  v += dpp_d<0x111>(v);       // row_shr:1 (lanes without a source take 0)
+  v += dpp_d<0x112>(v);       // row_shr:2
+  v += dpp_d<0x114>(v);       // row_shr:4
+  v += dpp_d<0x118>(v);       // row_shr:8
+  v += dpp_d<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
+  v += dpp_d<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+  return (int64_t)v;
 }
+__device__ __forceinline__ int64_t readlane64(int64_t x, int l) {
+  return ((int64_t)__builtin_amdgcn_readlane((int)(x >> 32), l) << 32) | (uint32_t)__builtin_amdgcn_readlane((int)x, l);
+}
+__device__ __forceinline__ Seq readlane_seq(const Seq &q, int l) {
+  return Seq{__builtin_amdgcn_readlane(q.t0, l), __builtin_amdgcn_readlane(q.n, l), __builtin_amdgcn_readlane(q.row, l),
+             __builtin_amdgcn_readlane(q.total, l)};
+}
+
+// Walks the sequences from the one that holds a block on.  Up to 64 sequences are read once,
+// one a lane; more of them are summed first and then searched 64 at a time.  Every wave does
+// the same.
+struct Walk {
+  int s0;       // sequences s0 .. s0 + 63 are in the lanes
+  Seq mine;
+  int64_t size;  // blocks of this lane's sequence
+  int at;       // lane of the current one
+  int64_t cum;  // blocks before it
+
+  __device__ __forceinline__ void read(const AttnArgs &a, int from) {
+    s0 = from;
+    const int s = from + (threadIdx.x & 63);
+    mine = read_seq(a, min(s, a.b.n_seqs - 1));
+    size = s < a.b.n_seqs ? total_blocks(a, seq_size(a, mine)) : 0;
+  }
+  // blocks of all sequences; leaves the first 64 in the lanes
+  __device__ __forceinline__ int64_t total(const AttnArgs &a) {
+    int64_t sum = 0;
+    for (int s = (a.b.n_seqs - 1) / 64 * 64; s >= 0; s -= 64) {
+      read(a, s);
+      sum += readlane64(wave_incl_scan64(size), 63);
+    }
+    return sum;
+  }
+  // to the sequence that holds block x (below the total)
+  __device__ __forceinline__ void find(const AttnArgs &a, int64_t x) {
+    int64_t before = 0;
+    while (true) {
+      const int64_t inc = wave_incl_scan64(size), all = readlane64(inc, 63);
+      if (x < before + all || s0 + 64 >= a.b.n_seqs) {
+        const uint64_t over = __ballot(before + inc > x);
+        at = over ? __builtin_ctzll(over) : 63;
+        cum = before + readlane64(inc - size, at);
+        return;
+      }
+      before += all;
+      read(a, s0 + 64);
+    }
+  }
+  // to the next sequence that has blocks (there is one)
+  __device__ __forceinline__ void next(const AttnArgs &a) {
+    cum += readlane64(size, at);
+    uint64_t some = __ballot(size > 0) & ~((uint64_t(2) << at) - 1);
+    while (!some && s0 + 64 < a.b.n_seqs) {
+      read(a, s0 + 64);
+      some = __ballot(size > 0);
+    }
+    at = some ? __builtin_ctzll(some) : 63;
+  }
+  __device__ __forceinline__ Seq seq() const { return readlane_seq(mine, at); }
+};
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) k_attn_rows(AttnArgs a) {
@@ -281,64 +355,34 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) k_attn_rows(AttnAr
   extern __shared__ __align__(16) uint8_t lds_raw[];
   __shared__ float ml[kWaves][2][kAttnRows];
   __shared__ int odd;  // some value that not all rows see is an infinity or NaN
-  __shared__ int64_t sums[kWaves], found_cum;
-  __shared__ int found;
   const int wg = blockIdx.x;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
 
   // this workgroup's run, and the sequence where it starts
-  int64_t mine = 0;
-  for (int s = tid; s < a.b.n_seqs; s += kThreads) mine += total_blocks(a, seq_size(a, s));
-  {
-    const int64_t w = wave_incl_scan64(mine);
-    if (lane == 63) sums[wave] = w;
-  }
-  if (tid == 0) odd = 0;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) total += sums[i];
+  Walk walk;
+  const int64_t total = walk.total(a);
   const Runs runs(total, a.wgs);
-  if (tid == 0) a.rec[wg].n = 0;  // results to be joined from this workgroup on: none so far
+  if (tid == 0) {
+    odd = 0;
+    a.rec[wg].n = 0;  // results to be joined from this workgroup on: none so far
+  }
   if (total == 0 || wg >= runs.n) return;
   int64_t cur = runs.start(wg);
   const int64_t end = runs.start(wg + 1);
-  {
-    int64_t before = 0;
-    for (int s0 = 0; s0 < a.b.n_seqs; s0 += kThreads) {
-      const int s = s0 + tid;
-      const int64_t v = s < a.b.n_seqs ? (a.b.n_seqs <= kThreads ? mine : total_blocks(a, seq_size(a, s))) : 0;
-      const int64_t inc = wave_incl_scan64(v);
-      __syncthreads();
-      if (lane == 63) sums[wave] = inc;
-      __syncthreads();
-      int64_t at = before + inc - v;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) {
-        if (i < wave) at += sums[i];
-        before += sums[i];
-      }
-      if (at <= cur && cur < at + v) {
-        found = s;
-        found_cum = at;
-      }
-      if (cur < before) break;
-    }
-    __syncthreads();
-  }
-  int seq = __builtin_amdgcn_readfirstlane(found);
-  int64_t cum = found_cum;  // blocks before the sequence
+  walk.find(a, cur);
+  __syncthreads();
 
   const int n = lane & 15, g = lane >> 4;  // query row of the lane, lane group
   const uint32_t vbuf = lds_addr(lds_raw) + wave * L::kWaveLds;
   while (true) {
-  const SeqSize z = seq_size(a, seq);
+  const Seq sq = walk.seq();
+  const SeqSize z = seq_size(a, sq);
+  const int64_t cum = walk.cum;
   const int seg = (int)div_u64((uint64_t)(cur - cum), (uint64_t)z.blocks), o0 = (int)(cur - cum - (int64_t)seg * z.blocks);
   const int o1 = (int)min((int64_t)z.blocks, o0 + (end - cur));
   const int kvh = __builtin_amdgcn_readfirstlane(seg % a.kv.n_kv);
   Tile t;
-  t.seq = seq;
-  set_tile(a, (int64_t)(seg / a.kv.n_kv) * kAttnRows, kAttnRows, t);
+  set_tile(a, sq, (int64_t)(seg / a.kv.n_kv) * kAttnRows, kAttnRows, t);
 
   // this lane's query row
   const int rr = t.r0 + n;
@@ -544,17 +588,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) k_attn_rows(AttnAr
   if (cur == end) return;
   __syncthreads();  // buffers, sums and the flag are free again
   if (tid == 0) odd = 0;
-  if (cur == cum + total_blocks(a, z)) {  // the next sequence that has new tokens
-    cum = cur;
-    for (int s0 = seq + 1;; s0 += 64) {
-      const uint64_t some = __ballot(s0 + lane < a.b.n_seqs && seq_size(a, s0 + lane).tiles > 0);
-      if (some) {
-        seq = s0 + __builtin_ctzll(some);
-        break;
-      }
-      if (s0 + 64 >= a.b.n_seqs) return;  // (never: blocks are left)
-    }
-  }
+  if (cur == cum + total_blocks(a, z)) walk.next(a);
   __syncthreads();
   }
 }
@@ -873,11 +907,13 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(AttnArgs a) {
 // Join the runs' partial results of segments that several workgroups share: workgroup x takes
 // the segment, if any, that starts in run x, rows in turn.  Run x's results lie in its second
 // slot, the following runs' in their first ones.
+constexpr int kJoinThreads = 512;
+
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) k_attn_join_runs(AttnArgs a) {
-  constexpr int kVecs = D / 4, kGroups = kThreads / kVecs;
+__global__ void __launch_bounds__(kJoinThreads) k_attn_join_runs(AttnArgs a) {
+  constexpr int kVecs = D / 4, kGroups = kJoinThreads / kVecs, kW = kJoinThreads / 64;
   __shared__ f32x4 sums[kGroups][kVecs];
-  __shared__ float weight[kMaxRuns], red[2][kWaves];
+  __shared__ float weight[kMaxRuns], red[2][kW];
   const int wg = blockIdx.x;
   const AttnRec rec = a.rec[wg];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -885,15 +921,15 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_runs(AttnArgs a) {
   for (int r = blockIdx.y; rec.n > 0 && r < rec.nr; r += gridDim.y) {
     auto at = [&](int s) { return (2 * (int64_t)(wg + s) + (s == 0)) * kAttnRows + r; };
     float mw = -INFINITY;
-    for (int s = tid; s < rec.n; s += kThreads) mw = fmaxf(mw, a.part_ml[2 * at(s)]);
+    for (int s = tid; s < rec.n; s += kJoinThreads) mw = fmaxf(mw, a.part_ml[2 * at(s)]);
     mw = wave_max(mw);
     if (lane == 0) red[0][tid >> 6] = mw;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) mw = fmaxf(mw, red[0][i]);
+    for (int i = 0; i < kW; ++i) mw = fmaxf(mw, red[0][i]);
     const float mu = mw == -INFINITY ? 0.0f : mw;
     float sum = 0.0f;
-    for (int s = tid; s < rec.n; s += kThreads) {
+    for (int s = tid; s < rec.n; s += kJoinThreads) {
       const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at(s)] - mu);
       sum += f * a.part_ml[2 * at(s) + 1];
       weight[s] = f;
@@ -903,14 +939,14 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_runs(AttnArgs a) {
     __syncthreads();
     sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) sum += red[1][i];
+    for (int i = 0; i < kW; ++i) sum += red[1][i];
     f32x4 v = {0, 0, 0, 0};
-    for (int s0 = g; s0 < rec.n; s0 += 4 * kGroups) {
-      f32x4 x[4];
+    for (int s0 = g; s0 < rec.n; s0 += 8 * kGroups) {
+      f32x4 x[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = *(const f32x4 *)(a.part + at(min(s0 + i * kGroups, rec.n - 1)) * D + 4 * c);
+      for (int i = 0; i < 8; ++i) x[i] = *(const f32x4 *)(a.part + at(min(s0 + i * kGroups, rec.n - 1)) * D + 4 * c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 8; ++i)
         if (s0 + i * kGroups < rec.n) v += weight[s0 + i * kGroups] * x[i];
     }
     sums[g][c] = v;
@@ -947,7 +983,7 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     const hipError_t e = allow_lds(k_attn_rows<D, F16>, Rows<D>::kLds, done);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((k_attn_rows<D, F16>), dim3(a.wgs), dim3(kThreads), Rows<D>::kLds, s, a);
-    hipLaunchKernelGGL((k_attn_join_runs<D, F16>), dim3(a.wgs, a.join_rows), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((k_attn_join_runs<D, F16>), dim3(a.wgs, a.join_rows), dim3(kJoinThreads), 0, s, a);
   } else {
     static std::atomic<uint64_t> done{0};
     constexpr int lds = kStages * 2 * kAttnKeys * D * 2 + 16, nw = attn_tile(D) / 32;
