@@ -618,11 +618,16 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-constexpr int kStages = 3;  // K and V blocks in LDS: one in use, two in flight
+// K and V blocks in LDS: one in use, the others in flight.  Two of 256-wide heads (64 KiB) leave
+// room for two workgroups on a compute unit, whose matrix and vector phases then overlap: a
+// 4096-token chunk at 32K takes 2042 us; three stages and one workgroup 3248 us, or 2073 us with
+// eight waves.  Narrower heads have room for three.
+constexpr int stages(int dim) { return dim == 256 ? 2 : 3; }
 
 template <int D, bool F16, int NW>
 __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   constexpr int kBuf = kAttnKeys * D * 2;      // one K or V block, bytes
+  constexpr int kStages = stages(D);
   constexpr int kInstr = kBuf / 1024 / NW;     // load instructions a wave issues for one block
   constexpr int kRowsPer = 512 / D;            // LDS rows of one instruction
   static_assert(kInstr >= 1, "every wave loads");
@@ -710,12 +715,12 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   // pages of the block in use, the next, and the one after (for this wave's loads)
   int pg = page_of(b0), pg1 = page_of(b0 + 1), pg2 = page_of(b0 + 2);
   if (b0 < b1) load(b0, pg, 0);
-  if (b0 + 1 < b1) load(b0 + 1, pg1, 1);
+  if (kStages > 2 && b0 + 1 < b1) load(b0 + 1, pg1, 1);
   int stage = 0;
   for (int blk = b0; blk < b1; ++blk) {
     const int key0 = blk * kAttnKeys;
     const uint32_t kbuf = lds0 + stage * 2 * kBuf, vbuf = kbuf + kBuf;
-    if (blk + 1 < b1) wait_vm<2 * kInstr>(); else wait_vm<0>();
+    if (kStages > 2 && blk + 1 < b1) wait_vm<2 * kInstr>(); else wait_vm<0>();
     // where some key is hidden from some row, its weight there is 0 and its value must be
     // finite: absent keys' values (behind the end, in a bad page) become zeros, and so do
     // infinities and NaN, which are put back at the end where they are seen
@@ -732,11 +737,11 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
     wait_lds();
     lds_barrier();
     const int pg3 = page_of(blk + 3);
-    if (blk + 2 < b1) load(blk + 2, pg2, stage == 0 ? 2 : stage - 1);
+    if (blk + kStages - 1 < b1) load(blk + kStages - 1, kStages > 2 ? pg2 : pg1, stage == 0 ? kStages - 1 : stage - 1);
     pg = pg1;
     pg1 = pg2;
     pg2 = pg3;
-    stage = stage == 2 ? 0 : stage + 1;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
     if (key0 >= any_hi || key0 + kAttnKeys <= any_lo) continue;
 
     // the chunk's number enters the swizzled address by exclusive or: one register and one
@@ -986,7 +991,7 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((k_attn_join_runs<D, F16>), dim3(a.wgs, a.join_rows), dim3(kJoinThreads), 0, s, a);
   } else {
     static std::atomic<uint64_t> done{0};
-    constexpr int lds = kStages * 2 * kAttnKeys * D * 2 + 16, nw = attn_tile(D) / 32;
+    constexpr int lds = stages(D) * 2 * kAttnKeys * D * 2 + 16, nw = kAttnTile / 32;
     const hipError_t e = allow_lds(k_attn_tile<D, F16, nw>, lds, done);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((k_attn_tile<D, F16, nw>), dim3(a.tiles, a.kv.n_kv, a.splits), dim3(64 * nw), lds, s, a);
@@ -1001,7 +1006,7 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
 AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int window, int H, int n_kv, int dim) {
   AttnShape s{};
   const int64_t G = H / n_kv;
-  s.rows = max_q * G > 2 * kAttnRows ? attn_tile(dim) : kAttnRows;
+  s.rows = max_q * G > 2 * kAttnRows ? kAttnTile : kAttnRows;
   s.tiles = (int)(T * G / s.rows + n_seqs);
   if (T == 0) return s;
   if (s.rows == kAttnRows) {

@@ -37,9 +37,7 @@ struct RopeArgs {
 hipError_t launch_rope_append(const RopeArgs &a, hipStream_t s);
 
 constexpr int kAttnRows = 16;   // query rows (token x head of a group) of a small tile
-// Query rows of a large tile: eight waves of 32, or four where a block of keys has too few bytes
-// for eight to load.
-constexpr int attn_tile(int dim) { return dim == 64 ? 128 : 256; }
+constexpr int kAttnTile = 128;  // query rows of a large tile: four waves of 32
 constexpr int kAttnKeys = 32;   // keys of one block
 
 // A segment (row tile and key/value head) whose keys n consecutive workgroups share.
@@ -55,7 +53,7 @@ struct AttnArgs {
   float *part;     // unnormalised partial outputs: [T * H][splits][dim], small tiles [wgs][2][16][dim]
   float *part_ml;  // [..][2] of each: running maximum (base-2 exponent) and sum
   int T, H, G;     // G: query heads of one key/value head
-  int rows;        // rows of a tile: kAttnRows or attn_tile(dim)
+  int rows;        // rows of a tile: kAttnRows or kAttnTile
   int tiles;       // bound on the number of row tiles
   int splits, split_blocks;
   int wgs, join_rows;  // small tiles: workgroups, and rows that the join takes at once
