@@ -6,9 +6,12 @@ Calls are enqueued on torch's current stream of the tensors' device and never wa
 
 from __future__ import annotations
 
+import struct
+
 import torch
 
 from . import binding as B
+from ._device import int32, on, stream
 
 _DTYPES = {torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_FP16}
 _SCALINGS = {"none": B.MOE_ROPE_NONE, "linear": B.MOE_ROPE_LINEAR, "ntk": B.MOE_ROPE_NTK, "yarn": B.MOE_ROPE_YARN}
@@ -23,49 +26,54 @@ def rope_freqs(rot_dim: int, base: float = 1e4, scaling: str = "none", factor: f
     return torch.tensor(f, dtype=torch.float64, device=device), mscale
 
 
-def _need(name, t, dtype, device, dim=None):
-    if t.dtype != dtype or t.device != device or (dim is not None and t.dim() != dim):
-        raise ValueError(f"{name}: {dtype} tensor{'' if dim is None else f' of {dim} dimensions'} on {device} required")
+# moe_heads, moe_paged_kv and moe_batch as bytes (packing them costs a fraction of building
+# ctypes structures)
+_HEADS = struct.Struct("Pqq").pack
+_KV = struct.Struct("PPqqqiiiiixxxx").pack
+_BATCH = struct.Struct("PPPPiiixxxx").pack
 
 
-def _ints(name, t, device, dim):
-    _need(name, t, torch.int32, device, dim)
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous tensor required")
-    return t.data_ptr()
-
-
-def _heads(name, t, T, heads, D, dtype, device):
-    _need(name, t, dtype, device, 3)
-    if t.shape != (T, heads, D) or (D > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name}: [{T}][{heads}][{D}] with a contiguous last dimension required")
+def _heads(name, t, T, heads, D, dtype, index):
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (T, heads, D):
+        raise ValueError(f"{name}: {dtype} [{T}][{heads}][{D}] on cuda:{index} required")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"{name}: contiguous last dimension required")
     # strides of dimensions of one element say nothing
-    return B.moe_heads(t.data_ptr(), t.stride(0) if T > 1 else 0, t.stride(1) if heads > 1 else 0)
+    return _HEADS(t.data_ptr(), s[0] if T > 1 else 0, s[1] if heads > 1 else 0)
 
 
-def _cache(k_cache, v_cache, device):
-    if k_cache.dtype not in _DTYPES or not k_cache.is_cuda or k_cache.device != device or k_cache.dim() != 4:
-        raise ValueError(f"k_cache: bfloat16 or float16 [n_pages][page_size][n_kv_heads][head_dim] on {device} required")
-    if v_cache.dtype != k_cache.dtype or v_cache.device != device or v_cache.shape != k_cache.shape:
+def _cache(k, v, index):
+    """(moe_paged_kv, page size, KV heads, head width)"""
+    dtype, shape = k.dtype, k.shape
+    if dtype not in _DTYPES or k.get_device() != index or index < 0 or len(shape) != 4:
+        raise ValueError("k_cache: bfloat16 or float16 [n_pages][page_size][n_kv_heads][head_dim] on q's GPU required")
+    if v.dtype is not dtype or v.get_device() != index or v.shape != shape:
         raise ValueError("v_cache must have k_cache's type, device and shape")
-    n_pages, page, heads, D = k_cache.shape
-    st = [s if n > 1 else 0 for s, n in zip(k_cache.stride(), k_cache.shape)]
-    if st != [s if n > 1 else 0 for s, n in zip(v_cache.stride(), v_cache.shape)] or st[3] != 1:
+    n_pages, page, heads, D = shape
+    s = k.stride()
+    if s != v.stride() or s[3] != 1:
         raise ValueError("k_cache and v_cache must have the same strides and a contiguous last dimension")
-    return B.moe_paged_kv(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], n_pages, page, heads, D,
-                          _DTYPES[k_cache.dtype])
+    kv = _KV(k.data_ptr(), v.data_ptr(), s[0] if n_pages > 1 else 0, s[1] if page > 1 else 0, s[2] if heads > 1 else 0,
+             n_pages, page, heads, D, _DTYPES[dtype])
+    return kv, heads, D
 
 
-def _batch(table, q_start, kv_len, row, device):
-    n = q_start.shape[0] - 1 if q_start.dim() == 1 else -1
-    if row is not None and (row.dim() != 1 or row.shape[0] != n):
-        raise ValueError("row: int32 [n_seqs] required")
-    b = B.moe_batch(_ints("q_start", q_start, device, 1), _ints("kv_len", kv_len, device, 1),
-                    _ints("table", table, device, 2), None if row is None else _ints("row", row, device, 1), n,
-                    table.shape[0], table.shape[1])
-    if kv_len.shape[0] != table.shape[0]:
+def _batch(table, q_start, kv_len, row, index):
+    """(moe_batch, sequences)"""
+    if table.dim() != 2 or q_start.dim() != 1 or kv_len.dim() != 1:
+        raise ValueError("table: [n_rows][cols], q_start: [n_seqs + 1] and kv_len: [n_rows] required")
+    n = q_start.shape[0] - 1
+    rows, cols = table.shape
+    if kv_len.shape[0] != rows:
         raise ValueError("kv_len must have one entry for each row of table")
-    return b
+    r = None
+    if row is not None:
+        r = int32("row", row, index)
+        if row.shape != (n,):
+            raise ValueError("row: int32 [n_seqs] required")
+    return _BATCH(int32("q_start", q_start, index), int32("kv_len", kv_len, index), int32("table", table, index), r or 0, n,
+                  rows, cols), n
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -80,36 +88,35 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torc
     table: int32 [n_rows][cols]; q_start: int32 [n_seqs + 1]; kv_len: int32 [n_rows], new tokens
     included; row: int32 [n_seqs] (default: sequence b has row b); pos: int32 [T] (default: each
     token's position); inv_freq: float64 [rot / 2] of ``rope_freqs`` (None: no rotation).  Returns
-    q_out (may be q itself; by default a new tensor).  Tokens behind q_start[-1] are padding: their
+    q_out (may be q itself; by default a new tensor like q).  Tokens behind q_start[-1] are padding: their
     rows of q_out are left as they were (of a new tensor: unset)."""
-    dev = q.device
-    kv = _cache(k_cache, v_cache, dev)
-    b = _batch(table, q_start, kv_len, row, dev)
+    index, dtype = q.get_device(), k_cache.dtype
+    kv, n_kv, D = _cache(k_cache, v_cache, index)
+    b, _ = _batch(table, q_start, kv_len, row, index)
     if q.dim() != 3:
         raise ValueError("q: [T][n_heads][head_dim] required")
-    T, H, D = q.shape[0], q.shape[1], kv.head_dim
+    T, H, _ = q.shape
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    hq = _heads("q", q, T, H, D, k_cache.dtype, dev)
-    ho = _heads("q_out", q_out, T, H, D, k_cache.dtype, dev)
-    hk = _heads("k", k, T, kv.n_kv_heads, D, k_cache.dtype, dev)
-    hv = _heads("v", v, T, kv.n_kv_heads, D, k_cache.dtype, dev)
+        q_out = torch.empty_like(q)
+    hq = _heads("q", q, T, H, D, dtype, index)
+    ho = hq if q_out is q else _heads("q_out", q_out, T, H, D, dtype, index)
+    hk = _heads("k", k, T, n_kv, D, dtype, index)
+    hv = _heads("v", v, T, n_kv, D, dtype, index)
     fp, rot = None, 0
     if inv_freq is not None:
-        _need("inv_freq", inv_freq, torch.float64, dev, 1)
-        if not inv_freq.is_contiguous():
-            raise ValueError("inv_freq: contiguous tensor required")
+        if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != index or inv_freq.dim() != 1 or \
+                not inv_freq.is_contiguous():
+            raise ValueError(f"inv_freq: contiguous float64 vector on cuda:{index} required")
         fp, rot = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
     pp = None
     if pos is not None:
-        pp = _ints("pos", pos, dev, 1)
-        if pos.shape[0] != T:
+        pp = int32("pos", pos, index)
+        if pos.shape != (T,):
             raise ValueError("pos: int32 [T] required")
-    if T == 0:
-        return q_out
-    with torch.cuda.device(dev):
-        B.moe_rope_append(kv, b, T, hq, ho, H, hk, hv, pp, fp, rot, mscale,
-                          B.MOE_ROPE_INTERLEAVED if interleaved else 0, torch.cuda.current_stream(dev).cuda_stream)
+    if T:
+        with on(index):
+            B.moe_rope_append(kv, b, T, hq, ho, H, hk, hv, pp, fp, rot, mscale,
+                              B.MOE_ROPE_INTERLEAVED if interleaved else 0, stream(index))
     return q_out
 
 
@@ -125,37 +132,34 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, ta
     ``paged_attn_workspace`` bytes (by default one is allocated for the call).  Returns out, or
     (out, lse) with lse float32 [T][n_heads] where lse is given or return_lse is set.  Rows of
     padding tokens behind q_start[-1] are left as they were (of a new tensor: unset)."""
-    dev = q.device
-    kv = _cache(k_cache, v_cache, dev)
-    b = _batch(table, q_start, kv_len, row, dev)
+    index, dtype = q.get_device(), k_cache.dtype
+    kv, n_kv, D = _cache(k_cache, v_cache, index)
+    b, n_seqs = _batch(table, q_start, kv_len, row, index)
     if q.dim() != 3:
         raise ValueError("q: [T][n_heads][head_dim] required")
-    T, H, D = q.shape[0], q.shape[1], kv.head_dim
+    T, H, _ = q.shape
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty_like(q)
     if lse is None and return_lse:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    hq = _heads("q", q, T, H, D, k_cache.dtype, dev)
-    ho = _heads("out", out, T, H, D, k_cache.dtype, dev)
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    hq = _heads("q", q, T, H, D, dtype, index)
+    ho = _heads("out", out, T, H, D, dtype, index)
     lp = None
     if lse is not None:
-        _need("lse", lse, torch.float32, dev, 2)
-        if lse.shape != (T, H) or not lse.is_contiguous():
-            raise ValueError("lse: contiguous float32 [T][n_heads] required")
+        if lse.dtype is not torch.float32 or lse.get_device() != index or lse.shape != (T, H) or not lse.is_contiguous():
+            raise ValueError(f"lse: contiguous float32 [{T}][{H}] on cuda:{index} required")
         lp = lse.data_ptr()
-    n = B.moe_paged_attn_workspace(kv, T, b.n_seqs, max_q, max_kv, H, window)
     if workspace is None:
+        n = B.moe_paged_attn_workspace(kv, T, n_seqs, max_q, max_kv, H, window)
         if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    else:
-        _need("workspace", workspace, torch.uint8, dev, 1)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace: contiguous uint8 tensor required")
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace: contiguous uint8 tensor on cuda:{index} required")
     wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     if T:
-        with torch.cuda.device(dev):
+        with on(index):
             B.moe_paged_attn(kv, b, T, max_q, max_kv, hq, H, ho, lp, D ** -0.5 if scale is None else scale, window,
-                             B.MOE_ATTN_FULL if full else 0, wp, wn, torch.cuda.current_stream(dev).cuda_stream)
+                             B.MOE_ATTN_FULL if full else 0, wp, wn, stream(index))
     return out if lse is None else (out, lse)
 
 

@@ -152,7 +152,7 @@ def lib() -> ctypes.CDLL:
             L.moe_gdn_scan.argtypes = [ctypes.c_int32] * 5 + [P] * 7 + [P]
             L.moe_gdn_step.restype = ctypes.c_int
             L.moe_gdn_step.argtypes = [ctypes.c_int32] * 5 + [P] * 6 + [ctypes.c_int32, P, P, P]
-            KV, BA, HD = ctypes.POINTER(moe_paged_kv), ctypes.POINTER(moe_batch), ctypes.POINTER(moe_heads)
+            KV = BA = HD = P  # structures by reference, or their bytes (see _ref)
             L.moe_rope_freqs.restype = ctypes.c_int
             L.moe_rope_freqs.argtypes = [ctypes.c_int32, ctypes.c_double, ctypes.c_int, ctypes.c_double, I64, P, P]
             L.moe_rope_append.restype = ctypes.c_int
@@ -164,7 +164,8 @@ def lib() -> ctypes.CDLL:
             L.moe_paged_attn.restype = ctypes.c_int
             L.moe_paged_attn.argtypes = [KV, BA, I64, I64, I64, HD, ctypes.c_int32, HD, P, ctypes.c_float,
                                          ctypes.c_int32, ctypes.c_uint32, P, SZ, P]
-            PG, PM, I32 = ctypes.POINTER(moe_pages), ctypes.POINTER(moe_page_memory), ctypes.c_int32
+            PG = PM = P
+            I32 = ctypes.c_int32
             L.moe_pages_workspace.restype = ctypes.c_int
             L.moe_pages_workspace.argtypes = [PG, I32, ctypes.POINTER(SZ)]
             L.moe_pages_grow.restype = ctypes.c_int
@@ -190,6 +191,11 @@ def lib() -> ctypes.CDLL:
 def _check(fn: str, st: int):
     if st != MOE_OK:
         raise MoeError(fn, st)
+
+
+def _ref(x):
+    """A structure argument: a ctypes structure, or the bytes of one."""
+    return x if type(x) is bytes else ctypes.byref(x)
 
 
 def moe_status_string(status: int) -> str:
@@ -280,55 +286,64 @@ def moe_rope_freqs(rot_dim: int, base: float, scaling: int = MOE_ROPE_NONE, fact
 def moe_rope_append(kv: moe_paged_kv, batch: moe_batch, T: int, q: moe_heads, q_out: moe_heads, n_heads: int,
                     k: moe_heads, v: moe_heads, pos_ptr: int | None, inv_freq_ptr: int | None, rot_dim: int,
                     mscale: float, flags: int, stream: int) -> None:
-    _check("moe_rope_append", lib().moe_rope_append(kv, batch, T, q, q_out, n_heads, k, v, pos_ptr, inv_freq_ptr,
-                                                    rot_dim, mscale, flags, stream))
+    st = (_lib or lib()).moe_rope_append(_ref(kv), _ref(batch), T, _ref(q), _ref(q_out), n_heads, _ref(k), _ref(v),
+                                         pos_ptr, inv_freq_ptr, rot_dim, mscale, flags, stream)
+    if st:
+        raise MoeError("moe_rope_append", st)
 
 
 def moe_paged_attn_workspace(kv: moe_paged_kv, T: int, n_seqs: int, max_q: int, max_kv: int, n_heads: int,
                              window: int = 0) -> int:
     n = ctypes.c_size_t()
-    _check("moe_paged_attn_workspace", lib().moe_paged_attn_workspace(kv, T, n_seqs, max_q, max_kv, n_heads,
-                                                                              window, n))
+    st = (_lib or lib()).moe_paged_attn_workspace(_ref(kv), T, n_seqs, max_q, max_kv, n_heads, window, ctypes.byref(n))
+    if st:
+        raise MoeError("moe_paged_attn_workspace", st)
     return n.value
 
 
 def moe_paged_attn(kv: moe_paged_kv, batch: moe_batch, T: int, max_q: int, max_kv: int, q: moe_heads, n_heads: int,
                    out: moe_heads, lse_ptr: int | None, scale: float, window: int, flags: int, ws_ptr: int | None,
                    ws_bytes: int, stream: int) -> None:
-    _check("moe_paged_attn", lib().moe_paged_attn(kv, batch, T, max_q, max_kv, q, n_heads, out, lse_ptr, scale, window,
-                                                  flags, ws_ptr, ws_bytes, stream))
+    st = (_lib or lib()).moe_paged_attn(_ref(kv), _ref(batch), T, max_q, max_kv, _ref(q), n_heads, _ref(out), lse_ptr,
+                                        scale, window, flags, ws_ptr, ws_bytes, stream)
+    if st:
+        raise MoeError("moe_paged_attn", st)
 
 
 def moe_pages_workspace(pages: moe_pages, n: int) -> int:
     size = ctypes.c_size_t()
-    _check("moe_pages_workspace", lib().moe_pages_workspace(pages, n, size))
+    _check("moe_pages_workspace", lib().moe_pages_workspace(_ref(pages), n, size))
     return size.value
 
 
 def moe_pages_grow(src: moe_pages, dst: moe_pages, n: int, seqs_ptr: int | None, tokens_ptr: int | None,
                    error_ptr: int, ws_ptr: int, ws_bytes: int, stream: int) -> None:
-    _check("moe_pages_grow", lib().moe_pages_grow(src, dst, n, seqs_ptr, tokens_ptr, error_ptr, ws_ptr, ws_bytes, stream))
+    st = (_lib or lib()).moe_pages_grow(_ref(src), _ref(dst), n, seqs_ptr, tokens_ptr, error_ptr, ws_ptr, ws_bytes, stream)
+    if st:
+        raise MoeError("moe_pages_grow", st)
 
 
 def moe_pages_fork(src: moe_pages, dst: moe_pages, mem: moe_page_memory, n: int, src_ptr: int | None,
                    dst_ptr: int | None, error_ptr: int, ws_ptr: int, ws_bytes: int, stream: int) -> None:
-    _check("moe_pages_fork", lib().moe_pages_fork(src, dst, mem, n, src_ptr, dst_ptr, error_ptr, ws_ptr, ws_bytes,
-                                                  stream))
+    st = (_lib or lib()).moe_pages_fork(_ref(src), _ref(dst), _ref(mem), n, src_ptr, dst_ptr, error_ptr, ws_ptr, ws_bytes,
+                                        stream)
+    if st:
+        raise MoeError("moe_pages_fork", st)
 
 
 def moe_pages_free(src: moe_pages, dst: moe_pages, n: int, seqs_ptr: int | None, error_ptr: int, ws_ptr: int,
                    ws_bytes: int, stream: int) -> None:
-    _check("moe_pages_free", lib().moe_pages_free(src, dst, n, seqs_ptr, error_ptr, ws_ptr, ws_bytes, stream))
+    _check("moe_pages_free", lib().moe_pages_free(_ref(src), _ref(dst), n, seqs_ptr, error_ptr, ws_ptr, ws_bytes, stream))
 
 
 def moe_pages_compact(src: moe_pages, dst: moe_pages, mem: moe_page_memory, error_ptr: int, ws_ptr: int,
                       ws_bytes: int, stream: int) -> None:
-    _check("moe_pages_compact", lib().moe_pages_compact(src, dst, mem, error_ptr, ws_ptr, ws_bytes, stream))
+    _check("moe_pages_compact", lib().moe_pages_compact(_ref(src), _ref(dst), _ref(mem), error_ptr, ws_ptr, ws_bytes, stream))
 
 
 def moe_pages_copy(mem: moe_page_memory, n_pages: int, n: int, src_ptr: int | None, dst_ptr: int | None,
                    stream: int) -> None:
-    _check("moe_pages_copy", lib().moe_pages_copy(mem, n_pages, n, src_ptr, dst_ptr, stream))
+    _check("moe_pages_copy", lib().moe_pages_copy(_ref(mem), n_pages, n, src_ptr, dst_ptr, stream))
 
 
 def moe_pages_check(error_ptr: int, stream: int) -> int:

@@ -6,6 +6,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
+from ._device import on, stream
 
 D = 128
 
@@ -48,20 +49,21 @@ def gdn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Ten
     if k.dim() != 3 or v.dim() != 3 or state.dim() != 4:
         raise ValueError("q, k, v must be [R][heads][128] and state [n_slots][n_vheads][128][128]")
     R, hk, dk = k.shape
-    hv, dv = v.shape[1], v.shape[2]
+    _, hv, dv = v.shape
+    index = v.get_device()
     if out is None:
         out = torch.empty_like(v)
-    dev = v.device
-    for name, t, dt in (("q", q, torch.bfloat16), ("k", k, torch.bfloat16), ("v", v, torch.bfloat16),
-                        ("alpha", alpha, torch.float32), ("beta", beta, torch.float32),
-                        ("state", state, torch.float32), ("slot", slot, torch.int32), ("out", out, torch.bfloat16)):
-        if t.dtype != dt or not t.is_cuda or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous {dt} tensor on {dev} required")
-    if q.shape != k.shape or v.shape[0] != R or alpha.shape != (R, hv) or beta.shape != (R, hv) or slot.shape != (R,):
+    bf16, f32 = torch.bfloat16, torch.float32
+    for name, t, dt in (("q", q, bf16), ("k", k, bf16), ("v", v, bf16), ("alpha", alpha, f32), ("beta", beta, f32),
+                        ("state", state, f32), ("slot", slot, torch.int32), ("out", out, bf16)):
+        if t.dtype is not dt or index < 0 or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous {dt} tensor on v's GPU required")
+    gates = (R, hv)
+    if q.shape != k.shape or v.shape[0] != R or alpha.shape != gates or beta.shape != gates or slot.shape != (R,):
         raise ValueError("shape mismatch")
     if state.shape[1:] != (hv, dv, dk) or out.shape != v.shape:
         raise ValueError("state must be [n_slots][n_vheads][d_v][d_k], out as v")
-    with torch.cuda.device(dev):
-        B.moe_gdn_step(R, hk, hv, dk, dv, _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(state),
-                       state.shape[0], _ptr(slot), _ptr(out), torch.cuda.current_stream(dev).cuda_stream)
+    with on(index):
+        B.moe_gdn_step(R, hk, hv, dk, dv, q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), beta.data_ptr(),
+                       state.data_ptr(), state.shape[0], slot.data_ptr(), out.data_ptr(), stream(index))
     return out

@@ -7,31 +7,35 @@ Calls are enqueued on torch's current stream of the pool's device and never wait
 
 from __future__ import annotations
 
+import struct
+
 import torch
 
 from . import binding as B
+from ._device import int32, on, stream
+
+_MEMORY = struct.Struct("Pqqqixxxx").pack  # moe_page_memory as bytes
 
 
-def _ints(name, t, device, n=None):
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous int32 vector on {device} required")
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"{name}: {n} entries required")
-    return t.data_ptr()
+def _ints(name, t, index, n=None):
+    p = int32(name, t, index)
+    if t.dim() != 1 or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name}: a vector{'' if n is None else f' of {n} entries'} required")
+    return p
 
 
-def _memory(cache, n_pages, device):
+def _memory(cache, n_pages, index):
     """cache: [n_planes][n_pages][...], each page one contiguous block."""
-    if not cache.is_cuda or cache.device != device or cache.dim() < 3 or cache.shape[1] != n_pages:
-        raise ValueError(f"cache: [n_planes][{n_pages}][...] on {device} required")
-    if cache.shape[0] < 1 or not cache[0, 0].is_contiguous():
-        raise ValueError("cache: each page must be contiguous")
-    size = cache.element_size()
-    page = size
-    for n in cache.shape[2:]:
+    shape, s, size = cache.shape, cache.stride(), cache.element_size()
+    if cache.get_device() != index or index < 0 or len(shape) < 3 or shape[1] != n_pages or shape[0] < 1:
+        raise ValueError(f"cache: [n_planes][{n_pages}][...] on the pool's GPU required")
+    page = 1
+    for n, st in zip(reversed(shape[2:]), reversed(s[2:])):
+        if n != 1 and st != page:
+            raise ValueError("cache: each page must be contiguous")
         page *= n
-    st = [s * size if n > 1 else 0 for s, n in zip(cache.stride()[:2], cache.shape[:2])]
-    return B.moe_page_memory(cache.data_ptr(), st[0], st[1], page, cache.shape[0])
+    return _MEMORY(cache.data_ptr(), s[0] * size if shape[0] > 1 else 0, s[1] * size if n_pages > 1 else 0, page * size,
+                   shape[0])
 
 
 class PagePool:
@@ -60,6 +64,8 @@ class PagePool:
         self.error = zeros(1)
         self.ws = torch.empty(size, dtype=torch.uint8, device=self.device)
         # the arrays are the pool's for its life: fill them, do not replace them
+        self._index, self._error = self.device.index, self.error.data_ptr()
+        self._ws, self._ws_bytes = self.ws.data_ptr(), size
         self._c = B.moe_pages(self.table.data_ptr(), self.lens.data_ptr(), self.refs.data_ptr(), max_seqs, max_pages,
                               n_pages, page_size)
 
@@ -75,14 +81,13 @@ class PagePool:
         return out
 
     def _tail(self, out):
-        return (out.error.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
-                torch.cuda.current_stream(self.device).cuda_stream)
+        return out._error, self._ws, self._ws_bytes, stream(self._index)
 
     def grow(self, seqs: torch.Tensor, tokens: torch.Tensor, out: "PagePool | None" = None) -> "PagePool":
         """Sequences seqs (int32, distinct) grow by tokens (int32) each."""
         out, n = self._out(out), seqs.shape[0]
-        s, t = _ints("seqs", seqs, self.device), _ints("tokens", tokens, self.device, n)
-        with torch.cuda.device(self.device):
+        s, t = _ints("seqs", seqs, self._index), _ints("tokens", tokens, self._index, n)
+        with on(self._index):
             B.moe_pages_grow(self._c, out._c, n, s, t, *self._tail(out))
         return out
 
@@ -91,33 +96,33 @@ class PagePool:
         """Empty sequences dst (int32, distinct) become copies of src (int32): full pages are
         shared, a last page that is not full is copied.  cache: [n_planes][n_pages][...]."""
         out, n = self._out(out), src.shape[0]
-        s, d = _ints("src", src, self.device), _ints("dst", dst, self.device, n)
-        m = _memory(cache, self.n_pages, self.device)
-        with torch.cuda.device(self.device):
+        s, d = _ints("src", src, self._index), _ints("dst", dst, self._index, n)
+        m = _memory(cache, self.n_pages, self._index)
+        with on(self._index):
             B.moe_pages_fork(self._c, out._c, m, n, s, d, *self._tail(out))
         return out
 
     def free(self, seqs: torch.Tensor, out: "PagePool | None" = None) -> "PagePool":
         """Sequences seqs (int32, distinct) end."""
         out, n = self._out(out), seqs.shape[0]
-        s = _ints("seqs", seqs, self.device)
-        with torch.cuda.device(self.device):
+        s = _ints("seqs", seqs, self._index)
+        with on(self._index):
             B.moe_pages_free(self._c, out._c, n, s, *self._tail(out))
         return out
 
     def compact(self, cache: torch.Tensor, out: "PagePool | None" = None) -> "PagePool":
         """The pages in use move to the lowest numbers.  cache: [n_planes][n_pages][...]."""
         out = self._out(out)
-        m = _memory(cache, self.n_pages, self.device)
-        with torch.cuda.device(self.device):
+        m = _memory(cache, self.n_pages, self._index)
+        with on(self._index):
             B.moe_pages_compact(self._c, out._c, m, *self._tail(out))
         return out
 
     def check(self) -> int:
         """moe_pages_check: 0 (MOE_OK), or the first error of the calls whose result this pool took
         (MOE_ERR_SHAPE, MOE_ERR_ALLOC) since ``clear_error``; waits for the stream."""
-        with torch.cuda.device(self.device):
-            return B.moe_pages_check(self.error.data_ptr(), torch.cuda.current_stream(self.device).cuda_stream)
+        with on(self._index):
+            return B.moe_pages_check(self._error, stream(self._index))
 
     def clear_error(self) -> None:
         self.error.zero_()
@@ -126,8 +131,10 @@ class PagePool:
 def copy_pages(cache: torch.Tensor, src: torch.Tensor, dst: torch.Tensor) -> None:
     """Page src[i] is copied to page dst[i] in every plane of cache [n_planes][n_pages][...] (see
     ``moe_pages_copy``)."""
-    dev, n = cache.device, src.shape[0]
-    s, d = _ints("src", src, dev), _ints("dst", dst, dev, n)
-    m = _memory(cache, cache.shape[1], dev)
-    with torch.cuda.device(dev):
-        B.moe_pages_copy(m, cache.shape[1], n, s, d, torch.cuda.current_stream(dev).cuda_stream)
+    index, n = cache.get_device(), src.shape[0]
+    if index < 0:
+        raise ValueError("cache: a GPU tensor required")
+    s, d = _ints("src", src, index), _ints("dst", dst, index, n)
+    m = _memory(cache, cache.shape[1], index)
+    with on(index):
+        B.moe_pages_copy(m, cache.shape[1], n, s, d, stream(index))
