@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPlanThreads = 1024;
+constexpr int kNear = 2048;  // requests whose prefix sums are searched in LDS
 constexpr int kCopyVecs = 4;                                  // 16-byte vectors a lane has in flight
 constexpr int64_t kCopyChunk = int64_t(kThreads) * 16 * kCopyVecs;  // bytes per workgroup step
 
@@ -209,6 +210,8 @@ __device__ __forceinline__ int status(const PageArgs &a, int total_free) {
 template <PageOp OP>
 __global__ void __launch_bounds__(kThreads) k_pages_apply(PageArgs a) {
   __shared__ int sums[kThreads / 64];
+  __shared__ int counts[64];
+  __shared__ int near_base[OP == PageOp::Compact ? 1 : kNear];
   const int tid = threadIdx.x;
   const int groups = (a.n_pages + kPageGroup - 1) / kPageGroup;
   const int w = blockIdx.x;
@@ -219,6 +222,7 @@ __global__ void __launch_bounds__(kThreads) k_pages_apply(PageArgs a) {
     if (OP == PageOp::Compact) a.hdr[1] = a.n_pages - total;
     // the group of page `used` writes the number of pages that move, if there are free pages
     if (OP == PageOp::Compact && (st != kOk || total == 0)) a.hdr[2] = 0;
+    if (OP == PageOp::Fork) a.hdr[3] = st;
     if (st != kOk) atomicCAS(a.error, 0, st);
   }
   if (st != kOk) return;
@@ -229,14 +233,35 @@ __global__ void __launch_bounds__(kThreads) k_pages_apply(PageArgs a) {
     const int used = a.n_pages - total;  // compact: pages below this number stay
     const int need = OP == PageOp::Compact ? 0 : a.hdr[1];
     if (OP != PageOp::Compact && rank >= need) return;
-    const int p0 = w * kPageGroup, p1 = min(a.n_pages, p0 + kPageGroup);
-    for (int q = p0; q < p1; q += kThreads) {
-      const int p = q + tid;
-      const bool is_free = p < p1 && a.in.refs[p] <= 0;
-      int n;
-      const int r = rank + block_excl<kThreads>(is_free, sums, n);
-      rank += n;
-      if (p >= p1) continue;
+    // the group's pages, kThreads at a time: which are free, and the ranks by counts of waves
+    constexpr int kSteps = kPageGroup / kThreads, kW = kThreads / 64;
+    static_assert(kSteps * kW == 64, "a wave scans the counts");
+    const int p0 = w * kPageGroup, lane = tid & 63;
+    uint32_t free_bits = 0, in_bits = 0;
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      const int p = p0 + q * kThreads + tid;
+      const int refs = a.in.refs[min(p, a.n_pages - 1)];
+      if (p < a.n_pages) in_bits |= 1u << q;
+      if (p < a.n_pages && refs <= 0) free_bits |= 1u << q;
+    }
+    // prefix sums of the requests, for the searches below
+    const bool near = a.n < kNear;
+    if (OP != PageOp::Compact && near)
+      for (int i = tid; i < a.n; i += kThreads) near_base[i] = a.base[i];
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      const int n = __popcll(__ballot(free_bits >> q & 1));
+      if (lane == 0) counts[q * kW + (tid >> 6)] = n;
+    }
+    __syncthreads();
+    const int mine = counts[lane], before = wave_incl_scan(mine) - mine;  // of (step, wave) = lane
+    for (int q = 0; q < kSteps; ++q) {
+      const bool is_free = free_bits >> q & 1;
+      const uint64_t ahead = __ballot(is_free) & ((uint64_t(1) << lane) - 1);
+      const int r = rank + __shfl(before, q * kW + (tid >> 6), 64) + (int)__popcll(ahead);
+      if (!(in_bits >> q & 1)) continue;
+      const int p = p0 + q * kThreads + tid;
       if (OP == PageOp::Compact) {
         // free pages below `used` take, rank by rank, the used ones at and behind it
         if (p == used) a.hdr[2] = r;
@@ -248,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) k_pages_apply(PageArgs a) {
         int lo = 0, len = a.n;
         while (len > 1) {
           const int half = len / 2;
-          if (a.base[lo + half] <= r) {
+          if ((near ? near_base[lo + half] : a.base[lo + half]) <= r) {
             lo += half;
             len -= half;
           } else {
@@ -309,11 +334,7 @@ __device__ __forceinline__ void copy_pages(const PageMem &m, int64_t pairs, F pa
 
 // Fork: last pages that are not full.
 __global__ void __launch_bounds__(kThreads) k_pages_tails(PageArgs a) {
-  __shared__ int sums[kThreads / 64];
-  int total;
-  const int groups = (a.n_pages + kPageGroup - 1) / kPageGroup;
-  free_before(a, 0, groups, sums, total);
-  if (status<PageOp::Fork>(a, total) != kOk) return;
+  if (a.hdr[3] != kOk) return;
   copy_pages(a.mem, a.n, [&](int64_t i, int &src, int &dst) {
     if (a.base[i + 1] == a.base[i]) return false;
     const int s = a.a[i];

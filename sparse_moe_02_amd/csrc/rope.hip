@@ -20,6 +20,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMany = 3;    // chunks a thread of a large call
+constexpr int kFew = 1024;  // workgroups of one chunk a thread that leave room on the chip
 
 template <bool F16>
 __device__ __forceinline__ float to_f32(uint16_t v) {
@@ -35,63 +37,58 @@ union Chunk {
   uint16_t e[8];
 };
 
-template <bool F16>
+// How the elements of a pair lie: half a rotation apart in whole chunks, side by side, or half
+// a rotation apart anyhow.
+enum class Pairs { Chunks, Adjacent, Any };
+
+// kPer chunks a thread.
+template <bool F16, int kPer, Pairs kPairs>
 __global__ void __launch_bounds__(kThreads) k_rope_append(RopeArgs a) {
   __shared__ float cs[128], sn[128];
   const int t = blockIdx.x;
   const int tid = threadIdx.x;
   const Batch &b = a.b;
+  const int shift = a.kv.dim == 256 ? 5 : a.kv.dim == 128 ? 4 : 3;  // log2 of a head's chunks
+  const int R = a.R, half = R / 2;
+  const int n_kv = a.k.p ? a.kv.n_kv : 0;
+  const int heads = a.H + 2 * n_kv;
+
+  // this thread's chunks of the token's heads, read before anything is known of its sequence,
+  // and without branches, which would wait for the loads one by one
+  uint4 x[kPer], y[kPer];
+  int head[kPer], kind[kPer];  // kind: q, k, v
+  const int i0 = tid % (1 << shift) * 8;
+  const bool in_rot = i0 < R;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int h0 = min(((int)(blockIdx.y * kPer + j) * kThreads + tid) >> shift, heads - 1);
+    kind[j] = h0 < a.H ? 0 : h0 < a.H + n_kv ? 1 : 2;
+    head[j] = h0 - (kind[j] > 0 ? a.H : 0) - (kind[j] > 1 ? n_kv : 0);
+    const Heads h = kind[j] == 0 ? a.q : kind[j] == 1 ? a.k : a.v;
+    const uint16_t *src = h.p + (int64_t)t * h.ts + (int64_t)head[j] * h.hs;
+    x[j] = *(const uint4 *)(src + i0);
+    // element i pairs with i + half (i < half) or i - half
+    if (kPairs == Pairs::Chunks) y[j] = *(const uint4 *)(src + (!in_rot ? i0 : i0 < half ? i0 + half : i0 - half));
+    if (kPairs == Pairs::Any) {
+      Chunk c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = i0 + e;
+        c.e[e] = src[i >= R ? i : i < half ? i + half : i - half];
+      }
+      y[j] = c.w;
+    }
+  }
   if (t >= b.q_start[b.n_seqs]) return;  // padding behind the last sequence
 
   // the token's sequence, position and cache place
   const int seq = wave_find(b.n_seqs, t, [&](int i) { return (int64_t)b.q_start[i]; });
   const int row = batch_row(b, seq);
   const int64_t p = (row < 0 ? 0 : (int64_t)b.kv_len[row]) - b.q_start[seq + 1] + t;
+  const int64_t col = p >> a.kv.page_shift;
+  int page = -1;
+  if (n_kv && row >= 0 && p >= 0 && col < b.cols) page = b.table[(int64_t)row * b.cols + col];
   const double pos = a.pos ? (double)a.pos[t] : (double)p;
-
-  // this thread's chunk of the token's heads
-  const int D = a.kv.dim, cph = D / 8;
-  const int slot = blockIdx.y * kThreads + tid;
-  const int head = slot / cph, i0 = (slot % cph) * 8;
-  const int n_kv = a.k.p ? a.kv.n_kv : 0;
-  const int kind = head < a.H ? 0 : head < a.H + n_kv ? 1 : head < a.H + 2 * n_kv ? 2 : 3;
-
-  const uint16_t *src = nullptr;
-  uint16_t *dst = nullptr;
-  if (kind == 0) {
-    src = a.q.p + (int64_t)t * a.q.ts + (int64_t)head * a.q.hs;
-    dst = a.qo.p + (int64_t)t * a.qo.ts + (int64_t)head * a.qo.hs;
-  } else if (kind < 3) {
-    const int h = head - a.H - (kind == 2 ? n_kv : 0);
-    const Heads &x = kind == 1 ? a.k : a.v;
-    src = x.p + (int64_t)t * x.ts + (int64_t)h * x.hs;
-    const int64_t col = p >> a.kv.page_shift;
-    if (row >= 0 && p >= 0 && col < b.cols) {
-      const int page = b.table[(int64_t)row * b.cols + col];
-      if ((unsigned)page < (unsigned)a.kv.n_pages)
-        dst = (kind == 1 ? a.kv.k : a.kv.v) + (int64_t)page * a.kv.ps +
-              (p & ((1 << a.kv.page_shift) - 1)) * a.kv.ts + (int64_t)h * a.kv.hs;
-    }
-  }
-  const int R = a.R, half = R / 2;
-  const bool rot = kind < 2 && i0 < R;
-  Chunk x, y;
-  x.w = y.w = make_uint4(0, 0, 0, 0);
-  if (dst) {
-    x.w = *(const uint4 *)(src + i0);
-    if (rot && !a.interleaved) {
-      // element i pairs with i + half (i < half) or i - half
-      if (half % 8 == 0) {
-        y.w = *(const uint4 *)(src + (i0 < half ? i0 + half : i0 - half));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int i = i0 + e;
-          if (i < R) y.e[e] = src[i < half ? i + half : i - half];
-        }
-      }
-    }
-  }
   for (int i = tid; i < half; i += kThreads) {
     const double turns = pos * a.freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
     const float r = (float)(turns - __builtin_rint(turns));
@@ -101,27 +98,61 @@ __global__ void __launch_bounds__(kThreads) k_rope_append(RopeArgs a) {
     sn[i] = a.mscale * s;
   }
   __syncthreads();
-  if (!dst) return;
-  if (rot) {
+  const bool stored = (unsigned)page < (unsigned)a.kv.n_pages;
+  const int64_t place = stored ? page * a.kv.ps + (p & ((1 << a.kv.page_shift) - 1)) * a.kv.ts : 0;
+  // a chunk's pairs are the same in every head
+  float c8[8], s8[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = i0 + e;
-      if (i >= R) break;
-      if (a.interleaved) {
-        if (e & 1) continue;
-        const float u = to_f32<F16>(x.e[e]), v = to_f32<F16>(x.e[e + 1]);
-        const float c = cs[i / 2], s = sn[i / 2];
-        x.e[e] = from_f32<F16>(u * c - v * s);
-        x.e[e + 1] = from_f32<F16>(u * s + v * c);
+  for (int e = 0; e < 8; ++e) {
+    const int i = i0 + e, pair = kPairs == Pairs::Adjacent ? i / 2 : i < half ? i : i - half;
+    c8[e] = i < R ? cs[pair] : 1.0f;
+    s8[e] = i < R ? (i < half || kPairs == Pairs::Adjacent ? sn[pair] : -sn[pair]) : 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (((int)(blockIdx.y * kPer + j) * kThreads + tid) >> shift >= heads || (kind[j] > 0 && !stored)) continue;
+    Chunk u, v;
+    u.w = x[j];
+    if (kind[j] < 2 && in_rot) {
+      if (kPairs == Pairs::Adjacent) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float p0 = to_f32<F16>(u.e[e]), p1 = to_f32<F16>(u.e[e + 1]);
+          const uint16_t q0 = from_f32<F16>(p0 * c8[e] - p1 * s8[e]), q1 = from_f32<F16>(p0 * s8[e] + p1 * c8[e]);
+          u.e[e] = i0 + e < R ? q0 : u.e[e];
+          u.e[e + 1] = i0 + e < R ? q1 : u.e[e + 1];
+        }
       } else {
-        const float u = to_f32<F16>(x.e[e]), v = to_f32<F16>(y.e[e]);
-        const bool lo = i < half;
-        const float c = cs[lo ? i : i - half], s = sn[lo ? i : i - half];
-        x.e[e] = from_f32<F16>(lo ? u * c - v * s : v * s + u * c);
+        v.w = y[j];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint16_t q = from_f32<F16>(to_f32<F16>(u.e[e]) * c8[e] - to_f32<F16>(v.e[e]) * s8[e]);
+          u.e[e] = i0 + e < R ? q : u.e[e];
+        }
       }
     }
+    uint16_t *dst = kind[j] == 0 ? a.qo.p + (int64_t)t * a.qo.ts + (int64_t)head[j] * a.qo.hs
+                                 : (kind[j] == 1 ? a.kv.k : a.kv.v) + place + (int64_t)head[j] * a.kv.hs;
+    *(uint4 *)(dst + i0) = u.w;
   }
-  *(uint4 *)(dst + i0) = x.w;
+}
+
+template <bool F16, Pairs kPairs>
+void launch(const RopeArgs &a, int per, int parts, hipStream_t s) {
+  const dim3 grid(a.T, parts);
+  if (per == 1)
+    hipLaunchKernelGGL((k_rope_append<F16, 1, kPairs>), grid, dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_rope_append<F16, kMany, kPairs>), grid, dim3(kThreads), 0, s, a);
+}
+template <bool F16>
+void launch(const RopeArgs &a, int per, int parts, hipStream_t s) {
+  if (a.interleaved)
+    launch<F16, Pairs::Adjacent>(a, per, parts, s);
+  else if (a.R % 16 == 0)
+    launch<F16, Pairs::Chunks>(a, per, parts, s);
+  else
+    launch<F16, Pairs::Any>(a, per, parts, s);
 }
 
 }  // namespace
@@ -129,11 +160,12 @@ __global__ void __launch_bounds__(kThreads) k_rope_append(RopeArgs a) {
 hipError_t launch_rope_append(const RopeArgs &a, hipStream_t s) {
   const int heads = a.H + (a.k.p ? 2 * a.kv.n_kv : 0);
   if (a.T <= 0 || heads == 0) return hipSuccess;
-  const dim3 grid(a.T, (heads * (a.kv.dim / 8) + kThreads - 1) / kThreads);
+  const int chunks = heads * (a.kv.dim / 8), blocks = (chunks + kThreads - 1) / kThreads;
+  const int per = (int64_t)a.T * blocks <= kFew ? 1 : kMany;
   if (a.kv.fp16)
-    hipLaunchKernelGGL(k_rope_append<true>, grid, dim3(kThreads), 0, s, a);
+    launch<true>(a, per, (blocks + per - 1) / per, s);
   else
-    hipLaunchKernelGGL(k_rope_append<false>, grid, dim3(kThreads), 0, s, a);
+    launch<false>(a, per, (blocks + per - 1) / per, s);
   return hipGetLastError();
 }
 
