@@ -33,6 +33,7 @@ typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kMaxSplits = 256;
+constexpr int kTileSlots = 512;  // workgroups of k_attn_tile that splits aim at: two a compute unit
 constexpr int kMaxRuns = 1024;  // workgroups of k_attn_rows at most
 // workgroups of k_attn_rows that fill the chip (registers allow 1, 2 or 3 on a compute unit)
 constexpr int runs_of(int dim) { return dim == 256 ? 256 : dim == 128 ? 512 : 768; }
@@ -49,8 +50,10 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
 // (lo, hi) rounded to nearest even and packed.
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (F16)
-    return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) | (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16;
+  if constexpr (F16) {
+    typedef __attribute__((__vector_size__(2 * sizeof(_Float16)))) _Float16 f16x2;
+    return __builtin_bit_cast(uint32_t, f16x2{(_Float16)lo, (_Float16)hi});
+  }
   else
     return pack_bf16x2(lo, hi);
 }
@@ -624,6 +627,8 @@ __device__ __forceinline__ void lds_barrier() {
 // eight waves.  Narrower heads have room for three.
 constexpr int stages(int dim) { return dim == 256 ? 2 : 3; }
 
+constexpr float kLag = 8.0f;
+
 template <int D, bool F16, int NW>
 __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   constexpr int kBuf = kAttnKeys * D * 2;      // one K or V block, bytes
@@ -669,6 +674,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   // is the largest product
   const float scale = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);  // 0: of queries of zeros
   const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+  const float lag = kLag / scale;
   // (lanes without a row read the tile's first one, and take zeros)
   const uint16_t *qp = a.q.p + (int64_t)(live ? tok : t.t0 + t.r0 / a.G) * a.q.ts +
                        (int64_t)(live ? head : kvh * a.G + t.r0 % a.G) * a.q.hs;
@@ -688,7 +694,13 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   const int pmask = (1 << a.kv.page_shift) - 1;
   // the rows that this wave loads lie in one 16-key half of a block
   const int my_r0 = wave * kInstr * kRowsPer;
-  auto page_of = [&](int blk) { return page_at(a, trow, blk * kAttnKeys + (my_r0 & 16)); };
+  // A block's pages, one a half: read as they are one block before they are needed, so that
+  // nobody waits for the scalar loads
+  auto peek = [&](int key) { return trow[min(key >> a.kv.page_shift, a.b.cols - 1)]; };
+  auto checked = [&](int key, int page) {  // -1: no page
+    return key >> a.kv.page_shift < a.b.cols && (unsigned)page < (unsigned)a.kv.n_pages ? page : -1;
+  };
+  auto page_of = [&](int key) { return checked(key, peek(key)); };
   uint32_t voff[kInstr];
 #pragma unroll
   for (int i = 0; i < kInstr; ++i) {
@@ -712,14 +724,19 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
   float m = -INFINITY, l = 0.0f;  // m: of the unscaled products
 
-  // pages of the block in use, the next, and the one after (for this wave's loads)
-  int pg = page_of(b0), pg1 = page_of(b0 + 1), pg2 = page_of(b0 + 2);
-  if (b0 < b1) load(b0, pg, 0);
-  if (kStages > 2 && b0 + 1 < b1) load(b0 + 1, pg1, 1);
+  // pages of the block in use and the ones in flight, checked; and of the one after them
+  const bool upper = my_r0 & 16;
+  const int k0 = b0 * kAttnKeys;
+  int this0 = page_of(k0), this1 = page_of(k0 + 16), next0 = page_of(k0 + 32), next1 = page_of(k0 + 48);
+  int last0 = page_of(k0 + 64), last1 = page_of(k0 + 80);
+  if (b0 < b1) load(b0, upper ? this1 : this0, 0);
+  if (kStages > 2 && b0 + 1 < b1) load(b0 + 1, upper ? next1 : next0, 1);
+  int ahead0 = peek(k0 + 96), ahead1 = peek(k0 + 112);
   int stage = 0;
   for (int blk = b0; blk < b1; ++blk) {
     const int key0 = blk * kAttnKeys;
     const uint32_t kbuf = lds0 + stage * 2 * kBuf, vbuf = kbuf + kBuf;
+    const int pg = upper ? this1 : this0;
     if (kStages > 2 && blk + 1 < b1) wait_vm<2 * kInstr>(); else wait_vm<0>();
     // where some key is hidden from some row, its weight there is 0 and its value must be
     // finite: absent keys' values (behind the end, in a bad page) become zeros, and so do
@@ -736,11 +753,15 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
     }
     wait_lds();
     lds_barrier();
-    const int pg3 = page_of(blk + 3);
-    if (blk + kStages - 1 < b1) load(blk + kStages - 1, kStages > 2 ? pg2 : pg1, stage == 0 ? kStages - 1 : stage - 1);
-    pg = pg1;
-    pg1 = pg2;
-    pg2 = pg3;
+    const int have0 = this0 < 0 ? 0 : max(0, min(16, t.len - key0));
+    const int have1 = this1 < 0 ? 0 : max(0, min(16, t.len - key0 - 16));
+    if (blk + kStages - 1 < b1)
+      load(blk + kStages - 1, kStages > 2 ? (upper ? last1 : last0) : (upper ? next1 : next0),
+           stage == 0 ? kStages - 1 : stage - 1);
+    this0 = next0, this1 = next1;
+    next0 = last0, next1 = last1;
+    last0 = checked(key0 + 96, ahead0), last1 = checked(key0 + 112, ahead1);
+    ahead0 = peek(key0 + 128), ahead1 = peek(key0 + 144);
     stage = stage + 1 == kStages ? 0 : stage + 1;
     if (key0 >= any_hi || key0 + kAttnKeys <= any_lo) continue;
 
@@ -750,14 +771,39 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
     f32x16 s;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+    // K from LDS kAhead matrix instructions before its use: left to itself the compiler reads
+    // each operand right before the instruction and waits out the latency every time
+    constexpr int kSteps = D / 16;
+    constexpr int kAhead = D == 256 ? 3 : 4;
+    u32x4 kf[kAhead];
+    auto read_k = [&](int c) {
+      return *(const __attribute__((address_space(3))) u32x4 *)(uintptr_t)(ka ^ (c * 32));
+    };
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      const u32x4 kf = *(const __attribute__((address_space(3))) u32x4 *)(uintptr_t)(ka ^ (c * 32));
-      s = mfma32<F16>(kf, qf[c], s);
+    for (int c = 0; c < kAhead; ++c) kf[c] = read_k(c);
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c) {
+      __builtin_amdgcn_sched_barrier(0);
+      s = mfma32<F16>(kf[c % kAhead], qf[c], s);
+      if (c + kAhead < kSteps) kf[c % kAhead] = read_k(c + kAhead);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    // the first of V, for after the softmax; rows kr, kr + 8, kr + 16, kr + 24 (swz(kr + 8) =
+    // swz(kr) ^ swz(8), and 16 changes nothing)
+    const int l16 = lane & 15, kr = 4 * half + (l16 >> 2);
+    const uint32_t va = vbuf + kr * D * 2 + (((2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ swz<D>(kr)) * 16 + (l16 & 1) * 8);
+    auto read_v = [&](int i) {  // operand i: 32 columns from 32 (i / 2), keys 16 (i % 2) ..
+      const uint32_t a0 = va ^ (i / 2 * 64), a1 = a0 ^ (swz<D>(8) * 16);
+      const int r = 16 * (i % 2);
+      const uint64_t v0 = tr_read(a0 + r * D * 2), v1 = tr_read(a1 + (r + 8) * D * 2);
+      return u32x4{(uint32_t)v0, (uint32_t)(v0 >> 32), (uint32_t)v1, (uint32_t)(v1 >> 32)};
+    };
+    constexpr int kAheadV = D == 256 ? 2 : 4;
+    u32x4 vf[kAheadV];
+#pragma unroll
+    for (int i = 0; i < kAheadV; ++i) vf[i] = read_v(i);
+    __builtin_amdgcn_sched_barrier(0);
     bool whole = key0 + kAttnKeys <= all_hi && key0 >= all_lo;
-    const int have0 = page_at(a, trow, key0) < 0 ? 0 : max(0, min(16, t.len - key0));
-    const int have1 = page_at(a, trow, key0 + 16) < 0 ? 0 : max(0, min(16, t.len - key0 - 16));
     whole = whole && have0 + have1 == kAttnKeys;
     if (!whole) {
 #pragma unroll
@@ -769,41 +815,37 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
     float mx = s[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
-    const float mn = fmaxf(m, halves_max(mx));
-    const float mu = mn == -INFINITY ? 0.0f : mn;
-    const float f = __builtin_amdgcn_exp2f((m - mu) * scale);
-    m = mn;
-    const float off = -mu * scale;
+    // the reference m follows the maximum only where it lags by more than kLag (as a base-2
+    // exponent), so weights stay below 2^kLag and the outputs are hardly ever rescaled
+    mx = halves_max(mx);
+    if (__ballot(mx > m + lag)) {
+      const float mn = fmaxf(m, mx);
+      const float f = __builtin_amdgcn_exp2f((m - (mn == -INFINITY ? 0.0f : mn)) * scale);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) acc[d] *= f;
+    }
+    const float off = m == -INFINITY ? 0.0f : -m * scale;
     float ps = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale, off));
       ps += s[i];
     }
-    l = l * f + ps;
-    if (__ballot(f != 1.0f)) {
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) acc[d] *= f;
-    }
+    l += ps;
     u32x4 pf4[2];
 #pragma unroll
     for (int i = 0; i < 8; ++i) pf4[i / 4][i % 4] = pack2<F16>(s[2 * i], s[2 * i + 1]);
 
-    {
-      // rows kr, kr + 8, kr + 16, kr + 24; swz(kr + 8) = swz(kr) ^ swz(8), and 16 changes nothing
-      const int l16 = lane & 15, kr = 4 * half + (l16 >> 2);
-      const uint32_t va = vbuf + kr * D * 2 + (((2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ swz<D>(kr)) * 16 + (l16 & 1) * 8);
+    constexpr int kParts = D / 16;
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) {
-        const uint32_t a0 = va ^ (d * 64), a1 = va ^ (d * 64) ^ (swz<D>(8) * 16);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint64_t v0 = tr_read(a0 + 16 * h * D * 2), v1 = tr_read(a1 + (16 * h + 8) * D * 2);
-          const u32x4 vf = {(uint32_t)v0, (uint32_t)(v0 >> 32), (uint32_t)v1, (uint32_t)(v1 >> 32)};
-          acc[d] = mfma32<F16>(vf, pf4[h], acc[d]);
-        }
-      }
+    for (int i = 0; i < kParts; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      acc[i / 2] = mfma32<F16>(vf[i % kAheadV], pf4[i % 2], acc[i / 2]);
+      if (i + kAheadV < kParts) vf[i % kAheadV] = read_v(i + kAheadV);
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   l = halves_sum(l);
@@ -811,8 +853,11 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   const bool fix = odd != 0;
   if (!live && !fix) return;
   const int64_t row = (int64_t)tok * a.H + head;
-  if (!live) {
-  } else if (a.splits == 1) {
+  // a tile whose keys are all in the first split needs no join: its other splits are empty, and
+  // the first one's sum of -1 says that the row is done
+  const bool direct = a.splits == 1 || nblk <= a.split_blocks;
+  if (!live || (direct && split > 0)) {
+  } else if (direct) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t *o = a.out.p + (int64_t)tok * a.out.ts + (int64_t)head * a.out.hs + 4 * half;
 #pragma unroll
@@ -824,6 +869,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
         *(uint2 *)(o + 32 * d + 8 * i) = w;
       }
     if (a.lse && half == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m * scale + __log2f(l)) * kLn2;
+    if (a.splits > 1 && half == 0) a.part_ml[2 * row * a.splits + 1] = -1.0f;
   } else {
     const int64_t at = row * a.splits + split;
     if (b0 < b1)
@@ -842,7 +888,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "agent");
   put_back<D, F16>(a, t, kvh, b0, b1, all_lo_t, all_hi_t, t.r0 + wave * 32, t.r0 + wave * 32 + wn, 1,
                    [&](int, int64_t tk, int64_t hd) {
-                     return a.splits == 1 ? nullptr : a.part + ((tk * a.H + hd) * a.splits + split) * D;
+                     return direct ? nullptr : a.part + ((tk * a.H + hd) * a.splits + split) * D;
                    });
 }
 
@@ -859,6 +905,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(AttnArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int64_t tk = r / a.H, hd = r % a.H;
   if (tk >= a.b.q_start[a.b.n_seqs]) return;
+  if (a.part_ml[2 * r * a.splits + 1] < 0.0f) return;  // done already
   float ms[kRegs], ls[kRegs], mw = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kRegs; ++i) {
@@ -907,6 +954,71 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(AttnArgs a) {
   *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + 4 * c) =
       make_uint2(pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv));
   if (a.lse && tid == 0) a.lse[r] = sum == 0.0f ? -INFINITY : (mw + __log2f(sum)) * kLn2;
+}
+
+// The same for up to kFewSplits splits, where there are many rows: kRows rows a wave, their loads
+// in flight together.  D / 4 lanes take a split, so 64 / (D / 4) of them are read at once and
+// summed across lanes.
+constexpr int kFewSplits = 4;
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads) k_attn_join_few(AttnArgs a) {
+  constexpr int kVecs = D / 4, kGroups = 64 / kVecs, kN = kFewSplits / kGroups, kRows = 4;
+  const int lane = threadIdx.x & 63, c = lane % kVecs, g = lane / kVecs;
+  const int64_t r0 = ((int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6)) * kRows;
+  const int64_t end = (int64_t)min(a.T, a.b.q_start[a.b.n_seqs]) * a.H;
+  float m[kRows][kN], l[kRows][kN];
+  bool todo[kRows];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const float *ml = a.part_ml + min(r0 + j, (int64_t)a.T * a.H - 1) * a.splits * 2;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int s = g + i * kGroups;
+      m[j][i] = s < a.splits ? ml[2 * s] : -INFINITY;
+      l[j][i] = s < a.splits ? ml[2 * s + 1] : 0.0f;
+    }
+  }
+  f32x4 x[kRows][kN];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    // (a first sum of -1: the row is done)
+    todo[j] = r0 + j < end && __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(l[j][0]))) >= 0.0f;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      x[j][i] = f32x4{0, 0, 0, 0};
+      if (todo[j] && l[j][i] != 0.0f)  // (empty splits are not written)
+        x[j][i] = *((const f32x4 *)(a.part + ((r0 + j) * a.splits + g + i * kGroups) * D) + c);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    if (!todo[j]) continue;
+    float mw = -INFINITY, sum = 0.0f;
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kN; ++i) mw = fmaxf(mw, m[j][i]);
+#pragma unroll
+    for (int o = kVecs; o < 64; o <<= 1) mw = fmaxf(mw, __shfl_xor(mw, o, 64));
+    const float mu = mw == -INFINITY ? 0.0f : mw;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const float f = __builtin_amdgcn_exp2f(m[j][i] - mu);
+      sum += f * l[j][i];
+      v += f * x[j][i];
+    }
+#pragma unroll
+    for (int o = kVecs; o < 64; o <<= 1) {
+      sum += __shfl_xor(sum, o, 64);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += __shfl_xor(v[e], o, 64);
+    }
+    if (g > 0) continue;
+    const int64_t r = r0 + j, tk = r / a.H, hd = r % a.H;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + 4 * c) =
+        make_uint2(pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv));
+    if (a.lse && lane == 0) a.lse[r] = sum == 0.0f ? -INFINITY : (mw + __log2f(sum)) * kLn2;
+  }
 }
 
 // Join the runs' partial results of segments that several workgroups share: workgroup x takes
@@ -995,8 +1107,10 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     const hipError_t e = allow_lds(k_attn_tile<D, F16, nw>, lds, done);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((k_attn_tile<D, F16, nw>), dim3(a.tiles, a.kv.n_kv, a.splits), dim3(64 * nw), lds, s, a);
-    if (a.splits > 1)
+    if (a.splits > kFewSplits)
       hipLaunchKernelGGL((k_attn_join<D, F16>), dim3(a.T * a.H), dim3(kThreads), 0, s, a);
+    else if (a.splits > 1)
+      hipLaunchKernelGGL((k_attn_join_few<D, F16>), dim3(((int64_t)a.T * a.H + 4 * kWaves - 1) / (4 * kWaves)), dim3(kThreads), 0, s, a);
   }
   return hipGetLastError();
 }
@@ -1024,7 +1138,7 @@ AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int w
   busy = (busy < 1 ? 1 : busy) * n_seqs;
   if (busy > s.tiles) busy = s.tiles;
   busy *= n_kv;
-  const int64_t want = 256 / (busy < 1 ? 1 : busy);
+  const int64_t want = kTileSlots / (busy < 1 ? 1 : busy);
   if (window > 0 && max_kv > window + max_q) max_kv = window + max_q;
   const int64_t blocks = (max_kv + kAttnKeys - 1) / kAttnKeys + 1;
   int64_t per = (blocks + (want < 1 ? 1 : want) - 1) / (want < 1 ? 1 : want);  // blocks of a split
