@@ -1120,7 +1120,14 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
 AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int window, int H, int n_kv, int dim) {
   AttnShape s{};
   const int64_t G = H / n_kv;
-  s.rows = max_q * G > 2 * kAttnRows ? kAttnTile : kAttnRows;
+  // Tiles of few rows over many long sequences: equal runs of keys (k_attn_rows).  Otherwise the
+  // chunk kernel, its keys split: several workgroups on a compute unit hide each other's starts.
+  // Measured on decodes of heads of 256 / 128 / 64, us with runs and with splits: 64 sequences up
+  // to 16K 174 and 203; 64 up to 4K 104 and 142; 32 up to 8K 60 and 97; but one at 4K 16.1 and
+  // 13.7, 16 up to 8K 39 and 32, 64 up to 1200 37 and 25, 200 up to 300 46 and 21.  More than
+  // 16 rows a sequence: 16 sequences of 4 tokens and 8 heads at 8K 43 and 32.
+  const bool runs = max_q * G <= kAttnRows && (int64_t)n_seqs * n_kv >= 48 && max_kv >= 16 * (int64_t)dim;
+  s.rows = runs ? kAttnRows : kAttnTile;
   s.tiles = (int)(T * G / s.rows + n_seqs);
   if (T == 0) return s;
   if (s.rows == kAttnRows) {

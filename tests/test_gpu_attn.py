@@ -315,6 +315,110 @@ def test_graph_replays_follow_the_lengths():
         assert (go == eo).all() and (gl == el).all(), i
 
 
+# ------------------------------------------------- few rows over many long sequences (equal runs)
+# (bounds of one token and 10^6 keys, with 48 or more sequences x key/value heads, choose that
+# launch whatever the lengths are)
+
+def _runs(c, **kw):
+    assert len(c.new) * c.hk >= 48
+    return c.attn(max_q=1, max_kv=10 ** 6, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("H,hk,D", [(16, 8, 256), (24, 12, 64), (48, 16, 128), (16, 16, 256)])
+def test_runs_decode(H, hk, D, dtype):
+    c = Case([1] * 6, [1, 31, 32, 33, 500, 1300], H, hk, D, dtype, page=16, seed=H)
+    a, b = _runs(c), _runs(c)
+    c.check(*a, f"runs {H}/{hk}/{D} {dtype}")
+    assert all((x == y).all() for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("window", [0, 1, 40])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_runs_ragged(D, window):
+    """Several tokens, several tiles of rows a sequence (more than the bound says), sequences
+    without tokens or keys, padding."""
+    c = Case([3, 0, 40, 1, 0, 0, 5, 2], [3, 40, 41, 129, 0, 7, 700, 1], 32, 8, D, page=32, pad=3, seed=D + window)
+    c.check(*_runs(c, window=window), f"runs ragged {D} {window}", window=window)
+
+
+def test_runs_full_and_negative_scale():
+    c = Case([2, 3, 1, 9, 1, 1], [200, 3, 100, 65, 31, 33], 16, 8, 128, page=16, layout="head", seed=31)
+    c.check(*_runs(c, full=True), "runs full", full=True)
+    for scale in (0.0, -0.3):
+        c.check(*_runs(c, scale=scale), f"runs scale {scale}", scale=scale)
+
+
+@pytest.mark.parametrize("n", [63, 64, 65, 300])
+def test_runs_over_many_sequences(n):
+    """More sequences than a wave has lanes, most of them short, some empty."""
+    rng = np.random.default_rng(n)
+    new = [int(x) for x in rng.integers(0, 3, n)]
+    total = [a + int(x) for a, x in zip(new, rng.integers(0, 90, n))]
+    total[n // 2] += 900
+    c = Case(new, total, 4, 2, 64, page=16, layout="pairs", seed=n)
+    row = rng.permutation(n).astype(np.int32)
+    # rows in another order: lengths and new tokens no longer match, so some tokens see nothing
+    out, lse = _runs(c, row=c.dev(row))
+    c.check(out, lse, f"runs over {n}", row=row)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("D", [64, 256])
+def test_runs_unseen_places(bad, D):
+    new, total = [1, 20, 45, 1, 1, 1], [77, 20, 131, 64, 33, 1]
+    c = Case(new, total, 16, 8, D, page=32, seed=6, fill=bad)
+    c.check(*_runs(c), f"runs fill {bad}")
+    ref = Case(new, total, 16, 8, D, page=32, seed=6, fill=0.0)
+    for p in (100, 117):
+        c.kc[c.table[2, p // 32], p % 32] = bad
+        c.vc[c.table[2, p // 32], p % 32] = bad
+    (out, lse), (ro, rl) = _runs(c), _runs(ref)
+    t = 21 + (100 - 86)
+    assert np.array_equal(_np(out)[:t], _np(ro)[:t]) and np.array_equal(_np(lse)[:t], _np(rl)[:t])
+    assert not np.isfinite(_np(out)[t:66]).all()
+    assert np.array_equal(_np(out)[66:], _np(ro)[66:])
+
+
+def test_runs_bad_rows_and_pages():
+    c = Case([1, 5, 2, 1, 1, 1], [100, 70, 64, 90, 600, 30], 16, 8, 128, page=16, seed=11)
+    table, kv = c.table.copy(), c.kv_len.copy()
+    table[0, 2], table[1, 0], table[1, 4], table[4, 7] = c.n_pages, -7, 2 ** 31 - 1, -1
+    kv[3] = 10 ** 6
+    row = np.array([2, 9, -1, 3, 4, 0], np.int32)
+    from sparse_moe_02_amd.attn import paged_attn
+
+    out, lse = paged_attn(c.q, c.kc, c.vc, c.dev(table), c.dev(c.q_start), c.dev(kv), 1, 10 ** 6, row=c.dev(row),
+                          return_lse=True)
+    c.check(out, lse, "runs bad rows", row=row, table=table, kv_len=kv)
+
+
+def test_runs_values_of_infinity_that_are_seen():
+    c = Case([1] * 6, [50, 400, 40, 33, 64, 1], 16, 8, 64, seed=8)
+    c.vc[c.table[1, 4], 3, 0, 5] = float("inf")
+    c.vc[c.table[1, 4], 4, 7, 6] = float("nan")
+    o = _np(_runs(c)[0])
+    assert np.isposinf(o[1, :2, 5]).all() and np.isnan(o[1, 14:, 6]).all()
+    o[1, :2, 5] = o[1, 14:, 6] = 0
+    assert np.isfinite(o).all()
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 32), (256, 64)])
+def test_bad_page_beside_values_that_are_not_finite(D, page):
+    """A block of keys with one half in a bad page and a NaN that is seen in the other half."""
+    for runs in (False, True):
+        c = Case([1, 1, 1, 1, 1, 1], [200] * 6, 16, 8, D, page=16, seed=page)
+        table = c.table.copy()
+        table[0, 3] = -1                                 # keys 48 .. 63
+        c.vc[table[0, 2], 5, 0, 7] = float("nan")        # key 37
+        from sparse_moe_02_amd.attn import paged_attn
+
+        out = _np(paged_attn(c.q, c.kc, c.vc, c.dev(table), c.dev(c.q_start), c.dev(c.kv_len), 1, 10 ** 6 if runs else 1))
+        assert np.isnan(out[0, :2, 7]).all()
+        out[0, :2, 7] = 0
+        assert np.isfinite(out).all(), runs
+
+
 # ------------------------------------------------------------------------ rotary append
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
