@@ -628,11 +628,16 @@ __device__ __forceinline__ void lds_barrier() {
 constexpr int stages(int dim) { return dim == 256 ? 2 : 3; }
 
 constexpr float kLag = 8.0f;
+// What a wave is given the issue slots for while others of its SIMD do the other thing.  Measured
+// with Matrix / Softmax / None: 4096 tokens at 32K, heads of 256, 1927 / 1997 / 2022 us; 4096 at
+// 16K, heads of 128, 1150 / 1133 / 1101; 4096 at 8K, heads of 64, 211 / 199 / 216.
+enum class First { Matrix, Softmax, None };
 
 template <int D, bool F16, int NW>
 __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   constexpr int kBuf = kAttnKeys * D * 2;      // one K or V block, bytes
   constexpr int kStages = stages(D);
+  constexpr First kFirst = D == 256 ? First::Matrix : D == 64 ? First::Softmax : First::None;
   constexpr int kInstr = kBuf / 1024 / NW;     // load instructions a wave issues for one block
   constexpr int kRowsPer = 512 / D;            // LDS rows of one instruction
   static_assert(kInstr >= 1, "every wave loads");
@@ -674,7 +679,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   // is the largest product
   const float scale = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);  // 0: of queries of zeros
   const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-  const float lag = kLag / scale;
+  const float lag = fminf(kLag / scale, 1e30f);  // (finite, so that it is exceeded from -infinity on)
   // (lanes without a row read the tile's first one, and take zeros)
   const uint16_t *qp = a.q.p + (int64_t)(live ? tok : t.t0 + t.r0 / a.G) * a.q.ts +
                        (int64_t)(live ? head : kvh * a.G + t.r0 % a.G) * a.q.hs;
@@ -781,12 +786,15 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
     };
 #pragma unroll
     for (int c = 0; c < kAhead; ++c) kf[c] = read_k(c);
+    if (kFirst == First::Matrix) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int c = 0; c < kSteps; ++c) {
       __builtin_amdgcn_sched_barrier(0);
       s = mfma32<F16>(kf[c % kAhead], qf[c], s);
       if (c + kAhead < kSteps) kf[c % kAhead] = read_k(c + kAhead);
     }
+    if (kFirst == First::Matrix) __builtin_amdgcn_s_setprio(0);
+    if (kFirst == First::Softmax) __builtin_amdgcn_s_setprio(1);
     __builtin_amdgcn_sched_barrier(0);
     // the first of V, for after the softmax; rows kr, kr + 8, kr + 16, kr + 24 (swz(kr + 8) =
     // swz(kr) ^ swz(8), and 16 changes nothing)
@@ -839,12 +847,15 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
     for (int i = 0; i < 8; ++i) pf4[i / 4][i % 4] = pack2<F16>(s[2 * i], s[2 * i + 1]);
 
     constexpr int kParts = D / 16;
+    if (kFirst == First::Matrix) __builtin_amdgcn_s_setprio(1);
+    if (kFirst == First::Softmax) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
       __builtin_amdgcn_sched_barrier(0);
       acc[i / 2] = mfma32<F16>(vf[i % kAheadV], pf4[i % 2], acc[i / 2]);
       if (i + kAheadV < kParts) vf[i % kAheadV] = read_v(i + kAheadV);
     }
+    if (kFirst == First::Matrix) __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -1143,6 +1154,7 @@ AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int w
   // tiles that can hold rows, and splits that fill the chip with them
   int64_t busy = (max_q * G + s.rows - 1) / s.rows;
   busy = (busy < 1 ? 1 : busy) * n_seqs;
+  if (busy < T * G / s.rows) busy = T * G / s.rows;  // (whatever max_q says)
   if (busy > s.tiles) busy = s.tiles;
   busy *= n_kv;
   const int64_t want = kTileSlots / (busy < 1 ? 1 : busy);

@@ -171,7 +171,7 @@ def test_layouts(layout, page):
     c.check(*c.attn(), f"layout {layout} page {page}")
 
 
-@pytest.mark.parametrize("scale", [0.0, 0.5, -0.2, 3.0])
+@pytest.mark.parametrize("scale", [0.0, 0.5, -0.2, 3.0, 1e-38, -1e-44])
 def test_scale(scale):
     c = Case([1, 20], [100, 20], 4, 2, 64, seed=3)
     c.check(*c.attn(scale=scale), f"scale {scale}", scale=scale)
@@ -278,6 +278,54 @@ def test_places_beyond_32_bits():
     q = rope_append(c.q, c.k, c.v, big_k, big_v, c.dev(table), c.dev(c.q_start), c.dev(c.kv_len), f, mscale=m)
     q2 = rope_append(c.q, c.k, c.v, c.kc, c.vc, *c.args(), f, mscale=m)
     assert (q == q2).all() and (big_k[far:] == c.kc).all() and (big_v[far:] == c.vc).all()
+
+
+def test_calls_on_two_streams_at_once():
+    """Two batches attended to at the same time, each many times, against each alone."""
+    import torch
+
+    cs = [Case([1] * 6, [900, 31, 32, 33, 500, 77], 16, 2, 256, seed=41), Case([64, 200], [64, 900], 8, 2, 128, seed=42)]
+    alone = [c.attn() for c in cs]
+    st = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in st:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, s) in enumerate(zip(cs, st)):
+            with torch.cuda.stream(s):
+                got[i].append(c.attn())
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all((o == alone[i][0]).all() and (m == alone[i][1]).all() for o, m in got[i])
+
+
+def test_one_workspace_for_two_graphs():
+    """Two captured calls of different shape share a workspace, replayed in turn on one stream."""
+    import torch
+
+    from sparse_moe_02_amd.attn import paged_attn_workspace
+
+    cs = [Case([1, 1], [2000, 700], 16, 2, 256, seed=43), Case([40, 3], [900, 60], 16, 2, 256, seed=44)]
+    n = max(paged_attn_workspace(c.T, 2, max(c.new), max(c.total), 16, 2, 256) for c in cs)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    eager = [c.attn() for c in cs]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    for c in cs:
+        g = torch.cuda.CUDAGraph()
+        args = c.args()
+        from sparse_moe_02_amd.attn import paged_attn
+
+        with torch.cuda.graph(g, stream=st):
+            outs.append(paged_attn(c.q, c.kc, c.vc, *args, max(c.new), max(c.total), return_lse=True, workspace=ws))
+        graphs.append((g, args))
+    for _ in range(4):
+        for i in (0, 1):
+            graphs[i][0].replay()
+            torch.cuda.synchronize()
+            assert (outs[i][0] == eager[i][0]).all() and (outs[i][1] == eager[i][1]).all()
+        ws.random_()
 
 
 def test_graph_replays_follow_the_lengths():
