@@ -128,8 +128,8 @@ moe_status moe_rope_append(const moe_paged_kv *kv, const moe_batch *batch, int64
  * out and lse may overlap nothing that is read, the workspace, or each other
  * (MOE_ERR_ALIAS).  Scores, softmax statistics and sums are binary32; the weights of the
  * value sum are rounded to dtype (they enter the matrix units in it).  For one shape of
- * launch, results are bitwise repeatable.  T: 0 .. 2^20, T * n_heads / n_kv_heads <= 2^27
- * (MOE_ERR_TOKENS). */
+ * launch, results are bitwise repeatable.  T: 0 .. 2^20, T * n_heads <= 2^29,
+ * n_seqs * n_kv_heads <= 2^22 (MOE_ERR_TOKENS). */
 #define MOE_ATTN_FULL 1u
 moe_status moe_paged_attn_workspace(const moe_paged_kv *kv, int64_t T, int32_t n_seqs, int64_t max_q,
                                     int64_t max_kv, int32_t n_heads, int32_t window, size_t *bytes);

@@ -115,8 +115,10 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torc
             raise ValueError("pos: int32 [T] required")
     if T:
         with on(index):
-            B.moe_rope_append(kv, b, T, hq, ho, H, hk, hv, pp, fp, rot, mscale,
-                              B.MOE_ROPE_INTERLEAVED if interleaved else 0, stream(index))
+            st = (B._lib or B.lib()).moe_rope_append(kv, b, T, hq, ho, H, hk, hv, pp, fp, rot, mscale,
+                                                     B.MOE_ROPE_INTERLEAVED if interleaved else 0, stream(index))
+        if st:
+            raise B.MoeError("moe_rope_append", st)
     return q_out
 
 
@@ -158,8 +160,11 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, ta
     wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     if T:
         with on(index):
-            B.moe_paged_attn(kv, b, T, max_q, max_kv, hq, H, ho, lp, D ** -0.5 if scale is None else scale, window,
-                             B.MOE_ATTN_FULL if full else 0, wp, wn, stream(index))
+            st = (B._lib or B.lib()).moe_paged_attn(kv, b, T, max_q, max_kv, hq, H, ho, lp,
+                                                    D ** -0.5 if scale is None else scale, window,
+                                                    B.MOE_ATTN_FULL if full else 0, wp, wn, stream(index))
+        if st:
+            raise B.MoeError("moe_paged_attn", st)
     return out if lse is None else (out, lse)
 
 

@@ -215,8 +215,26 @@ __global__ void __launch_bounds__(kThreads) k_pages_apply(PageArgs a) {
   const int tid = threadIdx.x;
   const int groups = (a.n_pages + kPageGroup - 1) / kPageGroup;
   const int w = blockIdx.x;
+  // the group's pages, kThreads at a time: which are free (read before anything is known of the
+  // call, like the prefix sums of the requests, for the searches below)
+  constexpr int kSteps = kPageGroup / kThreads, kW = kThreads / 64;
+  static_assert(kSteps * kW == 64, "a wave scans the counts");
+  const int p0 = w * kPageGroup, lane = tid & 63;
+  const bool near = a.n < kNear;
+  uint32_t free_bits = 0, in_bits = 0;
+  if (OP != PageOp::Free && w < groups) {
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      const int p = p0 + q * kThreads + tid;
+      const int refs = a.in.refs[min(p, a.n_pages - 1)];
+      if (p < a.n_pages) in_bits |= 1u << q;
+      if (p < a.n_pages && refs <= 0) free_bits |= 1u << q;
+    }
+    if (OP != PageOp::Compact && near)
+      for (int i = tid; i < a.n; i += kThreads) near_base[i] = a.base[i];
+  }
   int total;
-  int rank = free_before(a, w, groups, sums, total);
+  const int rank = free_before(a, w, groups, sums, total);
   const int st = status<OP>(a, total);
   if (w == 0 && tid == 0) {
     if (OP == PageOp::Compact) a.hdr[1] = a.n_pages - total;
@@ -233,22 +251,6 @@ __global__ void __launch_bounds__(kThreads) k_pages_apply(PageArgs a) {
     const int used = a.n_pages - total;  // compact: pages below this number stay
     const int need = OP == PageOp::Compact ? 0 : a.hdr[1];
     if (OP != PageOp::Compact && rank >= need) return;
-    // the group's pages, kThreads at a time: which are free, and the ranks by counts of waves
-    constexpr int kSteps = kPageGroup / kThreads, kW = kThreads / 64;
-    static_assert(kSteps * kW == 64, "a wave scans the counts");
-    const int p0 = w * kPageGroup, lane = tid & 63;
-    uint32_t free_bits = 0, in_bits = 0;
-#pragma unroll
-    for (int q = 0; q < kSteps; ++q) {
-      const int p = p0 + q * kThreads + tid;
-      const int refs = a.in.refs[min(p, a.n_pages - 1)];
-      if (p < a.n_pages) in_bits |= 1u << q;
-      if (p < a.n_pages && refs <= 0) free_bits |= 1u << q;
-    }
-    // prefix sums of the requests, for the searches below
-    const bool near = a.n < kNear;
-    if (OP != PageOp::Compact && near)
-      for (int i = tid; i < a.n; i += kThreads) near_base[i] = a.base[i];
 #pragma unroll
     for (int q = 0; q < kSteps; ++q) {
       const int n = __popcll(__ballot(free_bits >> q & 1));

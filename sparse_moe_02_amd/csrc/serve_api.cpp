@@ -175,7 +175,8 @@ moe_status check_attn_sizes(int64_t T, int32_t n_seqs, int64_t max_q, int64_t ma
   if (T < 0 || T > kMaxTokens) return MOE_ERR_TOKENS;
   if (n_seqs < 1 || n_seqs > 65535 || max_q < 0 || max_kv < 0) return MOE_ERR_SHAPE;
   if (n_heads < 1 || n_heads > 4096 || n_heads % kv.n_kv_heads) return MOE_ERR_SHAPE;
-  if (T * (n_heads / kv.n_kv_heads) > int64_t(1) << 27) return MOE_ERR_TOKENS;
+  // (launches of at most 2^24 workgroups)
+  if (T * n_heads > int64_t(1) << 29 || (int64_t)n_seqs * kv.n_kv_heads > int64_t(1) << 22) return MOE_ERR_TOKENS;
   return MOE_OK;
 }
 

@@ -118,7 +118,9 @@ def test_bad_attention_arguments(B):
     H = B.moe_heads
     assert _attn(B, T=-1) == TOKENS and _attn(B, T=(1 << 20) + 1) == TOKENS
     assert _attn(B, H=0) == SHAPE and _attn(B, H=7) == SHAPE and _attn(B, H=8192) == SHAPE
-    assert _attn(B, kv=_kv(B, n_kv_heads=1, token_stride=128), T=1 << 20, H=256, wsn=1 << 60) == TOKENS
+    assert _attn(B, kv=_kv(B, n_kv_heads=1, token_stride=128), T=1 << 20, H=1024, wsn=1 << 60) == TOKENS
+    assert _attn(B, kv=_kv(B, n_kv_heads=128, token_stride=128 * 128, page_stride=32 * 128 * 128), H=128,
+                 batch=_batch(B, n_seqs=65535, n_rows=65535), wsn=1 << 60) == TOKENS
     assert _attn(B, max_q=-1) == SHAPE and _attn(B, max_kv=-1) == SHAPE
     assert _attn(B, window=-1) == SHAPE and _attn(B, window=5, flags=1) == SHAPE and _attn(B, flags=2) == SHAPE
     assert _attn(B, scale=math.nan) == SHAPE and _attn(B, scale=math.inf) == SHAPE
