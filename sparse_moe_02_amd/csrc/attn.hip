@@ -94,11 +94,15 @@ __device__ __forceinline__ void wait_vm() {
 }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// 16-byte chunk c of LDS row r lies at chunk c ^ swz(r): 16 rows at one chunk, and 16 rows of
-// a 2-chunk column, then spread over all banks.
+// 16-byte chunk c of LDS row r lies at chunk c ^ swz(r).  K is read 16 rows at a time at one
+// chunk, V four rows in a row at four chunks in a row: swz is different for 16 rows (8 of rows of
+// 128 bytes, of which two lie side by side over the banks), and takes four consecutive rows to
+// four different groups of four chunks, so either read touches every bank once.  (With swz = r,
+// whose four consecutive rows stay in one group, 60 % of the LDS cycles were conflicts.)
+// It is linear in the bits of r.
 template <int D>
 __device__ __forceinline__ int swz(int r) {
-  return D == 64 ? (r >> 1) & 7 : r & 15;
+  return D == 64 ? (r & 2) << 1 | (r >> 2 & 3) : (r & 3) << 2 | (r >> 2 & 3);
 }
 
 // Page table entries are read as constants: by the scalar unit, whose loads have a counter of
