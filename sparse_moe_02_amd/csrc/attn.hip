@@ -3,7 +3,7 @@
 // Per query row: out = sum_j p_j v_j / sum_j p_j, p_j = exp(scale q.k_j - m), with the running
 // maximum m, sum and output rescaled as keys go by (one pass over K and V).  Scores, m, the
 // sum and the output are binary32; p_j is rounded to the cache's type to enter the matrix
-// units, and the sum is of the unrounded weights.
+// units, and the output is the quotient of sums over the rounded weights.
 //
 // k_attn_rows: a tile of 16 query rows -- (token, head) pairs of one key/value head, so the
 // heads that share it share every load -- against one split of the keys.  Four waves take
@@ -62,6 +62,25 @@ __device__ __forceinline__ float unpack(uint32_t w, bool hi) {
   const uint16_t v = (uint16_t)(hi ? w >> 16 : w & 0xffff);
   return F16 ? fp16_to_f32(v) : bf16_to_f32(v);
 }
+// c plus both values of a word
+template <bool F16>
+__device__ __forceinline__ float add2(uint32_t w, float c) {
+  if constexpr (F16) {
+    typedef __attribute__((__vector_size__(2 * sizeof(_Float16)))) _Float16 f16x2;
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), f16x2{(_Float16)1.0f, (_Float16)1.0f}, c, false);
+  } else {
+    return dot2_bf16(w, 0x3f803f80u, c);
+  }
+}
+// What is kept of a row besides its weighted sum of values: the reference (base-2 exponent), the
+// sum of the rounded weights, which the values' sum is divided by (so that a weight's rounding
+// only shifts the mean of the values), and that of the unrounded ones, for the log-sum-exp.
+struct Stats {
+  float m, l, e;
+};
+__device__ __forceinline__ float lse_of(float m, float e) { return e == 0.0f ? -INFINITY : (m + __log2f(e)) * kLn2; }
+__device__ __forceinline__ float reciprocal_of(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+
 // whether a value is an infinity or NaN
 template <bool F16>
 __device__ __forceinline__ bool nonfinite16(uint32_t w) {
@@ -360,7 +379,7 @@ template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) k_attn_rows(AttnArgs a) {
   using L = Rows<D>;
   extern __shared__ __align__(16) uint8_t lds_raw[];
-  __shared__ float ml[kWaves][2][kAttnRows];
+  __shared__ Stats ml[kWaves][kAttnRows];
   __shared__ int odd;  // some value that not all rows see is an infinity or NaN
   const int wg = blockIdx.x;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -425,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) k_attn_rows(AttnAr
   f32x4 acc[D / 16];
 #pragma unroll
   for (int d = 0; d < D / 16; ++d) acc[d] = f32x4{0, 0, 0, 0};
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, l = 0.0f, es = 0.0f;
 
   const TableRow trow = table_row(a, t.row);
   const int pmask = (1 << a.kv.page_shift) - 1;
@@ -517,12 +536,15 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) k_attn_rows(AttnAr
       p[i] = __builtin_amdgcn_exp2f(p[i] - mu);
       ps += p[i];
     }
-    l = l * f + ps;
+    es = es * f + ps;
+    l *= f;
     if (__ballot(f != 1.0f)) {
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) acc[d] *= f;
     }
     const u32x4 pf4 = {pack2<F16>(p[0], p[1]), pack2<F16>(p[2], p[3]), pack2<F16>(p[4], p[5]), pack2<F16>(p[6], p[7])};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l = add2<F16>(pf4[i], l);
 
     {
       const int vk = 4 * g + (n >> 2);  // LDS row this lane addresses for the transposing reads
@@ -542,43 +564,41 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) k_attn_rows(AttnAr
 
   // join the waves: each writes its rows over its own buffers
   l = groups_sum(l);
+  es = groups_sum(es);
   float *o = (float *)(lds_raw + wave * L::kWaveLds);
 #pragma unroll
   for (int d = 0; d < D / 16; ++d) *(f32x4 *)(o + n * L::kOStride + 16 * d + 4 * g) = acc[d];
   if (g == 0) {
-    ml[wave][0][n] = m;
-    ml[wave][1][n] = l;
+    ml[wave][n] = Stats{m, l, es};
   }
   __syncthreads();
   constexpr int kVecs = D / 4;  // 4-element vectors of a row
   for (int i = tid; i < t.nr * kVecs; i += kThreads) {
     const int r = i / kVecs, c = (i % kVecs) * 4;
-    float mw = ml[0][0][r];
+    float mw = ml[0][r].m;
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) mw = fmaxf(mw, ml[w][0][r]);
+    for (int w = 1; w < kWaves; ++w) mw = fmaxf(mw, ml[w][r].m);
     const float mu = mw == -INFINITY ? 0.0f : mw;
     f32x4 v = {0, 0, 0, 0};
-    float sum = 0.0f;
+    float sum = 0.0f, esum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      const float f = __builtin_amdgcn_exp2f(ml[w][0][r] - mu);
-      sum += f * ml[w][1][r];
+      const float f = __builtin_amdgcn_exp2f(ml[w][r].m - mu);
+      sum += f * ml[w][r].l;
+      esum += f * ml[w][r].e;
       v += f * *(const f32x4 *)((const float *)(lds_raw + w * L::kWaveLds) + r * L::kOStride + c);
     }
     const int q = t.r0 + r;
     const int64_t tk = t.t0 + q / a.G, hd = kvh * a.G + q % a.G;
     if (alone) {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float inv = reciprocal_of(sum);
       const uint2 w = {pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv)};
       *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + c) = w;
-      if (a.lse && c == 0) a.lse[tk * a.H + hd] = sum == 0.0f ? -INFINITY : (mw + __log2f(sum)) * kLn2;
+      if (a.lse && c == 0) a.lse[tk * a.H + hd] = lse_of(mw, esum);
     } else {
       const int64_t at = slot + r;
       *(f32x4 *)(a.part + at * D + c) = v;
-      if (c == 0) {
-        a.part_ml[2 * at] = mw;
-        a.part_ml[2 * at + 1] = sum;
-      }
+      if (c == 0) a.stats[at] = AttnStats{mw, sum, esum, 0.0f};
     }
   }
   if (odd) {  // (a barrier lies behind its last write)
@@ -734,7 +754,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
-  float m = -INFINITY, l = 0.0f;  // m: of the unscaled products
+  float m = -INFINITY, l = 0.0f, es = 0.0f;  // m: of the unscaled products
 
   // pages of the block in use and the ones in flight, checked; and of the one after them
   const bool upper = my_r0 & 16;
@@ -838,6 +858,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
       const float f = __builtin_amdgcn_exp2f((m - (mn == -INFINITY ? 0.0f : mn)) * scale);
       m = mn;
       l *= f;
+      es *= f;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d) acc[d] *= f;
     }
@@ -848,10 +869,13 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
       s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale, off));
       ps += s[i];
     }
-    l += ps;
+    es += ps;
     u32x4 pf4[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) pf4[i / 4][i % 4] = pack2<F16>(s[2 * i], s[2 * i + 1]);
+    for (int i = 0; i < 8; ++i) {
+      pf4[i / 4][i % 4] = pack2<F16>(s[2 * i], s[2 * i + 1]);
+      l = add2<F16>(pf4[i / 4][i % 4], l);
+    }
 
     constexpr int kParts = D / 16;
     if (kFirst == First::Matrix) __builtin_amdgcn_s_setprio(1);
@@ -867,6 +891,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   }
 
   l = halves_sum(l);
+  es = halves_sum(es);
   __syncthreads();
   const bool fix = odd != 0;
   if (!live && !fix) return;
@@ -876,7 +901,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   const bool direct = a.splits == 1 || nblk <= a.split_blocks;
   if (!live || (direct && split > 0)) {
   } else if (direct) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = reciprocal_of(l);
     uint16_t *o = a.out.p + (int64_t)tok * a.out.ts + (int64_t)head * a.out.hs + 4 * half;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
@@ -886,8 +911,8 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
                          pack2<F16>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv)};
         *(uint2 *)(o + 32 * d + 8 * i) = w;
       }
-    if (a.lse && half == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m * scale + __log2f(l)) * kLn2;
-    if (a.splits > 1 && half == 0) a.part_ml[2 * row * a.splits + 1] = -1.0f;
+    if (a.lse && half == 0) a.lse[row] = lse_of(m == -INFINITY ? m : m * scale, es);
+    if (a.splits > 1 && half == 0) a.stats[row * a.splits].l = -1.0f;
   } else {
     const int64_t at = row * a.splits + split;
     if (b0 < b1)
@@ -897,10 +922,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
       for (int i = 0; i < 4; ++i)
         *(f32x4 *)(a.part + at * D + 32 * d + 8 * i + 4 * half) =
             f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
-    if (half == 0) {
-      a.part_ml[2 * at] = m == -INFINITY ? m : m * scale;
-      a.part_ml[2 * at + 1] = l;
-    }
+    if (half == 0) a.stats[at] = AttnStats{m == -INFINITY ? m : m * scale, l, es, 0.0f};
   }
   if (!fix) return;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "agent");
@@ -923,29 +945,27 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(AttnArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int64_t tk = r / a.H, hd = r % a.H;
   if (tk >= a.b.q_start[a.b.n_seqs]) return;
-  if (a.part_ml[2 * r * a.splits + 1] < 0.0f) return;  // done already
-  float ms[kRegs], ls[kRegs], mw = -INFINITY;
+  if (a.stats[r * a.splits].l < 0.0f) return;  // done already
+  AttnStats st[kRegs];
+  float mw = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kRegs; ++i) {
-    ms[i] = -INFINITY;
-    ls[i] = 0.0f;
-    if (64 * i + lane < a.splits) {
-      const float *ml = a.part_ml + (r * a.splits + 64 * i + lane) * 2;
-      ms[i] = ml[0];
-      ls[i] = ml[1];
-    }
-    mw = fmaxf(mw, ms[i]);
+    st[i] = AttnStats{-INFINITY, 0.0f, 0.0f, 0.0f};
+    if (64 * i + lane < a.splits) st[i] = a.stats[r * a.splits + 64 * i + lane];
+    mw = fmaxf(mw, st[i].m);
   }
   mw = wave_max(mw);
   const float mu = mw == -INFINITY ? 0.0f : mw;
-  float sum = 0.0f;
+  float sum = 0.0f, esum = 0.0f;
 #pragma unroll
   for (int i = 0; i < kRegs; ++i) {
-    const float f = ls[i] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ms[i] - mu);
-    sum += f * ls[i];
+    const float f = st[i].l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(st[i].m - mu);
+    sum += f * st[i].l;
+    esum += f * st[i].e;
     if (tid < 64) weight[64 * i + lane] = f;
   }
   sum = wave_sum(sum);
+  esum = wave_sum(esum);
   __syncthreads();
   const int c = tid % kVecs, g = tid / kVecs;
   const f32x4 *p = (const f32x4 *)(a.part + r * a.splits * D) + c;
@@ -968,10 +988,10 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(AttnArgs a) {
   if (g > 0) return;
 #pragma unroll
   for (int i = 1; i < kGroups; ++i) v += sums[i][c];
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = reciprocal_of(sum);
   *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + 4 * c) =
       make_uint2(pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv));
-  if (a.lse && tid == 0) a.lse[r] = sum == 0.0f ? -INFINITY : (mw + __log2f(sum)) * kLn2;
+  if (a.lse && tid == 0) a.lse[r] = lse_of(mw, esum);
 }
 
 // The same for up to kFewSplits splits, where there are many rows: kRows rows a wave, their loads
@@ -984,58 +1004,60 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_few(AttnArgs a) {
   const int lane = threadIdx.x & 63, c = lane % kVecs, g = lane / kVecs;
   const int64_t r0 = ((int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6)) * kRows;
   const int64_t end = (int64_t)min(a.T, a.b.q_start[a.b.n_seqs]) * a.H;
-  float m[kRows][kN], l[kRows][kN];
+  AttnStats st[kRows][kN];
   bool todo[kRows];
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
-    const float *ml = a.part_ml + min(r0 + j, (int64_t)a.T * a.H - 1) * a.splits * 2;
+    const AttnStats *p = a.stats + min(r0 + j, (int64_t)a.T * a.H - 1) * a.splits;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int s = g + i * kGroups;
-      m[j][i] = s < a.splits ? ml[2 * s] : -INFINITY;
-      l[j][i] = s < a.splits ? ml[2 * s + 1] : 0.0f;
+      st[j][i] = p[min(s, a.splits - 1)];
+      if (s >= a.splits) st[j][i] = AttnStats{-INFINITY, 0.0f, 0.0f, 0.0f};
     }
   }
   f32x4 x[kRows][kN];
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
     // (a first sum of -1: the row is done)
-    todo[j] = r0 + j < end && __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(l[j][0]))) >= 0.0f;
+    todo[j] = r0 + j < end && !(__int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(st[j][0].l))) < 0.0f);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       x[j][i] = f32x4{0, 0, 0, 0};
-      if (todo[j] && l[j][i] != 0.0f)  // (empty splits are not written)
+      if (todo[j] && st[j][i].l != 0.0f)  // (empty splits are not written)
         x[j][i] = *((const f32x4 *)(a.part + ((r0 + j) * a.splits + g + i * kGroups) * D) + c);
     }
   }
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
     if (!todo[j]) continue;
-    float mw = -INFINITY, sum = 0.0f;
+    float mw = -INFINITY, sum = 0.0f, esum = 0.0f;
     f32x4 v = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < kN; ++i) mw = fmaxf(mw, m[j][i]);
+    for (int i = 0; i < kN; ++i) mw = fmaxf(mw, st[j][i].m);
 #pragma unroll
     for (int o = kVecs; o < 64; o <<= 1) mw = fmaxf(mw, __shfl_xor(mw, o, 64));
     const float mu = mw == -INFINITY ? 0.0f : mw;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const float f = __builtin_amdgcn_exp2f(m[j][i] - mu);
-      sum += f * l[j][i];
+      const float f = __builtin_amdgcn_exp2f(st[j][i].m - mu);
+      sum += f * st[j][i].l;
+      esum += f * st[j][i].e;
       v += f * x[j][i];
     }
 #pragma unroll
     for (int o = kVecs; o < 64; o <<= 1) {
       sum += __shfl_xor(sum, o, 64);
+      esum += __shfl_xor(esum, o, 64);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] += __shfl_xor(v[e], o, 64);
     }
     if (g > 0) continue;
     const int64_t r = r0 + j, tk = r / a.H, hd = r % a.H;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float inv = reciprocal_of(sum);
     *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + 4 * c) =
         make_uint2(pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv));
-    if (a.lse && lane == 0) a.lse[r] = sum == 0.0f ? -INFINITY : (mw + __log2f(sum)) * kLn2;
+    if (a.lse && lane == 0) a.lse[r] = lse_of(mw, esum);
   }
 }
 
@@ -1048,7 +1070,7 @@ template <int D, bool F16>
 __global__ void __launch_bounds__(kJoinThreads) k_attn_join_runs(AttnArgs a) {
   constexpr int kVecs = D / 4, kGroups = kJoinThreads / kVecs, kW = kJoinThreads / 64;
   __shared__ f32x4 sums[kGroups][kVecs];
-  __shared__ float weight[kMaxRuns], red[2][kW];
+  __shared__ float weight[kMaxRuns], red[3][kW];
   const int wg = blockIdx.x;
   const AttnRec rec = a.rec[wg];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -1056,25 +1078,34 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join_runs(AttnArgs a) {
   for (int r = blockIdx.y; rec.n > 0 && r < rec.nr; r += gridDim.y) {
     auto at = [&](int s) { return (2 * (int64_t)(wg + s) + (s == 0)) * kAttnRows + r; };
     float mw = -INFINITY;
-    for (int s = tid; s < rec.n; s += kJoinThreads) mw = fmaxf(mw, a.part_ml[2 * at(s)]);
+    for (int s = tid; s < rec.n; s += kJoinThreads) mw = fmaxf(mw, a.stats[at(s)].m);
     mw = wave_max(mw);
     if (lane == 0) red[0][tid >> 6] = mw;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kW; ++i) mw = fmaxf(mw, red[0][i]);
     const float mu = mw == -INFINITY ? 0.0f : mw;
-    float sum = 0.0f;
+    float sum = 0.0f, esum = 0.0f;
     for (int s = tid; s < rec.n; s += kJoinThreads) {
-      const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at(s)] - mu);
-      sum += f * a.part_ml[2 * at(s) + 1];
+      const AttnStats st = a.stats[at(s)];
+      const float f = __builtin_amdgcn_exp2f(st.m - mu);
+      sum += f * st.l;
+      esum += f * st.e;
       weight[s] = f;
     }
     sum = wave_sum(sum);
-    if (lane == 0) red[1][tid >> 6] = sum;
+    esum = wave_sum(esum);
+    if (lane == 0) {
+      red[1][tid >> 6] = sum;
+      red[2][tid >> 6] = esum;
+    }
     __syncthreads();
-    sum = 0.0f;
+    sum = esum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kW; ++i) sum += red[1][i];
+    for (int i = 0; i < kW; ++i) {
+      sum += red[1][i];
+      esum += red[2][i];
+    }
     f32x4 v = {0, 0, 0, 0};
     for (int s0 = g; s0 < rec.n; s0 += 8 * kGroups) {
       f32x4 x[8];
@@ -1089,11 +1120,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join_runs(AttnArgs a) {
     if (g == 0) {
 #pragma unroll
       for (int i = 1; i < kGroups; ++i) v += sums[i][c];
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float inv = reciprocal_of(sum);
       const int64_t tk = rec.t0 + (rec.r0 + r) / a.G, hd = rec.kvh * a.G + (rec.r0 + r) % a.G;
       *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + 4 * c) =
           make_uint2(pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv));
-      if (a.lse && tid == 0) a.lse[tk * a.H + hd] = sum == 0.0f ? -INFINITY : (mw + __log2f(sum)) * kLn2;
+      if (a.lse && tid == 0) a.lse[tk * a.H + hd] = lse_of(mw, esum);
     }
     __syncthreads();
   }
@@ -1153,8 +1184,8 @@ AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int w
     s.wgs = runs_of(dim);
     s.join_rows = (int)(max_q * G < 1 ? 1 : max_q * G < kAttnRows ? max_q * G : kAttnRows);
     const size_t slots = (size_t)2 * s.wgs * kAttnRows;
-    s.off_ml = slots * dim * 4;
-    s.off_rec = s.off_ml + slots * 8;
+    s.off_stats = slots * dim * 4;
+    s.off_rec = s.off_stats + slots * sizeof(AttnStats);
     s.ws_bytes = s.off_rec + s.wgs * sizeof(AttnRec);
     return s;
   }
@@ -1174,8 +1205,8 @@ AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int w
   s.split_blocks = (int)per;
   if (s.splits > 1) {
     const size_t rows = (size_t)T * H * s.splits;
-    s.off_ml = (rows * dim * 4 + 255) & ~(size_t)255;
-    s.ws_bytes = s.off_ml + rows * 8;
+    s.off_stats = (rows * dim * 4 + 255) & ~(size_t)255;
+    s.ws_bytes = s.off_stats + rows * sizeof(AttnStats);
   }
   return s;
 }

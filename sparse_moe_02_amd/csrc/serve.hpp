@@ -40,6 +40,12 @@ constexpr int kAttnRows = 16;   // query rows (token x head of a group) of a sma
 constexpr int kAttnTile = 128;  // query rows of a large tile: four waves of 32
 constexpr int kAttnKeys = 32;   // keys of one block
 
+// Of a partial output: reference (base-2 exponent), sums of the rounded and of the unrounded
+// weights.
+struct AttnStats {
+  float m, l, e, pad;
+};
+
 // A segment (row tile and key/value head) whose keys n consecutive workgroups share.
 struct AttnRec {
   int n, t0, r0, nr, kvh;
@@ -51,7 +57,7 @@ struct AttnArgs {
   Heads q, out;
   float *lse;      // [T][H] or null
   float *part;     // unnormalised partial outputs: [T * H][splits][dim], small tiles [wgs][2][16][dim]
-  float *part_ml;  // [..][2] of each: running maximum (base-2 exponent) and sum
+  AttnStats *stats;  // of each
   int T, H, G;     // G: query heads of one key/value head
   int rows;        // rows of a tile: kAttnRows or kAttnTile
   int tiles;       // bound on the number of row tiles
@@ -65,7 +71,7 @@ struct AttnArgs {
 // What the launch is shaped by, from host-known sizes alone.
 struct AttnShape {
   int rows, tiles, splits, split_blocks, wgs, join_rows;
-  size_t ws_bytes, off_ml, off_rec;
+  size_t ws_bytes, off_stats, off_rec;
 };
 AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int window, int H, int n_kv, int dim);
 hipError_t launch_paged_attn(const AttnArgs &a, hipStream_t s);

@@ -401,7 +401,7 @@ moe_status moe_paged_attn(const moe_paged_kv *kv, const moe_batch *batch, int64_
   a.out = dev_heads(*out);
   a.lse = lse;
   a.part = static_cast<float *>(workspace);
-  a.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + sh.off_ml);
+  a.stats = reinterpret_cast<AttnStats *>(static_cast<char *>(workspace) + sh.off_stats);
   a.T = (int)T;
   a.H = n_heads;
   a.G = n_heads / kv->n_kv_heads;
