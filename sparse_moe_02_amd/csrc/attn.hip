@@ -1,22 +1,29 @@
 // Attention of a ragged batch of new tokens over the paged cache.
 //
-// Per query row: out = sum_j p_j v_j / sum_j p_j, p_j = exp(scale q.k_j - m), with the running
-// maximum m, sum and output rescaled as keys go by (one pass over K and V).  Scores, m, the
-// sum and the output are binary32; p_j is rounded to the cache's type to enter the matrix
-// units, and the output is the quotient of sums over the rounded weights.
+// Per query row: out = sum_j p_j v_j / sum_j p_j, p_j = exp(scale q.k_j - m), with a reference m,
+// the sums and the output rescaled as keys go by (one pass over K and V).  Scores, m, sums and
+// outputs are binary32; p_j is rounded to the cache's type to enter the matrix units.
 //
-// k_attn_rows: a tile of 16 query rows -- (token, head) pairs of one key/value head, so the
-// heads that share it share every load -- against one split of the keys.  Four waves take
-// blocks of 32 keys in turn, each with a private 32-key K and V buffer in LDS filled by
-// direct-to-LDS loads: the next block's K is in flight during softmax and P V, its V during
-// the next Q K.  Both products are computed transposed with v_mfma_f32_16x16x32:
-// S^T = K Q^T leaves a lane one query's scores, 4 keys at a time; with the contraction
-// index of P V ordered the same way (slot j of lane group g is key 16 (j / 4) + 4 g + j % 4)
-// those registers are P^T's operand as they are, and V^T comes from ds_read_b64_tr_b16.
-// LDS rows are swizzled by 16-byte chunk so neither read has bank conflicts beyond its width.
-// The waves' and then the splits' partial results are joined by their maxima, in fixed order.
+// A query row is a (token, head) pair; the rows of one key/value head's group are packed into
+// tiles, so the heads that share a key/value head share every load.  Keys go by in blocks of 32.
+// Both products are computed transposed: S^T = K Q^T leaves a lane one query's scores, 4 keys
+// at a time, and with the contraction index of P V ordered the same way those registers are
+// P^T's operand as they are; V^T comes from ds_read_b64_tr_b16.
 //
-// Bound: memory for single tokens (K and V read once per split).
+//   k_attn_tile  128 rows, four waves of 32 (v_mfma_f32_32x32x16), every wave all keys; blocks of
+//                K and V in an LDS ring filled by direct-to-LDS loads.  Where tiles are few,
+//                their keys are split over workgroups, joined by k_attn_join(_few).
+//                Bound: matrix units (4 flops per row, visible key and element).  4096 tokens at
+//                32K, 16/2 heads of 256: 1.85 ms, 1.11 PFLOP/s (a large library product reaches
+//                1.22), the clock held down by power; 24 chunks of 0 to 509 tokens, window 1024,
+//                32/8 heads of 128: 0.14 ms, 0.57 PFLOP/s (starts, and a second round of tiles).
+//                One token at 4K: 13.7 us, a chain of dependent loads and a second launch.
+//   k_attn_rows  16 rows, four waves sharing the keys out (v_mfma_f32_16x16x32); the keys of all
+//                sequences cut into equal runs, joined by k_attn_join_runs.  For few rows over
+//                many long sequences.  Bound: memory.  One token of 64 sequences up to 16K:
+//                172 us, 5.0 TB/s (a copy reaches 5.2).
+//
+// Results of splits and runs are joined by their references, in fixed order.
 #include <atomic>
 
 #include "paged.hpp"
@@ -375,6 +382,11 @@ struct Walk {
   __device__ __forceinline__ Seq seq() const { return readlane_seq(mine, at); }
 };
 
+// 16 rows against runs of blocks.  The four waves take blocks in turn; each holds the next block in
+// registers while it works on one -- K as the matrix operand itself, V on its way to the wave's
+// LDS buffer, from where it is read transposed.  (Blocks by direct-to-LDS loads and splits of
+// fixed length took 203 us for the 64 sequences up to 16K that take 172 us here: long
+// sequences kept a few compute units busy.)
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) k_attn_rows(AttnArgs a) {
   using L = Rows<D>;
@@ -657,6 +669,8 @@ constexpr float kLag = 8.0f;
 // 16K, heads of 128, 1150 / 1133 / 1101; 4096 at 8K, heads of 64, 211 / 199 / 216.
 enum class First { Matrix, Softmax, None };
 
+// 32 rows a wave, NW waves.  A workgroup's waves pass one barrier a block: behind it the block is
+// there for all, and the buffer of the block before it is free for the loads of the next.
 template <int D, bool F16, int NW>
 __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   constexpr int kBuf = kAttnKeys * D * 2;      // one K or V block, bytes

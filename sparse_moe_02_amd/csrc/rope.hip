@@ -6,11 +6,13 @@
 // theta reaches 1e5 rad and more, where binary32 keeps no fraction of a turn: it is formed
 // and reduced to a turn in binary64, the sine and cosine of the rest in binary32.
 //
-// Bound: memory (each element read and written once; 2 bytes each).  A workgroup takes 256
-// 16-byte chunks of one token's concatenated heads [q | k | v]: sines and cosines of the
-// token's rot_dim / 2 pairs are computed once per workgroup into LDS.  Chunks never straddle
-// heads, a head's chunks never straddle workgroups, and all of a workgroup's loads precede
-// its stores, so q_out may be q.
+// Bound: memory (each element read and written once; 2 bytes each).  A workgroup takes 16-byte
+// chunks of one token's concatenated heads [q | k | v]: sines and cosines of the token's
+// rot_dim / 2 pairs are computed once per workgroup into LDS.  Chunks never straddle heads, a
+// head's chunks never straddle workgroups, and all of a workgroup's loads precede its stores, so
+// q_out may be q.  The data loads do not wait for the token's sequence, and a large call's threads
+// take three chunks each: 4096 tokens of 16 + 2 + 2 heads of 256 take 17.0 us, 4.9 TB/s (one
+// chunk a thread 23.1, two 22.0, four 18.0).  16 tokens: 4.3 us, the launch and four dependent loads.
 #include "paged.hpp"
 
 #pragma clang fp contract(off)
