@@ -65,6 +65,9 @@ moe_status moe_gdn_scan(int32_t T, int32_t n_kheads, int32_t n_vheads, int32_t d
  *   slot       int32 [R], 4-byte aligned: a row whose slot lies outside [0, n_slots) is
  *              padding: it touches no state, and its output is zeros
  *   out        bf16 [R][n_vheads][128], o_t rounded to nearest even, 2-byte aligned
+ * A decay of 0 takes the slot's old state as zeros whatever it holds, so a slot starts a new
+ * sequence without being cleared.  Every row looks through the slots for its like, which is meant
+ * for up to some thousand rows.
  * out and state may overlap neither an input nor each other (MOE_ERR_ALIAS).  Status codes as
  * moe_gdn_scan (MOE_ERR_SHAPE also for n_slots < 1).  May be captured in a graph: slot is
  * read when the kernel runs. */

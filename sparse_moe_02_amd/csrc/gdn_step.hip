@@ -12,7 +12,8 @@
 // of its state loads in flight at once.
 //
 // Rows of one slot are applied in row order: the workgroup of the slot's first row takes
-// them all, the state staying in registers; the workgroups of the others end.
+// them all, the state staying in registers; the workgroups of the others end.  A decay of 0 takes
+// the old state as zeros, whatever it holds (0 times NaN is no zero).
 #include "serve.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
@@ -69,6 +70,12 @@ __global__ void __launch_bounds__(kThreads) k_gdn_step(GdnStepArgs a) {
     unpack8(make_uint4(k0.x, k0.y, k1.x, k1.y), kf);
     unpack8(make_uint4(q0.x, q0.y, q1.x, q1.y), qf);
     const float alpha = a.alpha[(int64_t)r * a.hv + h], beta = a.beta[(int64_t)r * a.hv + h];
+    if (alpha == 0.0f) {
+#pragma unroll
+      for (int i = 0; i < kRowsPer; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) st[i][e] = 0.0f;
+    }
     const int64_t ob = ((int64_t)r * a.hv + h) * kD + c0 + grp;
     float kq = 0.0f;
 #pragma unroll

@@ -92,6 +92,23 @@ def test_extreme_gates():
     _check(d, "extreme gates")
 
 
+def test_a_decay_of_zero_starts_anew_whatever_the_slot_held():
+    import torch
+
+    from sparse_moe_02_amd.gdn import gdn_step
+
+    d = _inputs([0, 1, 1, 2], 4, 2, 4, 15)
+    d["alpha"][0] = 0.0  # the slot's first row
+    d["alpha"][2, 1] = 0.0  # its second row, one head
+    clean = {k: v.clone() for k, v in d.items()}
+    clean["state"][0] = 0.0
+    d["state"][0] = float("nan")
+    d["state"][0, 1] = float("inf")
+    out, ref = gdn_step(**d), gdn_step(**clean)
+    assert torch.equal(out, ref) and torch.equal(d["state"], clean["state"])
+    _check({**_inputs([0, 1, 1, 2], 4, 2, 4, 15), "alpha": d["alpha"].clone()}, "decays of zero")
+
+
 def test_steps_follow_the_scan():
     """A prompt's scan, then its next tokens as steps: the scan over all of them."""
     import torch
