@@ -113,14 +113,14 @@ moe_status moe_rope_append(const moe_paged_kv *kv, const moe_batch *batch, int64
  * head h / (n_heads / n_kv_heads),
  *     out = sum_j softmax_j(scale * q . k_j) v_j
  * over the positions j < kv_len that it sees: j <= p (all of them with MOE_ATTN_FULL), and
- * j > p - window where window > 0.  A token that sees nothing gets zeros, and a log-sum-exp
- * of -infinity.  Positions it does not see have no influence, whatever their cache places
- * hold (NaN among it).
+ * j > p - window where window > 0.  A token that sees nothing, or whose scores are all
+ * -infinity, gets zeros, and a log-sum-exp of -infinity.  Positions it does not see have no
+ * influence, whatever their cache places hold (NaN among it).
  *   max_q, max_kv  (host) upper bounds of n_b and kv_len that the launch is shaped by.
  *                  Smaller numbers than the true ones cost time, not results.
  *   q, out         [T][n_heads][head_dim]; n_heads a multiple of n_kv_heads, <= 4096
  *   lse            float32 [T][n_heads] or NULL: natural log of the sum of exp(scale q . k)
- *   scale          finite
+ *   scale          finite, also times log2(e)
  *   window         >= 0; 0 with MOE_ATTN_FULL
  *   workspace      256-byte aligned, at least the bytes that moe_paged_attn_workspace gives
  *                  for the same sizes; may be NULL where that is 0.  It holds nothing

@@ -413,222 +413,222 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) k_attn_rows(AttnAr
   const int n = lane & 15, g = lane >> 4;  // query row of the lane, lane group
   const uint32_t vbuf = lds_addr(lds_raw) + wave * L::kWaveLds;
   while (true) {
-  const Seq sq = walk.seq();
-  const SeqSize z = seq_size(a, sq);
-  const int64_t cum = walk.cum;
-  const int seg = (int)div_u64((uint64_t)(cur - cum), (uint64_t)z.blocks), o0 = (int)(cur - cum - (int64_t)seg * z.blocks);
-  const int o1 = (int)min((int64_t)z.blocks, o0 + (end - cur));
-  const int kvh = __builtin_amdgcn_readfirstlane(seg % a.kv.n_kv);
-  Tile t;
-  set_tile(a, sq, (int64_t)(seg / a.kv.n_kv) * kAttnRows, kAttnRows, t);
+    const Seq sq = walk.seq();
+    const SeqSize z = seq_size(a, sq);
+    const int64_t cum = walk.cum;
+    const int seg = (int)div_u64((uint64_t)(cur - cum), (uint64_t)z.blocks), o0 = (int)(cur - cum - (int64_t)seg * z.blocks);
+    const int o1 = (int)min((int64_t)z.blocks, o0 + (end - cur));
+    const int kvh = __builtin_amdgcn_readfirstlane(seg % a.kv.n_kv);
+    Tile t;
+    set_tile(a, sq, (int64_t)(seg / a.kv.n_kv) * kAttnRows, kAttnRows, t);
 
-  // this lane's query row
-  const int rr = t.r0 + n;
-  const bool live = n < t.nr;
-  const int tok = t.t0 + rr / a.G, head = kvh * a.G + rr % a.G;
-  const int64_t pos = live ? t.first + rr / a.G : -1;
-  // visible keys: first_key .. last_key
-  const int last_key = (int)(a.full ? (live ? (int64_t)t.len - 1 : -1) : min(pos, (int64_t)t.len - 1));
-  const int first_key = a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
-  // every row of the tile sees all keys of [all_lo, all_hi); lanes without a row (queries of
-  // zeros) go along, and nothing of theirs is stored
-  const int64_t pf = t.first + t.r0 / a.G, pl = t.first + (t.r0 + t.nr - 1) / a.G;
-  const int all_hi = (int)(a.full ? (int64_t)t.len : min(pf + 1, (int64_t)t.len));
-  const int64_t all_lo = a.window ? pl - a.window + 1 : 0;
+    // this lane's query row
+    const int rr = t.r0 + n;
+    const bool live = n < t.nr;
+    const int tok = t.t0 + rr / a.G, head = kvh * a.G + rr % a.G;
+    const int64_t pos = live ? t.first + rr / a.G : -1;
+    // visible keys: first_key .. last_key
+    const int last_key = (int)(a.full ? (live ? (int64_t)t.len - 1 : -1) : min(pos, (int64_t)t.len - 1));
+    const int first_key = a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
+    // every row of the tile sees all keys of [all_lo, all_hi); lanes without a row (queries of
+    // zeros) go along, and nothing of theirs is stored
+    const int64_t pf = t.first + t.r0 / a.G, pl = t.first + (t.r0 + t.nr - 1) / a.G;
+    const int all_hi = (int)(a.full ? (int64_t)t.len : min(pf + 1, (int64_t)t.len));
+    const int64_t all_lo = a.window ? pl - a.window + 1 : 0;
 
-  // (lanes without a row read the tile's first one, and take zeros)
-  const uint16_t *qp = a.q.p + (int64_t)(live ? tok : t.t0 + t.r0 / a.G) * a.q.ts +
-                       (int64_t)(live ? head : kvh * a.G + t.r0 % a.G) * a.q.hs;
-  u32x4 qf[D / 32];
+    // (lanes without a row read the tile's first one, and take zeros)
+    const uint16_t *qp = a.q.p + (int64_t)(live ? tok : t.t0 + t.r0 / a.G) * a.q.ts +
+                         (int64_t)(live ? head : kvh * a.G + t.r0 % a.G) * a.q.hs;
+    u32x4 qf[D / 32];
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) qf[c] = *(const u32x4 *)(qp + 32 * c + 8 * g);
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c)
-    if (!live) qf[c] = u32x4{0, 0, 0, 0};
-
-  // this run's blocks of the segment
-  const int blk0 = t.lo / kAttnKeys, nblk = (t.hi + kAttnKeys - 1) / kAttnKeys - blk0;
-  const int b0 = blk0 + min(nblk, o0), b1 = blk0 + min(nblk, o1);
-  const bool alone = o0 == 0 && o1 == z.blocks;
-  // partial results: of a segment that goes on in the next run, and of one from the run before
-  const int64_t slot = (2 * (int64_t)wg + (o0 == 0)) * kAttnRows;
-
-  f32x4 acc[D / 16];
-#pragma unroll
-  for (int d = 0; d < D / 16; ++d) acc[d] = f32x4{0, 0, 0, 0};
-  float m = -INFINITY, l = 0.0f, es = 0.0f;
-
-  const TableRow trow = table_row(a, t.row);
-  const int pmask = (1 << a.kv.page_shift) - 1;
-  auto page_of = [&](int key) { return page_at(a, trow, key); };
-  auto base = [&](const uint16_t *plane, int page, int key) {
-    return (const char *)uniform_ptr(plane + (int64_t)max(page, 0) * a.kv.ps + (int64_t)(key & pmask) * a.kv.ts +
-                                     (int64_t)kvh * a.kv.hs);
-  };
-  // K comes in the layout of the matrix operand (lane: key n of a half, 8 elements from 8 g of
-  // each 32), V in rows of whole cache lines
-  constexpr int kChunks = D / 8, kRowsPer = 64 / kChunks, kVLoads = kAttnKeys / kRowsPer;
-  const int ts2 = (int)a.kv.ts * 2;
-  const int koff = n * ts2 + 16 * g, vrow = lane / kChunks;
-  const int voff = vrow * ts2 + lane % kChunks * 16;
-  u32x4 kr[2][D / 32], vr[kVLoads];
-  auto load = [&](int key0, int pg0, int pg1) {
-    const char *k0 = base(a.kv.k, pg0, key0), *k1 = base(a.kv.k, pg1, key0 + 16);
-    const char *v0 = base(a.kv.v, pg0, key0), *v1 = base(a.kv.v, pg1, key0 + 16);
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) kr[0][c] = *(const u32x4 *)(k0 + koff + 64 * c);
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) kr[1][c] = *(const u32x4 *)(k1 + koff + 64 * c);
-#pragma unroll
-    for (int i = 0; i < kVLoads; ++i)
-      vr[i] = *(const u32x4 *)((i < kVLoads / 2 ? v0 : v1) + (voff + i % (kVLoads / 2) * kRowsPer * ts2));
-  };
-
-  int blk = b0 + wave;
-  int pg0 = -1, pg1 = -1;
-  if (blk < b1) {
-    pg0 = page_of(blk * kAttnKeys);
-    pg1 = page_of(blk * kAttnKeys + 16);
-    load(blk * kAttnKeys, pg0, pg1);
-  }
-  for (; blk < b1; blk += kWaves) {
-    const int key0 = blk * kAttnKeys;
-    // (a block behind the last one is not loaded: its numbers are those of this one)
-    const int next = blk + kWaves < b1 ? key0 + kWaves * kAttnKeys : key0;
-    const int npg0 = page_of(next), npg1 = page_of(next + 16);
-    // keys present in the halves (behind the sequence's end, or in a bad page: absent)
-    const int have0 = pg0 < 0 ? 0 : max(0, min(16, t.len - key0));
-    const int have1 = pg1 < 0 ? 0 : max(0, min(16, t.len - key0 - 16));
-
-    f32x4 s[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+    for (int c = 0; c < D / 32; ++c) qf[c] = *(const u32x4 *)(qp + 32 * c + 8 * g);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) s[h] = mfma16<F16>(kr[h][c], qf[c], s[h]);
+      if (!live) qf[c] = u32x4{0, 0, 0, 0};
 
-    const bool edge = key0 + kAttnKeys > all_hi || key0 < all_lo;
-    const bool whole = have0 + have1 == kAttnKeys && !edge;
-    if (!whole) {
-      uint32_t bad = 0;
+    // this run's blocks of the segment
+    const int blk0 = t.lo / kAttnKeys, nblk = (t.hi + kAttnKeys - 1) / kAttnKeys - blk0;
+    const int b0 = blk0 + min(nblk, o0), b1 = blk0 + min(nblk, o1);
+    const bool alone = o0 == 0 && o1 == z.blocks;
+    // partial results: of a segment that goes on in the next run, and of one from the run before
+    const int64_t slot = (2 * (int64_t)wg + (o0 == 0)) * kAttnRows;
+
+    f32x4 acc[D / 16];
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) acc[d] = f32x4{0, 0, 0, 0};
+    float m = -INFINITY, l = 0.0f, es = 0.0f;
+
+    const TableRow trow = table_row(a, t.row);
+    const int pmask = (1 << a.kv.page_shift) - 1;
+    auto page_of = [&](int key) { return page_at(a, trow, key); };
+    auto base = [&](const uint16_t *plane, int page, int key) {
+      return (const char *)uniform_ptr(plane + (int64_t)max(page, 0) * a.kv.ps + (int64_t)(key & pmask) * a.kv.ts +
+                                       (int64_t)kvh * a.kv.hs);
+    };
+    // K comes in the layout of the matrix operand (lane: key n of a half, 8 elements from 8 g of
+    // each 32), V in rows of whole cache lines
+    constexpr int kChunks = D / 8, kRowsPer = 64 / kChunks, kVLoads = kAttnKeys / kRowsPer;
+    const int ts2 = (int)a.kv.ts * 2;
+    const int koff = n * ts2 + 16 * g, vrow = lane / kChunks;
+    const int voff = vrow * ts2 + lane % kChunks * 16;
+    u32x4 kr[2][D / 32], vr[kVLoads];
+    auto load = [&](int key0, int pg0, int pg1) {
+      const char *k0 = base(a.kv.k, pg0, key0), *k1 = base(a.kv.k, pg1, key0 + 16);
+      const char *v0 = base(a.kv.v, pg0, key0), *v1 = base(a.kv.v, pg1, key0 + 16);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) kr[0][c] = *(const u32x4 *)(k0 + koff + 64 * c);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) kr[1][c] = *(const u32x4 *)(k1 + koff + 64 * c);
+#pragma unroll
+      for (int i = 0; i < kVLoads; ++i)
+        vr[i] = *(const u32x4 *)((i < kVLoads / 2 ? v0 : v1) + (voff + i % (kVLoads / 2) * kRowsPer * ts2));
+    };
+
+    int blk = b0 + wave;
+    int pg0 = -1, pg1 = -1;
+    if (blk < b1) {
+      pg0 = page_of(blk * kAttnKeys);
+      pg1 = page_of(blk * kAttnKeys + 16);
+      load(blk * kAttnKeys, pg0, pg1);
+    }
+    for (; blk < b1; blk += kWaves) {
+      const int key0 = blk * kAttnKeys;
+      // (a block behind the last one is not loaded: its numbers are those of this one)
+      const int next = blk + kWaves < b1 ? key0 + kWaves * kAttnKeys : key0;
+      const int npg0 = page_of(next), npg1 = page_of(next + 16);
+      // keys present in the halves (behind the sequence's end, or in a bad page: absent)
+      const int have0 = pg0 < 0 ? 0 : max(0, min(16, t.len - key0));
+      const int have1 = pg1 < 0 ? 0 : max(0, min(16, t.len - key0 - 16));
+
+      f32x4 s[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[h] = mfma16<F16>(kr[h][c], qf[c], s[h]);
+
+      const bool edge = key0 + kAttnKeys > all_hi || key0 < all_lo;
+      const bool whole = have0 + have1 == kAttnKeys && !edge;
+      if (!whole) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < kVLoads; ++i) {
+          const int r = i * kRowsPer + vrow;
+          const bool absent = (r & 15) >= (r < 16 ? have0 : have1);
+          if (edge) bad |= make_finite<F16>(vr[i], absent);
+          else if (absent) vr[i] = u32x4{0, 0, 0, 0};
+        }
+        if (bad) odd = 1;
+      }
 #pragma unroll
       for (int i = 0; i < kVLoads; ++i) {
         const int r = i * kRowsPer + vrow;
-        const bool absent = (r & 15) >= (r < 16 ? have0 : have1);
-        if (edge) bad |= make_finite<F16>(vr[i], absent);
-        else if (absent) vr[i] = u32x4{0, 0, 0, 0};
+        *(__attribute__((address_space(3))) u32x4 *)(uintptr_t)(vbuf + r * D * 2 + (((lane % kChunks) ^ swz<D>(r)) * 16)) = vr[i];
       }
-      if (bad) odd = 1;
-    }
-#pragma unroll
-    for (int i = 0; i < kVLoads; ++i) {
-      const int r = i * kRowsPer + vrow;
-      *(__attribute__((address_space(3))) u32x4 *)(uintptr_t)(vbuf + r * D * 2 + (((lane % kChunks) ^ swz<D>(r)) * 16)) = vr[i];
-    }
-    if (blk + kWaves < b1) load(next, npg0, npg1);
+      if (blk + kWaves < b1) load(next, npg0, npg1);
 
-    float p[8];
-    float mx = -INFINITY;
+      float p[8];
+      float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float x = s[i / 4][i % 4] * a.scale_log2;
-      if (!whole) {
-        const int o = 4 * g + i % 4, key = key0 + 16 * (i / 4) + o;
-        if (o >= (i / 4 ? have1 : have0) || key > last_key || key < first_key) x = -INFINITY;
+      for (int i = 0; i < 8; ++i) {
+        float x = s[i / 4][i % 4] * a.scale_log2;
+        if (!whole) {
+          const int o = 4 * g + i % 4, key = key0 + 16 * (i / 4) + o;
+          if (o >= (i / 4 ? have1 : have0) || key > last_key || key < first_key) x = -INFINITY;
+        }
+        p[i] = x;
+        mx = fmaxf(mx, x);
       }
-      p[i] = x;
-      mx = fmaxf(mx, x);
-    }
-    const float mn = fmaxf(m, groups_max(mx));
-    const float mu = mn == -INFINITY ? 0.0f : mn;  // nothing seen yet: exp2(-inf - 0) = 0
-    const float f = __builtin_amdgcn_exp2f(m - mu);
-    m = mn;
-    float ps = 0.0f;
+      const float mn = fmaxf(m, groups_max(mx));
+      const float mu = mn == -INFINITY ? 0.0f : mn;  // nothing seen yet: exp2(-inf - 0) = 0
+      const float f = __builtin_amdgcn_exp2f(m - mu);
+      m = mn;
+      float ps = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(p[i] - mu);
-      ps += p[i];
-    }
-    es = es * f + ps;
-    l *= f;
-    if (__ballot(f != 1.0f)) {
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) acc[d] *= f;
-    }
-    const u32x4 pf4 = {pack2<F16>(p[0], p[1]), pack2<F16>(p[2], p[3]), pack2<F16>(p[4], p[5]), pack2<F16>(p[6], p[7])};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) l = add2<F16>(pf4[i], l);
-
-    {
-      const int vk = 4 * g + (n >> 2);  // LDS row this lane addresses for the transposing reads
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) {
-        const int c = 2 * d + ((n & 3) >> 1);
-        const uint32_t o = (uint32_t)((c ^ swz<D>(vk)) * 16 + (n & 1) * 8 + vk * D * 2);
-        const uint32_t o2 = (uint32_t)((c ^ swz<D>(vk + 16)) * 16 + (n & 1) * 8 + (vk + 16) * D * 2);
-        const uint64_t v0 = tr_read(vbuf + o), v1 = tr_read(vbuf + o2);
-        const u32x4 vf = {(uint32_t)v0, (uint32_t)(v0 >> 32), (uint32_t)v1, (uint32_t)(v1 >> 32)};
-        acc[d] = mfma16<F16>(vf, pf4, acc[d]);
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(p[i] - mu);
+        ps += p[i];
       }
-    }
-    pg0 = npg0;
-    pg1 = npg1;
-  }
+      es = es * f + ps;
+      l *= f;
+      if (__ballot(f != 1.0f)) {
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) acc[d] *= f;
+      }
+      const u32x4 pf4 = {pack2<F16>(p[0], p[1]), pack2<F16>(p[2], p[3]), pack2<F16>(p[4], p[5]), pack2<F16>(p[6], p[7])};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l = add2<F16>(pf4[i], l);
 
-  // join the waves: each writes its rows over its own buffers
-  l = groups_sum(l);
-  es = groups_sum(es);
-  float *o = (float *)(lds_raw + wave * L::kWaveLds);
+      {
+        const int vk = 4 * g + (n >> 2);  // LDS row this lane addresses for the transposing reads
 #pragma unroll
-  for (int d = 0; d < D / 16; ++d) *(f32x4 *)(o + n * L::kOStride + 16 * d + 4 * g) = acc[d];
-  if (g == 0) {
-    ml[wave][n] = Stats{m, l, es};
-  }
-  __syncthreads();
-  constexpr int kVecs = D / 4;  // 4-element vectors of a row
-  for (int i = tid; i < t.nr * kVecs; i += kThreads) {
-    const int r = i / kVecs, c = (i % kVecs) * 4;
-    float mw = ml[0][r].m;
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) mw = fmaxf(mw, ml[w][r].m);
-    const float mu = mw == -INFINITY ? 0.0f : mw;
-    f32x4 v = {0, 0, 0, 0};
-    float sum = 0.0f, esum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = __builtin_amdgcn_exp2f(ml[w][r].m - mu);
-      sum += f * ml[w][r].l;
-      esum += f * ml[w][r].e;
-      v += f * *(const f32x4 *)((const float *)(lds_raw + w * L::kWaveLds) + r * L::kOStride + c);
+        for (int d = 0; d < D / 16; ++d) {
+          const int c = 2 * d + ((n & 3) >> 1);
+          const uint32_t o = (uint32_t)((c ^ swz<D>(vk)) * 16 + (n & 1) * 8 + vk * D * 2);
+          const uint32_t o2 = (uint32_t)((c ^ swz<D>(vk + 16)) * 16 + (n & 1) * 8 + (vk + 16) * D * 2);
+          const uint64_t v0 = tr_read(vbuf + o), v1 = tr_read(vbuf + o2);
+          const u32x4 vf = {(uint32_t)v0, (uint32_t)(v0 >> 32), (uint32_t)v1, (uint32_t)(v1 >> 32)};
+          acc[d] = mfma16<F16>(vf, pf4, acc[d]);
+        }
+      }
+      pg0 = npg0;
+      pg1 = npg1;
     }
-    const int q = t.r0 + r;
-    const int64_t tk = t.t0 + q / a.G, hd = kvh * a.G + q % a.G;
-    if (alone) {
-      const float inv = reciprocal_of(sum);
-      const uint2 w = {pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv)};
-      *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + c) = w;
-      if (a.lse && c == 0) a.lse[tk * a.H + hd] = lse_of(mw, esum);
-    } else {
-      const int64_t at = slot + r;
-      *(f32x4 *)(a.part + at * D + c) = v;
-      if (c == 0) a.stats[at] = AttnStats{mw, sum, esum, 0.0f};
+
+    // join the waves: each writes its rows over its own buffers
+    l = groups_sum(l);
+    es = groups_sum(es);
+    float *o = (float *)(lds_raw + wave * L::kWaveLds);
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) *(f32x4 *)(o + n * L::kOStride + 16 * d + 4 * g) = acc[d];
+    if (g == 0) {
+      ml[wave][n] = Stats{m, l, es};
     }
-  }
-  if (odd) {  // (a barrier lies behind its last write)
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "agent");
     __syncthreads();
-    put_back<D, F16>(a, t, kvh, b0, b1, (int)min(all_lo, (int64_t)INT32_MAX), all_hi, t.r0 + wave, t.r0 + t.nr, kWaves,
-                     [&](int r, int64_t, int64_t) { return alone ? nullptr : a.part + (slot + r - t.r0) * D; });
-  }
-  if (o0 == 0 && o1 < z.blocks) {  // the first of the workgroups that share the segment
-    if (tid == 0) a.rec[wg] = AttnRec{runs.holder(cum + (int64_t)(seg + 1) * z.blocks - 1) - wg + 1, t.t0, t.r0, t.nr, kvh};
-    return;
-  }
-  cur += o1 - o0;
-  if (cur == end) return;
-  __syncthreads();  // buffers, sums and the flag are free again
-  if (tid == 0) odd = 0;
-  if (cur == cum + total_blocks(a, z)) walk.next(a);
-  __syncthreads();
+    constexpr int kVecs = D / 4;  // 4-element vectors of a row
+    for (int i = tid; i < t.nr * kVecs; i += kThreads) {
+      const int r = i / kVecs, c = (i % kVecs) * 4;
+      float mw = ml[0][r].m;
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) mw = fmaxf(mw, ml[w][r].m);
+      const float mu = mw == -INFINITY ? 0.0f : mw;
+      f32x4 v = {0, 0, 0, 0};
+      float sum = 0.0f, esum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ml[w][r].m - mu);
+        sum += f * ml[w][r].l;
+        esum += f * ml[w][r].e;
+        v += f * *(const f32x4 *)((const float *)(lds_raw + w * L::kWaveLds) + r * L::kOStride + c);
+      }
+      const int q = t.r0 + r;
+      const int64_t tk = t.t0 + q / a.G, hd = kvh * a.G + q % a.G;
+      if (alone) {
+        const float inv = reciprocal_of(sum);
+        const uint2 w = {pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv)};
+        *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + c) = w;
+        if (a.lse && c == 0) a.lse[tk * a.H + hd] = lse_of(mw, esum);
+      } else {
+        const int64_t at = slot + r;
+        *(f32x4 *)(a.part + at * D + c) = v;
+        if (c == 0) a.stats[at] = AttnStats{mw, sum, esum, 0.0f};
+      }
+    }
+    if (odd) {  // (a barrier lies behind its last write)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "agent");
+      __syncthreads();
+      put_back<D, F16>(a, t, kvh, b0, b1, (int)min(all_lo, (int64_t)INT32_MAX), all_hi, t.r0 + wave, t.r0 + t.nr, kWaves,
+                       [&](int r, int64_t, int64_t) { return alone ? nullptr : a.part + (slot + r - t.r0) * D; });
+    }
+    if (o0 == 0 && o1 < z.blocks) {  // the first of the workgroups that share the segment
+      if (tid == 0) a.rec[wg] = AttnRec{runs.holder(cum + (int64_t)(seg + 1) * z.blocks - 1) - wg + 1, t.t0, t.r0, t.nr, kvh};
+      return;
+    }
+    cur += o1 - o0;
+    if (cur == end) return;
+    __syncthreads();  // buffers, sums and the flag are free again
+    if (tid == 0) odd = 0;
+    if (cur == cum + total_blocks(a, z)) walk.next(a);
+    __syncthreads();
   }
 }
 
@@ -929,13 +929,14 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
     if (a.splits > 1 && half == 0) a.stats[row * a.splits].l = -1.0f;
   } else {
     const int64_t at = row * a.splits + split;
-    if (b0 < b1)
+    if (b0 < b1) {
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
+      for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *(f32x4 *)(a.part + at * D + 32 * d + 8 * i + 4 * half) =
-            f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+        for (int i = 0; i < 4; ++i)
+          *(f32x4 *)(a.part + at * D + 32 * d + 8 * i + 4 * half) =
+              f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+    }
     if (half == 0) a.stats[at] = AttnStats{m == -INFINITY ? m : m * scale, l, es, 0.0f};
   }
   if (!fix) return;

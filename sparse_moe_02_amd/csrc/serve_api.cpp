@@ -378,7 +378,8 @@ moe_status moe_paged_attn(const moe_paged_kv *kv, const moe_batch *batch, int64_
   if ((st = check_batch(batch, kv->page_size)) != MOE_OK) return st;
   if ((st = check_attn_sizes(T, batch->n_seqs, max_q, max_kv, n_heads, *kv)) != MOE_OK) return st;
   if (flags & ~MOE_ATTN_FULL) return MOE_ERR_SHAPE;
-  if (window < 0 || (window > 0 && (flags & MOE_ATTN_FULL)) || !std::isfinite(scale)) return MOE_ERR_SHAPE;
+  const float scale_log2 = scale * 1.44269504088896341f;  // scores are kept as base-2 exponents
+  if (window < 0 || (window > 0 && (flags & MOE_ATTN_FULL)) || !std::isfinite(scale_log2)) return MOE_ERR_SHAPE;
   if (T == 0) return MOE_OK;
   if ((st = check_heads(q)) != MOE_OK || (st = check_heads(out)) != MOE_OK) return st;
   if (!aligned(lse, 4)) return MOE_ERR_ALIGN;
@@ -414,7 +415,7 @@ moe_status moe_paged_attn(const moe_paged_kv *kv, const moe_batch *batch, int64_
   a.rec = reinterpret_cast<AttnRec *>(static_cast<char *>(workspace) + sh.off_rec);
   a.window = window;
   a.full = flags & MOE_ATTN_FULL;
-  a.scale_log2 = scale * 1.44269504088896341f;  // scores are kept as base-2 exponents
+  a.scale_log2 = scale_log2;
   return launch_paged_attn(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

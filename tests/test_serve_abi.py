@@ -124,6 +124,7 @@ def test_bad_attention_arguments(B):
     assert _attn(B, max_q=-1) == SHAPE and _attn(B, max_kv=-1) == SHAPE
     assert _attn(B, window=-1) == SHAPE and _attn(B, window=5, flags=1) == SHAPE and _attn(B, flags=2) == SHAPE
     assert _attn(B, scale=math.nan) == SHAPE and _attn(B, scale=math.inf) == SHAPE
+    assert _attn(B, scale=3e38) == SHAPE and _attn(B, scale=-3e38) == SHAPE  # finite, but not times log2(e)
     assert _attn(B, q=H(None, 1024, 128)) == NULL and _attn(B, out=H(None, 1024, 128)) == NULL
     assert _attn(B, q=H(4 * M + 4, 1024, 128)) == ALIGN and _attn(B, q=H(4 * M, 1028, 128)) == ALIGN
     assert _attn(B, q=H(4 * M, -1024, 128)) == SHAPE
