@@ -2,15 +2,16 @@
 //
 // A call is a plan over the requests (checks, fresh pages needed and their prefix sums), a
 // count of free pages by groups of kPageGroup, and an application in which every workgroup
-// takes its own share: a group's workgroup knows the rank of its first free page from the counts
-// before it, so the page of rank r goes to the request whose prefix sums bracket r, and no list
-// of free pages is ever kept.  Ranks are positions, not arrival order: results are the same on
-// every run, and refs of shared pages change by integer atomics, whose order does not matter.
+// takes its own share: the page of rank r among the free ones goes to the request whose prefix
+// sums bracket r.  A group's workgroup knows the rank of its first free page from the counts before
+// it; where requests look for their pages instead (fork), a group lists its first ones.  Ranks
+// are positions, not arrival order: results are the same on every run, and refs of shared pages
+// change by integer atomics, whose order does not matter.
 //
 // Bound: latency for the tables (two launches of small integer work: 256 sequences growing in a
 // pool of 65536 pages take 9.2 us); memory for the pages copied (16 bytes per lane, kCopyVecs in
 // flight): a compaction that moves some 450 pages of 32 KB in 20 planes takes 121 us for them,
-// 4.9 TB/s, and 32 forks that copy a page each in as many planes 9 of 18 us.
+// 4.9 TB/s, and 32 forks that copy a page each in as many planes 14.4 us for everything.
 #include "paged.hpp"
 
 namespace moe {
@@ -150,14 +151,28 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_plan(PageArgs a) {
   }
   w -= 1;
   if (w < groups) {
-    const int p0 = w * kPageGroup, p1 = min(a.n_pages, p0 + kPageGroup);
-    int n = 0;
-    for (int p = p0 + tid; p < p1; p += kPlanThreads) {
-      const int r = a.in.refs[p];
-      n += r <= 0;
-      if (copy) a.out.refs[p] = r;
+    constexpr int kSteps = kPageGroup / kPlanThreads;
+    const int p0 = w * kPageGroup + tid;
+    int refs[kSteps], n = 0;
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      const int p = p0 + q * kPlanThreads;
+      refs[q] = p < a.n_pages ? a.in.refs[p] : 1;
+      n += refs[q] <= 0;
+      if (copy && p < a.n_pages) a.out.refs[p] = refs[q];
     }
-    n = block_sum<kPlanThreads>(n, sums);
+    if (OP == PageOp::Fork) {  // the group's free pages, in order
+      n = 0;
+#pragma unroll
+      for (int q = 0; q < kSteps; ++q) {
+        int total;
+        const int r = n + block_excl<kPlanThreads>(refs[q] <= 0, sums, total);
+        if (refs[q] <= 0 && r < a.n) a.fresh[w * kPageGroup + r] = p0 + q * kPlanThreads;
+        n += total;
+      }
+    } else {
+      n = block_sum<kPlanThreads>(n, sums);
+    }
     if (tid == 0) a.free_n[w] = n;
     return;
   }
@@ -207,8 +222,8 @@ __device__ __forceinline__ int status(const PageArgs &a, int total_free) {
   return kOk;
 }
 
-// Second launch.  One workgroup per group hands out its free pages (compact: lists its free
-// pages and its pages that move); then one per request applies it.
+// Second launch (Fork has its own).  One workgroup per group hands out its free pages (compact:
+// lists its free pages and its pages that move); then one per request applies it.
 template <PageOp OP>
 __global__ void __launch_bounds__(kThreads) k_pages_apply(PageArgs a) {
   __shared__ int sums[kThreads / 64];
@@ -242,7 +257,6 @@ __global__ void __launch_bounds__(kThreads) k_pages_apply(PageArgs a) {
     if (OP == PageOp::Compact) a.hdr[1] = a.n_pages - total;
     // the group of page `used` writes the number of pages that move, if there are free pages
     if (OP == PageOp::Compact && (st != kOk || total == 0)) a.hdr[2] = 0;
-    if (OP == PageOp::Fork) a.hdr[3] = st;
     if (st != kOk) atomicCAS(a.error, 0, st);
   }
   if (st != kOk) return;
@@ -284,30 +298,17 @@ __global__ void __launch_bounds__(kThreads) k_pages_apply(PageArgs a) {
             len = half;
           }
         }
-        const int s = a.a[lo];
-        if (OP == PageOp::Grow) {
-          a.out.table[(int64_t)s * a.cols + a.col[lo] + (r - a.base[lo])] = p;
-        } else {
-          a.out.table[(int64_t)a.b[lo] * a.cols + (a.in.len[s] >> a.page_shift)] = p;
-          a.fresh[lo] = p;
-        }
+        a.out.table[(int64_t)a.a[lo] * a.cols + a.col[lo] + (r - a.base[lo])] = p;
         a.out.refs[p] = 1;
       }
     }
     return;
   }
-  const int i = w - groups;
-  if (OP == PageOp::Free || OP == PageOp::Fork) {
-    const int s = a.a[i], len = a.in.len[s];
-    const int n = OP == PageOp::Fork ? len >> a.page_shift : pages_of(len, a.page_shift);
-    for (int c = tid; c < n; c += kThreads) {
-      const int p = a.in.table[(int64_t)s * a.cols + c];
-      atomicAdd(&a.out.refs[p], OP == PageOp::Fork ? 1 : -1);
-      if (OP == PageOp::Fork) a.out.table[(int64_t)a.b[i] * a.cols + c] = p;
-    }
-    // nobody else reads this length: a destination is no source, and sequences end once
-    __syncthreads();
-    if (tid == 0) a.out.len[OP == PageOp::Fork ? a.b[i] : s] = OP == PageOp::Fork ? len : 0;
+  if (OP == PageOp::Free) {
+    const int s = a.a[w - groups], n = pages_of(a.in.len[s], a.page_shift);
+    for (int c = tid; c < n; c += kThreads) atomicAdd(&a.out.refs[a.in.table[(int64_t)s * a.cols + c]], -1);
+    __syncthreads();  // nobody else reads this length: sequences end once
+    if (tid == 0) a.out.len[s] = 0;
   }
 }
 
@@ -325,27 +326,70 @@ __device__ __forceinline__ void copy_part(const PageMem &m, int plane, int src, 
     if (at + threadIdx.x * 16 + i * kThreads * 16 < m.bytes) *(u32x4 *)(d + i * kThreads * 16) = v[i];
 }
 
-// Walks this workgroup's share of `pairs` copies in every plane.
+// Walks this workgroup's share of `pairs` copies in every plane; the first `others` workgroups
+// do something else.
 template <class F>
-__device__ __forceinline__ void copy_pages(const PageMem &m, int64_t pairs, F pair) {
+__device__ __forceinline__ void copy_pages(const PageMem &m, int64_t pairs, int others, F pair) {
   const int64_t parts = (m.bytes + kCopyChunk - 1) / kCopyChunk, per = parts * m.n_planes;
-  for (int64_t x = blockIdx.x; x < pairs * per; x += gridDim.x) {
+  for (int64_t x = blockIdx.x - others; x < pairs * per; x += gridDim.x - others) {
     const int64_t i = x / per, y = x % per;
     int src, dst;
     if (pair(i, src, dst)) copy_part(m, (int)(y / parts), src, dst, y % parts * kCopyChunk);
   }
 }
 
-// Fork: last pages that are not full.
-__global__ void __launch_bounds__(kThreads) k_pages_tails(PageArgs a) {
-  if (a.hdr[3] != kOk) return;
-  copy_pages(a.mem, a.n, [&](int64_t i, int &src, int &dst) {
-    if (a.base[i + 1] == a.base[i]) return false;
-    const int s = a.a[i];
-    src = a.in.table[(int64_t)s * a.cols + (a.in.len[s] >> a.page_shift)];
-    dst = a.fresh[i];
-    return true;
-  });
+// The free page of a rank, by a whole wave, from the lists of the groups.
+__device__ __forceinline__ int fresh_page(const PageArgs &a, int rank, int groups) {
+  const int lane = threadIdx.x & 63;
+  for (int g = 0;; g += 64) {
+    const int n = g + lane < groups ? a.free_n[g + lane] : 0, upto = wave_incl_scan(n);
+    const uint64_t behind = __ballot(upto > rank);
+    if (behind || g + 64 >= groups) {
+      const int l = behind ? __builtin_ctzll(behind) : 0;
+      return a.fresh[(int64_t)(g + l) * kPageGroup + rank - __builtin_amdgcn_readlane(upto - n, l)];
+    }
+    rank -= __builtin_amdgcn_readlane(upto, 63);
+  }
+}
+
+// Fork's second launch: one workgroup per request shares its full pages, the others copy last
+// pages that are not full.  Both find a fresh page in the lists of the first launch, so the copies
+// need not wait for a launch of their own (32 forks, 17.5 -> 14.4 us).
+__global__ void __launch_bounds__(kThreads) k_pages_fork(PageArgs a) {
+  __shared__ int sums[kThreads / 64];
+  const int tid = threadIdx.x;
+  const int groups = (a.n_pages + kPageGroup - 1) / kPageGroup;
+  int total;
+  free_before(a, 0, groups, sums, total);
+  const int st = status<PageOp::Fork>(a, total);
+  if (blockIdx.x == 0 && tid == 0 && st != kOk) atomicCAS(a.error, 0, st);
+  if (st != kOk) return;
+  const int i = blockIdx.x;
+  if (i >= a.n) {
+    copy_pages(a.mem, a.n, a.n, [&](int64_t i, int &src, int &dst) {
+      if (a.base[i + 1] == a.base[i]) return false;
+      const int s = a.a[i];
+      src = a.in.table[(int64_t)s * a.cols + (a.in.len[s] >> a.page_shift)];
+      dst = fresh_page(a, a.base[i], groups);
+      return true;
+    });
+    return;
+  }
+  const int s = a.a[i], len = a.in.len[s], n = len >> a.page_shift;
+  const int64_t to = (int64_t)a.b[i] * a.cols;
+  for (int c = tid; c < n; c += kThreads) {
+    const int p = a.in.table[(int64_t)s * a.cols + c];
+    atomicAdd(&a.out.refs[p], 1);
+    a.out.table[to + c] = p;
+  }
+  if (a.base[i + 1] != a.base[i]) {
+    const int p = fresh_page(a, a.base[i], groups);
+    if (tid == 0) {
+      a.out.table[to + n] = p;
+      a.out.refs[p] = 1;
+    }
+  }
+  if (tid == 0) a.out.len[a.b[i]] = len;  // (nobody reads it: a destination is no source)
 }
 
 // Compact: pages, refs and tables follow the lists.
@@ -375,7 +419,7 @@ __global__ void __launch_bounds__(kThreads) k_pages_move(PageArgs a) {
       if (a.moved[n - 1 - lo] == p) a.out.table[s * a.cols + c] = a.fresh[lo];
     }
   }
-  copy_pages(a.mem, n, [&](int64_t i, int &src, int &dst) {
+  copy_pages(a.mem, n, 0, [&](int64_t i, int &src, int &dst) {
     src = a.moved[n - 1 - i];
     dst = a.fresh[i];
     return true;
@@ -383,7 +427,7 @@ __global__ void __launch_bounds__(kThreads) k_pages_move(PageArgs a) {
 }
 
 __global__ void __launch_bounds__(kThreads) k_pages_copy(PageMem m, int n_pages, int n, const int32_t *from, const int32_t *to) {
-  copy_pages(m, n, [&](int64_t i, int &src, int &dst) {
+  copy_pages(m, n, 0, [&](int64_t i, int &src, int &dst) {
     src = from[i];
     dst = to[i];
     return (unsigned)src < (unsigned)n_pages && (unsigned)dst < (unsigned)n_pages;
@@ -403,9 +447,11 @@ hipError_t launch(const PageArgs &a, hipStream_t s) {
   const int rows = a.out.table != a.in.table ? a.n_seqs : 0;
   const int checks = OP == PageOp::Compact ? a.n_seqs : OP == PageOp::Grow ? 0 : a.n;
   hipLaunchKernelGGL(k_pages_plan<OP>, dim3(1 + groups + rows + checks), dim3(kPlanThreads), 0, s, a);
-  const int each = OP == PageOp::Free || OP == PageOp::Fork ? a.n : 0;
-  hipLaunchKernelGGL(k_pages_apply<OP>, dim3(groups + each), dim3(kThreads), 0, s, a);
-  if (OP == PageOp::Fork && a.n > 0) hipLaunchKernelGGL(k_pages_tails, dim3(copy_grid(a.mem, a.n)), dim3(kThreads), 0, s, a);
+  if (OP == PageOp::Fork) {
+    if (a.n > 0) hipLaunchKernelGGL(k_pages_fork, dim3(a.n + copy_grid(a.mem, a.n)), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(k_pages_apply<OP>, dim3(groups + (OP == PageOp::Free ? a.n : 0)), dim3(kThreads), 0, s, a);
   if (OP == PageOp::Compact)
     hipLaunchKernelGGL(k_pages_move, dim3(copy_grid(a.mem, a.n_pages)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
@@ -426,7 +472,7 @@ PageWs page_ws(int n_seqs, int n_pages, int n) {
   w.base = take((size_t)n + 1);
   w.col = take(n);
   w.longer = take(n);
-  w.fresh = take(n > n_pages ? n : n_pages);
+  w.fresh = take(n_pages);
   w.moved = take(n_pages);
   w.total = o;
   return w;

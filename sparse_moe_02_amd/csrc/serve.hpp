@@ -107,13 +107,13 @@ struct PageArgs {
   const int32_t *a, *b;  // grow: sequences, tokens; fork: sources, destinations; free: sequences
   int32_t *error;
   // workspace
-  int32_t *hdr;        // [0] status of the requests, [1] fresh pages needed, [2] pages that move,
-                       // [3] fork: status of the call
+  int32_t *hdr;        // [0] status of the requests, [1] fresh pages needed, [2] pages that move
   int32_t *free_n;     // [groups] free pages of the group
   int32_t *bad;        // [requests, or sequences (compact)] a table entry lies outside the pool
   int32_t *base;       // [n + 1] fresh pages needed before the request
   int32_t *col, *longer;  // [n] grow: pages held before, length after
-  int32_t *fresh;      // [n] fork: the request's fresh page; compact: [n_pages] free page by rank
+  int32_t *fresh;      // fork: [groups][kPageGroup] a group's first free pages; compact: [n_pages] free
+                       // page by rank
   int32_t *moved;      // compact: [n_pages] page that moves, by rank from the pool's end
 };
 struct PageWs {
