@@ -1,7 +1,8 @@
 """Build of the HIP library (libmoe_mi355x.so) with hipcc for gfx950.
 
 Compiles every source under ``csrc/`` in parallel into ``_build/`` and links the
-shared library next to this file.  Always recompiles.
+shared library next to this file, and the wrappers' tensor reader (``tensors.cpp``, host code
+against torch's headers).  Always recompiles.
 """
 
 from __future__ import annotations
@@ -10,6 +11,7 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -18,6 +20,8 @@ LIB = os.path.join(HERE, "libmoe_mi355x.so")
 ROOT_INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 PROBES_SRC = os.path.join(HERE, "probes", "probes.hip")
 PROBES_LIB = os.path.join(HERE, "probes", "libmoe_probes.so")
+TENSORS_SRC = os.path.join(HERE, "tensors.cpp")
+TENSORS_LIB = os.path.join(HERE, "_tensors.so")
 
 ARCH = "gfx950"
 # packed-fp32 instructions are disabled: plain fp32 code only
@@ -58,11 +62,28 @@ def _link(objs, lib):
     return lib
 
 
+def _build_tensors() -> None:
+    import torch
+
+    root, tmp = os.path.dirname(torch.__file__), TENSORS_LIB + ".tmp"
+    r = subprocess.run([hipcc(), "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared", "-D__HIP_PLATFORM_AMD__",
+                        "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include/torch/csrc/api/include"),
+                        "-I", sysconfig.get_paths()["include"], "-I", "/opt/rocm/include", TENSORS_SRC, "-o", tmp,
+                        "-L", os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"hipcc failed for {TENSORS_SRC}:\n{r.stderr}")
+    os.replace(tmp, TENSORS_LIB)
+
+
 def build(jobs: int = 8) -> str:
-    """The layer's library, then the benchmark's probe library (a separate .so)."""
+    """The layer's library, then the benchmark's probe library (a separate .so), and the tensor
+    reader."""
     os.makedirs(BUILD, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
+        reader = ex.submit(_build_tensors)
         objs = list(ex.map(_compile, sources() + [PROBES_SRC]))
+        reader.result()
     _link(objs[:-1], LIB)
     _link(objs[-1:], PROBES_LIB)
     return LIB

@@ -6,7 +6,13 @@ import contextlib
 
 import torch
 
+try:
+    from . import _tensors as N  # noqa: F401
+except ImportError as e:  # built with the library
+    raise ImportError(f"the tensor reader is not built ({e}): run __graft_entry__.build()") from e
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _here = contextlib.nullcontext()
 
 
@@ -17,11 +23,4 @@ def stream(index: int) -> int:
 
 def on(index: int):
     """Context in which the device is the current one."""
-    return _here if torch.cuda.current_device() == index else torch.cuda.device(index)
-
-
-def int32(name: str, t: torch.Tensor, index: int) -> int:
-    """Address of a contiguous int32 tensor on the device."""
-    if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous torch.int32 tensor on cuda:{index} required")
-    return t.data_ptr()
+    return _here if _device() == index else torch.cuda.device(index)

@@ -6,12 +6,10 @@ Calls are enqueued on torch's current stream of the tensors' device and never wa
 
 from __future__ import annotations
 
-import struct
-
 import torch
 
 from . import binding as B
-from ._device import int32, on, stream
+from ._device import N, on, stream
 
 _DTYPES = {torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_FP16}
 _SCALINGS = {"none": B.MOE_ROPE_NONE, "linear": B.MOE_ROPE_LINEAR, "ntk": B.MOE_ROPE_NTK, "yarn": B.MOE_ROPE_YARN}
@@ -24,56 +22,6 @@ def rope_freqs(rot_dim: int, base: float = 1e4, scaling: str = "none", factor: f
         raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
     f, mscale = B.moe_rope_freqs(rot_dim, base, _SCALINGS[scaling], factor, trained)
     return torch.tensor(f, dtype=torch.float64, device=device), mscale
-
-
-# moe_heads, moe_paged_kv and moe_batch as bytes (packing them costs a fraction of building
-# ctypes structures)
-_HEADS = struct.Struct("Pqq").pack
-_KV = struct.Struct("PPqqqiiiiixxxx").pack
-_BATCH = struct.Struct("PPPPiiixxxx").pack
-
-
-def _heads(name, t, T, heads, D, dtype, index):
-    if t.dtype is not dtype or t.get_device() != index or t.shape != (T, heads, D):
-        raise ValueError(f"{name}: {dtype} [{T}][{heads}][{D}] on cuda:{index} required")
-    s = t.stride()
-    if s[2] != 1:
-        raise ValueError(f"{name}: contiguous last dimension required")
-    # strides of dimensions of one element say nothing
-    return _HEADS(t.data_ptr(), s[0] if T > 1 else 0, s[1] if heads > 1 else 0)
-
-
-def _cache(k, v, index):
-    """(moe_paged_kv, page size, KV heads, head width)"""
-    dtype, shape = k.dtype, k.shape
-    if dtype not in _DTYPES or k.get_device() != index or index < 0 or len(shape) != 4:
-        raise ValueError("k_cache: bfloat16 or float16 [n_pages][page_size][n_kv_heads][head_dim] on q's GPU required")
-    if v.dtype is not dtype or v.get_device() != index or v.shape != shape:
-        raise ValueError("v_cache must have k_cache's type, device and shape")
-    n_pages, page, heads, D = shape
-    s = k.stride()
-    if s != v.stride() or s[3] != 1:
-        raise ValueError("k_cache and v_cache must have the same strides and a contiguous last dimension")
-    kv = _KV(k.data_ptr(), v.data_ptr(), s[0] if n_pages > 1 else 0, s[1] if page > 1 else 0, s[2] if heads > 1 else 0,
-             n_pages, page, heads, D, _DTYPES[dtype])
-    return kv, heads, D
-
-
-def _batch(table, q_start, kv_len, row, index):
-    """(moe_batch, sequences)"""
-    if table.dim() != 2 or q_start.dim() != 1 or kv_len.dim() != 1:
-        raise ValueError("table: [n_rows][cols], q_start: [n_seqs + 1] and kv_len: [n_rows] required")
-    n = q_start.shape[0] - 1
-    rows, cols = table.shape
-    if kv_len.shape[0] != rows:
-        raise ValueError("kv_len must have one entry for each row of table")
-    r = None
-    if row is not None:
-        r = int32("row", row, index)
-        if row.shape != (n,):
-            raise ValueError("row: int32 [n_seqs] required")
-    return _BATCH(int32("q_start", q_start, index), int32("kv_len", kv_len, index), int32("table", table, index), r or 0, n,
-                  rows, cols), n
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -90,29 +38,19 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torc
     token's position); inv_freq: float64 [rot / 2] of ``rope_freqs`` (None: no rotation).  Returns
     q_out (may be q itself; by default a new tensor like q).  Tokens behind q_start[-1] are padding: their
     rows of q_out are left as they were (of a new tensor: unset)."""
-    index, dtype = q.get_device(), k_cache.dtype
-    kv, n_kv, D = _cache(k_cache, v_cache, index)
-    b, _ = _batch(table, q_start, kv_len, row, index)
-    if q.dim() != 3:
-        raise ValueError("q: [T][n_heads][head_dim] required")
-    T, H, _ = q.shape
+    index = q.get_device()
+    kv, n_kv, D, dtype = N.cache(k_cache, v_cache, index)
+    b, _ = N.batch(table, q_start, kv_len, row, index)
     if q_out is None:
         q_out = torch.empty_like(q)
-    hq = _heads("q", q, T, H, D, dtype, index)
-    ho = hq if q_out is q else _heads("q_out", q_out, T, H, D, dtype, index)
-    hk = _heads("k", k, T, n_kv, D, dtype, index)
-    hv = _heads("v", v, T, n_kv, D, dtype, index)
+    hq, T, H = N.heads("q", q, -1, -1, D, dtype, index)
+    ho = hq if q_out is q else N.heads("q_out", q_out, T, H, D, dtype, index)[0]
+    hk = N.heads("k", k, T, n_kv, D, dtype, index)[0]
+    hv = N.heads("v", v, T, n_kv, D, dtype, index)[0]
     fp, rot = None, 0
     if inv_freq is not None:
-        if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != index or inv_freq.dim() != 1 or \
-                not inv_freq.is_contiguous():
-            raise ValueError(f"inv_freq: contiguous float64 vector on cuda:{index} required")
-        fp, rot = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
-    pp = None
-    if pos is not None:
-        pp = int32("pos", pos, index)
-        if pos.shape != (T,):
-            raise ValueError("pos: int32 [T] required")
+        fp, rot = N.address("inv_freq", inv_freq, N.FP64, index, -1), 2 * inv_freq.shape[0]
+    pp = None if pos is None else N.address("pos", pos, N.INT32, index, T)
     if T:
         with on(index):
             st = (B._lib or B.lib()).moe_rope_append(kv, b, T, hq, ho, H, hk, hv, pp, fp, rot, mscale,
@@ -134,30 +72,23 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, ta
     ``paged_attn_workspace`` bytes (by default one is allocated for the call).  Returns out, or
     (out, lse) with lse float32 [T][n_heads] where lse is given or return_lse is set.  Rows of
     padding tokens behind q_start[-1] are left as they were (of a new tensor: unset)."""
-    index, dtype = q.get_device(), k_cache.dtype
-    kv, n_kv, D = _cache(k_cache, v_cache, index)
-    b, n_seqs = _batch(table, q_start, kv_len, row, index)
-    if q.dim() != 3:
-        raise ValueError("q: [T][n_heads][head_dim] required")
-    T, H, _ = q.shape
+    index = q.get_device()
+    kv, _, D, dtype = N.cache(k_cache, v_cache, index)
+    b, n_seqs = N.batch(table, q_start, kv_len, row, index)
+    hq, T, H = N.heads("q", q, -1, -1, D, dtype, index)
     if out is None:
         out = torch.empty_like(q)
     if lse is None and return_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    hq = _heads("q", q, T, H, D, dtype, index)
-    ho = _heads("out", out, T, H, D, dtype, index)
-    lp = None
-    if lse is not None:
-        if lse.dtype is not torch.float32 or lse.get_device() != index or lse.shape != (T, H) or not lse.is_contiguous():
-            raise ValueError(f"lse: contiguous float32 [{T}][{H}] on cuda:{index} required")
-        lp = lse.data_ptr()
+    ho = N.heads("out", out, T, H, D, dtype, index)[0]
+    lp = None if lse is None else N.address("lse", lse, N.FP32, index, T, H)
     if workspace is None:
         n = B.moe_paged_attn_workspace(kv, T, n_seqs, max_q, max_kv, H, window)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    elif workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"workspace: contiguous uint8 tensor on cuda:{index} required")
-    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    wp, wn = None, 0
+    if workspace is not None:
+        wp, wn = N.address("workspace", workspace, N.UINT8, index), workspace.numel()
     if T:
         with on(index):
             st = (B._lib or B.lib()).moe_paged_attn(kv, b, T, max_q, max_kv, hq, H, ho, lp,

@@ -6,7 +6,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from ._device import on, stream
+from ._device import N, on, stream
 
 D = 128
 
@@ -50,20 +50,16 @@ def gdn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Ten
         raise ValueError("q, k, v must be [R][heads][128] and state [n_slots][n_vheads][128][128]")
     R, hk, dk = k.shape
     _, hv, dv = v.shape
-    index = v.get_device()
+    index, n_slots = v.get_device(), state.shape[0]
     if out is None:
         out = torch.empty_like(v)
-    bf16, f32 = torch.bfloat16, torch.float32
-    for name, t, dt in (("q", q, bf16), ("k", k, bf16), ("v", v, bf16), ("alpha", alpha, f32), ("beta", beta, f32),
-                        ("state", state, f32), ("slot", slot, torch.int32), ("out", out, bf16)):
-        if t.dtype is not dt or index < 0 or t.get_device() != index or not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous {dt} tensor on v's GPU required")
-    gates = (R, hv)
-    if q.shape != k.shape or v.shape[0] != R or alpha.shape != gates or beta.shape != gates or slot.shape != (R,):
-        raise ValueError("shape mismatch")
-    if state.shape[1:] != (hv, dv, dk) or out.shape != v.shape:
-        raise ValueError("state must be [n_slots][n_vheads][d_v][d_k], out as v")
+    at, bf16, f32 = N.address, N.BF16, N.FP32
+    args = (at("q", q, bf16, index, R, hk, dk), at("k", k, bf16, index, R, hk, dk), at("v", v, bf16, index, R, hv, dv),
+            at("alpha", alpha, f32, index, R, hv), at("beta", beta, f32, index, R, hv),
+            at("state", state, f32, index, n_slots, hv, dv, dk), n_slots, at("slot", slot, N.INT32, index, R),
+            at("out", out, bf16, index, R, hv, dv))
     with on(index):
-        B.moe_gdn_step(R, hk, hv, dk, dv, q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), beta.data_ptr(),
-                       state.data_ptr(), state.shape[0], slot.data_ptr(), out.data_ptr(), stream(index))
+        st = (B._lib or B.lib()).moe_gdn_step(R, hk, hv, dk, dv, *args, stream(index))
+    if st:
+        raise B.MoeError("moe_gdn_step", st)
     return out

@@ -7,35 +7,10 @@ Calls are enqueued on torch's current stream of the pool's device and never wait
 
 from __future__ import annotations
 
-import struct
-
 import torch
 
 from . import binding as B
-from ._device import int32, on, stream
-
-_MEMORY = struct.Struct("Pqqqixxxx").pack  # moe_page_memory as bytes
-
-
-def _ints(name, t, index, n=None):
-    p = int32(name, t, index)
-    if t.dim() != 1 or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name}: a vector{'' if n is None else f' of {n} entries'} required")
-    return p
-
-
-def _memory(cache, n_pages, index):
-    """cache: [n_planes][n_pages][...], each page one contiguous block."""
-    shape, s, size = cache.shape, cache.stride(), cache.element_size()
-    if cache.get_device() != index or index < 0 or len(shape) < 3 or shape[1] != n_pages or shape[0] < 1:
-        raise ValueError(f"cache: [n_planes][{n_pages}][...] on the pool's GPU required")
-    page = 1
-    for n, st in zip(reversed(shape[2:]), reversed(s[2:])):
-        if n != 1 and st != page:
-            raise ValueError("cache: each page must be contiguous")
-        page *= n
-    return _MEMORY(cache.data_ptr(), s[0] * size if shape[0] > 1 else 0, s[1] * size if n_pages > 1 else 0, page * size,
-                   shape[0])
+from ._device import N, on, stream
 
 
 class PagePool:
@@ -86,7 +61,8 @@ class PagePool:
     def grow(self, seqs: torch.Tensor, tokens: torch.Tensor, out: "PagePool | None" = None) -> "PagePool":
         """Sequences seqs (int32, distinct) grow by tokens (int32) each."""
         out, n = self._out(out), seqs.shape[0]
-        s, t = _ints("seqs", seqs, self._index), _ints("tokens", tokens, self._index, n)
+        s = N.address("seqs", seqs, N.INT32, self._index, n)
+        t = N.address("tokens", tokens, N.INT32, self._index, n)
         with on(self._index):
             B.moe_pages_grow(self._c, out._c, n, s, t, *self._tail(out))
         return out
@@ -96,8 +72,9 @@ class PagePool:
         """Empty sequences dst (int32, distinct) become copies of src (int32): full pages are
         shared, a last page that is not full is copied.  cache: [n_planes][n_pages][...]."""
         out, n = self._out(out), src.shape[0]
-        s, d = _ints("src", src, self._index), _ints("dst", dst, self._index, n)
-        m = _memory(cache, self.n_pages, self._index)
+        s = N.address("src", src, N.INT32, self._index, n)
+        d = N.address("dst", dst, N.INT32, self._index, n)
+        m = N.memory(cache, self.n_pages, self._index)
         with on(self._index):
             B.moe_pages_fork(self._c, out._c, m, n, s, d, *self._tail(out))
         return out
@@ -105,7 +82,7 @@ class PagePool:
     def free(self, seqs: torch.Tensor, out: "PagePool | None" = None) -> "PagePool":
         """Sequences seqs (int32, distinct) end."""
         out, n = self._out(out), seqs.shape[0]
-        s = _ints("seqs", seqs, self._index)
+        s = N.address("seqs", seqs, N.INT32, self._index, n)
         with on(self._index):
             B.moe_pages_free(self._c, out._c, n, s, *self._tail(out))
         return out
@@ -113,7 +90,7 @@ class PagePool:
     def compact(self, cache: torch.Tensor, out: "PagePool | None" = None) -> "PagePool":
         """The pages in use move to the lowest numbers.  cache: [n_planes][n_pages][...]."""
         out = self._out(out)
-        m = _memory(cache, self.n_pages, self._index)
+        m = N.memory(cache, self.n_pages, self._index)
         with on(self._index):
             B.moe_pages_compact(self._c, out._c, m, *self._tail(out))
         return out
@@ -134,7 +111,7 @@ def copy_pages(cache: torch.Tensor, src: torch.Tensor, dst: torch.Tensor) -> Non
     index, n = cache.get_device(), src.shape[0]
     if index < 0:
         raise ValueError("cache: a GPU tensor required")
-    s, d = _ints("src", src, index), _ints("dst", dst, index, n)
-    m = _memory(cache, cache.shape[1], index)
+    s, d = N.address("src", src, N.INT32, index, n), N.address("dst", dst, N.INT32, index, n)
+    m = N.memory(cache, cache.shape[1], index)
     with on(index):
         B.moe_pages_copy(m, cache.shape[1], n, s, d, stream(index))
