@@ -2,7 +2,9 @@
 
 The layer runs in hand-written HIP kernels behind the C ABI of ``include/moe.h``;
 ``binding`` marshals arguments to it and ``layer.MoeLayer`` keeps one layer's device
-tensors, plan and workspace.  Importing this package does not load the library;
+tensors, plan and workspace.  ``gdn`` has the Gated DeltaNet scan and its single-token step,
+``attn`` rotary positions with the append to a paged cache and attention over it, ``pages``
+the cache's bookkeeping.  Importing this package does not load the library;
 the first call does, and fails loudly if it has not been built.
 """
 
