@@ -17,7 +17,7 @@
 //                32K, 16/2 heads of 256: 1.85 ms, 1.11 PFLOP/s (a large library product reaches
 //                1.22), the clock held down by power; 24 chunks of 0 to 509 tokens, window 1024,
 //                32/8 heads of 128: 0.14 ms, 0.57 PFLOP/s (starts, and a second round of tiles).
-//                One token at 4K: 13.7 us, a chain of dependent loads and a second launch.
+//                One token at 4K: 13.4 us, a chain of dependent loads and a second launch.
 //   k_attn_rows  16 rows, four waves sharing the keys out (v_mfma_f32_16x16x32); the keys of all
 //                sequences cut into equal runs, joined by k_attn_join_runs.  For few rows over
 //                many long sequences.  Bound: memory.  One token of 64 sequences up to 16K:
@@ -41,6 +41,7 @@ typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kMaxSplits = 256;
 constexpr int kTileSlots = 512;  // workgroups of k_attn_tile that splits aim at: two a compute unit
+constexpr int kWhole = 7;        // blocks that are worth no second launch
 constexpr int kMaxRuns = 1024;  // workgroups of k_attn_rows at most
 // workgroups of k_attn_rows that fill the chip (registers allow 1, 2 or 3 on a compute unit)
 constexpr int runs_of(int dim) { return dim == 256 ? 256 : dim == 128 ? 512 : 768; }
@@ -1188,7 +1189,7 @@ AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int w
   // chunk kernel, its keys split: several workgroups on a compute unit hide each other's starts.
   // Measured on decodes of heads of 256 / 128 / 64, us with runs and with splits: 64 sequences up
   // to 16K 174 and 203; 64 up to 4K 104 and 142; 32 up to 8K 60 and 97; but one at 4K 16.1 and
-  // 13.7, 16 up to 8K 39 and 32, 64 up to 1200 37 and 25, 200 up to 300 46 and 21.  More than
+  // 13.4, 16 up to 8K 39 and 32, 64 up to 1200 37 and 25, 200 up to 300 46 and 21.  More than
   // 16 rows a sequence: 16 sequences of 4 tokens and 8 heads at 8K 43 and 32.
   const bool runs = max_q * G <= kAttnRows && (int64_t)n_seqs * n_kv >= 48 && max_kv >= 16 * (int64_t)dim;
   s.rows = runs ? kAttnRows : kAttnTile;
@@ -1214,7 +1215,11 @@ AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int w
   if (window > 0 && max_kv > window + max_q) max_kv = window + max_q;
   const int64_t blocks = (max_kv + kAttnKeys - 1) / kAttnKeys + 1;
   int64_t per = (blocks + (want < 1 ? 1 : want) - 1) / (want < 1 ? 1 : want);  // blocks of a split
-  if (per < kWaves) per = kWaves;
+  // Two blocks at least: one token at 4096 keys, 2 heads of 256, 13.4 us, 15.1 with one block, 14.1
+  // with four (at 500 keys 11.5, 10.9 and 13.6).  Few blocks are not split at all: 8 heads of
+  // 128, 160 keys 8.9 us, 11.4 split; but 250 keys of 2 heads of 256 15.5 and 11.5.
+  if (per < 2) per = 2;
+  if (blocks <= kWhole) per = blocks;
   if (per * kMaxSplits < blocks) per = (blocks + kMaxSplits - 1) / kMaxSplits;
   s.splits = T * H > 1 << 22 ? 1 : (int)((blocks + per - 1) / per);
   s.split_blocks = (int)per;
