@@ -15,7 +15,7 @@
 //                their keys are split over workgroups, joined by k_attn_join(_few).
 //                Bound: matrix units (4 flops per row, visible key and element).  4096 tokens at
 //                32K, 16/2 heads of 256: 1.85 ms, 1.11 PFLOP/s (a large library product reaches
-//                1.22), the clock held down by power; 24 chunks of 0 to 509 tokens, window 1024,
+//                1.22; the same over zeros 1.35 ms: power); 24 chunks of 0 to 509 tokens, window 1024,
 //                32/8 heads of 128: 0.14 ms, 0.57 PFLOP/s (starts, and a second round of tiles).
 //                One token at 4K: 13.4 us, a chain of dependent loads and a second launch.
 //   k_attn_rows  16 rows, four waves sharing the keys out (v_mfma_f32_16x16x32); the keys of all
@@ -741,8 +741,8 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   const int pmask = (1 << a.kv.page_shift) - 1;
   // the rows that this wave loads lie in one 16-key half of a block
   const int my_r0 = wave * kInstr * kRowsPer;
-  // A block's pages, one a half: read as they are one block before they are needed, so that
-  // nobody waits for the scalar loads
+  // A block's pages, one a half: read as they are one block before they are needed, ahead of the
+  // block's barrier, so that nobody waits for the scalar loads (which share a counter with LDS reads)
   auto peek = [&](int key) { return trow[min(key >> a.kv.page_shift, a.b.cols - 1)]; };
   auto checked = [&](int key, int page) {  // -1: no page
     return key >> a.kv.page_shift < a.b.cols && (unsigned)page < (unsigned)a.kv.n_pages ? page : -1;
@@ -784,6 +784,9 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
     const int key0 = blk * kAttnKeys;
     const uint32_t kbuf = lds0 + stage * 2 * kBuf, vbuf = kbuf + kBuf;
     const int pg = upper ? this1 : this0;
+    const int then0 = checked(key0 + 96, ahead0), then1 = checked(key0 + 112, ahead1);
+    ahead0 = peek(key0 + 128), ahead1 = peek(key0 + 144);
+    __builtin_amdgcn_sched_barrier(0);
     if (kStages > 2 && blk + 1 < b1) wait_vm<2 * kInstr>(); else wait_vm<0>();
     // where some key is hidden from some row, its weight there is 0 and its value must be
     // finite: absent keys' values (behind the end, in a bad page) become zeros, and so do
@@ -807,8 +810,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
            stage == 0 ? kStages - 1 : stage - 1);
     this0 = next0, this1 = next1;
     next0 = last0, next1 = last1;
-    last0 = checked(key0 + 96, ahead0), last1 = checked(key0 + 112, ahead1);
-    ahead0 = peek(key0 + 128), ahead1 = peek(key0 + 144);
+    last0 = then0, last1 = then1;
     stage = stage + 1 == kStages ? 0 : stage + 1;
     if (key0 >= any_hi || key0 + kAttnKeys <= any_lo) continue;
 
