@@ -677,6 +677,26 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+// N instructions of 64 chunks of 16 bytes from base on, to consecutive places of LDS.
+template <int N>
+__device__ __forceinline__ void dma_rows(const void *base, const uint32_t (&voff)[N], uint32_t lds) {
+  const void *b = uniform_ptr(base);
+  const uint32_t at = __builtin_amdgcn_readfirstlane(lds);
+#define MOE_NEXT "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+  if constexpr (N == 1)
+    dma16(base, voff[0], lds);
+  else if constexpr (N == 2)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %3\n\t" MOE_NEXT
+                 "global_load_lds_dwordx4 %2, %3\n" ::"s"(at), "v"(voff[0]), "v"(voff[1]), "s"(b)
+                 : "memory", "m0", "scc");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %5\n\t" MOE_NEXT
+                 "global_load_lds_dwordx4 %2, %5\n\t" MOE_NEXT "global_load_lds_dwordx4 %3, %5\n\t" MOE_NEXT
+                 "global_load_lds_dwordx4 %4, %5\n" ::"s"(at), "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3]), "s"(b)
+                 : "memory", "m0", "scc");
+#undef MOE_NEXT
+}
+
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
@@ -698,13 +718,13 @@ enum class First { Matrix, Softmax, None };
 // 32 rows a wave, NW waves.  A workgroup's waves pass one barrier a block: behind it the block is
 // there for all, and the buffer of the block before it is free for the loads of the next.
 template <int D, bool F16, int NW>
-__global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
+__global__ void __launch_bounds__(64 * NW, D == 256 ? 2 : D == 128 ? 3 : 4) k_attn_tile(AttnArgs a) {
   constexpr int kBuf = kAttnKeys * D * 2;      // one K or V block, bytes
   constexpr int kStages = stages(D);
   constexpr First kFirst = D == 256 ? First::Matrix : D == 64 ? First::Softmax : First::None;
   constexpr int kInstr = kBuf / 1024 / NW;     // load instructions a wave issues for one block
   constexpr int kRowsPer = 512 / D;            // LDS rows of one instruction
-  static_assert(kInstr >= 1, "every wave loads");
+  static_assert(kInstr == 1 || kInstr == 2 || kInstr == 4, "as dma_rows has them");
   extern __shared__ __align__(16) uint8_t lds_raw[];
   Tile t;
   // the key/value heads of one tile next to each other: 4096 tokens at 16K, 8 such heads of 128,
@@ -762,31 +782,35 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
   const int blk0 = t.lo / kAttnKeys, nblk = (t.hi + kAttnKeys - 1) / kAttnKeys - blk0;
   const int b0 = blk0 + min(nblk, split * a.split_blocks), b1 = blk0 + (split + 1 == a.splits ? nblk : min(nblk, (split + 1) * a.split_blocks));
 
-  const TableRow trow = table_row(a, t.row);
-  const int pmask = (1 << a.kv.page_shift) - 1;
   // the rows that this wave loads lie in one 16-key half of a block
-  const int my_r0 = wave * kInstr * kRowsPer;
-  // A block's pages, one a half: read as they are one block before they are needed, ahead of the
-  // block's barrier, so that nobody waits for the scalar loads (which share a counter with LDS reads)
-  auto peek = [&](int key) { return trow[min(key >> a.kv.page_shift, a.b.cols - 1)]; };
-  auto checked = [&](int key, int page) {  // -1: no page
-    return key >> a.kv.page_shift < a.b.cols && (unsigned)page < (unsigned)a.kv.n_pages ? page : -1;
+  const int my_r0 = wave * kInstr * kRowsPer, upper = my_r0 >> 4;
+  // Pages are looked up 64 halves at a time, one a lane, and a block's read from the lanes (numbers
+  // fetched and checked block by block take twice the scalar instructions: 4096 tokens at 32K 1898 us,
+  // 1849 this way; one token at 500 11.6 and 11.2).
+  constexpr int kPageStep = 16;  // blocks after which the next 64 halves are taken, which half overlap
+  const int32_t *table = a.b.table + (int64_t)max(t.row, 0) * a.b.cols;
+  auto pages_from = [&](int blk) {  // lane i: page of half i of the blocks from blk on, or -1
+    const int col = (blk * kAttnKeys + lane * 16) >> a.kv.page_shift;
+    const int page = table[min(col, a.b.cols - 1)];
+    return col < a.b.cols && (unsigned)page < (unsigned)a.kv.n_pages ? page : -1;
   };
-  auto page_of = [&](int key) { return checked(key, peek(key)); };
   uint32_t voff[kInstr];
 #pragma unroll
   for (int i = 0; i < kInstr; ++i) {
     const int r = my_r0 + i * kRowsPer + lane / (D / 8);
     voff[i] = (uint32_t)(((r & 15) * (int)a.kv.ts + (((lane % (D / 8)) ^ swz<D>(r)) * 8)) * 2);
   }
+  const char *kbase = (const char *)uniform_ptr(a.kv.k + (int64_t)kvh * a.kv.hs);
+  const uint64_t page_bytes = 2 * a.kv.ps;
+  const uint32_t row_bytes = 2 * (uint32_t)a.kv.ts;
+  const int64_t to_v = (const char *)a.kv.v - (const char *)a.kv.k;
+  const uint32_t in_page = ((1u << a.kv.page_shift) - 1) & ~15u;
   auto load = [&](int blk, int page, int stage) {
-    const int64_t o = (int64_t)max(page, 0) * a.kv.ps + (int64_t)((blk * kAttnKeys + (my_r0 & 16)) & pmask) * a.kv.ts +
-                      (int64_t)kvh * a.kv.hs;
+    const uint32_t row = ((uint32_t)blk * kAttnKeys + upper * 16) & in_page;
+    const char *k = kbase + ((uint32_t)page * page_bytes + row * row_bytes);
     const uint32_t at = lds0 + stage * 2 * kBuf + wave * kInstr * 1024;
-#pragma unroll
-    for (int i = 0; i < kInstr; ++i) dma16(a.kv.k + o, voff[i], at + i * 1024);
-#pragma unroll
-    for (int i = 0; i < kInstr; ++i) dma16(a.kv.v + o, voff[i], at + kBuf + i * 1024);
+    dma_rows<kInstr>(k, voff, at);
+    dma_rows<kInstr>(k + to_v, voff, at + kBuf);
   };
 
   f32x16 acc[D / 32];
@@ -796,46 +820,41 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
   float m = -INFINITY, l = 0.0f, es = 0.0f;  // m: of the unscaled products
 
-  // pages of the block in use and the ones in flight, checked; and of the one after them
-  const bool upper = my_r0 & 16;
-  const int k0 = b0 * kAttnKeys;
-  int this0 = page_of(k0), this1 = page_of(k0 + 16), next0 = page_of(k0 + 32), next1 = page_of(k0 + 48);
-  int last0 = page_of(k0 + 64), last1 = page_of(k0 + 80);
-  if (b0 < b1) load(b0, upper ? this1 : this0, 0);
-  if (kStages > 2 && b0 + 1 < b1) load(b0 + 1, upper ? next1 : next0, 1);
-  int ahead0 = peek(k0 + 96), ahead1 = peek(k0 + 112);
+  int pages = pages_from(b0), more = b0 + kPageStep < b1 ? pages_from(b0 + kPageStep) : -1, from = b0;
+  uint64_t absent = __ballot(pages < 0);
+  auto page_of = [&](int blk) { return __builtin_amdgcn_readlane(pages, 2 * (blk - from) + upper); };
+  pages = max(pages, 0);
+  if (b0 < b1) load(b0, page_of(b0), 0);
+  if (kStages > 2 && b0 + 1 < b1) load(b0 + 1, page_of(b0 + 1), 1);
   int stage = 0;
   for (int blk = b0; blk < b1; ++blk) {
     const int key0 = blk * kAttnKeys;
     const uint32_t kbuf = lds0 + stage * 2 * kBuf, vbuf = kbuf + kBuf;
-    const int pg = upper ? this1 : this0;
-    const int then0 = checked(key0 + 96, ahead0), then1 = checked(key0 + 112, ahead1);
-    ahead0 = peek(key0 + 128), ahead1 = peek(key0 + 144);
-    __builtin_amdgcn_sched_barrier(0);
     if (kStages > 2 && blk + 1 < b1) wait_vm<2 * kInstr>(); else wait_vm<0>();
+    if (blk - from == kPageStep) {
+      from = blk;
+      absent = __ballot(more < 0);
+      pages = max(more, 0);
+      if (from + kPageStep < b1) more = pages_from(from + kPageStep);
+    }
+    const uint32_t gone = (uint32_t)(absent >> (2 * (blk - from))) & 3;  // halves in bad pages
+    const bool mine_gone = gone >> upper & 1;
     // where some key is hidden from some row, its weight there is 0 and its value must be
     // finite: absent keys' values (behind the end, in a bad page) become zeros, and so do
     // infinities and NaN, which are put back at the end where they are seen
-    if (pg < 0 || key0 + kAttnKeys > all_hi_t || key0 < all_lo_t) {
+    if (mine_gone || key0 + kAttnKeys > all_hi_t || key0 < all_lo_t) {
 #pragma unroll
       for (int i = 0; i < kInstr; ++i) {
         const int r = my_r0 + i * kRowsPer + lane / (D / 8);
         auto *w = (__attribute__((address_space(3))) u32x4 *)(uintptr_t)(vbuf + (wave * kInstr + i) * 1024 + lane * 16);
         u32x4 v = *w;
-        if (make_finite<F16>(v, pg < 0 || key0 + r >= t.len)) odd = 1;
+        if (make_finite<F16>(v, mine_gone || key0 + r >= t.len)) odd = 1;
         *w = v;
       }
     }
     wait_lds();
     lds_barrier();
-    const int have0 = this0 < 0 ? 0 : max(0, min(16, t.len - key0));
-    const int have1 = this1 < 0 ? 0 : max(0, min(16, t.len - key0 - 16));
-    if (blk + kStages - 1 < b1)
-      load(blk + kStages - 1, kStages > 2 ? (upper ? last1 : last0) : (upper ? next1 : next0),
-           stage == 0 ? kStages - 1 : stage - 1);
-    this0 = next0, this1 = next1;
-    next0 = last0, next1 = last1;
-    last0 = then0, last1 = then1;
+    if (blk + kStages - 1 < b1) load(blk + kStages - 1, page_of(blk + kStages - 1), stage == 0 ? kStages - 1 : stage - 1);
     stage = stage + 1 == kStages ? 0 : stage + 1;
     if (key0 >= any_hi || key0 + kAttnKeys <= any_lo) continue;
 
@@ -880,9 +899,9 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attn_tile(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < kAheadV; ++i) vf[i] = read_v(i);
     __builtin_amdgcn_sched_barrier(0);
-    bool whole = key0 + kAttnKeys <= all_hi && key0 >= all_lo;
-    whole = whole && have0 + have1 == kAttnKeys;
-    if (!whole) {
+    if (key0 + kAttnKeys > all_hi || key0 < all_lo || gone) {
+      const int have0 = gone & 1 ? 0 : max(0, min(16, t.len - key0));
+      const int have1 = gone & 2 ? 0 : max(0, min(16, t.len - key0 - 16));
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int k = 8 * (i / 4) + 4 * half + i % 4, key = key0 + k;
