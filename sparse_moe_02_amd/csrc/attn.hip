@@ -17,7 +17,7 @@
 //                32K, 16/2 heads of 256: 1.85 ms, 1.11 PFLOP/s (a large library product reaches
 //                1.22; the same over zeros 1.35 ms: power); 24 chunks of 0 to 509 tokens, window 1024,
 //                32/8 heads of 128: 0.14 ms, 0.57 PFLOP/s (starts, and a second round of tiles).
-//                One token at 4K: 13.4 us, a chain of dependent loads and a second launch.
+//                One token at 4K: 12.1 us, a chain of dependent loads and a second launch.
 //   k_attn_rows  16 rows, four waves sharing the keys out (v_mfma_f32_16x16x32); the keys of all
 //                sequences cut into equal runs, joined by k_attn_join_runs.  For few rows over
 //                many long sequences.  Bound: memory.  One token of 64 sequences up to 16K:
@@ -205,7 +205,7 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &a, int x, int rows, Ti
     // Every sequence in a lane, so that a tile's is not read once more (a step in the chain of
     // loads), and the longer ones first, so that short tiles fill the last round: 30 chunks of up
     // to 300 tokens at up to 5000, 32/8 heads of 128, 274 us (328 in the order they come); one token
-    // of 16 sequences at 500 12.4 (13.0).  One sequence has nothing of either: 13.4 us (13.8 here).
+    // of 16 sequences at 500 12.4 (13.0).  One sequence has nothing of either: 0.4 us more here.
     const int lane = threadIdx.x & 63;
     const Seq mine = read_seq(a, min(lane, b.n_seqs - 1));
     const int tiles = lane < b.n_seqs ? (int)(((int64_t)mine.n * a.G + rows - 1) / rows) : 0;
@@ -998,10 +998,14 @@ __global__ void __launch_bounds__(64 * NW, D == 256 ? 2 : D == 128 ? 3 : 4) k_at
 // Join the splits' partial results: one workgroup per (token, head).  Every wave holds the
 // splits' weights, split s in lane s % 64; D / 4 threads take the splits of their group in
 // turn, four loads in flight, and the groups' sums are added in LDS.  Splits without keys have
-// weight 0 and their outputs are not read (they are not written either).
-template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) k_attn_join(AttnArgs a) {
-  constexpr int kVecs = D / 4, kGroups = kThreads / kVecs, kRegs = kMaxSplits / 64;
+// weight 0 and their outputs are not read (they are not written either).  NT threads: 256 where
+// their loads of one round reach all splits, 512 for more of them (one token at 4096 keys, 65
+// splits, 12.1 us, 13.1 with 256; 16 sequences at 500, 9 splits, 12.0 with 256, 12.3 with 512).
+constexpr int kJoinLoads = 4;
+constexpr int one_round(int dim) { return kJoinLoads * kThreads / (dim / 4); }
+template <int D, bool F16, int NT>
+__global__ void __launch_bounds__(NT) k_attn_join(AttnArgs a) {
+  constexpr int kVecs = D / 4, kGroups = NT / kVecs, kRegs = kMaxSplits / 64;
   __shared__ f32x4 sums[kGroups][kVecs];
   __shared__ float weight[kMaxSplits];
   const int64_t r = blockIdx.x;
@@ -1033,18 +1037,18 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(AttnArgs a) {
   const int c = tid % kVecs, g = tid / kVecs;
   const f32x4 *p = (const f32x4 *)(a.part + r * a.splits * D) + c;
   f32x4 v = {0, 0, 0, 0};
-  for (int s0 = g; s0 < a.splits; s0 += 4 * kGroups) {
-    f32x4 x[4];
-    float w[4];
+  for (int s0 = g; s0 < a.splits; s0 += kJoinLoads * kGroups) {
+    f32x4 x[kJoinLoads];
+    float w[kJoinLoads];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kJoinLoads; ++i) {
       const int s = s0 + i * kGroups;
       w[i] = s < a.splits ? weight[s] : 0.0f;
       x[i] = f32x4{0, 0, 0, 0};
       if (w[i] != 0.0f) x[i] = p[(int64_t)s * kVecs];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v += w[i] * x[i];
+    for (int i = 0; i < kJoinLoads; ++i) v += w[i] * x[i];
   }
   sums[g][c] = v;
   __syncthreads();
@@ -1219,8 +1223,10 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     const hipError_t e = allow_lds(k_attn_tile<D, F16, nw>, lds, done);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((k_attn_tile<D, F16, nw>), dim3(a.tiles * a.kv.n_kv, a.splits), dim3(64 * nw), lds, s, a);
-    if (a.splits > kFewSplits)
-      hipLaunchKernelGGL((k_attn_join<D, F16>), dim3(a.T * a.H), dim3(kThreads), 0, s, a);
+    if (a.splits > one_round(D))
+      hipLaunchKernelGGL((k_attn_join<D, F16, 512>), dim3(a.T * a.H), dim3(512), 0, s, a);
+    else if (a.splits > kFewSplits)
+      hipLaunchKernelGGL((k_attn_join<D, F16, kThreads>), dim3(a.T * a.H), dim3(kThreads), 0, s, a);
     else if (a.splits > 1)
       hipLaunchKernelGGL((k_attn_join_few<D, F16>), dim3(((int64_t)a.T * a.H + 4 * kWaves - 1) / (4 * kWaves)), dim3(kThreads), 0, s, a);
   }
@@ -1236,7 +1242,7 @@ AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int w
   // chunk kernel, its keys split: several workgroups on a compute unit hide each other's starts.
   // Measured on decodes of heads of 256 / 128 / 64, us with runs and with splits: 64 sequences up
   // to 16K 174 and 203; 64 up to 4K 104 and 142; 32 up to 8K 60 and 97; but one at 4K 16.1 and
-  // 13.4, 16 up to 8K 39 and 32, 64 up to 1200 37 and 25, 200 up to 300 46 and 21.  More than
+  // 12.1, 16 up to 8K 39 and 30, 64 up to 1200 37 and 25, 200 up to 300 46 and 21.  More than
   // 16 rows a sequence: 16 sequences of 4 tokens and 8 heads at 8K 43 and 32.
   const bool runs = max_q * G <= kAttnRows && (int64_t)n_seqs * n_kv >= 48 && max_kv >= 16 * (int64_t)dim;
   s.rows = runs ? kAttnRows : kAttnTile;
@@ -1262,8 +1268,8 @@ AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int w
   if (window > 0 && max_kv > window + max_q) max_kv = window + max_q;
   const int64_t blocks = (max_kv + kAttnKeys - 1) / kAttnKeys + 1;
   int64_t per = (blocks + (want < 1 ? 1 : want) - 1) / (want < 1 ? 1 : want);  // blocks of a split
-  // Two blocks at least: one token at 4096 keys, 2 heads of 256, 13.4 us, 15.1 with one block, 14.1
-  // with four (at 500 keys 11.5, 10.9 and 13.6).  Few blocks are not split at all: 8 heads of
+  // Two blocks at least: one token at 4096 keys, 2 heads of 256, 12.1 us, 12.7 with one block (at 500
+  // keys 11.1 and 10.3; four blocks took 2 us more there).  Few blocks are not split at all: 8 heads of
   // 128, 160 keys 8.9 us, 11.4 split; but 250 keys of 2 heads of 256 15.5 and 11.5.
   if (per < 2) per = 2;
   if (blocks <= kWhole) per = blocks;

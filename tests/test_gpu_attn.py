@@ -259,6 +259,14 @@ def test_one_split_and_many_agree():
         c.check(*a, f"max_kv {mk}")
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("ctx", [150, 190, 700, 2200, 5000])
+def test_splits_of_every_number(D, ctx):
+    """One token over one sequence: one launch, joins of few splits, of one round and of more."""
+    c = Case([1], [ctx], 4, 1, D, seed=21)
+    c.check(*c.attn(), f"{D} over {ctx}")
+
+
 def test_places_beyond_32_bits():
     """Pages whose elements lie beyond 2^32 bytes and 2^32 elements of a plane's start."""
     import torch
@@ -278,6 +286,17 @@ def test_places_beyond_32_bits():
     q = rope_append(c.q, c.k, c.v, big_k, big_v, c.dev(table), c.dev(c.q_start), c.dev(c.kv_len), f, mscale=m)
     q2 = rope_append(c.q, c.k, c.v, c.kc, c.vc, *c.args(), f, mscale=m)
     assert (q == q2).all() and (big_k[far:] == c.kc).all() and (big_v[far:] == c.vc).all()
+
+
+@pytest.mark.parametrize("n,window", [(2, 0), (17, 0), (64, 0), (64, 50), (65, 0), (130, 40)])
+def test_tiles_of_many_uneven_sequences(n, window):
+    """Sequences with and without new tokens, long and short, up to and above a wave's lanes."""
+    rng = np.random.default_rng(n)
+    new = [int(x) for x in rng.integers(0, 40, n)]
+    new[0], new[-1] = 90, 0
+    lens = [a + int(x) for a, x in zip(new, rng.integers(0, 2, n) * rng.integers(0, 500, n))]
+    c = Case(new, lens, 8, 2, 64, seed=n)
+    c.check(*c.attn(window=window), f"{n} sequences, window {window}", window=window)
 
 
 def test_calls_on_two_streams_at_once():
