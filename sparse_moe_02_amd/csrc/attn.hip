@@ -14,9 +14,9 @@
 //                K and V in an LDS ring filled by direct-to-LDS loads.  Where tiles are few,
 //                their keys are split over workgroups, joined by k_attn_join(_few).
 //                Bound: matrix units (4 flops per row, visible key and element).  4096 tokens at
-//                32K, 16/2 heads of 256: 1.85 ms, 1.11 PFLOP/s (a large library product reaches
+//                32K, 16/2 heads of 256: 1.78 ms, 1.16 PFLOP/s (a large library product reaches
 //                1.22; the same over zeros 1.35 ms: power); 24 chunks of 0 to 509 tokens, window 1024,
-//                32/8 heads of 128: 0.14 ms, 0.57 PFLOP/s (starts, and a second round of tiles).
+//                32/8 heads of 128: 0.13 ms, 0.62 PFLOP/s (starts, and a second round of tiles).
 //                One token at 4K: 12.1 us, a chain of dependent loads and a second launch.
 //   k_attn_rows  16 rows, four waves sharing the keys out (v_mfma_f32_16x16x32); the keys of all
 //                sequences cut into equal runs, joined by k_attn_join_runs.  For few rows over
