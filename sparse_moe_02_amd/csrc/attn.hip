@@ -132,8 +132,7 @@ __device__ __forceinline__ int swz(int r) {
   return D == 64 ? (r & 2) << 1 | (r >> 2 & 3) : (r & 3) << 2 | (r >> 2 & 3);
 }
 
-// Page table entries are read as constants: by the scalar unit, whose loads have a counter of
-// their own -- a vector load's wait would drain the direct-to-LDS loads in flight.
+// Single page table entries are read as constants, by the scalar unit.
 typedef const __attribute__((address_space(4))) int32_t *TableRow;
 
 // The page of the 16 keys from `key` on, or -1.

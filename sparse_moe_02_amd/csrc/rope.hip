@@ -81,12 +81,26 @@ __global__ void __launch_bounds__(kThreads) k_rope_append(RopeArgs a) {
       y[j] = c.w;
     }
   }
-  if (t >= b.q_start[b.n_seqs]) return;  // padding behind the last sequence
-
   // the token's sequence, position and cache place
-  const int seq = wave_find(b.n_seqs, t, [&](int i) { return (int64_t)b.q_start[i]; });
-  const int row = batch_row(b, seq);
-  const int64_t p = (row < 0 ? 0 : (int64_t)b.kv_len[row]) - b.q_start[seq + 1] + t;
+  int row, len, end;  // table row, its length, first token behind the sequence
+  if (b.n_seqs > 1 && b.n_seqs <= 64) {
+    // every sequence in a lane: one step less in the chain of loads (2777 tokens of 48 sequences 14.9
+    // us, 15.2 the other way; one sequence's numbers come faster as scalars, 17.6 and 19.7)
+    const int lane = tid & 63, i = min(lane, b.n_seqs - 1);
+    const int from = b.q_start[i], to = b.q_start[i + 1], r = batch_row(b, i), n = b.kv_len[max(r, 0)];
+    const int seq = max(0, 63 - (int)__builtin_clzll(__ballot(lane < b.n_seqs && from <= t) | 1));
+    if (t >= __builtin_amdgcn_readlane(to, b.n_seqs - 1)) return;  // padding behind the last sequence
+    row = __builtin_amdgcn_readlane(r, seq);
+    len = __builtin_amdgcn_readlane(n, seq);
+    end = __builtin_amdgcn_readlane(to, seq);
+  } else {
+    if (t >= b.q_start[b.n_seqs]) return;
+    const int seq = wave_find(b.n_seqs, t, [&](int i) { return (int64_t)b.q_start[i]; });
+    row = batch_row(b, seq);
+    len = b.kv_len[max(row, 0)];
+    end = b.q_start[seq + 1];
+  }
+  const int64_t p = (row < 0 ? 0 : (int64_t)len) - end + t;
   const int64_t col = p >> a.kv.page_shift;
   int page = -1;
   if (n_kv && row >= 0 && p >= 0 && col < b.cols) page = b.table[(int64_t)row * b.cols + col];

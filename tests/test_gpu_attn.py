@@ -516,6 +516,32 @@ def test_rope_append(D, rot, interleaved, dtype):
     assert np.array_equal(_np(c.vc), rv)
 
 
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 200])
+@pytest.mark.parametrize("most", [2, 40])
+def test_rope_append_of_many_sequences(n, most):
+    """Up to and above a wave's lanes, with empty sequences first, last and between, and padding."""
+    import torch
+
+    from oracle import serve
+    from sparse_moe_02_amd.attn import rope_append, rope_freqs
+
+    rng = np.random.default_rng(n)
+    new = [int(x) for x in rng.integers(0, most, n)]
+    new[0], new[n // 2] = (0 if n > 1 else 3), 3
+    c = Case(new, [x + int(y) for x, y in zip(new, rng.integers(0, 60, n))], 4, 2, 64, page=16, pad=3, seed=n + most)
+    f, m = rope_freqs(64, device="cuda")
+    row = rng.permutation(n).astype(np.int32)  # so lengths may be less than the new tokens: places before the sequence
+    q, k, v = _np(c.q), _np(c.k), _np(c.v)
+    rq, rk, rv = serve.rope_append(q, k, v, _np(c.kc), _np(c.vc), c.table, c.q_start, c.kv_len, f.cpu().numpy(), m, row=row)
+    out = torch.full_like(c.q, 9.0)
+    rope_append(c.q, c.k, c.v, c.kc, c.vc, *c.args(), f, mscale=m, row=c.dev(row), q_out=out)
+    end = int(c.q_start[-1])
+    u, big = 2.0 ** -8, 2e-6 * max(np.abs(q).max(), np.abs(k).max())
+    assert (out[end:] == 9).all() and np.array_equal(_np(c.vc), rv)
+    assert (np.abs(_np(out)[:end] - rq[:end]) <= u * np.abs(rq[:end]) + big).all()
+    assert (np.abs(_np(c.kc) - rk) <= u * np.abs(rk) + big).all()
+
+
 def test_rope_in_place_positions_and_rows():
     """q_out = q inside one projection's rows, given positions far out, rows in another order."""
     import torch
