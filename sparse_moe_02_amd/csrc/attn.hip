@@ -779,7 +779,8 @@ __global__ void __launch_bounds__(64 * NW, D == 256 ? 2 : D == 128 ? 3 : 4) k_at
   }
 
   const int blk0 = t.lo / kAttnKeys, nblk = (t.hi + kAttnKeys - 1) / kAttnKeys - blk0;
-  const int b0 = blk0 + min(nblk, split * a.split_blocks), b1 = blk0 + (split + 1 == a.splits ? nblk : min(nblk, (split + 1) * a.split_blocks));
+  const int b0 = blk0 + min(nblk, split * a.split_blocks);
+  const int b1 = blk0 + (split + 1 == a.splits ? nblk : min(nblk, (split + 1) * a.split_blocks));
 
   // the rows that this wave loads lie in one 16-key half of a block
   const int my_r0 = wave * kInstr * kRowsPer, upper = my_r0 >> 4;
