@@ -40,7 +40,9 @@ typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kMaxSplits = 256;
-constexpr int kTileSlots = 512;  // workgroups of k_attn_tile that splits aim at: two a compute unit
+// workgroups of k_attn_tile that splits aim at: two a compute unit, three of narrow heads (heads of 64,
+// 32 tokens of 8 sequences at 2K 19.1 us, 22.4 with two; of 128, 16 of 6 at 6K 30.6 and 28.6)
+constexpr int tile_slots(int dim) { return dim == 64 ? 768 : 512; }
 constexpr int kWhole = 7;        // blocks that are worth no second launch
 constexpr int kMaxRuns = 1024;  // workgroups of k_attn_rows at most
 // workgroups of k_attn_rows that fill the chip (registers allow 1, 2 or 3 on a compute unit)
@@ -1264,7 +1266,7 @@ AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int w
   if (busy < T * G / s.rows) busy = T * G / s.rows;  // (whatever max_q says)
   if (busy > s.tiles) busy = s.tiles;
   busy *= n_kv;
-  const int64_t want = kTileSlots / (busy < 1 ? 1 : busy);
+  const int64_t want = tile_slots(dim) / (busy < 1 ? 1 : busy);
   if (window > 0 && max_kv > window + max_q) max_kv = window + max_q;
   const int64_t blocks = (max_kv + kAttnKeys - 1) / kAttnKeys + 1;
   int64_t per = (blocks + (want < 1 ? 1 : want) - 1) / (want < 1 ? 1 : want);  // blocks of a split
