@@ -716,14 +716,16 @@ constexpr float kLag = 8.0f;
 // 16K, heads of 128, 1150 / 1133 / 1101; 4096 at 8K, heads of 64, 211 / 199 / 216.
 enum class First { Matrix, Softmax, None };
 
-// 32 rows a wave, NW waves.  A workgroup's waves pass one barrier a block: behind it the block is
+// 32 rows a wave, four waves.  A workgroup's waves pass one barrier a block: behind it the block is
 // there for all, and the buffer of the block before it is free for the loads of the next.
-template <int D, bool F16, int NW>
-__global__ void __launch_bounds__(64 * NW, D == 256 ? 2 : D == 128 ? 3 : 4) k_attn_tile(AttnArgs a) {
+// Waves on a SIMD: two, three, four by width (of 128, with 169 registers and so two waves, 24 ragged
+// chunks take 143 us; with 168 and three, 132).
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_attn_tile(AttnArgs a) {
   constexpr int kBuf = kAttnKeys * D * 2;      // one K or V block, bytes
   constexpr int kStages = stages(D);
   constexpr First kFirst = D == 256 ? First::Matrix : D == 64 ? First::Softmax : First::None;
-  constexpr int kInstr = kBuf / 1024 / NW;     // load instructions a wave issues for one block
+  constexpr int kInstr = kBuf / 1024 / kWaves;     // load instructions a wave issues for one block
   constexpr int kRowsPer = 512 / D;            // LDS rows of one instruction
   static_assert(kInstr == 1 || kInstr == 2 || kInstr == 4, "as dma_rows has them");
   extern __shared__ __align__(16) uint8_t lds_raw[];
@@ -731,7 +733,7 @@ __global__ void __launch_bounds__(64 * NW, D == 256 ? 2 : D == 128 ? 3 : 4) k_at
   // the key/value heads of one tile next to each other: 4096 tokens at 16K, 8 such heads of 128,
   // 1052 us; head after head 1128
   const int tile = blockIdx.x / (unsigned)a.kv.n_kv, kvh = blockIdx.x - tile * a.kv.n_kv;
-  if (!find_tile(a, tile, 32 * NW, t)) return;
+  if (!find_tile(a, tile, kAttnTile, t)) return;
   // Behind the buffers, so that these start at LDS address 0 (addresses are combined by
   // exclusive or): whether some value that not all rows see is an infinity or NaN.
   int &odd = *(int *)(lds_raw + kStages * 2 * kBuf);
@@ -1221,10 +1223,10 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((k_attn_join_runs<D, F16>), dim3(a.wgs, a.join_rows), dim3(kJoinThreads), 0, s, a);
   } else {
     static std::atomic<uint64_t> done{0};
-    constexpr int lds = stages(D) * 2 * kAttnKeys * D * 2 + 16, nw = kAttnTile / 32;
-    const hipError_t e = allow_lds(k_attn_tile<D, F16, nw>, lds, done);
+    constexpr int lds = stages(D) * 2 * kAttnKeys * D * 2 + 16;
+    const hipError_t e = allow_lds(k_attn_tile<D, F16>, lds, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn_tile<D, F16, nw>), dim3(a.tiles * a.kv.n_kv, a.splits), dim3(64 * nw), lds, s, a);
+    hipLaunchKernelGGL((k_attn_tile<D, F16>), dim3(a.tiles * a.kv.n_kv, a.splits), dim3(kThreads), lds, s, a);
     if (a.splits > one_round(D))
       hipLaunchKernelGGL((k_attn_join<D, F16, 512>), dim3(a.T * a.H), dim3(512), 0, s, a);
     else if (a.splits > kFewSplits)
