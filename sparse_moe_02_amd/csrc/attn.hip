@@ -670,6 +670,10 @@ __device__ __forceinline__ float halves_sum(float v) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
+__device__ __forceinline__ float uniform_f(float v) {
+  return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
+}
+
 template <bool F16>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
   if constexpr (F16)
@@ -711,6 +715,12 @@ __device__ __forceinline__ void lds_barrier() {
 constexpr int stages(int dim) { return dim == 256 ? 2 : 3; }
 
 constexpr float kLag = 8.0f;
+// A weight is 2^(s scale - fl(m scale)), one fused operation, off by the rounding of the reference's
+// product: below 2^-12 for scores (base-2 exponents) of up to 2^12, but from about 2^24 on by whole
+// powers of two, and from 2^31 on every weight of a row is 0 or infinite.  Where a row's reference is
+// further out than kFar, each of its scores is rounded as the reference is before the difference is
+// taken, so that the largest weight is 1, and the reference does not lag.
+constexpr float kFar = 4096.0f;
 // What a wave is given the issue slots for while others of its SIMD do the other thing.  Measured
 // with Matrix / Softmax / None: 4096 tokens at 32K, heads of 256, 1927 / 1997 / 2022 us; 4096 at
 // 16K, heads of 128, 1150 / 1133 / 1101; 4096 at 8K, heads of 64, 211 / 199 / 216.
@@ -769,7 +779,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
   // is the largest product
   const float scale = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);  // 0: of queries of zeros
   const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-  const float lag = fminf(kLag / scale, 1e30f);  // (finite, so that it is exceeded from -infinity on)
+  // (lag: finite, so that it is exceeded from -infinity on)
+  const float lag = uniform_f(fminf(kLag / scale, 1e30f)), far = uniform_f(lag * (kFar / kLag));
   // (lanes without a row read the tile's first one, and take zeros)
   const uint16_t *qp = a.q.p + (int64_t)(live ? tok : t.t0 + t.r0 / a.G) * a.q.ts +
                        (int64_t)(live ? head : kvh * a.G + t.r0 % a.G) * a.q.hs;
@@ -917,22 +928,29 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
 #pragma unroll
     for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
     // the reference m follows the maximum only where it lags by more than kLag (as a base-2
-    // exponent), so weights stay below 2^kLag and the outputs are hardly ever rescaled
+    // exponent), so weights stay below 2^kLag and the outputs are hardly ever rescaled; the scores of
+    // rows far out are taken relative to it here (each product rounded by itself: not fused)
     mx = halves_max(mx);
-    if (__ballot(mx > m + lag)) {
+    if (__ballot(mx > (fabsf(m) > far ? -INFINITY : m + lag))) {
       const float mn = fmaxf(m, mx);
-      const float f = __builtin_amdgcn_exp2f((m - (mn == -INFINITY ? 0.0f : mn)) * scale);
+      const float ms = mn == -INFINITY ? 0.0f : mn * scale;
+      const float f = __builtin_amdgcn_exp2f(m * scale - ms);
       m = mn;
+      if (__ballot(fabsf(m) > far && m > -INFINITY)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = fabsf(m) > far ? s[i] * scale - ms : s[i];
+      }
       l *= f;
       es *= f;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d) acc[d] *= f;
     }
-    const float off = m == -INFINITY ? 0.0f : -m * scale;
+    // (nothing seen yet, m = -infinity, is far out, too)
+    const float off = fabsf(m) > far ? 0.0f : -m * scale, to_exp = fabsf(m) > far ? 1.0f : scale;
     float ps = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale, off));
+      s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], to_exp, off));
       ps += s[i];
     }
     es += ps;
