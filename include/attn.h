@@ -127,9 +127,10 @@ moe_status moe_rope_append(const moe_paged_kv *kv, const moe_batch *batch, int64
  *                  between calls; calls that may run at the same time need one each.
  * out and lse may overlap nothing that is read, the workspace, or each other
  * (MOE_ERR_ALIAS).  Scores, softmax statistics and sums are binary32; the weights of the
- * value sum are rounded to dtype (they enter the matrix units in it).  For one shape of
- * launch, results are bitwise repeatable.  T: 0 .. 2^20, T * n_heads <= 2^29,
- * n_seqs * n_kv_heads <= 2^22 (MOE_ERR_TOKENS). */
+ * value sum are rounded to dtype (they enter the matrix units in it), those of fp16 below
+ * 2^-25 of the row's largest one by at most 2^-36 of that.  For one shape of launch, results
+ * are bitwise repeatable.  T: 0 .. 2^20, T * n_heads <= 2^29, n_seqs * n_kv_heads <= 2^22
+ * (MOE_ERR_TOKENS). */
 #define MOE_ATTN_FULL 1u
 moe_status moe_paged_attn_workspace(const moe_paged_kv *kv, int64_t T, int32_t n_seqs, int64_t max_q,
                                     int64_t max_kv, int32_t n_heads, int32_t window, size_t *bytes);

@@ -82,13 +82,28 @@ __device__ __forceinline__ float add2(uint32_t w, float c) {
     return dot2_bf16(w, 0x3f803f80u, c);
   }
 }
+// fp16 holds numbers of 2^-14 to 2^15 with all their bits and none below 2^-25, and a row with one
+// dominant key may have its value from keys far below that one.  So its weights are taken as 2^bias times
+// what they are: the largest is 2^15 in k_attn_rows, and 2^11 to 2^15 in k_attn_tile, whose reference
+// lags by up to 2^4.  Weights down to 2^-29 (2^-25) of the largest keep all bits, and 2^17 keys that
+// are too small to be held make up 2^-23 (2^-19) of a row at most.  (With the largest weight at 1, or
+// 2^8, all of 2^17 keys at e^-17.4 behind one at 0 were lost: 0.4 % of the row, 7 roundings of fp16.
+// The shorter lag costs 0 to 4 %: 512 tokens at 8K, heads of 256, 94.3 -> 97.8 us, 24 ragged chunks,
+// heads of 128, 122 -> 124.)  The factor is in all of a row's sums and cancels in its output.
+constexpr float lag_of(bool f16) { return f16 ? 4.0f : 8.0f; }
+constexpr float rows_bias(bool f16) { return f16 ? 15.0f : 0.0f; }
+constexpr float tile_bias(bool f16) { return f16 ? 15.0f - lag_of(true) : 0.0f; }
+
 // What is kept of a row besides its weighted sum of values: the reference (base-2 exponent), the
 // sum of the rounded weights, which the values' sum is divided by (so that a weight's rounding
-// only shifts the mean of the values), and that of the unrounded ones, for the log-sum-exp.
+// only shifts the mean of the values), and that of the unrounded ones, for the log-sum-exp; both sums
+// 2^bias times what they are.
 struct Stats {
   float m, l, e;
 };
-__device__ __forceinline__ float lse_of(float m, float e) { return e == 0.0f ? -INFINITY : (m + __log2f(e)) * kLn2; }
+__device__ __forceinline__ float lse_of(float m, float e, float bias) {
+  return e == 0.0f ? -INFINITY : (m + (__log2f(e) - bias)) * kLn2;
+}
 __device__ __forceinline__ float reciprocal_of(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
 // whether a value is an infinity or NaN
@@ -572,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) k_attn_rows(AttnAr
       float ps = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(p[i] - mu);
+        p[i] = __builtin_amdgcn_exp2f(F16 ? p[i] - mu + rows_bias(F16) : p[i] - mu);
         ps += p[i];
       }
       es = es * f + ps;
@@ -633,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) k_attn_rows(AttnAr
         const float inv = reciprocal_of(sum);
         const uint2 w = {pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv)};
         *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + c) = w;
-        if (a.lse && c == 0) a.lse[tk * a.H + hd] = lse_of(mw, esum);
+        if (a.lse && c == 0) a.lse[tk * a.H + hd] = lse_of(mw, esum, rows_bias(F16));
       } else {
         const int64_t at = slot + r;
         *(f32x4 *)(a.part + at * D + c) = v;
@@ -714,9 +729,8 @@ __device__ __forceinline__ void lds_barrier() {
 // eight waves.  Narrower heads have room for three.
 constexpr int stages(int dim) { return dim == 256 ? 2 : 3; }
 
-constexpr float kLag = 8.0f;
-// A weight is 2^(s scale - fl(m scale)), one fused operation, off by the rounding of the reference's
-// product: below 2^-12 for scores (base-2 exponents) of up to 2^12, but from about 2^24 on by whole
+// A weight is 2^(s scale + fl(bias - m scale)), one fused operation, off by the rounding of the
+// reference's term: below 2^-12 for scores (base-2 exponents) of up to 2^12, but from about 2^24 on by whole
 // powers of two, and from 2^31 on every weight of a row is 0 or infinite.  Where a row's reference is
 // further out than kFar, each of its scores is rounded as the reference is before the difference is
 // taken, so that the largest weight is 1, and the reference does not lag.
@@ -780,6 +794,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
   const float scale = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);  // 0: of queries of zeros
   const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
   // (lag: finite, so that it is exceeded from -infinity on)
+  constexpr float kLag = lag_of(F16), kBias = tile_bias(F16);
   const float lag = uniform_f(fminf(kLag / scale, 1e30f)), far = uniform_f(lag * (kFar / kLag));
   // (lanes without a row read the tile's first one, and take zeros)
   const uint16_t *qp = a.q.p + (int64_t)(live ? tok : t.t0 + t.r0 / a.G) * a.q.ts +
@@ -928,8 +943,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
 #pragma unroll
     for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
     // the reference m follows the maximum only where it lags by more than kLag (as a base-2
-    // exponent), so weights stay below 2^kLag and the outputs are hardly ever rescaled; the scores of
-    // rows far out are taken relative to it here (each product rounded by itself: not fused)
+    // exponent), so weights stay below 2^(kLag + kBias) and the outputs are hardly ever rescaled;
+    // the scores of rows far out are taken relative to it here (each product rounded by itself: not
+    // fused)
     mx = halves_max(mx);
     if (__ballot(mx > (fabsf(m) > far ? -INFINITY : m + lag))) {
       const float mn = fmaxf(m, mx);
@@ -946,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
       for (int d = 0; d < D / 32; ++d) acc[d] *= f;
     }
     // (nothing seen yet, m = -infinity, is far out, too)
-    const float off = fabsf(m) > far ? 0.0f : -m * scale, to_exp = fabsf(m) > far ? 1.0f : scale;
+    const float off = fabsf(m) > far ? kBias : __builtin_fmaf(-m, scale, kBias), to_exp = fabsf(m) > far ? 1.0f : scale;
     float ps = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -995,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
                          pack2<F16>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv)};
         *(uint2 *)(o + 32 * d + 8 * i) = w;
       }
-    if (a.lse && half == 0) a.lse[row] = lse_of(m == -INFINITY ? m : m * scale, es);
+    if (a.lse && half == 0) a.lse[row] = lse_of(m == -INFINITY ? m : m * scale, es, tile_bias(F16));
     if (a.splits > 1 && half == 0) a.stats[row * a.splits].l = -1.0f;
   } else {
     const int64_t at = row * a.splits + split;
@@ -1080,7 +1096,7 @@ __global__ void __launch_bounds__(NT) k_attn_join(AttnArgs a) {
   const float inv = reciprocal_of(sum);
   *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + 4 * c) =
       make_uint2(pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv));
-  if (a.lse && tid == 0) a.lse[r] = lse_of(mw, esum);
+  if (a.lse && tid == 0) a.lse[r] = lse_of(mw, esum, tile_bias(F16));
 }
 
 // The same for up to kFewSplits splits, where there are many rows: kRows rows a wave, their loads
@@ -1146,7 +1162,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_few(AttnArgs a) {
     const float inv = reciprocal_of(sum);
     *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + 4 * c) =
         make_uint2(pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv));
-    if (a.lse && lane == 0) a.lse[r] = lse_of(mw, esum);
+    if (a.lse && lane == 0) a.lse[r] = lse_of(mw, esum, tile_bias(F16));
   }
 }
 
@@ -1213,7 +1229,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join_runs(AttnArgs a) {
       const int64_t tk = rec.t0 + (rec.r0 + r) / a.G, hd = rec.kvh * a.G + (rec.r0 + r) % a.G;
       *(uint2 *)(a.out.p + tk * a.out.ts + hd * a.out.hs + 4 * c) =
           make_uint2(pack2<F16>(v[0] * inv, v[1] * inv), pack2<F16>(v[2] * inv, v[3] * inv));
-      if (a.lse && tid == 0) a.lse[tk * a.H + hd] = lse_of(mw, esum);
+      if (a.lse && tid == 0) a.lse[tk * a.H + hd] = lse_of(mw, esum, rows_bias(F16));
     }
     __syncthreads();
   }

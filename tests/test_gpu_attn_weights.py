@@ -72,3 +72,82 @@ def test_largest_scores(dtype, size, sign, runs):
                 assert abs(lse[t, h] - score) <= 2.0 ** -20 * abs(score) + 1e-6 * np.log(top.sum() + 1), (b, i, h)
             t += 1
     say(f"{dtype} {size} {sign} runs {runs}: every row its largest key")
+
+
+# ------------------------------------------------------------------------ long tails in fp16
+
+# The largest weight of a row is at least 2 to this power, so that fp16's smallest numbers (which round
+# by at most 2^-25) lie that much further below it.
+TILE, RUNS = 11, 15
+
+
+def _given(c, k, v, q=8.0):
+    """Every query is (q, 0, ...), and every sequence's keys are (k, 0, ...); v: [keys][D]."""
+    c.q[:] = 0
+    c.q[:, :, 0] = q
+    for b, length in enumerate(c.total):
+        at = c.dev(np.arange(length))
+        page = c.dev(c.table[b])[at // c.page].long()
+        c.kc[page, at % c.page] = 0
+        c.kc[page, at % c.page, :, 0] = c.dev(k[:length]).to(c.kc.dtype)[:, None]
+        c.vc[page, at % c.page] = c.dev(v[:length]).to(c.vc.dtype)[:, None]
+
+
+def _check(c, launch, what, per_top):
+    """per_top: keys for each key of the largest weight, at most."""
+    from oracle import serve
+
+    kw = {"unsplit": dict(max_kv=1), "split": {}, "runs": dict(max_q=1, max_kv=10 ** 6)}[launch]
+    out, lse = (_np(x) for x in c.attn(scale=0.125, **kw))
+    ro, rl, mass, _ = serve.paged_attn(_np(c.q), _np(c.kc), _np(c.vc), c.table, c.q_start, c.kv_len, 0.125)
+    u = 2.0 ** -11
+    # weights are rounded to 16 bits (u), or by 2^-25 below 2^-14; products here are exact, and a score of
+    # up to 2^6 is off by 2^-18 as a base-2 exponent
+    low = per_top * 2.0 ** -(25 + (RUNS if launch == "runs" else TILE)) * np.abs(_np(c.vc)).max()
+    tol = u * np.abs(ro) + (u + 2.0 ** -16) * mass + low
+    err = np.abs(out - ro) / tol
+    say(f"{what}, {launch}: output error / tolerance {err.max():.3f}, tolerance / mass {(tol / mass).max():.2e}")
+    assert (err <= 1.0).all(), what
+    # the sum of the weights is taken block by block of 32 keys, one binary32 addition after the other
+    # (each off by at most 2^-24 of the sum), which the logarithm takes as it is
+    added = -(-max(c.total) // 32) * 2.0 ** -24
+    assert (np.abs(lse - rl) <= 2.0 ** -20 * (1 + np.abs(rl)) + 2.0 ** -18 + added).all(), what
+
+
+@pytest.mark.parametrize("launch", ["unsplit", "split", "runs"])
+@pytest.mark.parametrize("every", [32, 1000])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_tail_behind_a_sink(D, every, launch):
+    """Keys of weight 1 whose values are zeros (one of `every`), the others at e^-15 to e^-18: the output
+    is the tail's share."""
+    n = 1000
+    rng = np.random.default_rng(D)
+    c = Case([1, 40, 1, 1, 1, 1], [n] * 6, 8, 8, D, "fp16", page=16, seed=D)
+    k, v = rng.uniform(-2.0, 1.0, n), 500 * (1 + rng.random((n, D)))
+    k[::every], v[::every] = 16.0, 0.0
+    _given(c, k, v)
+    _check(c, launch, f"tail of {D}, a sink of {every}", every)
+
+
+@pytest.mark.parametrize("launch", ["unsplit", "split", "runs"])
+@pytest.mark.parametrize("rise", [5.0, 20.0, -20.0])
+@pytest.mark.parametrize("D", [64, 256])
+def test_rising_scores(D, rise, launch):
+    """Scores that rise (or fall) evenly along the keys, so that the reference follows in small steps."""
+    n = 1000
+    rng = np.random.default_rng(7)
+    c = Case([1, 40, 1, 1, 1, 1], [n] * 6, 8, 8, D, "fp16", page=16, seed=D)
+    _given(c, np.linspace(0, rise, n), 1 + rng.random((n, D)))
+    _check(c, launch, f"scores rising by {rise}", n)
+
+
+@pytest.mark.parametrize("launch", ["unsplit", "split"])
+def test_tail_of_a_long_sequence(launch):
+    """131072 keys behind one sink, their weights in the subnormal range."""
+    n = 131072
+    rng = np.random.default_rng(1)
+    c = Case([1], [n], 1, 1, 64, "fp16", page=64, seed=1)
+    k, v = rng.uniform(-2.5, -1.5, n), 500 * (1 + rng.random((n, 64)))
+    k[0], v[0] = 16.0, 0.0
+    _given(c, k, v)
+    _check(c, launch, "long tail", n)
