@@ -151,3 +151,22 @@ def test_tail_of_a_long_sequence(launch):
     k[0], v[0] = 16.0, 0.0
     _given(c, k, v)
     _check(c, launch, "long tail", n)
+
+
+@pytest.mark.parametrize("launch", ["unsplit", "split", "runs"])
+@pytest.mark.parametrize("diff", [17.6, 18.5, 19.2])
+def test_sum_of_a_long_tail(diff, launch):
+    """Values of 1 are their own mean, whatever their weights: a key at 0 and 131072 at e^-diff, each below
+    the last bit of the sum that is divided by, and all of them above a rounding of fp16 (for the largest)."""
+    n = 131072
+    several = launch == "runs"  # (48 sequences choose equal runs, and the long one's spans several)
+    c = Case([1] * (48 if several else 1), [n] + [1] * (47 if several else 0), 1, 1, 64, "fp16", page=64, seed=1)
+    k = np.full(n, 16.0 - diff)
+    k[0] = 16.0
+    _given(c, k, np.ones((n, 64)))
+    kw = {"unsplit": dict(max_kv=1), "split": {}, "runs": dict(max_q=1, max_kv=10 ** 6)}[launch]
+    out = _np(c.attn(scale=0.125, **kw)[0])
+    # weights' roundings are the same above and below; of the two sums, one binary32 addition a block of
+    # 32 keys and one for 16, each off by at most 2^-24: 2^-12 and 2^-11
+    say(f"e^-{diff} {launch}: {np.abs(out - 1).max() * 2.0 ** 11:.2f} roundings")
+    assert (np.abs(out - 1) <= 2.0 ** -11 + 2.0 ** -12 + 2.0 ** -11).all()
