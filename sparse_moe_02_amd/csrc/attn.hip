@@ -1288,10 +1288,10 @@ AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int w
   // 12.1, 16 up to 8K 39 and 30, 64 up to 1200 37 and 25, 200 up to 300 46 and 21.  More than
   // 16 rows a sequence: 16 sequences of 4 tokens and 8 heads at 8K 43 and 32.
   // A window bounds the keys, and makes the sequences that exceed it equally long, so that splits are
-  // good up to twice as many: 64 sequences up to 16K (or 32K, heads of 256), windows of 2, 16, 32 and
-  // 64 widths, heads of 256 29, 119, 210, 393 and 15, 108, 199, 382; of 128 30, 120, 212, 397 and 15,
-  // 106, 200, 386; of 64 25, 66, 117, 209 and 15, 64, 118, 228; of lengths spread evenly over their
-  // logarithm, heads of 256 28, 88, 120, 140 and 15, 69, 110, 192.
+  // good up to twice as many: 64 sequences up to 16K (or 32K, heads of 256), windows of 128 keys and
+  // of 16, 32 and 64 widths, heads of 256 29, 119, 210, 393 and 15, 108, 199, 382; of 128 30, 120,
+  // 212, 397 and 15, 106, 200, 386; of 64 25, 66, 117, 209 and 15, 64, 118, 228; of lengths spread
+  // evenly over their logarithm, heads of 256 28, 88, 120, 140 and 15, 69, 110, 192.
   if (window > 0 && max_kv > window + max_q) max_kv = window + max_q;
   const bool runs = max_q * G <= kAttnRows && (int64_t)n_seqs * n_kv >= 48 &&
                     max_kv >= (window > 0 ? 32 : 16) * (int64_t)dim;
