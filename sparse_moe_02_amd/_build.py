@@ -76,6 +76,11 @@ def _build_tensors() -> None:
     os.replace(tmp, TENSORS_LIB)
 
 
+def built() -> bool:
+    """Whether the layer's library and the tensor reader are there."""
+    return os.path.exists(LIB) and os.path.exists(TENSORS_LIB)
+
+
 def build(jobs: int = 8) -> str:
     """The layer's library, then the benchmark's probe library (a separate .so), and the tensor
     reader."""

@@ -6,10 +6,23 @@ import contextlib
 
 import torch
 
+
+class _NotBuilt:
+    """In the tensor reader's place where it has not been built: its first use says so (or finds
+    it, if it was built since), so that what needs the library alone can be imported and run."""
+
+    def __getattr__(self, name):
+        try:
+            from . import _tensors
+        except ImportError as e:
+            raise ImportError(f"the tensor reader is not built ({e}): run __graft_entry__.build()") from e
+        return getattr(_tensors, name)
+
+
 try:
     from . import _tensors as N  # noqa: F401
-except ImportError as e:  # built with the library
-    raise ImportError(f"the tensor reader is not built ({e}): run __graft_entry__.build()") from e
+except ImportError:  # built with the library
+    N = _NotBuilt()
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device

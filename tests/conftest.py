@@ -18,3 +18,14 @@ def oracle_lib():
     import oracle
 
     return oracle.lib()
+
+
+@pytest.fixture(scope="session", autouse=True)
+def built():
+    """The library and the wrappers' tensor reader, built if either is missing."""
+    from sparse_moe_02_amd import _build
+
+    if not _build.built():
+        import __graft_entry__
+
+        __graft_entry__.build()
