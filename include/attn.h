@@ -77,7 +77,9 @@ typedef struct {               /* (host struct of device pointers), 4-byte align
  *   MOE_ROPE_YARN    by the pair's turns over the trained length, t = trained * f / 2 pi:
  *                    f where t >= 32, f / factor where t <= 1, linear in t between (Peng et
  *                    al., "YaRN: Efficient Context Window Extension of Large Language
- *                    Models", ICLR 2024); *mscale = 0.1 ln(factor) + 1
+ *                    Models", ICLR 2024); *mscale = 0.1 ln(factor) + 1.  Models trained with
+ *                    another ramp between the two (linear in the pair's index i, say) need
+ *                    frequencies of their own: moe_rope_append takes any
  * *mscale is 1 for the others.  rot_dim: even, 2 .. 256 (NTK: >= 4); base > 1; factor >= 1;
  * trained >= 1 (read for YARN only).  MOE_ERR_NULL, MOE_ERR_SHAPE. */
 typedef enum { MOE_ROPE_NONE = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_NTK = 2, MOE_ROPE_YARN = 3 } moe_rope_scaling;

@@ -14,14 +14,17 @@
 //                K and V in an LDS ring filled by direct-to-LDS loads.  Where tiles are few,
 //                their keys are split over workgroups, joined by k_attn_join(_few).
 //                Bound: matrix units (4 flops per row, visible key and element).  4096 tokens at
-//                32K, 16/2 heads of 256: 1.78 ms, 1.16 PFLOP/s (a large library product reaches
-//                1.22; the same over zeros 1.35 ms: power); 24 chunks of 0 to 509 tokens, window 1024,
-//                32/8 heads of 128: 0.13 ms, 0.62 PFLOP/s (starts, and a second round of tiles).
-//                One token at 4K: 12.1 us, a chain of dependent loads and a second launch.
+//                32K, 16/2 heads of 256: 1.77 to 1.82 ms by card, 1.16 to 1.13 PFLOP/s (a large library
+//                product reaches 1.22; the same over zeros 1.35 ms: power); 4096 at 16K, 32/8 heads of
+//                128, 1.04 ms (floor 0.79), and at 8K, 16/16 of 64, 0.186 ms (0.084): matrix units
+//                busy for 69, 48 and 23 % of the cycles, vector units 44, 55 and 48.  24 chunks of 0 to
+//                509 tokens, window 1024, 32/8 heads of 128, fp16: 0.127 ms, 0.64 PFLOP/s (masked
+//                parts of blocks, an uneven last round).  One token at 4K: 12.6 us, a chain of
+//                dependent loads and a second launch.
 //   k_attn_rows  16 rows, four waves sharing the keys out (v_mfma_f32_16x16x32); the keys of all
 //                sequences cut into equal runs, joined by k_attn_join_runs.  For few rows over
 //                many long sequences.  Bound: memory.  One token of 64 sequences up to 16K:
-//                172 us, 5.0 TB/s (a copy reaches 5.2).
+//                171 us, 5.0 TB/s (a copy reaches 5.2).
 //
 // Results of splits and runs are joined by their references, in fixed order.
 #include <atomic>
