@@ -14,7 +14,7 @@ import threading
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_mi355x.so")
 
-MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
+MOE_BF16, MOE_FP16, MOE_FP32, MOE_INT8, MOE_FP8 = range(5)
 MOE_OK = 0
 MOE_STAGE_ROUTE, MOE_STAGE_GROUP, MOE_STAGE_GATEUP, MOE_STAGE_DOWN, MOE_STAGE_FINAL = range(5)
 MOE_PREFILL_STAGES = 5
@@ -48,7 +48,7 @@ EXPORTED = ("moe_plan_create", "moe_plan_destroy", "moe_workspace_init", "moe_wo
             "moe_pack_qparams",
             "moe_pack_codes", "moe_status_string", "moe_version", "moe_gdn_scan", "moe_gdn_step", "moe_rope_freqs",
             "moe_rope_append", "moe_paged_attn_workspace", "moe_paged_attn", "moe_pages_workspace", "moe_pages_grow",
-            "moe_pages_fork", "moe_pages_free", "moe_pages_compact", "moe_pages_copy", "moe_pages_check")
+            "moe_pages_fork", "moe_pages_free", "moe_pages_compact", "moe_pages_copy", "moe_pages_check", "moe_rms_norm")
 
 # include/attn.h
 MOE_ROPE_NONE, MOE_ROPE_LINEAR, MOE_ROPE_NTK, MOE_ROPE_YARN = range(4)
@@ -180,6 +180,9 @@ def lib() -> ctypes.CDLL:
             L.moe_pages_copy.argtypes = [PM, I32, I32, P, P, P]
             L.moe_pages_check.restype = ctypes.c_int
             L.moe_pages_check.argtypes = [P, P]
+            F32 = ctypes.c_float
+            L.moe_rms_norm.restype = ctypes.c_int
+            L.moe_rms_norm.argtypes = [I64, I32, I32, ctypes.c_int, HD, HD, HD, P, F32, F32, ctypes.c_int, HD, I32, P, P]
             L.moe_status_string.restype = ctypes.c_char_p
             L.moe_status_string.argtypes = [ctypes.c_int]
             L.moe_version.restype = ctypes.c_char_p
@@ -353,6 +356,17 @@ def moe_pages_check(error_ptr: int, stream: int) -> int:
     if st not in (MOE_OK, MOE_ERR_SHAPE, MOE_ERR_ALLOC):
         raise MoeError("moe_pages_check", st)
     return st
+
+
+def _opt(x):
+    return None if x is None else _ref(x)
+
+
+def moe_rms_norm(T: int, n_heads: int, width: int, dtype: int, x: moe_heads, residual: moe_heads | None,
+                 sum: moe_heads | None, weight_ptr: int | None, offset: float, eps: float, out_dtype: int, out: moe_heads,
+                 group: int, scale_ptr: int | None, stream: int) -> None:
+    _check("moe_rms_norm", lib().moe_rms_norm(T, n_heads, width, dtype, _opt(x), _opt(residual), _opt(sum), weight_ptr, offset,
+                                              eps, out_dtype, _opt(out), group, scale_ptr, stream))
 
 
 def moe_pack_qparams(src_ptr: int, dst_ptr: int, rows: int, k: int, stream: int) -> None:

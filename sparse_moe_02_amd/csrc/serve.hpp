@@ -1,5 +1,6 @@
 // Launch interfaces of the serving operators: rotary append, paged attention, gated delta
-// steps (host side calls these from serve_api.cpp).
+// steps (host side calls these from serve_api.cpp), norm, 4-bit projections and sampling
+// (from step_api.cpp).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -122,5 +123,22 @@ struct PageWs {
 PageWs page_ws(int n_seqs, int n_pages, int n);
 hipError_t launch_pages(PageOp op, const PageArgs &a, hipStream_t s);
 hipError_t launch_pages_copy(const PageMem &m, int n_pages, int n, const int32_t *src, const int32_t *dst, hipStream_t s);
+
+// Norm with the residual's addition (norm.hip).
+struct Rows {  // [token][head][width], strides in elements
+  void *p;
+  int64_t ts, hs;
+};
+struct NormArgs {
+  Rows x, r, sum, out;  // r.p, sum.p null: none
+  const uint16_t *w;    // or null
+  float *scale;         // 8-bit outputs: [rows][groups]
+  int64_t rows;         // T * n
+  int n, W, group;      // group: W where a row is one
+  float offset, eps;
+  int out_kind;         // 0: the input's type, 1: int8, 2: e4m3
+  bool fp16, vec;       // vec: 16-byte rows
+};
+hipError_t launch_rms_norm(const NormArgs &a, hipStream_t s);
 
 }  // namespace moe

@@ -113,6 +113,26 @@ PyObject *py_heads(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// rows(name, tensor, T, heads, D, type, index): (moe_heads, T, heads, D) of [T][heads][D], or of [T][D] as one
+// head; T, heads or D -1: any
+PyObject *py_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 7, [&] {
+    const char *name = text(a[0]);
+    const at::Tensor &t = tensor(name, a[1]);
+    const int64_t sizes[3] = {integer(a[2]), integer(a[3]), integer(a[4])}, type = integer(a[5]), index = integer(a[6]);
+    const int dims = (int)t.dim(), last = dims - 1;
+    const int64_t flat[2] = {sizes[0], sizes[2]};
+    if ((int64_t)t.scalar_type() != type || index < 0 || t.get_device() != index ||
+        !(dims == 3 ? sizes_are(t, sizes, 3) : dims == 2 && (sizes[1] < 0 || sizes[1] == 1) && sizes_are(t, flat, 2)))
+      refuse(std::string(name) + ": " + type_text(type) + " " + sizes_text(sizes, 3) + " on cuda:" + std::to_string(index) +
+             " required");
+    if (t.size(last) > 1 && t.stride(last) != 1) refuse(std::string(name) + ": contiguous last dimension required");
+    const moe_heads h{t.data_ptr(), stride(t, 0), dims == 3 ? stride(t, 1) : 0};
+    return Py_BuildValue("NLii", bytes(h), (long long)t.size(0), dims == 3 ? small(name, t.size(1)) : 1,
+                         small(name, t.size(last)));
+  });
+}
+
 // cache(k, v, index): (moe_paged_kv, KV heads, head width, type)
 PyObject *py_cache(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(n, 3, [&] {
@@ -187,6 +207,7 @@ constexpr PyCFunction fast() {
 }
 PyMethodDef methods[] = {{"address", fast<py_address>(), METH_FASTCALL, nullptr},
                          {"heads", fast<py_heads>(), METH_FASTCALL, nullptr},
+                         {"rows", fast<py_rows>(), METH_FASTCALL, nullptr},
                          {"cache", fast<py_cache>(), METH_FASTCALL, nullptr},
                          {"batch", fast<py_batch>(), METH_FASTCALL, nullptr},
                          {"memory", fast<py_memory>(), METH_FASTCALL, nullptr},
@@ -201,7 +222,8 @@ PyMODINIT_FUNC PyInit__tensors() {
     const char *name;
     at::ScalarType type;
   } types[] = {{"BF16", at::kBFloat16}, {"FP16", at::kHalf}, {"FP32", at::kFloat},
-               {"FP64", at::kDouble},   {"INT32", at::kInt}, {"UINT8", at::kByte}};
+               {"FP64", at::kDouble},   {"INT32", at::kInt}, {"UINT8", at::kByte},
+               {"INT8", at::kChar},     {"FP8", at::kFloat8_e4m3fn}};
   for (const auto &t : types)
     if (m) PyModule_AddIntConstant(m, t.name, (long)t.type);
   return m;
