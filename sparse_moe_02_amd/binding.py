@@ -48,7 +48,8 @@ EXPORTED = ("moe_plan_create", "moe_plan_destroy", "moe_workspace_init", "moe_wo
             "moe_pack_qparams",
             "moe_pack_codes", "moe_status_string", "moe_version", "moe_gdn_scan", "moe_gdn_step", "moe_rope_freqs",
             "moe_rope_append", "moe_paged_attn_workspace", "moe_paged_attn", "moe_pages_workspace", "moe_pages_grow",
-            "moe_pages_fork", "moe_pages_free", "moe_pages_compact", "moe_pages_copy", "moe_pages_check", "moe_rms_norm")
+            "moe_pages_fork", "moe_pages_free", "moe_pages_compact", "moe_pages_copy", "moe_pages_check", "moe_rms_norm",
+            "moe_linear")
 
 # include/attn.h
 MOE_ROPE_NONE, MOE_ROPE_LINEAR, MOE_ROPE_NTK, MOE_ROPE_YARN = range(4)
@@ -105,6 +106,11 @@ class moe_pages(ctypes.Structure):
 class moe_page_memory(ctypes.Structure):
     _fields_ = [("base", ctypes.c_void_p), ("plane_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
                 ("page_bytes", ctypes.c_int64), ("n_planes", ctypes.c_int32)]
+
+
+class moe_linear_weights(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("n", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("qparam_dtype", ctypes.c_int)]
 
 
 class MoeError(RuntimeError):
@@ -183,6 +189,8 @@ def lib() -> ctypes.CDLL:
             F32 = ctypes.c_float
             L.moe_rms_norm.restype = ctypes.c_int
             L.moe_rms_norm.argtypes = [I64, I32, I32, ctypes.c_int, HD, HD, HD, P, F32, F32, ctypes.c_int, HD, I32, P, P]
+            L.moe_linear.restype = ctypes.c_int
+            L.moe_linear.argtypes = [P, I64, P, I64, ctypes.c_int, P, I32, P, I64, ctypes.c_int, P]
             L.moe_status_string.restype = ctypes.c_char_p
             L.moe_status_string.argtypes = [ctypes.c_int]
             L.moe_version.restype = ctypes.c_char_p
@@ -367,6 +375,12 @@ def moe_rms_norm(T: int, n_heads: int, width: int, dtype: int, x: moe_heads, res
                  group: int, scale_ptr: int | None, stream: int) -> None:
     _check("moe_rms_norm", lib().moe_rms_norm(T, n_heads, width, dtype, _opt(x), _opt(residual), _opt(sum), weight_ptr, offset,
                                               eps, out_dtype, _opt(out), group, scale_ptr, stream))
+
+
+def moe_linear(w: moe_linear_weights, T: int, x_ptr: int | None, x_stride: int, x_dtype: int, x_scale_ptr: int | None,
+               x_group: int, out_ptr: int | None, out_stride: int, out_dtype: int, stream: int) -> None:
+    _check("moe_linear", lib().moe_linear(_opt(w), T, x_ptr, x_stride, x_dtype, x_scale_ptr, x_group, out_ptr, out_stride,
+                                          out_dtype, stream))
 
 
 def moe_pack_qparams(src_ptr: int, dst_ptr: int, rows: int, k: int, stream: int) -> None:

@@ -27,8 +27,6 @@
 //                171 us, 5.0 TB/s (a copy reaches 5.2).
 //
 // Results of splits and runs are joined by their references, in fixed order.
-#include <atomic>
-
 #include "paged.hpp"
 
 #pragma clang fp contract(off)
@@ -1241,18 +1239,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join_runs(AttnArgs a) {
     }
     __syncthreads();
   }
-}
-
-// Sets the LDS limit of a kernel, once for each device (the attribute belongs to the device).
-template <class K>
-hipError_t allow_lds(K k, int lds, std::atomic<uint64_t> &done) {
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
-  if (dev <= 63 && done.load(std::memory_order_relaxed) >> dev & 1) return hipSuccess;
-  e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (e == hipSuccess && dev <= 63) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
-  return e;
 }
 
 template <int D, bool F16>

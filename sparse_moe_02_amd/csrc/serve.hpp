@@ -6,7 +6,21 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace moe {
+
+// Sets the LDS limit of a kernel, once for each device (the attribute belongs to the device).
+template <class K>
+hipError_t allow_lds(K k, int lds, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  if (dev <= 63 && done.load(std::memory_order_relaxed) >> dev & 1) return hipSuccess;
+  e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e == hipSuccess && dev <= 63) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  return e;
+}
 
 struct Heads {  // [token][head][head_dim] with strides in elements
   uint16_t *p;
@@ -140,5 +154,24 @@ struct NormArgs {
   bool fp16, vec;       // vec: 16-byte rows
 };
 hipError_t launch_rms_norm(const NormArgs &a, hipStream_t s);
+
+// Products of few rows with 4-bit weights (linear.hip).
+enum class LinX { Bf16, Fp16, Int8 };
+enum class LinOut { Bf16, Fp16, Fp32 };
+struct LinArgs {
+  const uint32_t *codes;
+  const uint16_t *scale, *bias;
+  const void *x;
+  const float *xs;      // int8: [T][xs_cols]
+  void *out;
+  int64_t xld, old;     // strides of x's and out's rows in elements
+  int64_t T;
+  int n, k;
+  int xs_cols, xs_shift;  // a group of 64 has scale (group >> xs_shift), 31: the row's
+  bool qbf16;
+  LinX x_type;
+  LinOut out_type;
+};
+hipError_t launch_linear(const LinArgs &a, hipStream_t s);
 
 }  // namespace moe

@@ -1,10 +1,11 @@
-// Host side of the C ABI declared in include/norm.h: argument checks and launches.  Every check
+// Host side of the C ABI declared in include/norm.h and include/linear.h: argument checks and launches.  Every check
 // precedes every launch.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
 #include <cstdint>
 
+#include "../../include/linear.h"
 #include "../../include/norm.h"
 #include "checks.hpp"
 
@@ -91,6 +92,53 @@ moe_status moe_rms_norm(int64_t T, int32_t n_heads, int32_t width, moe_dtype dty
   a.fp16 = dtype == MOE_FP16;
   a.vec = vec;
   return launch_rms_norm(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_linear(const moe_linear_weights *w, int64_t T, const void *x, int64_t x_stride, moe_dtype x_dtype,
+                      const float *x_scale, int32_t x_group, void *out, int64_t out_stride, moe_dtype out_dtype,
+                      hipStream_t stream) {
+  if (!w) return MOE_ERR_NULL;
+  if (w->n < 1 || w->n > 1 << 24 || w->k < 64 || w->k > 1 << 17 || w->k % 64) return MOE_ERR_SHAPE;
+  if (w->qparam_dtype != MOE_FP16 && w->qparam_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (x_dtype != MOE_BF16 && x_dtype != MOE_FP16 && x_dtype != MOE_INT8) return MOE_ERR_DTYPE;
+  if (out_dtype != MOE_BF16 && out_dtype != MOE_FP16 && out_dtype != MOE_FP32) return MOE_ERR_DTYPE;
+  if (T < 0 || T > kMaxTokens || T * w->n > int64_t(1) << 40) return MOE_ERR_TOKENS;
+  const bool int8 = x_dtype == MOE_INT8;
+  if (x_group != 0 && (!int8 || (x_group != 64 && x_group != 128) || w->k % x_group)) return MOE_ERR_SHAPE;
+  const int64_t xe = int8 ? 1 : 2, oe = out_dtype == MOE_FP32 ? 4 : 2;
+  if (x_stride < 0 || x_stride > int64_t(1) << 38 || out_stride > int64_t(1) << 38) return MOE_ERR_SHAPE;
+  if (T > 1 && out_stride < w->n) return MOE_ERR_SHAPE;
+  if (!w->codes || !w->scale || !w->bias) return MOE_ERR_NULL;
+  if (!aligned(w->codes, 16) || !aligned(w->scale, 16) || !aligned(w->bias, 16)) return MOE_ERR_ALIGN;
+  if (T == 0) return MOE_OK;
+  if (!x || !out || int8 != (x_scale != nullptr)) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || x_stride * xe % 16 || !aligned(x_scale, 4) || !aligned(out, oe)) return MOE_ERR_ALIGN;
+  const uint64_t rows = ((uint64_t)w->n + 15) / 16 * 16, kp = ((uint64_t)w->k + 127) / 128 * 128;
+  const int cols = !int8 ? 0 : x_group ? w->k / x_group : 1;
+  const Span so{out, (uint64_t)(((T - 1) * out_stride + w->n) * oe)};
+  for (const Span &r : {Span{x, (uint64_t)(((T - 1) * x_stride + w->k) * xe)}, Span{x_scale, 4 * (uint64_t)T * cols},
+                        Span{w->codes, rows * kp / 2}, Span{w->scale, rows * kp / 32}, Span{w->bias, rows * kp / 32}})
+    if (overlap(so, r)) return MOE_ERR_ALIAS;
+  const moe_status st = device_ok();
+  if (st != MOE_OK) return st;
+  LinArgs a{};
+  a.codes = w->codes;
+  a.scale = static_cast<const uint16_t *>(w->scale);
+  a.bias = static_cast<const uint16_t *>(w->bias);
+  a.x = x;
+  a.xs = x_scale;
+  a.out = out;
+  a.xld = x_stride;
+  a.old = out_stride;
+  a.T = T;
+  a.n = w->n;
+  a.k = w->k;
+  a.xs_cols = cols;
+  a.xs_shift = x_group == 0 ? 31 : x_group == 64 ? 0 : 1;
+  a.qbf16 = w->qparam_dtype == MOE_BF16;
+  a.x_type = int8 ? LinX::Int8 : x_dtype == MOE_BF16 ? LinX::Bf16 : LinX::Fp16;
+  a.out_type = out_dtype == MOE_FP32 ? LinOut::Fp32 : out_dtype == MOE_BF16 ? LinOut::Bf16 : LinOut::Fp16;
+  return launch_linear(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 }  // extern "C"

@@ -86,3 +86,42 @@ def test_norm_refusals(B):
                dict(to=B.MOE_INT8, scale=4 * M + size - 4), dict(to=B.MOE_INT8, scale=8 * M),
                dict(to=B.MOE_INT8, scale=9 * M, s=H(4 * M, 768, 256))):
         assert _norm(B, **kw) == ALIAS, kw
+
+
+# ----------------------------------------------------------------------------- linear
+
+def _linear(B, w=None, T=5, x=4 * M, xld=192, xt=0, xs=None, group=0, out=5 * M, old=100, to=0, **kw):
+    d = dict(codes=M, scale=2 * M, bias=3 * M, n=100, k=192, qparam_dtype=B.MOE_FP16)
+    d.update(kw)
+    return _status(B, B.moe_linear, w or B.moe_linear_weights(**d), T, x, xld, xt, xs, group, out, old, to, 0)
+
+
+def test_linear_valid_calls_reach_the_device_check(B):
+    for xt in (B.MOE_BF16, B.MOE_FP16):
+        for to in (B.MOE_BF16, B.MOE_FP16, B.MOE_FP32):
+            assert _linear(B, xt=xt, to=to, qparam_dtype=B.MOE_BF16) == DEVICE
+    assert _linear(B, xt=B.MOE_INT8, xs=6 * M) == DEVICE and _linear(B, xt=B.MOE_INT8, xs=6 * M, group=64) == DEVICE
+    assert _linear(B, xt=B.MOE_INT8, xs=6 * M, group=128, k=256, xld=256) == DEVICE
+    assert _linear(B, T=1, xld=0, old=0) == DEVICE and _linear(B, xld=0) == DEVICE and _linear(B, T=70) == DEVICE
+    assert _linear(B, out=5 * M + 2) == DEVICE
+    assert _linear(B, T=0, x=None, out=None) == 0
+
+
+def test_linear_refusals(B):
+    for kw in (dict(n=0), dict(n=(1 << 24) + 1), dict(k=0), dict(k=32), dict(k=96), dict(k=(1 << 17) + 64), dict(group=64),
+               dict(xt=B.MOE_INT8, xs=6 * M, group=32), dict(xt=B.MOE_INT8, xs=6 * M, group=128), dict(xld=-192), dict(old=99)):
+        assert _linear(B, **kw) == SHAPE, kw
+    for kw in (dict(qparam_dtype=B.MOE_FP32), dict(xt=B.MOE_FP32), dict(xt=B.MOE_FP8), dict(to=B.MOE_INT8)):
+        assert _linear(B, **kw) == DTYPE, kw
+    assert _linear(B, T=-1) == TOKENS and _linear(B, T=(1 << 20) + 1) == TOKENS and _linear(B, T=1 << 20, n=1 << 21) == TOKENS
+    for kw in (dict(codes=None), dict(scale=None), dict(bias=None), dict(x=None), dict(out=None), dict(xt=B.MOE_INT8), dict(xs=6 * M)):
+        assert _linear(B, **kw) == NULL, kw
+    assert _status(B, B.moe_linear, None, 1, M, 64, 0, None, 0, 2 * M, 64, 0, 0) == NULL
+    for kw in (dict(codes=M + 8), dict(scale=2 * M + 2), dict(bias=3 * M + 8), dict(x=4 * M + 8), dict(xld=196), dict(out=5 * M + 1),
+               dict(out=5 * M + 2, to=B.MOE_FP32), dict(xt=B.MOE_INT8, xs=6 * M + 2), dict(xt=B.MOE_INT8, xs=6 * M, xld=200)):
+        assert _linear(B, **kw) == ALIGN, kw
+    # 112 padded rows of 256 padded k: 14336 bytes of codes, 896 of scales
+    for kw in (dict(out=4 * M + 2), dict(out=M + 14334), dict(out=2 * M + 894), dict(out=3 * M), dict(out=M - 2 * (4 * 100 + 100) + 2),
+               dict(xt=B.MOE_INT8, xs=5 * M + 4)):
+        assert _linear(B, **kw) == ALIAS, kw
+    assert _linear(B, out=M + 14336) == DEVICE
