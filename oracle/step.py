@@ -50,11 +50,13 @@ def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     first = int(np.argmax(l))
     if not temperature > 0:
         return first, 1.0, 1.0
-    with np.errstate(invalid="ignore"):
-        w = (l == np.inf).astype(np.float64) if top == np.inf else np.where(l > -np.inf, np.exp((l - top) / temperature), 0.0)
+    l = np.minimum(l, 1e250)
+    far = np.where(l > -np.inf, l - l[first], 0.0) / (temperature if temperature < np.inf else 1e300)
+    w = np.where(l > -np.inf, np.exp(far), 0.0)
     order = np.lexsort((np.arange(len(l)), -l))
     order = order[l[order] > -np.inf]
     slack = 1.0
+    min_p = min(min_p, 1.0)
     if top_k > 0:
         order = order[:top_k]
     if top_p < 1:
@@ -62,9 +64,9 @@ def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         slack = min(slack, np.abs(upto / upto[-1] - top_p).min())
         order = order[:max(1, int((upto < top_p * upto[-1]).sum()) + 1)]
     if min_p > 0:
-        near = np.abs(w[order] - min_p)
+        near = np.abs(w[order] / min_p - 1)
         slack = min(slack, near[near > 0].min() if (near > 0).any() else 1.0)
-    kept = np.sort(order[(w[order] >= min_p) | (order == first)] if min_p > 0 else order)
+    kept = np.sort(order[w[order] >= min_p] if min_p > 0 else order)
     upto = np.cumsum(w[kept])
     u = min(max(u, 0.0), 1.0) if u == u else 0.0
     slack = min(slack, np.abs(upto / upto[-1] - u).min())

@@ -49,7 +49,7 @@ EXPORTED = ("moe_plan_create", "moe_plan_destroy", "moe_workspace_init", "moe_wo
             "moe_pack_codes", "moe_status_string", "moe_version", "moe_gdn_scan", "moe_gdn_step", "moe_rope_freqs",
             "moe_rope_append", "moe_paged_attn_workspace", "moe_paged_attn", "moe_pages_workspace", "moe_pages_grow",
             "moe_pages_fork", "moe_pages_free", "moe_pages_compact", "moe_pages_copy", "moe_pages_check", "moe_rms_norm",
-            "moe_linear")
+            "moe_linear", "moe_sample_workspace", "moe_sample")
 
 # include/attn.h
 MOE_ROPE_NONE, MOE_ROPE_LINEAR, MOE_ROPE_NTK, MOE_ROPE_YARN = range(4)
@@ -191,6 +191,10 @@ def lib() -> ctypes.CDLL:
             L.moe_rms_norm.argtypes = [I64, I32, I32, ctypes.c_int, HD, HD, HD, P, F32, F32, ctypes.c_int, HD, I32, P, P]
             L.moe_linear.restype = ctypes.c_int
             L.moe_linear.argtypes = [P, I64, P, I64, ctypes.c_int, P, I32, P, I64, ctypes.c_int, P]
+            L.moe_sample_workspace.restype = ctypes.c_int
+            L.moe_sample_workspace.argtypes = [I64, I32, ctypes.POINTER(SZ)]
+            L.moe_sample.restype = ctypes.c_int
+            L.moe_sample.argtypes = [I64, I32, P, I64, ctypes.c_int, P, P, P, P, P, P, P, P, SZ, P]
             L.moe_status_string.restype = ctypes.c_char_p
             L.moe_status_string.argtypes = [ctypes.c_int]
             L.moe_version.restype = ctypes.c_char_p
@@ -381,6 +385,19 @@ def moe_linear(w: moe_linear_weights, T: int, x_ptr: int | None, x_stride: int, 
                x_group: int, out_ptr: int | None, out_stride: int, out_dtype: int, stream: int) -> None:
     _check("moe_linear", lib().moe_linear(_opt(w), T, x_ptr, x_stride, x_dtype, x_scale_ptr, x_group, out_ptr, out_stride,
                                           out_dtype, stream))
+
+
+def moe_sample_workspace(R: int, V: int) -> int:
+    size = ctypes.c_size_t()
+    _check("moe_sample_workspace", (_lib or lib()).moe_sample_workspace(R, V, size))
+    return size.value
+
+
+def moe_sample(R: int, V: int, logits_ptr: int | None, row_stride: int, dtype: int, u_ptr: int | None,
+               temperature_ptr: int | None, top_k_ptr: int | None, top_p_ptr: int | None, min_p_ptr: int | None,
+               token_ptr: int | None, prob_ptr: int | None, ws_ptr: int | None, ws_bytes: int, stream: int) -> None:
+    _check("moe_sample", lib().moe_sample(R, V, logits_ptr, row_stride, dtype, u_ptr, temperature_ptr, top_k_ptr, top_p_ptr,
+                                          min_p_ptr, token_ptr, prob_ptr, ws_ptr, ws_bytes, stream))
 
 
 def moe_pack_qparams(src_ptr: int, dst_ptr: int, rows: int, k: int, stream: int) -> None:

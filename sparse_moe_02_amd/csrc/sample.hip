@@ -1,0 +1,690 @@
+// Choice of tokens from logits, with the random numbers given.
+//
+// Weights w = 2^(y - y_max), y = l log2(e) / temperature in binary64, are held as 64-bit fixed point,
+// so that sums are the same in any order.  What is kept is a prefix of the tokens sorted by logit
+// (descending) and index, and a token's place in that order is one 64-bit number (the logit's bits, ordered, over the
+// inverted index), so every cut is one such number, and nothing is sorted.
+//
+//   k_sample_chunks  a workgroup for each 4096 logits: their maximum, and, relative to the power of two
+//                    above it, the count and the sum of weights of each quarter of an octave.  Reads
+//                    every logit once.  Without filters only the sum.
+//   k_sample_pick    a workgroup a row: adds the chunks' bins up, which gives the bin that each cut
+//                    lies in; collects the tokens of that bin (or, for top-k, of all bins down to it) and selects
+//                    among them, a byte of their numbers at a time; the kept weight of each
+//                    chunk gives the chunk that u falls into, which is read once more.  Where a cut's bin
+//                    holds more than kList tokens, the selection goes over the row itself.
+//
+// Bound: memory for many rows, latency for few.
+#include "common.hpp"
+#include "serve.hpp"
+
+#pragma clang fp contract(off)
+
+namespace moe {
+
+namespace {
+
+constexpr int kChunk = kSampleChunk, kBins = kSampleBins, kPerOctave = 4;
+constexpr int kThreads = 256;       // of k_sample_chunks
+constexpr int kPick = 1024;         // of k_sample_pick
+constexpr int kList = 4096;         // tokens that are selected among in LDS
+constexpr int kMaxChunks = (1 << 20) / kChunk + 1;
+constexpr int kCopies = 4;          // of a chunk's bins, by lane, against conflicts
+
+// 2^(j / 64)
+__constant__ const double kPow[64] = {
+    0x1.0000000000000p+0, 0x1.02c9a3e778061p+0, 0x1.059b0d3158574p+0, 0x1.0874518759bc8p+0,
+    0x1.0b5586cf9890fp+0, 0x1.0e3ec32d3d1a2p+0, 0x1.11301d0125b51p+0, 0x1.1429aaea92de0p+0,
+    0x1.172b83c7d517bp+0, 0x1.1a35beb6fcb75p+0, 0x1.1d4873168b9aap+0, 0x1.2063b88628cd6p+0,
+    0x1.2387a6e756238p+0, 0x1.26b4565e27cddp+0, 0x1.29e9df51fdee1p+0, 0x1.2d285a6e4030bp+0,
+    0x1.306fe0a31b715p+0, 0x1.33c08b26416ffp+0, 0x1.371a7373aa9cbp+0, 0x1.3a7db34e59ff7p+0,
+    0x1.3dea64c123422p+0, 0x1.4160a21f72e2ap+0, 0x1.44e086061892dp+0, 0x1.486a2b5c13cd0p+0,
+    0x1.4bfdad5362a27p+0, 0x1.4f9b2769d2ca7p+0, 0x1.5342b569d4f82p+0, 0x1.56f4736b527dap+0,
+    0x1.5ab07dd485429p+0, 0x1.5e76f15ad2148p+0, 0x1.6247eb03a5585p+0, 0x1.6623882552225p+0,
+    0x1.6a09e667f3bcdp+0, 0x1.6dfb23c651a2fp+0, 0x1.71f75e8ec5f74p+0, 0x1.75feb564267c9p+0,
+    0x1.7a11473eb0187p+0, 0x1.7e2f336cf4e62p+0, 0x1.82589994cce13p+0, 0x1.868d99b4492edp+0,
+    0x1.8ace5422aa0dbp+0, 0x1.8f1ae99157736p+0, 0x1.93737b0cdc5e5p+0, 0x1.97d829fde4e50p+0,
+    0x1.9c49182a3f090p+0, 0x1.a0c667b5de565p+0, 0x1.a5503b23e255dp+0, 0x1.a9e6b5579fdbfp+0,
+    0x1.ae89f995ad3adp+0, 0x1.b33a2b84f15fbp+0, 0x1.b7f76f2fb5e47p+0, 0x1.bcc1e904bc1d2p+0,
+    0x1.c199bdd85529cp+0, 0x1.c67f12e57d14bp+0, 0x1.cb720dcef9069p+0, 0x1.d072d4a07897cp+0,
+    0x1.d5818dcfba487p+0, 0x1.da9e603db3285p+0, 0x1.dfc97337b9b5fp+0, 0x1.e502ee78b3ff6p+0,
+    0x1.ea4afa2a490dap+0, 0x1.efa1bee615a27p+0, 0x1.f50765b6e4540p+0, 0x1.fa7c1819e90d8p+0};
+
+struct Row {
+  double c;          // log2(e) / temperature
+  double p, m;       // top_p (1: off), min_p (0: off)
+  int k;             // 0: off
+  bool greedy, filtered;
+};
+__device__ __forceinline__ Row read_row(const SampleArgs &a, int r) {
+  Row o;
+  const float t = a.temperature ? a.temperature[r] : 1.0f;
+  o.greedy = !(t > 0.0f);
+  o.c = 1.4426950408889634 / (double)t;
+  const int k = a.top_k ? a.top_k[r] : 0;
+  o.k = k > 0 && k < a.V ? k : 0;
+  const float p = a.top_p ? a.top_p[r] : 1.0f, m = a.min_p ? a.min_p[r] : 0.0f;
+  o.p = p < 1.0f ? fmaxf(p, 0.0f) : 1.0;
+  o.m = m > 0.0f ? fminf(m, 1.0f) : 0.0;
+  o.filtered = o.k > 0 || o.p < 1.0 || o.m > 0.0;
+  return o;
+}
+
+// A logit's exponent; -infinity for tokens that are out.
+__device__ __forceinline__ double exponent_of(float l, double c) {
+  return l == -INFINITY ? -INFINITY : (l == INFINITY ? 1e250 : (double)l) * c;
+}
+// 2^t, t <= 0, times 2^bits: 2^f, 0 <= f < 1/64, by its series (off by less than 2^-48), times the table's
+// 2^(j / 64)
+__device__ __forceinline__ double weight_of(double t, int bits, const double *pow) {
+  t = fmax(t, -2048.0);  // (so are those that are out: 0)
+  const double n = __builtin_floor(t * 64.0);
+  const int i = (int)n;
+  const double x = (t - n * 0.015625) * 0.69314718055994531;
+  double s = __builtin_fma(x, 1.0 / 120, 1.0 / 24);
+  s = __builtin_fma(x, s, 1.0 / 6);
+  s = __builtin_fma(x, s, 0.5);
+  s = __builtin_fma(x, s, 1.0);
+  s = __builtin_fma(x, s, 1.0);
+  return __builtin_ldexp(s * pow[i & 63], (i >> 6) + bits);
+}
+// Rounded to a whole number (below 2^52).
+__device__ __forceinline__ uint64_t fixed_of(double w) {
+  return (uint64_t)__double_as_longlong(w + 0x1p52) & 0xfffffffffffffull;
+}
+
+// Order-preserving bits of a logit (both zeros alike).
+__device__ __forceinline__ uint32_t key_of(float l) {
+  const uint32_t b = __float_as_uint(l + 0.0f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float logit_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+// A token's place in the descending order.
+__device__ __forceinline__ uint64_t place_of(float l, int i) { return (uint64_t)key_of(l) << 32 | (0xffffffffu - (uint32_t)i); }
+__device__ __forceinline__ int index_of(uint64_t place) { return (int)(0xffffffffu - (uint32_t)place); }
+
+// A row of logits.  Rows may start anywhere; they are read in 16-byte blocks of kVec elements, counted from
+// the block that holds the first one (element i is number i + skip), and one by one where a block is
+// not the row's alone.
+template <int TYPE>
+struct Logits {
+  static constexpr int kSize = TYPE == 0 ? 4 : 2, kVec = 16 / kSize;
+  const uint8_t *base;
+  int skip, V;
+  __device__ __forceinline__ Logits(const SampleArgs &a, int r) {
+    const uint8_t *p = (const uint8_t *)a.logits + (int64_t)r * a.ld * kSize;
+    skip = (int)((uintptr_t)p & 15) / kSize;
+    base = p - skip * kSize;
+    V = a.V;
+  }
+  __device__ __forceinline__ float one(uint32_t w) const {
+    const float l = TYPE == 0 ? __uint_as_float(w) : TYPE == 1 ? bf16_to_f32((uint16_t)w) : fp16_to_f32((uint16_t)w);
+    return l == l ? l : -INFINITY;
+  }
+  // numbers n .. n + kVec - 1 (n a multiple of kVec); -infinity outside the row
+  __device__ __forceinline__ void load(int n, float (&o)[kVec]) const {
+    if (n >= skip && n + kVec <= skip + V) {
+      const u32x4 w = *(const u32x4 *)(base + (int64_t)n * kSize);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) o[e] = one(TYPE == 0 ? w[e % 4] : e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu);
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      o[e] = -INFINITY;
+      if (n + e < skip || n + e >= skip + V) continue;
+      if constexpr (TYPE == 0) o[e] = one(*(const uint32_t *)(base + (int64_t)(n + e) * 4));
+      else o[e] = one(*(const uint16_t *)(base + (int64_t)(n + e) * 2));
+    }
+  }
+};
+
+__device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t v, int d) { return (uint64_t)__shfl_xor((unsigned long long)v, d, 64); }
+__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += shfl_xor_u64(v, d);
+  return v;
+}
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = max(v, shfl_xor_u64(v, d));
+  return v;
+}
+__device__ __forceinline__ uint64_t wave_scan_u64(uint64_t v) {  // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t o = (uint64_t)__shfl_up((unsigned long long)v, d, 64);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+__device__ __forceinline__ void lds_add(uint64_t *p, uint64_t v) { atomicAdd((unsigned long long *)p, (unsigned long long)v); }
+
+__device__ __forceinline__ int bin_of(double t) { return t > -(double)kBins / kPerOctave ? min(kBins - 1, (int)(-t * kPerOctave)) : kBins - 1; }
+
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads) k_sample_chunks(SampleArgs a) {
+  using L = Logits<TYPE>;
+  constexpr int kVecs = kChunk / kThreads / L::kVec;  // blocks of a thread
+  __shared__ double pow[64];
+  __shared__ uint64_t mass[kCopies][kBins];
+  __shared__ uint32_t count[kCopies][kBins];
+  __shared__ float tops[kThreads / 64];
+  __shared__ uint64_t sums[kThreads / 64];
+  const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
+  const Row row = read_row(a, r);
+  const L logits(a, r);
+  if (tid < 64) pow[tid] = kPow[tid];
+  for (int i = tid; i < kCopies * kBins; i += kThreads) {
+    (&mass[0][0])[i] = 0;
+    (&count[0][0])[i] = 0;
+  }
+  float l[kVecs][L::kVec];
+  float top = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < kVecs; ++q) {
+    logits.load(c * kChunk + (q * kThreads + tid) * L::kVec, l[q]);
+#pragma unroll
+    for (int e = 0; e < L::kVec; ++e) top = fmaxf(top, l[q][e]);
+  }
+  top = wave_max(top);
+  if ((tid & 63) == 0) tops[tid >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+  SampleChunk *out = a.chunk + (int64_t)r * a.C + c;
+  if (row.greedy) {
+    uint64_t best = 0;
+#pragma unroll
+    for (int q = 0; q < kVecs; ++q)
+#pragma unroll
+      for (int e = 0; e < L::kVec; ++e)
+        if (l[q][e] == top && top > -INFINITY)
+          best = max(best, place_of(top, c * kChunk + (q * kThreads + tid) * L::kVec + e - logits.skip));
+    best = wave_max_u64(best);
+    if ((tid & 63) == 0) sums[tid >> 6] = best;
+    __syncthreads();
+    if (tid == 0) out->best = max(max(sums[0], sums[1]), max(sums[2], sums[3]));
+    return;
+  }
+  const double y0 = exponent_of(top, row.c), anchor = __builtin_ceil(y0);
+  uint64_t sum = 0;
+  const int copy = tid % kCopies;
+  if (top > -INFINITY) {
+#pragma unroll
+    for (int q = 0; q < kVecs; ++q)
+#pragma unroll
+      for (int e = 0; e < L::kVec; ++e) {
+        const double t = exponent_of(l[q][e], row.c) - anchor;
+        const uint64_t w = l[q][e] == -INFINITY ? 0 : fixed_of(weight_of(t, a.bits, pow));
+        sum += w;
+        if (row.filtered && l[q][e] > -INFINITY) {
+          const int b = bin_of(t);
+          lds_add(&mass[copy][b], w);
+          atomicAdd(&count[copy][b], 1u);
+        }
+      }
+  }
+  sum = wave_sum_u64(sum);
+  if ((tid & 63) == 0) sums[tid >> 6] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    out->top = y0;
+    out->total = sums[0] + sums[1] + sums[2] + sums[3];
+  }
+  if (!row.filtered) return;
+  for (int b = tid; b < kBins; b += kThreads) {
+    uint64_t m = 0;
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      m += mass[i][b];
+      n += count[i][b];
+    }
+    const int64_t at = ((int64_t)r * a.C + c) * kBins + b;
+    a.mass[at] = m;
+    a.count[at] = n;
+  }
+}
+
+// What the threads of k_sample_pick share.
+struct Shared {
+  double pow[64];
+  double anchor[kMaxChunks];
+  int shift[kMaxChunks];       // octaves of a chunk's anchor below the row's (64: out of reach)
+  uint64_t kept[kMaxChunks];   // kept weight of the chunks, then the sums up to each
+  uint64_t mass[kBins];        // of the row; then the sums down to each bin
+  uint32_t count[kBins];
+  uint64_t sel_mass[256];      // of a selection's step
+  uint32_t sel_count[256];
+  uint64_t red[kPick / 64];
+  uint64_t found[4];
+  int n;                       // tokens in the list
+};
+
+// The whole row, or the list of its tokens in LDS, as a set of (place, weight).
+struct List {
+  const uint64_t *place, *weight;
+  int n;
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    for (int i = threadIdx.x; i < n; i += kPick) f(place[i], weight[i]);
+  }
+};
+template <int TYPE>
+struct Whole {
+  const Logits<TYPE> &logits;
+  double c, anchor;
+  const double *pow;
+  int bits;
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    constexpr int kVec = Logits<TYPE>::kVec;
+    for (int n = threadIdx.x * kVec; n < logits.skip + logits.V; n += kPick * kVec) {
+      float l[kVec];
+      logits.load(n, l);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e)
+        if (l[e] > -INFINITY) f(place_of(l[e], n + e - logits.skip), fixed_of(weight_of(exponent_of(l[e], c) - anchor, bits, pow)));
+    }
+  }
+};
+
+// The least place `at` such that the tokens from it on (of those from `least` on) are at least `want` in number, or
+// weigh that much, and their weight; all of them where they do not reach that.  A byte of the places at a time,
+// from the top.
+struct Cut {
+  uint64_t at, weight;
+};
+template <class S>
+__device__ Cut select_from(const S &set, bool by_weight, uint64_t want, uint64_t least, Shared &sh) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  uint64_t prefix = 0, above = 0;
+  // the least place of the set that begins with the prefix (there are tokens outside the set between it and
+  // the prefix followed by zeros)
+  auto least_of = [&](int shift) {
+    uint64_t v = ~uint64_t(0);
+    set.each([&](uint64_t place, uint64_t) {
+      if (place >= least && (shift > 56 || place >> shift == prefix)) v = min(v, place);
+    });
+    v = ~wave_max_u64(~v);
+    if (lane == 0) sh.red[tid >> 6] = v;
+    __syncthreads();
+    v = sh.red[lane % (kPick / 64)];
+    __syncthreads();
+    return ~wave_max_u64(~v);
+  };
+  for (int shift = 56; shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256; i += kPick) {
+      sh.sel_mass[i] = 0;
+      sh.sel_count[i] = 0;
+    }
+    __syncthreads();
+    set.each([&](uint64_t place, uint64_t w) {
+      if (place < least || (shift < 56 && place >> (shift + 8) != prefix)) return;
+      const int b = (int)(place >> shift & 255);
+      lds_add(&sh.sel_mass[b], w);
+      atomicAdd(&sh.sel_count[b], 1u);
+    });
+    __syncthreads();
+    if (tid < 64) {
+      // lane i has bins 255 - 4 i down to 252 - 4 i
+      uint64_t own[4], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = 255 - 4 * lane - i;
+        own[i] = by_weight ? sh.sel_mass[b] : sh.sel_count[b];
+        sum += own[i];
+      }
+      const uint64_t upto = wave_scan_u64(sum);
+      const uint64_t hit = __ballot(upto >= want);
+      uint64_t before = upto - sum;
+      int bin = -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (bin < 0 && before + own[i] >= want) bin = 255 - 4 * lane - i;
+        if (bin < 0) before += own[i];
+      }
+      if (hit == 0) {
+        if (lane == 0) sh.found[0] = 256;
+      } else if (lane == __builtin_ctzll(hit)) {
+        sh.found[0] = (uint64_t)bin;
+        sh.found[1] = before;
+      }
+      // (weight above the bin)
+      uint64_t w = 0;
+      const int cut = hit == 0 ? -1 : __shfl(bin, __builtin_ctzll(hit), 64);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (255 - 4 * lane - i > cut) w += sh.sel_mass[255 - 4 * lane - i];
+      w = wave_sum_u64(w);
+      if (lane == 0) sh.found[2] = w;
+    }
+    __syncthreads();
+    const int bin = (int)sh.found[0];
+    const uint64_t before = sh.found[1], over = sh.found[2];
+    above += over;
+    if (bin > 255) {  // (in the first step only: the bin of a step reaches what is wanted of the next)
+      __syncthreads();
+      return Cut{least_of(64), above};
+    }
+    const uint32_t n = sh.sel_count[bin];
+    const uint64_t m = sh.sel_mass[bin];
+    __syncthreads();
+    prefix = prefix << 8 | (uint64_t)bin;
+    want -= before;
+    if (shift == 0) return Cut{prefix, above + m};
+    if (n == 1 || (!by_weight && n == want)) return Cut{least_of(shift), above + m};  // the whole bin
+  }
+  return Cut{least, above};  // (not reached)
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
+  using L = Logits<TYPE>;
+  extern __shared__ __align__(16) uint8_t lds_raw[];
+  uint64_t *places = (uint64_t *)lds_raw, *weights = places + kList;
+  __shared__ Shared sh;
+  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Row row = read_row(a, r);
+  const L logits(a, r);
+  const SampleChunk *chunk = a.chunk + (int64_t)r * a.C;
+  if (tid < 64) sh.pow[tid] = kPow[tid];
+
+  auto block_max = [&](uint64_t v) {
+    v = wave_max_u64(v);
+    if (lane == 0) sh.red[wave] = v;
+    __syncthreads();
+    v = sh.red[lane % (kPick / 64)];
+    __syncthreads();
+    return wave_max_u64(v);
+  };
+  if (row.greedy) {
+    uint64_t best = 0;
+    for (int c = tid; c < a.C; c += kPick) best = max(best, chunk[c].best);
+    best = block_max(best);
+    if (tid == 0) {
+      a.token[r] = best ? index_of(best) : -1;
+      if (a.prob) a.prob[r] = best ? 1.0f : 0.0f;
+    }
+    return;
+  }
+  // the largest exponent: binary64 numbers as ordered bits
+  auto ordered = [](double y) {
+    const uint64_t b = (uint64_t)__double_as_longlong(y + 0.0);
+    return b >> 63 ? ~b : b | uint64_t(1) << 63;
+  };
+  uint64_t most = 0;
+  for (int c = tid; c < a.C; c += kPick) {
+    const double y = chunk[c].top;
+    sh.anchor[c] = __builtin_ceil(y);
+    sh.kept[c] = 0;
+    most = max(most, ordered(y));
+  }
+  most = block_max(most);
+  const double y0 = __longlong_as_double((long long)(most >> 63 ? most & ~(uint64_t(1) << 63) : ~most));
+  if (y0 == -INFINITY) {
+    if (tid == 0) {
+      a.token[r] = -1;
+      if (a.prob) a.prob[r] = 0.0f;
+    }
+    return;
+  }
+  const double anchor = __builtin_ceil(y0);
+  for (int c = tid; c < a.C; c += kPick) {
+    const double d = anchor - sh.anchor[c];
+    sh.shift[c] = d < 64.0 ? (int)d : 64;
+  }
+  for (int i = tid; i < kBins; i += kPick) {
+    sh.mass[i] = 0;
+    sh.count[i] = 0;
+  }
+  __syncthreads();
+
+  uint64_t least = 0;          // places that are kept are at least this
+  double floor = -INFINITY;    // and exponents this
+  bool whole = false;          // the selection went over the row: weights relative to its anchor
+  if (!row.filtered) {
+    for (int c = tid; c < a.C; c += kPick) sh.kept[c] = sh.shift[c] < 64 ? chunk[c].total >> sh.shift[c] : 0;
+  } else {
+    const uint64_t *mass = a.mass + (int64_t)r * a.C * kBins;
+    const uint32_t *count = a.count + (int64_t)r * a.C * kBins;
+    // a chunk's bin among the row's
+    auto row_bin = [&](int c, int b) { return b == kBins - 1 ? b : min(kBins - 1, b + kPerOctave * sh.shift[c]); };
+    auto scaled = [&](int c, uint64_t m) { return sh.shift[c] < 64 ? m >> sh.shift[c] : 0; };
+    for (int i = tid; i < a.C * kBins; i += kPick) {
+      const uint32_t n = count[i];
+      if (n == 0) continue;
+      const int c = i / kBins, b = row_bin(c, i % kBins);
+      atomicAdd(&sh.count[b], n);
+      lds_add(&sh.mass[b], scaled(c, mass[i]));
+    }
+    __syncthreads();
+    if (wave == 0) {  // sums down to each bin
+      constexpr int kOwn = kBins / 64;
+      uint64_t m[kOwn], n[kOwn], ms = 0, ns = 0;
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        m[i] = ms += sh.mass[lane * kOwn + i];
+        n[i] = ns += sh.count[lane * kOwn + i];
+      }
+      const uint64_t mb = wave_scan_u64(ms) - ms, nb = wave_scan_u64(ns) - ns;
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        sh.mass[lane * kOwn + i] = mb + m[i];
+        sh.count[lane * kOwn + i] = (uint32_t)(nb + n[i]);
+      }
+    }
+    __syncthreads();
+    auto mass_above = [&](int b) { return b > 0 ? sh.mass[b - 1] : 0; };
+    auto count_above = [&](int b) { return b > 0 ? sh.count[b - 1] : 0u; };
+
+    int lo = 0, hi = -1;  // bins of which the list holds all tokens
+    // collects the tokens of bins b0 .. b1; false where they are too many
+    auto gather = [&](int b0, int b1) {
+      if (sh.count[b1] - count_above(b0) > (uint32_t)kList) return false;
+      __syncthreads();
+      if (tid == 0) sh.n = 0;
+      __syncthreads();
+      for (int c = wave; c < a.C; c += kPick / 64) {
+        const int s = sh.shift[c];
+        bool some = false;
+        for (int b = lane; b < kBins; b += 64) {
+          const int rb = row_bin(c, b);
+          some |= rb >= b0 && rb <= b1 && count[c * kBins + b] > 0;
+        }
+        if (!__ballot(some)) continue;
+        for (int n = c * kChunk + lane * L::kVec; n < (c + 1) * kChunk; n += 64 * L::kVec) {
+          float l[L::kVec];
+          logits.load(n, l);
+#pragma unroll
+          for (int e = 0; e < L::kVec; ++e) {
+            if (l[e] == -INFINITY) continue;
+            const double t = exponent_of(l[e], row.c) - sh.anchor[c];
+            const int b = row_bin(c, bin_of(t));
+            if (b < b0 || b > b1) continue;
+            const int at = atomicAdd(&sh.n, 1);
+            places[at] = place_of(l[e], n + e - logits.skip);
+            weights[at] = s < 64 ? fixed_of(weight_of(t, a.bits, sh.pow)) >> s : 0;
+          }
+        }
+      }
+      __syncthreads();
+      lo = b0;
+      hi = b1;
+      return true;
+    };
+    auto first_bin = [&](auto enough) {  // the first bin down to which `enough` holds
+      for (int b = 0; b < kBins; b += 64) {
+        const uint64_t yes = __ballot(enough(b + lane));
+        if (yes) return b + (int)__builtin_ctzll(yes);
+      }
+      return kBins - 1;
+    };
+
+    int cut = kBins;  // the bin of the cut
+    uint64_t total = sh.mass[kBins - 1];
+    if (row.k > 0 && (uint32_t)row.k < sh.count[kBins - 1]) {
+      cut = first_bin([&](int b) { return sh.count[b] >= (uint32_t)row.k; });
+      const int from = sh.count[cut] <= (uint32_t)kList ? 0 : cut;
+      if (gather(from, cut)) {
+        const Cut o = select_from(List{places, weights, sh.n}, false, (uint64_t)row.k - count_above(lo), 0, sh);
+        least = o.at;
+        total = mass_above(lo) + o.weight;
+      } else {
+        whole = true;
+      }
+    }
+    // of a share of the total: as a whole number, at least 1
+    auto share = [](double p, uint64_t t) {
+      const double x = __builtin_ceil(p * (double)t);
+      return max(min((uint64_t)x, t), uint64_t(1));
+    };
+    if (!whole && row.p < 1.0) {
+      const uint64_t want = share(row.p, total);
+      const int b = min(cut, first_bin([&](int i) { return sh.mass[i] >= want; }));
+      if ((lo <= b && b <= hi) || gather(b, b)) {
+        const uint64_t over = mass_above(lo);
+        least = max(least, select_from(List{places, weights, sh.n}, true, want > over ? want - over : 1, least, sh).at);
+        cut = b;
+      } else {
+        whole = true;
+      }
+    }
+    if (row.m > 0.0) floor = y0 + log2(row.m);
+    if (!whole && row.m > 0.0) {
+      const int b = bin_of(floor - anchor);
+      if (b <= cut && ((lo <= b && b <= hi) || gather(b, b))) cut = b;
+      else if (b <= cut) whole = true;
+    }
+    if (whole) {
+      const Whole<TYPE> set{logits, row.c, anchor, sh.pow, a.bits};
+      least = 0;
+      if (row.k > 0 && (uint32_t)row.k < sh.count[kBins - 1]) {
+        const Cut o = select_from(set, false, (uint64_t)row.k, 0, sh);
+        least = o.at;
+        total = o.weight;
+      } else {
+        total = sh.mass[kBins - 1];
+      }
+      if (row.p < 1.0) least = max(least, select_from(set, true, share(row.p, total), least, sh).at);
+      set.each([&](uint64_t place, uint64_t w) {
+        if (place >= least && exponent_of(logit_of((uint32_t)(place >> 32)), row.c) >= floor)
+          lds_add(&sh.kept[(index_of(place) + logits.skip) / kChunk], w);
+      });
+    } else {
+      const bool none = hi < 0;  // no cut: all bins
+      for (int i = tid; i < a.C * kBins; i += kPick) {
+        const uint32_t n = count[i];
+        const int c = i / kBins;
+        if (n > 0 && (none || row_bin(c, i % kBins) < lo)) lds_add(&sh.kept[c], scaled(c, mass[i]));
+      }
+      for (int i = tid; !none && i < sh.n; i += kPick)
+        if (places[i] >= least && exponent_of(logit_of((uint32_t)(places[i] >> 32)), row.c) >= floor)
+          lds_add(&sh.kept[(index_of(places[i]) + logits.skip) / kChunk], weights[i]);
+    }
+  }
+  __syncthreads();
+
+  // sums up to each chunk
+  if (wave == 0) {
+    uint64_t before = 0;
+    for (int c0 = 0; c0 < a.C; c0 += 64) {
+      const uint64_t v = c0 + lane < a.C ? sh.kept[c0 + lane] : 0;
+      const uint64_t upto = before + wave_scan_u64(v);
+      if (c0 + lane < a.C) sh.kept[c0 + lane] = upto;
+      before = (uint64_t)__shfl((unsigned long long)upto, 63, 64);
+    }
+  }
+  __syncthreads();
+  const uint64_t total = sh.kept[a.C - 1];
+  const float u0 = a.u[r];
+  const double u = u0 > 0.0f ? fminf(u0, 1.0f) : 0.0;
+  const uint64_t want = min((uint64_t)(u * (double)total), total - 1);  // (the first sum above it is wanted)
+  int c = 0;
+  {
+    int lo = 0, hi = a.C - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (sh.kept[mid] > want) hi = mid;
+      else lo = mid + 1;
+    }
+    c = lo;
+  }
+  // in the chunk, in its own weights
+  const int shift = whole ? 0 : sh.shift[c];
+  const double from = whole ? anchor : sh.anchor[c];
+  uint64_t target = (want - (c > 0 ? sh.kept[c - 1] : 0)) << shift;
+  constexpr int kHave = kChunk / L::kVec;  // threads with logits
+  float l[L::kVec];
+  uint64_t w[L::kVec], mine = 0, upto = 0, before = 0, all = 0;
+  const int n = c * kChunk + tid * L::kVec;
+#pragma unroll
+  for (int e = 0; e < L::kVec; ++e) l[e] = -INFINITY;
+  if (tid < kHave) logits.load(n, l);
+  for (int pass = 0; pass < 2 && all == 0; ++pass) {
+    mine = 0;
+#pragma unroll
+    for (int e = 0; e < L::kVec; ++e) {
+      const double y = exponent_of(l[e], row.c);
+      const bool keep = l[e] > -INFINITY && place_of(l[e], n + e - logits.skip) >= least && y >= floor;
+      w[e] = keep ? fixed_of(weight_of(y - from, a.bits, sh.pow)) : 0;
+      mine += w[e];
+    }
+    upto = wave_scan_u64(mine);
+    __syncthreads();
+    if (lane == 63) sh.red[wave] = upto;
+    __syncthreads();
+    before = all = 0;
+    for (int i = 0; i < kPick / 64; ++i) {
+      if (i < wave) before += sh.red[i];
+      all += sh.red[i];
+    }
+    // (the chunk has kept weight; a token that lies within a rounding of its bin's edge could be in the bins
+    // that are kept and yet behind the cut, and alone: then the chunk's tokens are taken as they are)
+    least = 0;
+    floor = -INFINITY;
+  }
+  if (all == 0) return;
+  target = min(target, all - 1);
+  before += upto - mine;
+  if (target >= before && target < before + mine) {
+    uint64_t sum = before;
+#pragma unroll
+    for (int e = 0; e < L::kVec; ++e) {
+      if (target >= sum && target < sum + w[e]) {
+        a.token[r] = n + e - logits.skip;
+        if (a.prob)
+          a.prob[r] = (float)(__builtin_ldexp(weight_of(exponent_of(l[e], row.c) - from, a.bits, sh.pow), -shift) / (double)total);
+      }
+      sum += w[e];
+    }
+  }
+}
+
+template <int TYPE>
+hipError_t launch(const SampleArgs &a, hipStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  constexpr int lds = 2 * kList * 8;
+  const hipError_t e = allow_lds(k_sample_pick<TYPE>, lds, done);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_sample_chunks<TYPE>), dim3(a.C, a.R), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((k_sample_pick<TYPE>), dim3(a.R), dim3(kPick), lds, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_sample(const SampleArgs &a, hipStream_t s) {
+  if (a.R <= 0) return hipSuccess;
+  switch (a.type) {
+    case 0: return launch<0>(a, s);
+    case 1: return launch<1>(a, s);
+    case 2: return launch<2>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace moe

@@ -174,4 +174,28 @@ struct LinArgs {
 };
 hipError_t launch_linear(const LinArgs &a, hipStream_t s);
 
+// Choice of tokens from logits (sample.hip).
+constexpr int kSampleChunk = 4096;  // logits of one workgroup of the first kernel
+constexpr int kSampleBins = 128;    // bins of a chunk's weights, a quarter of an octave each
+// Of a chunk: its largest logit (times log2(e) / temperature) and the sum of its weights; for a
+// temperature of 0 the largest logit's sort key and index.
+struct SampleChunk {
+  double top;
+  uint64_t total, best;
+};
+struct SampleArgs {
+  const void *logits;
+  int64_t ld;
+  int type;  // 0: fp32, 1: bf16, 2: fp16
+  const float *u, *temperature, *top_p, *min_p;
+  const int32_t *top_k;
+  int32_t *token;
+  float *prob;
+  int R, V, C, bits;  // C: chunks of a row; bits of a weight behind 1
+  SampleChunk *chunk;  // [R][C]
+  uint64_t *mass;      // [R][C][bins]
+  uint32_t *count;     // [R][C][bins]
+};
+hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
+
 }  // namespace moe

@@ -7,6 +7,7 @@
 
 #include "../../include/linear.h"
 #include "../../include/norm.h"
+#include "../../include/sample.h"
 #include "checks.hpp"
 
 using namespace moe;
@@ -30,6 +31,22 @@ bool same(const moe_heads &a, const moe_heads &b) {
 }
 Rows dev_rows(const moe_heads *x) {
   return x ? Rows{const_cast<void *>(x->p), x->token_stride, x->head_stride} : Rows{};
+}
+
+// Places of moe_sample's arrays in its workspace.
+struct SampleWs {
+  int chunks;
+  size_t mass, count, total;
+};
+SampleWs sample_ws(int64_t R, int32_t V) {
+  auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+  SampleWs w;
+  w.chunks = (V + 7 + kSampleChunk - 1) / kSampleChunk;  // (a row may start up to 7 elements behind a 16-byte block)
+  const size_t n = (size_t)R * w.chunks;
+  w.mass = up(n * sizeof(SampleChunk));
+  w.count = w.mass + up(n * kSampleBins * 8);
+  w.total = w.count + up(n * kSampleBins * 4);
+  return w;
 }
 
 }  // namespace
@@ -139,6 +156,63 @@ moe_status moe_linear(const moe_linear_weights *w, int64_t T, const void *x, int
   a.x_type = int8 ? LinX::Int8 : x_dtype == MOE_BF16 ? LinX::Bf16 : LinX::Fp16;
   a.out_type = out_dtype == MOE_FP32 ? LinOut::Fp32 : out_dtype == MOE_BF16 ? LinOut::Bf16 : LinOut::Fp16;
   return launch_linear(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_sample_workspace(int64_t R, int32_t V, size_t *bytes) {
+  if (!bytes) return MOE_ERR_NULL;
+  if (R < 0 || R > 65535) return MOE_ERR_TOKENS;
+  if (V < 1 || V > 1 << 20) return MOE_ERR_SHAPE;
+  *bytes = R ? sample_ws(R, V).total : 0;
+  return MOE_OK;
+}
+
+moe_status moe_sample(int64_t R, int32_t V, const void *logits, int64_t row_stride, moe_dtype dtype, const float *u,
+                      const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                      int32_t *token, float *prob, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (R < 0 || R > 65535) return MOE_ERR_TOKENS;
+  if (V < 1 || V > 1 << 20 || row_stride < 0 || row_stride > int64_t(1) << 38) return MOE_ERR_SHAPE;
+  if (dtype != MOE_FP32 && dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_DTYPE;
+  if (R == 0) return MOE_OK;
+  if (!logits || !u || !token) return MOE_ERR_NULL;
+  const int size = dtype == MOE_FP32 ? 4 : 2;
+  if (!aligned(logits, size)) return MOE_ERR_ALIGN;
+  for (const void *p : {(const void *)u, (const void *)temperature, (const void *)top_k, (const void *)top_p,
+                        (const void *)min_p, (const void *)token, (const void *)prob})
+    if (!aligned(p, 4)) return MOE_ERR_ALIGN;
+  const SampleWs ws = sample_ws(R, V);
+  if (!workspace || workspace_bytes < ws.total) return MOE_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MOE_ERR_ALIGN;
+  const uint64_t n = 4 * (uint64_t)R;
+  const Span st{token, n}, sp{prob, n}, sw{workspace, ws.total};
+  const Span read[] = {{logits, (uint64_t)(((R - 1) * row_stride + V) * size)}, {u, n}, {temperature, n}, {top_k, n}, {top_p, n}, {min_p, n}};
+  for (const Span &w : {st, sp, sw})
+    for (const Span &r : read)
+      if (overlap(w, r)) return MOE_ERR_ALIAS;
+  if (overlap(st, sp) || overlap(st, sw) || overlap(sp, sw)) return MOE_ERR_ALIAS;
+  const moe_status dev = device_ok();
+  if (dev != MOE_OK) return dev;
+  SampleArgs a{};
+  a.logits = logits;
+  a.ld = row_stride;
+  a.type = dtype == MOE_FP32 ? 0 : dtype == MOE_BF16 ? 1 : 2;
+  a.u = u;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.token = token;
+  a.prob = prob;
+  a.R = (int)R;
+  a.V = V;
+  a.C = ws.chunks;
+  int log2v = 0;
+  while (1 << log2v < V) ++log2v;
+  a.bits = 62 - log2v < 51 ? 62 - log2v : 51;
+  char *base = static_cast<char *>(workspace);
+  a.chunk = reinterpret_cast<SampleChunk *>(base);
+  a.mass = reinterpret_cast<uint64_t *>(base + ws.mass);
+  a.count = reinterpret_cast<uint32_t *>(base + ws.count);
+  return launch_sample(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 }  // extern "C"

@@ -125,3 +125,40 @@ def test_linear_refusals(B):
                dict(xt=B.MOE_INT8, xs=5 * M + 4)):
         assert _linear(B, **kw) == ALIAS, kw
     assert _linear(B, out=M + 14336) == DEVICE
+
+
+# ----------------------------------------------------------------------------- sample
+
+def _sample(B, R=5, V=1000, l=M, ld=1000, t=2, u=2 * M, temperature=None, k=None, p=None, m=None, token=3 * M, prob=None, ws=4 * M,
+            wsn=1 << 28):
+    return _status(B, B.moe_sample, R, V, l, ld, t, u, temperature, k, p, m, token, prob, ws, wsn, 0)
+
+
+def test_sample_valid_calls_reach_the_device_check(B):
+    for t in (B.MOE_FP32, B.MOE_BF16, B.MOE_FP16):
+        assert _sample(B, t=t) == DEVICE
+    more = dict(temperature=5 * M, k=6 * M, p=7 * M, m=8 * M, prob=9 * M)
+    assert _sample(B, **more) == DEVICE and _sample(B, V=1 << 20, ld=1 << 20) == DEVICE and _sample(B, ld=0) == DEVICE
+    assert _sample(B, l=M + 2, t=B.MOE_BF16) == DEVICE and _sample(B, temperature=2 * M) == DEVICE
+    assert _sample(B, R=0, l=None, u=None, token=None, ws=None, wsn=0) == 0
+    need = B.moe_sample_workspace(5, 1000)
+    assert need >= 5 * 128 * 12 and _sample(B, wsn=need) == DEVICE and _sample(B, wsn=need - 1) == WORKSPACE
+    assert B.moe_sample_workspace(0, 10) == 0
+
+
+def test_sample_refusals(B):
+    assert _sample(B, R=-1) == TOKENS and _sample(B, R=65536) == TOKENS
+    for kw in (dict(V=0), dict(V=(1 << 20) + 1), dict(ld=-1)):
+        assert _sample(B, **kw) == SHAPE, kw
+    assert _sample(B, t=B.MOE_INT8) == DTYPE and _sample(B, t=7) == DTYPE
+    for kw in (dict(l=None), dict(u=None), dict(token=None)):
+        assert _sample(B, **kw) == NULL, kw
+    assert _sample(B, ws=None) == WORKSPACE
+    for kw in (dict(l=M + 2), dict(u=2 * M + 1), dict(token=3 * M + 2), dict(prob=9 * M + 1), dict(k=6 * M + 2), dict(ws=4 * M + 128)):
+        assert _sample(B, **kw) == ALIGN, kw
+    size = 4 * 5 * 1000
+    for kw in (dict(token=M + size - 4), dict(prob=M), dict(token=2 * M), dict(prob=3 * M + 16), dict(token=4 * M), dict(prob=4 * M),
+               dict(temperature=3 * M), dict(k=9 * M, prob=9 * M + 16), dict(ws=M - 256), dict(ws=2 * M)):
+        assert _sample(B, **kw) == ALIAS, kw
+    for args, status in (((-1, 10), TOKENS), ((70000, 10), TOKENS), ((5, 0), SHAPE), ((5, (1 << 20) + 1), SHAPE)):
+        assert _status(B, B.moe_sample_workspace, *args) == status
