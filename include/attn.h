@@ -141,6 +141,34 @@ moe_status moe_paged_attn(const moe_paged_kv *kv, const moe_batch *batch, int64_
                           float *lse, float scale, int32_t window, uint32_t flags, void *workspace,
                           size_t workspace_bytes, hipStream_t stream);
 
+/* Groups of a batch's sequences that share a prefix, as moe_pages_fork leaves them: group g is the
+ * sequences group_start[g] .. group_start[g+1]-1 (consecutive; one alone is fine), and the first
+ * prefix_len[g] positions (0 is fine) of all of them hold the same keys and values.  group_start has to
+ * ascend from 0 to n_seqs; where it does not, outputs are undefined but no access leaves the
+ * arrays. */
+typedef struct {               /* (host struct of device pointers), 4-byte aligned */
+  const int32_t *group_start;  /* [n_groups + 1] */
+  const int32_t *prefix_len;   /* [n_groups] */
+  int32_t n_groups;            /* 1 .. n_seqs */
+} moe_prefix_groups;
+
+/* moe_paged_attn for such a batch: a prefix's keys and values are read once for the tokens of all
+ * sequences of its group, through the table row of the group's first sequence (a row outside the
+ * table: the prefix is absent), and each sequence's own positions behind it through its row; the two are
+ * joined.  Every new token has to stand behind its prefix: it sees the whole of it, wherever it stands, and
+ * of the positions from prefix_len on those that moe_paged_attn without a window shows it (of a
+ * sequence whose own row lies outside the table: none).
+ *   max_q, max_prefix, max_suffix   (host) upper bounds of n_b, of prefix_len and of kv_len - prefix_len
+ *                that the launch is shaped by.  Smaller numbers than the true ones cost time, not results.
+ * Other arguments and errors as moe_paged_attn; the workspace is never empty.  T * n_heads <= 2^20
+ * (MOE_ERR_TOKENS): meant for single tokens and drafts. */
+moe_status moe_prefix_attn_workspace(const moe_paged_kv *kv, int64_t T, int32_t n_seqs, int32_t n_groups, int64_t max_q,
+                                     int64_t max_prefix, int64_t max_suffix, int32_t n_heads, size_t *bytes);
+moe_status moe_prefix_attn(const moe_paged_kv *kv, const moe_batch *batch, const moe_prefix_groups *groups, int64_t T,
+                           int64_t max_q, int64_t max_prefix, int64_t max_suffix, const moe_heads *q, int32_t n_heads,
+                           const moe_heads *out, float *lse, float scale, uint32_t flags, void *workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -72,3 +72,42 @@ def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     slack = min(slack, np.abs(upto / upto[-1] - u).min())
     i = min(int((upto <= u * upto[-1]).sum()), int(np.flatnonzero(w[kept])[-1]))
     return int(kept[i]), float(w[kept[i]] / upto[-1]), float(slack)
+
+
+def prefix_attn(q, k_cache, v_cache, table, q_start, kv_len, group_start, prefix_len, scale, full=False, row=None):
+    """Returns (out, lse, mass, spread) as ``serve.paged_attn`` does."""
+    T, H, D = q.shape
+    n_pages, ps, hk, _ = k_cache.shape
+    out, mass = np.full((T, H, D), np.nan), np.full((T, H, D), np.nan)
+    lse, spread = np.full((T, H), np.nan), np.zeros((T, H))
+
+    def stored(r, a, b):
+        """(position, page, offset) of the positions a .. b - 1 of table row r that have a place."""
+        if not 0 <= r < len(table):
+            return []
+        b = min(b, table.shape[1] * ps)
+        return [(j, int(table[r, j // ps]), j % ps) for j in range(a, b) if 0 <= table[r, j // ps] < n_pages]
+
+    rows = list(range(len(q_start) - 1)) if row is None else [int(x) for x in row]
+    for g in range(len(prefix_len)):
+        prefix = max(int(prefix_len[g]), 0)
+        for b in range(int(group_start[g]), int(group_start[g + 1])):
+            r = rows[b]
+            n, t0 = int(q_start[b + 1] - q_start[b]), int(q_start[b])
+            total = int(kv_len[r]) if 0 <= r < len(table) else 0
+            shared = stored(rows[int(group_start[g])], 0, prefix)
+            own = stored(r, min(prefix, table.shape[1] * ps), max(total, 0))
+            for i in range(n):
+                keys = shared + [x for x in own if full or x[0] <= total - n + i]
+                if not keys:
+                    out[t0 + i], mass[t0 + i], lse[t0 + i] = 0.0, 0.0, -np.inf
+                    continue
+                at = tuple(np.array([x[c] for x in keys]) for c in (1, 2))
+                for h in range(H):
+                    K, V = (np.asarray(c[at[0], at[1], h // (H // hk)], np.float64) for c in (k_cache, v_cache))
+                    s = scale * (K @ np.asarray(q[t0 + i, h], np.float64))
+                    w = np.exp(s - s.max())
+                    out[t0 + i, h], mass[t0 + i, h] = w @ V / w.sum(), w @ np.abs(V) / w.sum()
+                    lse[t0 + i, h] = s.max() + np.log(w.sum())
+                    spread[t0 + i, h] = (np.abs(K) @ np.abs(np.asarray(q[t0 + i, h], np.float64))).max()
+    return out, lse, mass, spread

@@ -99,6 +99,51 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, ta
     return out if lse is None else (out, lse)
 
 
+def prefix_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
+                q_start: torch.Tensor, kv_len: torch.Tensor, group_start: torch.Tensor, prefix_len: torch.Tensor,
+                max_q: int, max_prefix: int, max_suffix: int, *, scale: float | None = None, full: bool = False,
+                row: torch.Tensor | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                return_lse: bool = False, workspace: torch.Tensor | None = None):
+    """``paged_attn`` of sequences that share prefixes, each prefix read once for all of a group (see
+    ``moe_prefix_attn``).
+
+    group_start: int32 [n_groups + 1], ascending from 0 to n_seqs; group g is the batch's sequences
+    group_start[g] .. group_start[g + 1] - 1, and their first prefix_len[g] (int32 [n_groups]) positions are the
+    same.  max_q, max_prefix and max_suffix bound the new tokens, the prefixes and the lengths behind
+    them (they shape the launch).  workspace: uint8 tensor of ``prefix_attn_workspace`` bytes (by
+    default one is allocated for the call).  Everything else as ``paged_attn``."""
+    index = q.get_device()
+    kv, _, D, dtype = N.cache(k_cache, v_cache, index)
+    b, n_seqs = N.batch(table, q_start, kv_len, row, index)
+    g, n_groups = N.groups(group_start, prefix_len, index)
+    hq, T, H = N.heads("q", q, -1, -1, D, dtype, index)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and return_lse:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    ho = N.heads("out", out, T, H, D, dtype, index)[0]
+    lp = None if lse is None else N.address("lse", lse, N.FP32, index, T, H)
+    if workspace is None:
+        n = B.moe_prefix_attn_workspace(kv, T, n_seqs, n_groups, max_q, max_prefix, max_suffix, H)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    wp, wn = N.address("workspace", workspace, N.UINT8, index), workspace.numel()
+    if T:
+        with on(index):
+            st = (B._lib or B.lib()).moe_prefix_attn(kv, b, g, T, max_q, max_prefix, max_suffix, hq, H, ho, lp,
+                                                     D ** -0.5 if scale is None else scale,
+                                                     B.MOE_ATTN_FULL if full else 0, wp, wn, stream(index))
+        if st:
+            raise B.MoeError("moe_prefix_attn", st)
+    return out if lse is None else (out, lse)
+
+
+def prefix_attn_workspace(T: int, n_seqs: int, n_groups: int, max_q: int, max_prefix: int, max_suffix: int, n_heads: int,
+                          n_kv_heads: int, head_dim: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of workspace that ``prefix_attn`` needs for these sizes."""
+    kv = B.moe_paged_kv(None, None, 0, 0, 0, 1, 16, n_kv_heads, head_dim, _DTYPES[dtype])
+    return B.moe_prefix_attn_workspace(kv, T, n_seqs, n_groups, max_q, max_prefix, max_suffix, n_heads)
+
+
 def paged_attn_workspace(T: int, n_seqs: int, max_q: int, max_kv: int, n_heads: int, n_kv_heads: int, head_dim: int,
                          dtype: torch.dtype = torch.bfloat16, window: int = 0) -> int:
     """Bytes of workspace that ``paged_attn`` needs for these sizes."""

@@ -49,7 +49,7 @@ EXPORTED = ("moe_plan_create", "moe_plan_destroy", "moe_workspace_init", "moe_wo
             "moe_pack_codes", "moe_status_string", "moe_version", "moe_gdn_scan", "moe_gdn_step", "moe_rope_freqs",
             "moe_rope_append", "moe_paged_attn_workspace", "moe_paged_attn", "moe_pages_workspace", "moe_pages_grow",
             "moe_pages_fork", "moe_pages_free", "moe_pages_compact", "moe_pages_copy", "moe_pages_check", "moe_rms_norm",
-            "moe_linear", "moe_sample_workspace", "moe_sample")
+            "moe_linear", "moe_sample_workspace", "moe_sample", "moe_prefix_attn_workspace", "moe_prefix_attn")
 
 # include/attn.h
 MOE_ROPE_NONE, MOE_ROPE_LINEAR, MOE_ROPE_NTK, MOE_ROPE_YARN = range(4)
@@ -95,6 +95,10 @@ class moe_batch(ctypes.Structure):
     _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p),
                 ("row", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("n_rows", ctypes.c_int32),
                 ("table_cols", ctypes.c_int32)]
+
+
+class moe_prefix_groups(ctypes.Structure):
+    _fields_ = [("group_start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p), ("n_groups", ctypes.c_int32)]
 
 
 class moe_pages(ctypes.Structure):
@@ -195,6 +199,10 @@ def lib() -> ctypes.CDLL:
             L.moe_sample_workspace.argtypes = [I64, I32, ctypes.POINTER(SZ)]
             L.moe_sample.restype = ctypes.c_int
             L.moe_sample.argtypes = [I64, I32, P, I64, ctypes.c_int, P, P, P, P, P, P, P, P, SZ, P]
+            L.moe_prefix_attn_workspace.restype = ctypes.c_int
+            L.moe_prefix_attn_workspace.argtypes = [KV, I64, I32, I32, I64, I64, I64, I32, ctypes.POINTER(SZ)]
+            L.moe_prefix_attn.restype = ctypes.c_int
+            L.moe_prefix_attn.argtypes = [KV, BA, P, I64, I64, I64, I64, HD, I32, HD, P, F32, ctypes.c_uint32, P, SZ, P]
             L.moe_status_string.restype = ctypes.c_char_p
             L.moe_status_string.argtypes = [ctypes.c_int]
             L.moe_version.restype = ctypes.c_char_p
@@ -323,6 +331,24 @@ def moe_paged_attn(kv: moe_paged_kv, batch: moe_batch, T: int, max_q: int, max_k
                                         scale, window, flags, ws_ptr, ws_bytes, stream)
     if st:
         raise MoeError("moe_paged_attn", st)
+
+
+def moe_prefix_attn_workspace(kv: moe_paged_kv, T: int, n_seqs: int, n_groups: int, max_q: int, max_prefix: int,
+                              max_suffix: int, n_heads: int) -> int:
+    n = ctypes.c_size_t()
+    st = (_lib or lib()).moe_prefix_attn_workspace(_ref(kv), T, n_seqs, n_groups, max_q, max_prefix, max_suffix, n_heads,
+                                                   ctypes.byref(n))
+    if st:
+        raise MoeError("moe_prefix_attn_workspace", st)
+    return n.value
+
+
+def moe_prefix_attn(kv: moe_paged_kv, batch: moe_batch, groups: moe_prefix_groups, T: int, max_q: int, max_prefix: int,
+                    max_suffix: int, q: moe_heads, n_heads: int, out: moe_heads, lse_ptr: int | None, scale: float,
+                    flags: int, ws_ptr: int | None, ws_bytes: int, stream: int) -> None:
+    _check("moe_prefix_attn", (_lib or lib()).moe_prefix_attn(_ref(kv), _ref(batch), _opt(groups), T, max_q, max_prefix,
+                                                              max_suffix, _ref(q), n_heads, _ref(out), lse_ptr, scale, flags,
+                                                              ws_ptr, ws_bytes, stream))
 
 
 def moe_pages_workspace(pages: moe_pages, n: int) -> int:

@@ -171,6 +171,7 @@ struct Tile {
   int64_t first;      // position of the sequence's first new token
   int len;            // keys stored: min(kv_len, columns * page size)
   int lo, hi;         // keys that any row of the tile sees lie in [lo, hi)
+  bool full;          // every row sees every key in there
 };
 
 // A sequence of the batch: first token, new tokens (0 where the numbers are no batch: nothing is
@@ -198,6 +199,7 @@ __device__ __forceinline__ bool set_tile(const AttnArgs &a, const Seq &q, int64_
   t.r0 = (int)r0;
   t.nr = min(rows, t.n * a.G - t.r0);
   t.row = q.row;
+  t.full = a.full;
   t.first = (int64_t)q.total - t.n;
   t.len = min(max(q.total, 0), a.b.cols << a.kv.page_shift);
   const int64_t p0 = t.first + t.r0 / a.G, p1 = t.first + (t.r0 + t.nr - 1) / a.G;
@@ -216,7 +218,7 @@ __device__ __forceinline__ Seq readlane_seq(const Seq &q, int l) {
 
 // The x-th tile of `rows`-row tiles to be taken, out of a.tiles or fewer: of a sequence the last
 // ones, which see most keys, first.
-__device__ __forceinline__ bool find_tile(const AttnArgs &a, int x, int rows, Tile &t) {
+__device__ __forceinline__ bool find_tile(const AttnArgs &a, int x, int rows, Tile &t, int &seq) {
   const Batch &b = a.b;
   if (b.n_seqs > 1 && b.n_seqs <= 64) {
     // Every sequence in a lane, so that a tile's is not read once more (a step in the chain of
@@ -236,15 +238,98 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &a, int x, int rows, Ti
       has = __ballot(upto > x);
       if (!has) return false;
     }
-    const int s = __builtin_ctzll(has);
+    const int s = seq = __builtin_ctzll(has);
     return set_tile(a, readlane_seq(mine, s), (int64_t)(__builtin_amdgcn_readlane(upto, s) - 1 - x) * rows, rows, t);
   }
   // Sequence b's tiles start at floor(q_start[b] G / rows) + b, which leaves room for
   // ceil(n_b G / rows) of them, so no list of tiles is needed
   x = a.tiles - 1 - x;
-  const int s = wave_find(b.n_seqs, x, [&](int i) { return (int64_t)b.q_start[i] * a.G / rows + i; });
+  const int s = seq = wave_find(b.n_seqs, x, [&](int i) { return (int64_t)b.q_start[i] * a.G / rows + i; });
   const Seq q = read_seq(a, s);
   return set_tile(a, q, ((int64_t)x - ((int64_t)q.t0 * a.G / rows + s)) * rows, rows, t);
+}
+
+// ------------------------------------------------------------ tiles of shared prefixes
+
+// In the prefix form a tile is one of a group's prefix -- rows of all its sequences' tokens, which are
+// consecutive, against the keys that these share -- or one of a sequence's suffix, whose keys start
+// behind its group's prefix.  Workgroups: first the prefixes' (tiles x key/value heads x splits), then
+// the suffixes'.
+struct Work {
+  int tile, kvh, split, per;  // per: blocks of a split
+  int slot;                   // of the row's partial results
+  bool prefix;
+};
+__device__ __forceinline__ Work work_of(const AttnArgs &a, int x) {
+  Work w;
+  const int n_kv = a.kv.n_kv, first = a.p_tiles * n_kv * a.p_splits;
+  w.prefix = x < first;
+  if (w.prefix) {
+    // The tiles that share keys follow each other at a distance of 8 workgroups, so that one XCD's cache
+    // brings these keys once.
+    const int parts = n_kv * a.p_splits, whole = parts / 8 * 8 * a.p_tiles;
+    int part;
+    if (x < whole) {
+      const int y = x / 8;
+      w.tile = y % a.p_tiles;
+      part = y / a.p_tiles * 8 + x % 8;
+    } else {
+      const int rest = parts % 8, y = x - whole;
+      w.tile = y / rest;
+      part = parts / 8 * 8 + y % rest;
+    }
+    w.kvh = part % n_kv;
+    w.split = part / n_kv;
+    w.per = a.p_blocks;
+    w.slot = w.split;
+  } else {
+    x -= first;
+    w.kvh = x % n_kv;
+    x /= n_kv;
+    const int s_splits = a.splits - a.p_splits;
+    w.split = x % s_splits;
+    w.tile = x / s_splits;
+    w.per = a.split_blocks;
+    w.slot = a.p_splits + w.split;
+  }
+  return w;
+}
+
+// Length of a group's prefix, within its table row.
+__device__ __forceinline__ int prefix_of(const AttnArgs &a, int g) {
+  return min(max(a.prefix_len[g], 0), a.b.cols << a.kv.page_shift);
+}
+__device__ __forceinline__ int group_at(const AttnArgs &a, int g) { return min(max(a.group_start[g], 0), a.b.n_seqs); }
+
+// The x-th row tile of the prefixes.  Group g's tiles start at floor(first token G / rows) + g.
+__device__ __forceinline__ bool find_prefix_tile(const AttnArgs &a, int x, Tile &t) {
+  const Batch &b = a.b;
+  const int g = wave_find(a.n_groups, x, [&](int i) { return (int64_t)b.q_start[group_at(a, i)] * a.G / kAttnTile + i; });
+  const int s0 = group_at(a, g), s1 = group_at(a, g + 1);
+  Seq q;
+  q.t0 = b.q_start[s0];
+  const int t1 = b.q_start[s1];
+  q.row = s0 < b.n_seqs ? batch_row(b, s0) : -1;
+  q.n = q.t0 < 0 || t1 > a.T || s1 <= s0 ? 0 : max(t1 - q.t0, 0);
+  t.t0 = q.t0;
+  t.n = q.n;
+  const int64_t r0 = ((int64_t)x - ((int64_t)q.t0 * a.G / kAttnTile + g)) * kAttnTile;
+  if (r0 < 0 || r0 >= (int64_t)t.n * a.G) return false;
+  t.r0 = (int)r0;
+  t.nr = min(kAttnTile, t.n * a.G - t.r0);
+  t.row = q.row;
+  t.full = true;
+  t.len = t.row < 0 ? 0 : prefix_of(a, g);
+  t.first = t.len;
+  t.lo = 0;
+  t.hi = t.len;
+  return true;
+}
+
+// Keys from the end of its group's prefix on: of a suffix's tile.
+__device__ __forceinline__ void cut_prefix(const AttnArgs &a, int seq, Tile &t) {
+  const int g = wave_find(a.n_groups, seq, [&](int i) { return (int64_t)a.group_start[i]; });
+  t.lo = min(prefix_of(a, g), t.hi);
 }
 
 // Values that not all rows of a tile see must be finite, for a hidden key's weight is 0: absent
@@ -290,7 +375,7 @@ __device__ void put_back(const AttnArgs &a, const Tile &t, int kvh, int b0, int 
     if (!__ballot(any)) continue;
     for (int r = r0; r < r1; r += step) {
       const int64_t p = t.first + r / a.G;
-      if ((!a.full && key > p) || (a.window && key <= p - a.window)) continue;
+      if ((!t.full && key > p) || (a.window && key <= p - a.window)) continue;
       const int64_t tk = t.t0 + r / a.G, hd = kvh * a.G + r % a.G;
       float *d = part(r, tk, hd);
 #pragma unroll
@@ -746,7 +831,8 @@ enum class First { Matrix, Softmax, None };
 // there for all, and the buffer of the block before it is free for the loads of the next.
 // Waves on a SIMD: two, three, four by width (of 128, with 169 registers and so two waves, 24 ragged
 // chunks take 143 us; with 168 and three, 132).
-template <int D, bool F16>
+// PREFIX: of shared prefixes and the suffixes behind them (work_of); every result is partial.
+template <int D, bool F16, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_attn_tile(AttnArgs a) {
   constexpr int kBuf = kAttnKeys * D * 2;      // one K or V block, bytes
   constexpr int kStages = stages(D);
@@ -758,12 +844,29 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
   Tile t;
   // the key/value heads of one tile next to each other: 4096 tokens at 16K, 8 such heads of 128,
   // 1052 us; head after head 1128
-  const int tile = blockIdx.x / (unsigned)a.kv.n_kv, kvh = blockIdx.x - tile * a.kv.n_kv;
-  if (!find_tile(a, tile, kAttnTile, t)) return;
+  Work work{};
+  if constexpr (PREFIX) {
+    work = work_of(a, blockIdx.x);
+  } else {
+    work.tile = blockIdx.x / (unsigned)a.kv.n_kv;
+    work.kvh = blockIdx.x - work.tile * a.kv.n_kv;
+    work.split = work.slot = blockIdx.y;
+    work.per = a.split_blocks;
+  }
+  const int kvh = work.kvh;
+  int seq;
+  if (PREFIX && work.prefix) {
+    if (!find_prefix_tile(a, work.tile, t)) return;
+  } else {
+    if (!find_tile(a, work.tile, kAttnTile, t, seq)) return;
+    if constexpr (PREFIX) cut_prefix(a, seq, t);
+  }
+  const bool full = PREFIX ? t.full : a.full;
+  const int splits = !PREFIX ? a.splits : work.prefix ? a.p_splits : a.splits - a.p_splits;
   // Behind the buffers, so that these start at LDS address 0 (addresses are combined by
   // exclusive or): whether some value that not all rows see is an infinity or NaN.
   int &odd = *(int *)(lds_raw + kStages * 2 * kBuf);
-  const int split = blockIdx.y;
+  const int split = work.split;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   if (tid == 0) odd = 0;
   __syncthreads();
@@ -777,19 +880,19 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
   const bool live = n < wn;
   const int tok = t.t0 + rr / a.G, head = kvh * a.G + rr % a.G;
   const int64_t pos = live ? t.first + rr / a.G : -1;
-  const int last_key = (int)(a.full ? (live ? (int64_t)t.len - 1 : -1) : min(pos, (int64_t)t.len - 1));
-  const int first_key = a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
+  const int last_key = (int)(full ? (live ? (int64_t)t.len - 1 : -1) : min(pos, (int64_t)t.len - 1));
+  const int first_key = PREFIX ? t.lo : a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
   const int64_t pf = t.first + w0 / a.G, pl = t.first + (w0 + max(wn, 1) - 1) / a.G;
   // all rows of the wave see the keys of [all_lo, all_hi); some row sees those of [any_lo, any_hi)
-  const int all_hi = (int)(a.full ? (int64_t)t.len : min(pf + 1, (int64_t)t.len));
-  const int all_lo = a.window ? (int)max(pl - a.window + 1, (int64_t)0) : 0;
-  const int any_hi = wn == 0 ? 0 : (int)(a.full ? (int64_t)t.len : min(pl + 1, (int64_t)t.len));
-  const int any_lo = a.window ? (int)max(pf - a.window + 1, (int64_t)0) : 0;
+  const int all_hi = (int)(full ? (int64_t)t.len : min(pf + 1, (int64_t)t.len));
+  const int all_lo = PREFIX ? t.lo : a.window ? (int)max(pl - a.window + 1, (int64_t)0) : 0;
+  const int any_hi = wn == 0 ? 0 : (int)(full ? (int64_t)t.len : min(pl + 1, (int64_t)t.len));
+  const int any_lo = PREFIX ? t.lo : a.window ? (int)max(pf - a.window + 1, (int64_t)0) : 0;
 
   // keys below all_lo_t and from all_hi_t on are hidden from some row of the tile
   const int64_t tf = t.first + t.r0 / a.G, tl = t.first + (t.r0 + t.nr - 1) / a.G;
-  const int all_hi_t = (int)(a.full ? (int64_t)t.len : max(min(tf + 1, (int64_t)t.len), (int64_t)0));
-  const int all_lo_t = a.window ? (int)max(tl - a.window + 1, (int64_t)0) : 0;
+  const int all_hi_t = (int)(full ? (int64_t)t.len : max(min(tf + 1, (int64_t)t.len), (int64_t)0));
+  const int all_lo_t = PREFIX ? t.lo : a.window ? (int)max(tl - a.window + 1, (int64_t)0) : 0;
 
   // a negative scale is taken as a positive one on negated queries, so that the largest score
   // is the largest product
@@ -811,8 +914,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
   }
 
   const int blk0 = t.lo / kAttnKeys, nblk = (t.hi + kAttnKeys - 1) / kAttnKeys - blk0;
-  const int b0 = blk0 + min(nblk, split * a.split_blocks);
-  const int b1 = blk0 + (split + 1 == a.splits ? nblk : min(nblk, (split + 1) * a.split_blocks));
+  const int b0 = blk0 + min(nblk, split * work.per);
+  const int b1 = blk0 + (split + 1 == splits ? nblk : min(nblk, (split + 1) * work.per));
 
   // the rows that this wave loads lie in one 16-key half of a block
   const int my_r0 = wave * kInstr * kRowsPer, upper = my_r0 >> 4;
@@ -1004,7 +1107,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
   const int64_t row = (int64_t)tok * a.H + head;
   // a tile whose keys are all in the first split needs no join: its other splits are empty, and
   // the first one's sum of -1 says that the row is done
-  const bool direct = a.splits == 1 || nblk <= a.split_blocks;
+  const bool direct = !PREFIX && (a.splits == 1 || nblk <= a.split_blocks);
   if (!live || (direct && split > 0)) {
   } else if (direct) {
     const float inv = reciprocal_of(l);
@@ -1020,7 +1123,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
     if (a.lse && half == 0) a.lse[row] = lse_of(m == -INFINITY ? m : m * scale, es, tile_bias(F16));
     if (a.splits > 1 && half == 0) a.stats[row * a.splits].l = -1.0f;
   } else {
-    const int64_t at = row * a.splits + split;
+    const int64_t at = row * a.splits + work.slot;
     if (b0 < b1) {
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
@@ -1035,7 +1138,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "agent");
   put_back<D, F16>(a, t, kvh, b0, b1, all_lo_t, all_hi_t, t.r0 + wave * 32, t.r0 + wave * 32 + wn, 1,
                    [&](int, int64_t tk, int64_t hd) {
-                     return direct ? nullptr : a.part + ((tk * a.H + hd) * a.splits + split) * D;
+                     return direct ? nullptr : a.part + ((tk * a.H + hd) * a.splits + work.slot) * D;
                    });
 }
 
@@ -1241,9 +1344,28 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join_runs(AttnArgs a) {
   }
 }
 
+// Joins a.splits partial results of every row.
+template <int D, bool F16>
+void join(const AttnArgs &a, hipStream_t s) {
+  if (a.splits > one_round(D))
+    hipLaunchKernelGGL((k_attn_join<D, F16, 512>), dim3(a.T * a.H), dim3(512), 0, s, a);
+  else if (a.splits > kFewSplits)
+    hipLaunchKernelGGL((k_attn_join<D, F16, kThreads>), dim3(a.T * a.H), dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_attn_join_few<D, F16>), dim3(((int64_t)a.T * a.H + 4 * kWaves - 1) / (4 * kWaves)), dim3(kThreads), 0, s, a);
+}
+
 template <int D, bool F16>
 hipError_t launch(const AttnArgs &a, hipStream_t s) {
-  if (a.rows == kAttnRows) {
+  constexpr int lds = stages(D) * 2 * kAttnKeys * D * 2 + 16;
+  if (a.n_groups > 0) {
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = allow_lds(k_attn_tile<D, F16, true>, lds, done);
+    if (e != hipSuccess) return e;
+    const int wgs = a.kv.n_kv * (a.p_tiles * a.p_splits + a.tiles * (a.splits - a.p_splits));
+    hipLaunchKernelGGL((k_attn_tile<D, F16, true>), dim3(wgs), dim3(kThreads), lds, s, a);
+    join<D, F16>(a, s);
+  } else if (a.rows == kAttnRows) {
     static std::atomic<uint64_t> done{0};
     const hipError_t e = allow_lds(k_attn_rows<D, F16>, Rows<D>::kLds, done);
     if (e != hipSuccess) return e;
@@ -1251,16 +1373,10 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((k_attn_join_runs<D, F16>), dim3(a.wgs, a.join_rows), dim3(kJoinThreads), 0, s, a);
   } else {
     static std::atomic<uint64_t> done{0};
-    constexpr int lds = stages(D) * 2 * kAttnKeys * D * 2 + 16;
-    const hipError_t e = allow_lds(k_attn_tile<D, F16>, lds, done);
+    const hipError_t e = allow_lds(k_attn_tile<D, F16, false>, lds, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn_tile<D, F16>), dim3(a.tiles * a.kv.n_kv, a.splits), dim3(kThreads), lds, s, a);
-    if (a.splits > one_round(D))
-      hipLaunchKernelGGL((k_attn_join<D, F16, 512>), dim3(a.T * a.H), dim3(512), 0, s, a);
-    else if (a.splits > kFewSplits)
-      hipLaunchKernelGGL((k_attn_join<D, F16, kThreads>), dim3(a.T * a.H), dim3(kThreads), 0, s, a);
-    else if (a.splits > 1)
-      hipLaunchKernelGGL((k_attn_join_few<D, F16>), dim3(((int64_t)a.T * a.H + 4 * kWaves - 1) / (4 * kWaves)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((k_attn_tile<D, F16, false>), dim3(a.tiles * a.kv.n_kv, a.splits), dim3(kThreads), lds, s, a);
+    if (a.splits > 1) join<D, F16>(a, s);
   }
   return hipGetLastError();
 }
@@ -1319,6 +1435,35 @@ AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int w
     s.off_stats = (rows * dim * 4 + 255) & ~(size_t)255;
     s.ws_bytes = s.off_stats + rows * sizeof(AttnStats);
   }
+  return s;
+}
+
+AttnShape prefix_shape(int64_t T, int n_seqs, int n_groups, int64_t max_q, int64_t max_prefix, int64_t max_suffix, int H, int n_kv,
+                       int dim) {
+  AttnShape s{};
+  const int64_t G = H / n_kv;
+  s.rows = kAttnTile;
+  s.p_tiles = (int)(T * G / kAttnTile + n_groups);
+  s.tiles = (int)(T * G / kAttnTile + n_seqs);
+  if (T == 0) return s;
+  // Splits of one length for both, of a length that makes them fill the chip.
+  const int64_t p_blocks = (max_prefix + kAttnKeys - 1) / kAttnKeys, s_blocks = (max_suffix + kAttnKeys - 1) / kAttnKeys + 1;
+  int64_t busy = (max_q * G + kAttnTile - 1) / kAttnTile;
+  busy = (busy < 1 ? 1 : busy) * n_seqs;
+  if (busy < T * G / kAttnTile) busy = T * G / kAttnTile;
+  if (busy > s.tiles) busy = s.tiles;
+  const int64_t p_busy = (T * G + kAttnTile - 1) / kAttnTile;
+  const int64_t total = n_kv * (p_busy * p_blocks + busy * s_blocks);
+  int64_t per = (total + tile_slots(dim) - 1) / tile_slots(dim);
+  if (per < 2) per = 2;
+  auto splits = [&](int64_t blocks) { return (blocks + per - 1) / per; };
+  while (splits(p_blocks) + splits(s_blocks) > kMaxSplits) ++per;
+  s.p_splits = (int)(p_blocks > 0 ? splits(p_blocks) : 1);
+  s.splits = s.p_splits + (int)splits(s_blocks);
+  s.p_blocks = s.split_blocks = (int)per;
+  const size_t rows = (size_t)T * H * s.splits;
+  s.off_stats = (rows * dim * 4 + 255) & ~(size_t)255;
+  s.ws_bytes = s.off_stats + rows * sizeof(AttnStats);
   return s;
 }
 

@@ -82,13 +82,18 @@ struct AttnArgs {
   int window;
   bool full;
   float scale_log2;
+  // shared prefixes (n_groups > 0): the first p_splits of the splits are of the prefixes
+  const int32_t *group_start, *prefix_len;
+  int n_groups, p_tiles, p_splits, p_blocks;
 };
 // What the launch is shaped by, from host-known sizes alone.
 struct AttnShape {
-  int rows, tiles, splits, split_blocks, wgs, join_rows;
+  int rows, tiles, splits, split_blocks, wgs, join_rows, p_tiles, p_splits, p_blocks;
   size_t ws_bytes, off_stats, off_rec;
 };
 AttnShape attn_shape(int64_t T, int n_seqs, int64_t max_q, int64_t max_kv, int window, int H, int n_kv, int dim);
+AttnShape prefix_shape(int64_t T, int n_seqs, int n_groups, int64_t max_q, int64_t max_prefix, int64_t max_suffix, int H, int n_kv,
+                       int dim);
 hipError_t launch_paged_attn(const AttnArgs &a, hipStream_t s);
 
 struct GdnStepArgs {

@@ -99,6 +99,80 @@ AttnShape shape_of(int64_t T, int32_t n_seqs, int64_t max_q, int64_t max_kv, int
                     kv.n_kv_heads, kv.head_dim);
 }
 
+bool meets_groups(const Span &s, const moe_prefix_groups *g) {
+  return g && (overlap(s, {g->group_start, 4 * ((uint64_t)g->n_groups + 1)}) || overlap(s, {g->prefix_len, 4 * (uint64_t)g->n_groups}));
+}
+
+// What moe_paged_attn and moe_prefix_attn (groups not null) share behind the checks of sizes; shape()
+// gives the launch's.
+template <class F>
+moe_status attn_call(const moe_paged_kv &kv, const moe_batch &batch, const moe_prefix_groups *groups, int64_t T, const moe_heads *q,
+                     int32_t n_heads, const moe_heads *out, float *lse, float scale, int32_t window, uint32_t flags, F shape,
+                     void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  moe_status st;
+  if (flags & ~MOE_ATTN_FULL) return MOE_ERR_SHAPE;
+  const float scale_log2 = scale * 1.44269504088896341f;  // scores are kept as base-2 exponents
+  if (window < 0 || (window > 0 && (flags & MOE_ATTN_FULL)) || !std::isfinite(scale_log2)) return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if ((st = check_heads(q)) != MOE_OK || (st = check_heads(out)) != MOE_OK) return st;
+  if (!aligned(lse, 4)) return MOE_ERR_ALIGN;
+  const int64_t D = kv.head_dim;
+  if (!heads_distinct(*out, T, n_heads, D)) return MOE_ERR_SHAPE;
+  const AttnShape sh = shape();
+  if (sh.ws_bytes > 0 && (!workspace || workspace_bytes < sh.ws_bytes)) return MOE_ERR_WORKSPACE;
+  if (sh.ws_bytes > 0 && !aligned(workspace, 256)) return MOE_ERR_ALIGN;
+  const Span sq = span(*q, T, n_heads, D), ck = kv_span(kv, kv.k), cv = kv_span(kv, kv.v);
+  const Span so = span(*out, T, n_heads, D), sl{lse, 4 * (uint64_t)T * n_heads}, sw{workspace, sh.ws_bytes};
+  if (heads_overlap(*out, n_heads, *q, n_heads, T, D)) return MOE_ERR_ALIAS;
+  if (overlap(sl, sq) || overlap(sw, sq) || overlap(so, sl) || overlap(so, sw) || overlap(sl, sw)) return MOE_ERR_ALIAS;
+  for (const Span &w : {so, sl, sw})
+    if (overlap(w, ck) || overlap(w, cv) || meets_batch(w, batch) || meets_groups(w, groups)) return MOE_ERR_ALIAS;
+  if ((st = device_ok()) != MOE_OK) return st;
+  AttnArgs a{};
+  a.kv = dev_kv(kv);
+  a.b = dev_batch(batch);
+  a.q = dev_heads(*q);
+  a.out = dev_heads(*out);
+  a.lse = lse;
+  a.part = static_cast<float *>(workspace);
+  a.stats = reinterpret_cast<AttnStats *>(static_cast<char *>(workspace) + sh.off_stats);
+  a.T = (int)T;
+  a.H = n_heads;
+  a.G = n_heads / kv.n_kv_heads;
+  a.rows = sh.rows;
+  a.tiles = sh.tiles;
+  a.splits = sh.splits;
+  a.split_blocks = sh.split_blocks;
+  a.wgs = sh.wgs;
+  a.join_rows = sh.join_rows;
+  a.rec = reinterpret_cast<AttnRec *>(static_cast<char *>(workspace) + sh.off_rec);
+  a.window = window;
+  a.full = flags & MOE_ATTN_FULL;
+  a.scale_log2 = scale_log2;
+  if (groups) {
+    a.group_start = groups->group_start;
+    a.prefix_len = groups->prefix_len;
+    a.n_groups = groups->n_groups;
+    a.p_tiles = sh.p_tiles;
+    a.p_splits = sh.p_splits;
+    a.p_blocks = sh.p_blocks;
+  }
+  return launch_paged_attn(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status check_prefix_sizes(int64_t T, int32_t n_seqs, int32_t n_groups, int64_t max_q, int64_t max_prefix, int64_t max_suffix,
+                              int32_t n_heads, const moe_paged_kv &kv) {
+  const moe_status st = check_attn_sizes(T, n_seqs, max_q, max_prefix, n_heads, kv);
+  if (st != MOE_OK) return st;
+  if (n_groups < 1 || n_groups > n_seqs || max_suffix < 0) return MOE_ERR_SHAPE;
+  return T * n_heads > int64_t(1) << 20 ? MOE_ERR_TOKENS : MOE_OK;
+}
+AttnShape shape_of(int64_t T, int32_t n_seqs, int32_t n_groups, int64_t max_q, int64_t max_prefix, int64_t max_suffix,
+                   int32_t n_heads, const moe_paged_kv &kv) {
+  return prefix_shape(T, n_seqs, n_groups, std::min<int64_t>(max_q, kMaxTokens), std::min<int64_t>(max_prefix, int64_t(1) << 30),
+                      std::min<int64_t>(max_suffix, int64_t(1) << 30), n_heads, kv.n_kv_heads, kv.head_dim);
+}
+
 // ------------------------------------------------------------------------ pages
 
 moe_status check_pages(const moe_pages *p) {
@@ -290,46 +364,34 @@ moe_status moe_paged_attn(const moe_paged_kv *kv, const moe_batch *batch, int64_
   if (st != MOE_OK) return st;
   if ((st = check_batch(batch, kv->page_size)) != MOE_OK) return st;
   if ((st = check_attn_sizes(T, batch->n_seqs, max_q, max_kv, n_heads, *kv)) != MOE_OK) return st;
-  if (flags & ~MOE_ATTN_FULL) return MOE_ERR_SHAPE;
-  const float scale_log2 = scale * 1.44269504088896341f;  // scores are kept as base-2 exponents
-  if (window < 0 || (window > 0 && (flags & MOE_ATTN_FULL)) || !std::isfinite(scale_log2)) return MOE_ERR_SHAPE;
-  if (T == 0) return MOE_OK;
-  if ((st = check_heads(q)) != MOE_OK || (st = check_heads(out)) != MOE_OK) return st;
-  if (!aligned(lse, 4)) return MOE_ERR_ALIGN;
-  const int64_t D = kv->head_dim;
-  if (!heads_distinct(*out, T, n_heads, D)) return MOE_ERR_SHAPE;
-  const AttnShape sh = shape_of(T, batch->n_seqs, max_q, max_kv, window, n_heads, *kv);
-  if (sh.ws_bytes > 0 && (!workspace || workspace_bytes < sh.ws_bytes)) return MOE_ERR_WORKSPACE;
-  if (sh.ws_bytes > 0 && !aligned(workspace, 256)) return MOE_ERR_ALIGN;
-  const Span sq = span(*q, T, n_heads, D), ck = kv_span(*kv, kv->k), cv = kv_span(*kv, kv->v);
-  const Span so = span(*out, T, n_heads, D), sl{lse, 4 * (uint64_t)T * n_heads}, sw{workspace, sh.ws_bytes};
-  if (heads_overlap(*out, n_heads, *q, n_heads, T, D)) return MOE_ERR_ALIAS;
-  if (overlap(sl, sq) || overlap(sw, sq) || overlap(so, sl) || overlap(so, sw) || overlap(sl, sw)) return MOE_ERR_ALIAS;
-  for (const Span &w : {so, sl, sw})
-    if (overlap(w, ck) || overlap(w, cv) || meets_batch(w, *batch)) return MOE_ERR_ALIAS;
-  if ((st = device_ok()) != MOE_OK) return st;
-  AttnArgs a{};
-  a.kv = dev_kv(*kv);
-  a.b = dev_batch(*batch);
-  a.q = dev_heads(*q);
-  a.out = dev_heads(*out);
-  a.lse = lse;
-  a.part = static_cast<float *>(workspace);
-  a.stats = reinterpret_cast<AttnStats *>(static_cast<char *>(workspace) + sh.off_stats);
-  a.T = (int)T;
-  a.H = n_heads;
-  a.G = n_heads / kv->n_kv_heads;
-  a.rows = sh.rows;
-  a.tiles = sh.tiles;
-  a.splits = sh.splits;
-  a.split_blocks = sh.split_blocks;
-  a.wgs = sh.wgs;
-  a.join_rows = sh.join_rows;
-  a.rec = reinterpret_cast<AttnRec *>(static_cast<char *>(workspace) + sh.off_rec);
-  a.window = window;
-  a.full = flags & MOE_ATTN_FULL;
-  a.scale_log2 = scale_log2;
-  return launch_paged_attn(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+  return attn_call(*kv, *batch, nullptr, T, q, n_heads, out, lse, scale, window, flags,
+                   [&] { return shape_of(T, batch->n_seqs, max_q, max_kv, window, n_heads, *kv); }, workspace, workspace_bytes,
+                   stream);
+}
+
+moe_status moe_prefix_attn_workspace(const moe_paged_kv *kv, int64_t T, int32_t n_seqs, int32_t n_groups, int64_t max_q,
+                                     int64_t max_prefix, int64_t max_suffix, int32_t n_heads, size_t *bytes) {
+  if (!bytes) return MOE_ERR_NULL;
+  moe_status st = check_kv(kv, false);
+  if (st != MOE_OK) return st;
+  if ((st = check_prefix_sizes(T, n_seqs, n_groups, max_q, max_prefix, max_suffix, n_heads, *kv)) != MOE_OK) return st;
+  *bytes = shape_of(T, n_seqs, n_groups, max_q, max_prefix, max_suffix, n_heads, *kv).ws_bytes;
+  return MOE_OK;
+}
+
+moe_status moe_prefix_attn(const moe_paged_kv *kv, const moe_batch *batch, const moe_prefix_groups *groups, int64_t T,
+                           int64_t max_q, int64_t max_prefix, int64_t max_suffix, const moe_heads *q, int32_t n_heads,
+                           const moe_heads *out, float *lse, float scale, uint32_t flags, void *workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+  moe_status st = check_kv(kv, true);
+  if (st != MOE_OK) return st;
+  if ((st = check_batch(batch, kv->page_size)) != MOE_OK) return st;
+  if (!groups || !groups->group_start || !groups->prefix_len) return MOE_ERR_NULL;
+  if (!aligned(groups->group_start, 4) || !aligned(groups->prefix_len, 4)) return MOE_ERR_ALIGN;
+  if ((st = check_prefix_sizes(T, batch->n_seqs, groups->n_groups, max_q, max_prefix, max_suffix, n_heads, *kv)) != MOE_OK) return st;
+  return attn_call(*kv, *batch, groups, T, q, n_heads, out, lse, scale, 0, flags,
+                   [&] { return shape_of(T, batch->n_seqs, groups->n_groups, max_q, max_prefix, max_suffix, n_heads, *kv); },
+                   workspace, workspace_bytes, stream);
 }
 
 moe_status moe_gdn_step(int32_t R, int32_t n_kheads, int32_t n_vheads, int32_t d_k, int32_t d_v, const void *q,

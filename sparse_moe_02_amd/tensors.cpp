@@ -178,6 +178,19 @@ PyObject *py_batch(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// groups(group_start, prefix_len, index): (moe_prefix_groups, groups)
+PyObject *py_groups(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 3, [&] {
+    const int64_t index = integer(a[2]), any = -1;
+    moe_prefix_groups g{};
+    g.group_start = (const int32_t *)address("group_start", a[0], at::kInt, index, &any, 1);
+    const int64_t groups = THPVariable_Unpack(a[0]).size(0) - 1;
+    g.prefix_len = (const int32_t *)address("prefix_len", a[1], at::kInt, index, &groups, 1);
+    g.n_groups = small("group_start", groups);
+    return Py_BuildValue("Ni", bytes(g), g.n_groups);
+  });
+}
+
 // memory(cache, n_pages, index): moe_page_memory of a cache [n_planes][n_pages][...]
 PyObject *py_memory(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(n, 3, [&] {
@@ -210,6 +223,7 @@ PyMethodDef methods[] = {{"address", fast<py_address>(), METH_FASTCALL, nullptr}
                          {"rows", fast<py_rows>(), METH_FASTCALL, nullptr},
                          {"cache", fast<py_cache>(), METH_FASTCALL, nullptr},
                          {"batch", fast<py_batch>(), METH_FASTCALL, nullptr},
+                         {"groups", fast<py_groups>(), METH_FASTCALL, nullptr},
                          {"memory", fast<py_memory>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

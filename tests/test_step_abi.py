@@ -162,3 +162,44 @@ def test_sample_refusals(B):
         assert _sample(B, **kw) == ALIAS, kw
     for args, status in (((-1, 10), TOKENS), ((70000, 10), TOKENS), ((5, 0), SHAPE), ((5, (1 << 20) + 1), SHAPE)):
         assert _status(B, B.moe_sample_workspace, *args) == status
+
+
+# ------------------------------------------------------------------------------ prefix
+
+def _prefix(B, T=6, max_q=3, max_prefix=100, max_suffix=20, H=8, lse=None, scale=0.1, flags=0, ws=10 * M, wsn=1 << 29, groups=True,
+            gs=11 * M, pl=11 * M + 4096, n_groups=2, n_seqs=4, q=4 * M, out=5 * M, **kw):
+    d = dict(k=M, v=2 * M, page_stride=32 * 2 * 128, token_stride=2 * 128, head_stride=128, n_pages=10, page_size=32, n_kv_heads=2,
+             head_dim=128, dtype=B.MOE_BF16)
+    d.update(kw)
+    b = B.moe_batch(3 * M, 3 * M + 4096, 3 * M + 8192, None, n_seqs, max(n_seqs, 1), 5)
+    g = B.moe_prefix_groups(gs, pl, n_groups) if groups else None
+    return _status(B, B.moe_prefix_attn, B.moe_paged_kv(**d), b, g, T, max_q, max_prefix, max_suffix, B.moe_heads(q, 8 * 128, 128), H,
+                   B.moe_heads(out, 8 * 128, 128), lse, scale, flags, ws, wsn, 0)
+
+
+def test_prefix_calls_and_refusals(B):
+    assert _prefix(B) == DEVICE and _prefix(B, lse=12 * M, flags=B.MOE_ATTN_FULL, dtype=B.MOE_FP16) == DEVICE
+    assert _prefix(B, max_q=0, max_prefix=0, max_suffix=0) == DEVICE and _prefix(B, n_groups=4) == DEVICE
+    assert _prefix(B, T=0, ws=None, wsn=0) == 0
+    for kw in (dict(n_groups=0), dict(n_groups=5), dict(max_prefix=-1), dict(max_suffix=-1), dict(max_q=-1), dict(n_seqs=0), dict(H=3),
+               dict(head_dim=96), dict(flags=2), dict(scale=float("nan"))):
+        assert _prefix(B, **kw) == SHAPE, kw
+    for kw in (dict(groups=False), dict(gs=None), dict(pl=None), dict(q=None), dict(out=None)):
+        assert _prefix(B, **kw) == NULL, kw
+    for kw in (dict(gs=11 * M + 2), dict(pl=11 * M + 1), dict(ws=10 * M + 64), dict(lse=12 * M + 2)):
+        assert _prefix(B, **kw) == ALIGN, kw
+    assert _prefix(B, T=(1 << 17) + 1) == TOKENS and _prefix(B, dtype=B.MOE_FP32) == DTYPE
+    kv = B.moe_paged_kv(None, None, 0, 0, 0, 1, 16, 2, 128, B.MOE_BF16)
+    need = B.moe_prefix_attn_workspace(kv, 6, 4, 2, 3, 100, 20, 8)
+    assert need >= 6 * 8 * 2 * 128 * 4 and _prefix(B, wsn=need) == DEVICE and _prefix(B, wsn=need - 1) == WORKSPACE
+    for kw in (dict(out=11 * M - 4096), dict(lse=11 * M + 4100), dict(ws=11 * M), dict(lse=11 * M + 8), dict(lse=10 * M), dict(out=4 * M)):
+        assert _prefix(B, **kw) == ALIAS, kw
+
+
+def test_prefix_launches_stay_within_what_a_join_holds(B):
+    kv = B.moe_paged_kv(None, None, 0, 0, 0, 1, 16, 2, 128, B.MOE_BF16)
+    for T, seqs, groups, mq, mp, ms in ((1, 1, 1, 1, 1 << 30, 1 << 30), (6, 3, 3, 2, 0, 0), (1 << 17, 1 << 15, 7, 4, 16384, 500),
+                                         (64, 64, 1, 1, 16384, 512), (2, 2, 2, 1, 1 << 40, 3)):
+        n = B.moe_prefix_attn_workspace(kv, T, seqs, groups, mq, mp, ms, 8)
+        slots = n / (T * 8 * (128 * 4 + 16))
+        assert 2 <= slots <= 256.01, (T, slots)
