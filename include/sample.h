@@ -12,7 +12,7 @@
  *      total; its probability is its weight over that total.
  * A temperature of 0 (or below, or NaN) takes the largest logit, of equal ones the lowest index, with
  * probability 1.  Numbers that are NaN switch their step off (u: 0); u is cut to [0, 1).  A logit of
- * +infinity counts as 1e250.  A row without any token gives -1, with probability 0.
+ * +infinity counts as the largest float32.  A row without any token gives -1, with probability 0.
  *
  * Weights are held in 64-bit fixed point, with 62 - ceil(log2 V) bits (at most 51) behind that of the
  * largest, or to that precision, so that sums do not depend on their order and results are

@@ -50,7 +50,7 @@ def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     first = int(np.argmax(l))
     if not temperature > 0:
         return first, 1.0, 1.0
-    l = np.minimum(l, 1e250)
+    l = np.minimum(l, float(np.finfo(np.float32).max))
     far = np.where(l > -np.inf, l - l[first], 0.0) / (temperature if temperature < np.inf else 1e300)
     w = np.where(l > -np.inf, np.exp(far), 0.0)
     order = np.lexsort((np.arange(len(l)), -l))

@@ -2,17 +2,17 @@
 //
 // Weights w = 2^(y - y_max), y = l log2(e) / temperature in binary64, are held as 64-bit fixed point,
 // so that sums are the same in any order.  What is kept is a prefix of the tokens sorted by logit
-// (descending) and index, and a token's place in that order is one 64-bit number (the logit's bits, ordered, over the
-// inverted index), so every cut is one such number, and nothing is sorted.
+// (descending) and index, and a token's place in that order is one 64-bit number (the logit's bits, ordered,
+// over the inverted index), so every cut is one such number, and nothing is sorted.
 //
 //   k_sample_chunks  a workgroup for each 4096 logits: their maximum, and, relative to the power of two
 //                    above it, the count and the sum of weights of each quarter of an octave.  Reads
 //                    every logit once.  Without filters only the sum.
 //   k_sample_pick    a workgroup a row: adds the chunks' bins up, which gives the bin that each cut
-//                    lies in; collects the tokens of that bin (or, for top-k, of all bins down to it) and selects
-//                    among them, a byte of their numbers at a time; the kept weight of each
-//                    chunk gives the chunk that u falls into, which is read once more.  Where a cut's bin
-//                    holds more than kList tokens, the selection goes over the row itself.
+//                    lies in; collects the tokens of that bin (for top-k, of all bins down to it) and selects
+//                    among them, 8 bits of their places at a time; the kept weight of each chunk gives the
+//                    chunk that u falls into, which is read once more.  Where a cut's bins hold more than
+//                    kList tokens, each step of the selection reads them from the row.
 //
 // Bound: memory for many rows, latency for few.
 #include "common.hpp"
@@ -27,7 +27,7 @@ namespace {
 constexpr int kChunk = kSampleChunk, kBins = kSampleBins, kPerOctave = 4;
 constexpr int kThreads = 256;       // of k_sample_chunks
 constexpr int kPick = 1024;         // of k_sample_pick
-constexpr int kList = 4096;         // tokens that are selected among in LDS
+constexpr int kList = 8192;         // tokens that are selected among in LDS
 constexpr int kMaxChunks = (1 << 20) / kChunk + 1;
 constexpr int kCopies = 4;          // of a chunk's bins, by lane, against conflicts
 
@@ -60,7 +60,7 @@ __device__ __forceinline__ Row read_row(const SampleArgs &a, int r) {
   Row o;
   const float t = a.temperature ? a.temperature[r] : 1.0f;
   o.greedy = !(t > 0.0f);
-  o.c = 1.4426950408889634 / (double)t;
+  o.c = fmax(1.4426950408889634 / (double)t, 1e-300);  // (not 0, so that -infinity stays what it is)
   const int k = a.top_k ? a.top_k[r] : 0;
   o.k = k > 0 && k < a.V ? k : 0;
   const float p = a.top_p ? a.top_p[r] : 1.0f, m = a.min_p ? a.min_p[r] : 0.0f;
@@ -70,27 +70,36 @@ __device__ __forceinline__ Row read_row(const SampleArgs &a, int r) {
   return o;
 }
 
-// A logit's exponent; -infinity for tokens that are out.
-__device__ __forceinline__ double exponent_of(float l, double c) {
-  return l == -INFINITY ? -INFINITY : (l == INFINITY ? 1e250 : (double)l) * c;
-}
-// 2^t, t <= 0, times 2^bits: 2^f, 0 <= f < 1/64, by its series (off by less than 2^-48), times the table's
-// 2^(j / 64)
-__device__ __forceinline__ double weight_of(double t, int bits, const double *pow) {
-  t = fmax(t, -2048.0);  // (so are those that are out: 0)
+// 2^t times 2^bits, t = l c - anchor <= 0, and floor(64 t): 2^x, 0 <= x < 1/64, by its series (off by less
+// than 2^-48), times the table's 2^(j / 64 + bits).  (Of l = -infinity: 0.)
+struct Weight {
+  double w;
+  int n;
+  // whole part (the sum with 2^52 rounds; w < 2^52)
+  __device__ __forceinline__ uint64_t fixed() const { return (uint64_t)__double_as_longlong(w + 0x1p52) & 0xfffffffffffffull; }
+  // number of quarter octaves below the anchor
+  __device__ __forceinline__ int bin() const { return min(kBins - 1, -n >> 4); }
+};
+static_assert(64 / kPerOctave == 16, "as Weight::bin has it");
+__device__ __forceinline__ Weight weight_of(double t, const double *pow) {
+  t = fmax(t, -2048.0);
   const double n = __builtin_floor(t * 64.0);
   const int i = (int)n;
-  const double x = (t - n * 0.015625) * 0.69314718055994531;
-  double s = __builtin_fma(x, 1.0 / 120, 1.0 / 24);
-  s = __builtin_fma(x, s, 1.0 / 6);
-  s = __builtin_fma(x, s, 0.5);
+  const double x = __builtin_fma(n, -0.015625, t);
+  constexpr double k1 = 0.69314718055994531, k2 = k1 * k1 / 2, k3 = k2 * k1 / 3, k4 = k3 * k1 / 4, k5 = k4 * k1 / 5;
+  double s = __builtin_fma(x, k5, k4);
+  s = __builtin_fma(x, s, k3);
+  s = __builtin_fma(x, s, k2);
+  s = __builtin_fma(x, s, k1);
   s = __builtin_fma(x, s, 1.0);
-  s = __builtin_fma(x, s, 1.0);
-  return __builtin_ldexp(s * pow[i & 63], (i >> 6) + bits);
+  return Weight{__builtin_amdgcn_ldexp(s * pow[i & 63], i >> 6), i};
 }
-// Rounded to a whole number (below 2^52).
-__device__ __forceinline__ uint64_t fixed_of(double w) {
-  return (uint64_t)__double_as_longlong(w + 0x1p52) & 0xfffffffffffffull;
+__device__ __forceinline__ Weight weight_of(float l, double c, double anchor, const double *pow) {
+  // (not fused: the anchor is above the rounded product, and far out that is off by whole octaves)
+  return weight_of((double)l * c - anchor, pow);
+}
+__device__ __forceinline__ void fill_pow(double *pow, int bits) {
+  if (threadIdx.x < 64) pow[threadIdx.x] = __builtin_amdgcn_ldexp(kPow[threadIdx.x], bits);
 }
 
 // Order-preserving bits of a logit (both zeros alike).
@@ -98,7 +107,8 @@ __device__ __forceinline__ uint32_t key_of(float l) {
   const uint32_t b = __float_as_uint(l + 0.0f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ float logit_of(uint32_t key) {
+__device__ __forceinline__ float logit_of(uint64_t place) {
+  const uint32_t key = (uint32_t)(place >> 32);
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 // A token's place in the descending order.
@@ -121,7 +131,7 @@ struct Logits {
   }
   __device__ __forceinline__ float one(uint32_t w) const {
     const float l = TYPE == 0 ? __uint_as_float(w) : TYPE == 1 ? bf16_to_f32((uint16_t)w) : fp16_to_f32((uint16_t)w);
-    return l == l ? l : -INFINITY;
+    return l == l ? fminf(l, 3.4028234664e38f) : -INFINITY;
   }
   // numbers n .. n + kVec - 1 (n a multiple of kVec); -infinity outside the row
   __device__ __forceinline__ void load(int n, float (&o)[kVec]) const {
@@ -163,33 +173,33 @@ __device__ __forceinline__ uint64_t wave_scan_u64(uint64_t v) {  // inclusive
 }
 __device__ __forceinline__ void lds_add(uint64_t *p, uint64_t v) { atomicAdd((unsigned long long *)p, (unsigned long long)v); }
 
-__device__ __forceinline__ int bin_of(double t) { return t > -(double)kBins / kPerOctave ? min(kBins - 1, (int)(-t * kPerOctave)) : kBins - 1; }
-
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads) k_sample_chunks(SampleArgs a) {
   using L = Logits<TYPE>;
   constexpr int kVecs = kChunk / kThreads / L::kVec;  // blocks of a thread
   __shared__ double pow[64];
-  __shared__ uint64_t mass[kCopies][kBins];
-  __shared__ uint32_t count[kCopies][kBins];
+  __shared__ uint64_t mass[kBins][kCopies];
+  __shared__ uint32_t count[kBins][kCopies];
   __shared__ float tops[kThreads / 64];
   __shared__ uint64_t sums[kThreads / 64];
   const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
-  const Row row = read_row(a, r);
   const L logits(a, r);
-  if (tid < 64) pow[tid] = kPow[tid];
-  for (int i = tid; i < kCopies * kBins; i += kThreads) {
-    (&mass[0][0])[i] = 0;
-    (&count[0][0])[i] = 0;
-  }
   float l[kVecs][L::kVec];
   float top = -INFINITY;
 #pragma unroll
-  for (int q = 0; q < kVecs; ++q) {
-    logits.load(c * kChunk + (q * kThreads + tid) * L::kVec, l[q]);
+  for (int q = 0; q < kVecs; ++q) logits.load(c * kChunk + (q * kThreads + tid) * L::kVec, l[q]);
+  const Row row = read_row(a, r);
+  fill_pow(pow, a.bits);
+  if (row.filtered) {
+    for (int i = tid; i < kCopies * kBins; i += kThreads) {
+      (&mass[0][0])[i] = 0;
+      (&count[0][0])[i] = 0;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kVecs; ++q)
 #pragma unroll
     for (int e = 0; e < L::kVec; ++e) top = fmaxf(top, l[q][e]);
-  }
   top = wave_max(top);
   if ((tid & 63) == 0) tops[tid >> 6] = top;
   __syncthreads();
@@ -209,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) k_sample_chunks(SampleArgs a) {
     if (tid == 0) out->best = max(max(sums[0], sums[1]), max(sums[2], sums[3]));
     return;
   }
-  const double y0 = exponent_of(top, row.c), anchor = __builtin_ceil(y0);
+  const double y0 = (double)top * row.c, anchor = __builtin_ceil(y0);
   uint64_t sum = 0;
   const int copy = tid % kCopies;
   if (top > -INFINITY) {
@@ -217,13 +227,12 @@ __global__ void __launch_bounds__(kThreads) k_sample_chunks(SampleArgs a) {
     for (int q = 0; q < kVecs; ++q)
 #pragma unroll
       for (int e = 0; e < L::kVec; ++e) {
-        const double t = exponent_of(l[q][e], row.c) - anchor;
-        const uint64_t w = l[q][e] == -INFINITY ? 0 : fixed_of(weight_of(t, a.bits, pow));
-        sum += w;
+        const Weight w = weight_of(l[q][e], row.c, anchor, pow);
+        sum += w.fixed();
         if (row.filtered && l[q][e] > -INFINITY) {
-          const int b = bin_of(t);
-          lds_add(&mass[copy][b], w);
-          atomicAdd(&count[copy][b], 1u);
+          const int b = w.bin();
+          lds_add(&mass[b][copy], w.fixed());
+          atomicAdd(&count[b][copy], 1u);
         }
       }
   }
@@ -240,8 +249,8 @@ __global__ void __launch_bounds__(kThreads) k_sample_chunks(SampleArgs a) {
     uint32_t n = 0;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
-      m += mass[i][b];
-      n += count[i][b];
+      m += mass[b][i];
+      n += count[b][i];
     }
     const int64_t at = ((int64_t)r * a.C + c) * kBins + b;
     a.mass[at] = m;
@@ -255,76 +264,171 @@ struct Shared {
   double anchor[kMaxChunks];
   int shift[kMaxChunks];       // octaves of a chunk's anchor below the row's (64: out of reach)
   uint64_t kept[kMaxChunks];   // kept weight of the chunks, then the sums up to each
+  int active[kMaxChunks];      // chunks that are read
   uint64_t mass[kBins];        // of the row; then the sums down to each bin
   uint32_t count[kBins];
   uint64_t sel_mass[256];      // of a selection's step
   uint32_t sel_count[256];
   uint64_t red[kPick / 64];
-  uint64_t found[4];
-  int n;                       // tokens in the list
+  uint64_t found[3];
+  int n, n_active;             // tokens in the list, chunks that are read
 };
 
-// The whole row, or the list of its tokens in LDS, as a set of (place, weight).
-struct List {
-  const uint64_t *place, *weight;
-  int n;
-  template <class F>
-  __device__ __forceinline__ void each(F f) const {
-    for (int i = threadIdx.x; i < n; i += kPick) f(place[i], weight[i]);
-  }
-};
+// The tokens of row bins lo .. hi as a set of (place, weight): in LDS, or read from the row each time.
 template <int TYPE>
-struct Whole {
-  const Logits<TYPE> &logits;
-  double c, anchor;
-  const double *pow;
-  int bits;
+struct Set {
+  using L = Logits<TYPE>;
+  const L &logits;
+  const Row &row;
+  Shared &sh;
+  uint64_t *places;
+  int lo = 0, hi = -1;  // none
+  bool listed = true;
+  float least_l, most_l;     // logits outside these are in none of the bins
+  uint64_t first, last;      // bounds of the places
+  __device__ __forceinline__ Set(const L &logits, const Row &row, Shared &sh, uint64_t *places)
+      : logits(logits), row(row), sh(sh), places(places) {}
+
+  // a chunk's bin among the row's
+  __device__ __forceinline__ int row_bin(int c, int b) const {
+    return b == kBins - 1 ? b : min(kBins - 1, b + kPerOctave * sh.shift[c]);
+  }
+  __device__ __forceinline__ uint64_t scaled(int c, uint64_t m) const { return sh.shift[c] < 64 ? m >> sh.shift[c] : 0; }
+
+  // f(logit, number, chunk, in the bins) for the logits of all active chunks, in whole waves; a wave's
+  // logits are of one chunk
   template <class F>
-  __device__ __forceinline__ void each(F f) const {
-    constexpr int kVec = Logits<TYPE>::kVec;
-    for (int n = threadIdx.x * kVec; n < logits.skip + logits.V; n += kPick * kVec) {
-      float l[kVec];
-      logits.load(n, l);
+  __device__ __forceinline__ void scan(F f) const {
+    constexpr int kPer = kPick * L::kVec / kChunk, kAhead = 4 / kPer;  // chunks of a step, steps in flight
+    const int tid = threadIdx.x, sub = tid / (kPick / kPer), off = tid % (kPick / kPer) * L::kVec;
+    for (int i = 0; i < sh.n_active; i += kPer * kAhead) {
+      float l[kAhead][L::kVec];
+      int c[kAhead];
 #pragma unroll
-      for (int e = 0; e < kVec; ++e)
-        if (l[e] > -INFINITY) f(place_of(l[e], n + e - logits.skip), fixed_of(weight_of(exponent_of(l[e], c) - anchor, bits, pow)));
+      for (int j = 0; j < kAhead; ++j) {
+        const int at = i + j * kPer + sub;
+        c[j] = at < sh.n_active ? sh.active[at] : -1;
+#pragma unroll
+        for (int e = 0; e < L::kVec; ++e) l[j][e] = -INFINITY;
+        if (c[j] >= 0) logits.load(c[j] * kChunk + off, l[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (c[j] < 0) continue;
+#pragma unroll
+        for (int e = 0; e < L::kVec; ++e) f(l[j][e], c[j] * kChunk + off + e, c[j]);
+      }
     }
   }
+  // whether a logit is in the bins, and its weight
+  __device__ __forceinline__ bool in(float l, int c, Weight &w) const {
+    if (!(l >= least_l && l <= most_l) || l == -INFINITY) return false;
+    w = weight_of(l, row.c, sh.anchor[c], sh.pow);
+    const int b = row_bin(c, w.bin());
+    return b >= lo && b <= hi;
+  }
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    if (listed) {
+      for (int i = threadIdx.x; i < sh.n; i += kPick) {
+        const int c = (index_of(places[i]) + logits.skip) / kChunk;
+        f(places[i], scaled(c, weight_of(logit_of(places[i]), row.c, sh.anchor[c], sh.pow).fixed()), c);
+      }
+    } else {
+      scan([&](float l, int n, int c) {
+        Weight w;
+        if (in(l, c, w)) f(place_of(l, n - logits.skip), scaled(c, w.fixed()), c);
+      });
+    }
+  }
+  // takes bins b0 .. b1
+  __device__ __forceinline__ void take(int b0, int b1, double anchor, int chunks) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    lo = b0;
+    hi = b1;
+    // bin b holds 2^t for t from (1 - 16 (b + 1)) / 64 up to (1 - 16 b) / 64 (bounds that are safe against every rounding)
+    constexpr double kStep = 1.0 / kPerOctave, kUp = 1.0 / 64;
+    auto bound = [&](double y, double way) {
+      const double x = (y + way * 1e-3) / row.c;
+      return (float)(x + way * 1e-6 * fabs(x));
+    };
+    most_l = fminf(bound(anchor - b0 * kStep + kUp, 1.0), 3.4028234664e38f);
+    least_l = b1 == kBins - 1 ? -INFINITY : bound(anchor - (b1 + 1) * kStep + kUp, -1.0);
+    first = (uint64_t)key_of(least_l) << 32;
+    last = (uint64_t)key_of(most_l) << 32 | 0xffffffffu;
+    listed = sh.count[b1] - (b0 > 0 ? sh.count[b0 - 1] : 0) <= (uint32_t)kList;
+    __syncthreads();
+    if (tid < 64) {  // chunks that reach the bins
+      int n = 0;
+      for (int c0 = 0; c0 < chunks; c0 += 64) {
+        const bool some = c0 + lane < chunks && kPerOctave * sh.shift[c0 + lane] <= b1 && sh.anchor[c0 + lane] > -INFINITY;
+        const uint64_t m = __ballot(some);
+        if (some) sh.active[n + __popcll(m & ((uint64_t(1) << lane) - 1))] = c0 + lane;
+        n += __popcll(m);
+      }
+      if (lane == 0) {
+        sh.n_active = n;
+        sh.n = 0;
+      }
+    }
+    __syncthreads();
+    if (!listed) return;
+    scan([&](float l, int n, int c) {
+      Weight w;
+      const bool hit = in(l, c, w);
+      const uint64_t m = __ballot(hit);
+      if (!m) return;
+      int at = 0;
+      if (lane == __builtin_ctzll(m)) at = atomicAdd(&sh.n, (int)__popcll(m));
+      at = __shfl(at, __builtin_ctzll(m), 64);
+      if (hit) places[at + __popcll(m & ((uint64_t(1) << lane) - 1))] = place_of(l, n - logits.skip);
+    });
+    __syncthreads();
+  }
 };
 
-// The least place `at` such that the tokens from it on (of those from `least` on) are at least `want` in number, or
-// weigh that much, and their weight; all of them where they do not reach that.  A byte of the places at a time,
-// from the top.
+__device__ __forceinline__ uint64_t block_max(uint64_t v, Shared &sh) {
+  const int lane = threadIdx.x & 63;
+  v = wave_max_u64(v);
+  if (lane == 0) sh.red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = sh.red[lane % (kPick / 64)];
+  __syncthreads();
+  return wave_max_u64(v);
+}
+
+// The least place `at` such that the set's tokens from it on (of those from `least` on) are at least `want` in
+// number, or weigh that much, and their weight; all of them where they do not reach that.  8 bits of the places at
+// a time, from the first one in which they differ.
 struct Cut {
   uint64_t at, weight;
 };
 template <class S>
-__device__ Cut select_from(const S &set, bool by_weight, uint64_t want, uint64_t least, Shared &sh) {
+__device__ __forceinline__ Cut select_from(const S &set, bool by_weight, uint64_t want, uint64_t least, Shared &sh) {
   const int tid = threadIdx.x, lane = tid & 63;
-  uint64_t prefix = 0, above = 0;
+  const uint64_t first = max(set.first, least), differ = first ^ set.last;
+  int bits = 64 - __builtin_clzll(differ | 1);  // bits that are not known yet
+  uint64_t prefix = bits < 64 ? set.last >> bits : 0, above = 0;
   // the least place of the set that begins with the prefix (there are tokens outside the set between it and
   // the prefix followed by zeros)
-  auto least_of = [&](int shift) {
+  auto least_of = [&](int rest) {
     uint64_t v = ~uint64_t(0);
-    set.each([&](uint64_t place, uint64_t) {
-      if (place >= least && (shift > 56 || place >> shift == prefix)) v = min(v, place);
+    set.each([&](uint64_t place, uint64_t, int) {
+      if (place >= least && (rest > 63 || place >> rest == prefix)) v = min(v, place);
     });
-    v = ~wave_max_u64(~v);
-    if (lane == 0) sh.red[tid >> 6] = v;
-    __syncthreads();
-    v = sh.red[lane % (kPick / 64)];
-    __syncthreads();
-    return ~wave_max_u64(~v);
+    return ~block_max(~v, sh);
   };
-  for (int shift = 56; shift >= 0; shift -= 8) {
+  bool started = false;
+  while (true) {
+    const int rest = max(bits - 8, 0);  // bits below this step's
     for (int i = tid; i < 256; i += kPick) {
       sh.sel_mass[i] = 0;
       sh.sel_count[i] = 0;
     }
     __syncthreads();
-    set.each([&](uint64_t place, uint64_t w) {
-      if (place < least || (shift < 56 && place >> (shift + 8) != prefix)) return;
-      const int b = (int)(place >> shift & 255);
+    set.each([&](uint64_t place, uint64_t w, int) {
+      if (place < least || (bits < 64 && place >> bits != prefix)) return;
+      const int b = (int)(place >> rest & ((1u << (bits - rest)) - 1));
       lds_add(&sh.sel_mass[b], w);
       atomicAdd(&sh.sel_count[b], 1u);
     });
@@ -347,15 +451,12 @@ __device__ Cut select_from(const S &set, bool by_weight, uint64_t want, uint64_t
         if (bin < 0 && before + own[i] >= want) bin = 255 - 4 * lane - i;
         if (bin < 0) before += own[i];
       }
-      if (hit == 0) {
-        if (lane == 0) sh.found[0] = 256;
-      } else if (lane == __builtin_ctzll(hit)) {
-        sh.found[0] = (uint64_t)bin;
+      const int cut = hit == 0 ? -1 : __shfl(bin, __builtin_ctzll(hit), 64);
+      if (hit == 0 ? lane == 0 : lane == __builtin_ctzll(hit)) {
+        sh.found[0] = (uint64_t)(cut < 0 ? 256 : cut);
         sh.found[1] = before;
       }
-      // (weight above the bin)
-      uint64_t w = 0;
-      const int cut = hit == 0 ? -1 : __shfl(bin, __builtin_ctzll(hit), 64);
+      uint64_t w = 0;  // weight above the bin
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (255 - 4 * lane - i > cut) w += sh.sel_mass[255 - 4 * lane - i];
@@ -364,47 +465,36 @@ __device__ Cut select_from(const S &set, bool by_weight, uint64_t want, uint64_t
     }
     __syncthreads();
     const int bin = (int)sh.found[0];
-    const uint64_t before = sh.found[1], over = sh.found[2];
-    above += over;
-    if (bin > 255) {  // (in the first step only: the bin of a step reaches what is wanted of the next)
-      __syncthreads();
-      return Cut{least_of(64), above};
-    }
-    const uint32_t n = sh.sel_count[bin];
-    const uint64_t m = sh.sel_mass[bin];
+    const uint64_t before = sh.found[1];
+    above += sh.found[2];
+    const uint32_t n = bin < 256 ? sh.sel_count[bin] : 0;
+    const uint64_t m = bin < 256 ? sh.sel_mass[bin] : 0;
     __syncthreads();
-    prefix = prefix << 8 | (uint64_t)bin;
+    if (bin > 255) return Cut{started ? least : least_of(64), above};  // (in the first step only)
+    started = true;
+    prefix = prefix << (bits - rest) | (uint64_t)bin;
     want -= before;
-    if (shift == 0) return Cut{prefix, above + m};
-    if (n == 1 || (!by_weight && n == want)) return Cut{least_of(shift), above + m};  // the whole bin
+    if (rest == 0) return Cut{prefix, above + m};
+    if (n == 1 || (!by_weight && n == want)) return Cut{least_of(rest), above + m};  // the whole bin
+    bits = rest;
   }
-  return Cut{least, above};  // (not reached)
 }
 
 template <int TYPE>
 __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   using L = Logits<TYPE>;
   extern __shared__ __align__(16) uint8_t lds_raw[];
-  uint64_t *places = (uint64_t *)lds_raw, *weights = places + kList;
   __shared__ Shared sh;
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Row row = read_row(a, r);
   const L logits(a, r);
   const SampleChunk *chunk = a.chunk + (int64_t)r * a.C;
-  if (tid < 64) sh.pow[tid] = kPow[tid];
+  fill_pow(sh.pow, a.bits);
 
-  auto block_max = [&](uint64_t v) {
-    v = wave_max_u64(v);
-    if (lane == 0) sh.red[wave] = v;
-    __syncthreads();
-    v = sh.red[lane % (kPick / 64)];
-    __syncthreads();
-    return wave_max_u64(v);
-  };
   if (row.greedy) {
     uint64_t best = 0;
     for (int c = tid; c < a.C; c += kPick) best = max(best, chunk[c].best);
-    best = block_max(best);
+    best = block_max(best, sh);
     if (tid == 0) {
       a.token[r] = best ? index_of(best) : -1;
       if (a.prob) a.prob[r] = best ? 1.0f : 0.0f;
@@ -423,7 +513,11 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
     sh.kept[c] = 0;
     most = max(most, ordered(y));
   }
-  most = block_max(most);
+  for (int i = tid; i < kBins; i += kPick) {
+    sh.mass[i] = 0;
+    sh.count[i] = 0;
+  }
+  most = block_max(most, sh);
   const double y0 = __longlong_as_double((long long)(most >> 63 ? most & ~(uint64_t(1) << 63) : ~most));
   if (y0 == -INFINITY) {
     if (tid == 0) {
@@ -437,29 +531,24 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
     const double d = anchor - sh.anchor[c];
     sh.shift[c] = d < 64.0 ? (int)d : 64;
   }
-  for (int i = tid; i < kBins; i += kPick) {
-    sh.mass[i] = 0;
-    sh.count[i] = 0;
-  }
   __syncthreads();
 
   uint64_t least = 0;          // places that are kept are at least this
   double floor = -INFINITY;    // and exponents this
-  bool whole = false;          // the selection went over the row: weights relative to its anchor
+  auto above_floor = [&](float l) { return (double)l * row.c >= floor; };
   if (!row.filtered) {
     for (int c = tid; c < a.C; c += kPick) sh.kept[c] = sh.shift[c] < 64 ? chunk[c].total >> sh.shift[c] : 0;
   } else {
     const uint64_t *mass = a.mass + (int64_t)r * a.C * kBins;
     const uint32_t *count = a.count + (int64_t)r * a.C * kBins;
-    // a chunk's bin among the row's
-    auto row_bin = [&](int c, int b) { return b == kBins - 1 ? b : min(kBins - 1, b + kPerOctave * sh.shift[c]); };
-    auto scaled = [&](int c, uint64_t m) { return sh.shift[c] < 64 ? m >> sh.shift[c] : 0; };
+    Set<TYPE> set(logits, row, sh, (uint64_t *)lds_raw);
     for (int i = tid; i < a.C * kBins; i += kPick) {
       const uint32_t n = count[i];
+      const uint64_t m = mass[i];
       if (n == 0) continue;
-      const int c = i / kBins, b = row_bin(c, i % kBins);
+      const int c = i / kBins, b = set.row_bin(c, i % kBins);
       atomicAdd(&sh.count[b], n);
-      lds_add(&sh.mass[b], scaled(c, mass[i]));
+      lds_add(&sh.mass[b], set.scaled(c, m));
     }
     __syncthreads();
     if (wave == 0) {  // sums down to each bin
@@ -480,42 +569,6 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
     __syncthreads();
     auto mass_above = [&](int b) { return b > 0 ? sh.mass[b - 1] : 0; };
     auto count_above = [&](int b) { return b > 0 ? sh.count[b - 1] : 0u; };
-
-    int lo = 0, hi = -1;  // bins of which the list holds all tokens
-    // collects the tokens of bins b0 .. b1; false where they are too many
-    auto gather = [&](int b0, int b1) {
-      if (sh.count[b1] - count_above(b0) > (uint32_t)kList) return false;
-      __syncthreads();
-      if (tid == 0) sh.n = 0;
-      __syncthreads();
-      for (int c = wave; c < a.C; c += kPick / 64) {
-        const int s = sh.shift[c];
-        bool some = false;
-        for (int b = lane; b < kBins; b += 64) {
-          const int rb = row_bin(c, b);
-          some |= rb >= b0 && rb <= b1 && count[c * kBins + b] > 0;
-        }
-        if (!__ballot(some)) continue;
-        for (int n = c * kChunk + lane * L::kVec; n < (c + 1) * kChunk; n += 64 * L::kVec) {
-          float l[L::kVec];
-          logits.load(n, l);
-#pragma unroll
-          for (int e = 0; e < L::kVec; ++e) {
-            if (l[e] == -INFINITY) continue;
-            const double t = exponent_of(l[e], row.c) - sh.anchor[c];
-            const int b = row_bin(c, bin_of(t));
-            if (b < b0 || b > b1) continue;
-            const int at = atomicAdd(&sh.n, 1);
-            places[at] = place_of(l[e], n + e - logits.skip);
-            weights[at] = s < 64 ? fixed_of(weight_of(t, a.bits, sh.pow)) >> s : 0;
-          }
-        }
-      }
-      __syncthreads();
-      lo = b0;
-      hi = b1;
-      return true;
-    };
     auto first_bin = [&](auto enough) {  // the first bin down to which `enough` holds
       for (int b = 0; b < kBins; b += 64) {
         const uint64_t yes = __ballot(enough(b + lane));
@@ -523,67 +576,57 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
       }
       return kBins - 1;
     };
+    auto has = [&](int b) { return set.lo <= b && b <= set.hi; };
 
     int cut = kBins;  // the bin of the cut
     uint64_t total = sh.mass[kBins - 1];
     if (row.k > 0 && (uint32_t)row.k < sh.count[kBins - 1]) {
       cut = first_bin([&](int b) { return sh.count[b] >= (uint32_t)row.k; });
-      const int from = sh.count[cut] <= (uint32_t)kList ? 0 : cut;
-      if (gather(from, cut)) {
-        const Cut o = select_from(List{places, weights, sh.n}, false, (uint64_t)row.k - count_above(lo), 0, sh);
-        least = o.at;
-        total = mass_above(lo) + o.weight;
-      } else {
-        whole = true;
-      }
+      set.take(sh.count[cut] <= (uint32_t)kList ? 0 : cut, cut, anchor, a.C);
+      const Cut o = select_from(set, false, (uint64_t)row.k - count_above(set.lo), 0, sh);
+      least = o.at;
+      total = mass_above(set.lo) + o.weight;
     }
-    // of a share of the total: as a whole number, at least 1
-    auto share = [](double p, uint64_t t) {
-      const double x = __builtin_ceil(p * (double)t);
-      return max(min((uint64_t)x, t), uint64_t(1));
-    };
-    if (!whole && row.p < 1.0) {
-      const uint64_t want = share(row.p, total);
+    if (row.p < 1.0) {
+      // the share as a whole number, at least 1
+      const uint64_t want = max(min((uint64_t)__builtin_ceil(row.p * (double)total), total), uint64_t(1));
       const int b = min(cut, first_bin([&](int i) { return sh.mass[i] >= want; }));
-      if ((lo <= b && b <= hi) || gather(b, b)) {
-        const uint64_t over = mass_above(lo);
-        least = max(least, select_from(List{places, weights, sh.n}, true, want > over ? want - over : 1, least, sh).at);
-        cut = b;
-      } else {
-        whole = true;
-      }
+      if (!has(b)) set.take(b, b, anchor, a.C);
+      const uint64_t over = mass_above(set.lo);
+      least = max(least, select_from(set, true, want > over ? want - over : 1, least, sh).at);
+      cut = b;
     }
-    if (row.m > 0.0) floor = y0 + log2(row.m);
-    if (!whole && row.m > 0.0) {
-      const int b = bin_of(floor - anchor);
-      if (b <= cut && ((lo <= b && b <= hi) || gather(b, b))) cut = b;
-      else if (b <= cut) whole = true;
+    if (row.m > 0.0) {
+      floor = y0 + log2(row.m);
+      const int b = weight_of(floor - anchor, sh.pow).bin();
+      if (b <= cut && !has(b)) set.take(b, b, anchor, a.C);
     }
-    if (whole) {
-      const Whole<TYPE> set{logits, row.c, anchor, sh.pow, a.bits};
-      least = 0;
-      if (row.k > 0 && (uint32_t)row.k < sh.count[kBins - 1]) {
-        const Cut o = select_from(set, false, (uint64_t)row.k, 0, sh);
-        least = o.at;
-        total = o.weight;
-      } else {
-        total = sh.mass[kBins - 1];
-      }
-      if (row.p < 1.0) least = max(least, select_from(set, true, share(row.p, total), least, sh).at);
-      set.each([&](uint64_t place, uint64_t w) {
-        if (place >= least && exponent_of(logit_of((uint32_t)(place >> 32)), row.c) >= floor)
-          lds_add(&sh.kept[(index_of(place) + logits.skip) / kChunk], w);
+    const bool none = set.hi < 0;  // no cut: all bins
+    for (int i = tid; i < a.C * kBins; i += kPick) {
+      const int c = i / kBins;
+      if ((none || set.row_bin(c, i % kBins) < set.lo) && count[i] > 0) lds_add(&sh.kept[c], set.scaled(c, mass[i]));
+    }
+    if (!none && set.listed) {
+      set.each([&](uint64_t place, uint64_t w, int c) {
+        if (place >= least && above_floor(logit_of(place))) lds_add(&sh.kept[c], w);
       });
-    } else {
-      const bool none = hi < 0;  // no cut: all bins
-      for (int i = tid; i < a.C * kBins; i += kPick) {
-        const uint32_t n = count[i];
-        const int c = i / kBins;
-        if (n > 0 && (none || row_bin(c, i % kBins) < lo)) lds_add(&sh.kept[c], scaled(c, mass[i]));
-      }
-      for (int i = tid; !none && i < sh.n; i += kPick)
-        if (places[i] >= least && exponent_of(logit_of((uint32_t)(places[i] >> 32)), row.c) >= floor)
-          lds_add(&sh.kept[(index_of(places[i]) + logits.skip) / kChunk], weights[i]);
+    } else if (!none) {  // (a wave's logits are of one chunk)
+      uint64_t sum = 0;
+      int at = -1;
+      auto flush = [&] {
+        const uint64_t v = wave_sum_u64(sum);
+        if (lane == 0 && v > 0) lds_add(&sh.kept[at], v);
+        sum = 0;
+      };
+      set.scan([&](float l, int n, int c) {
+        if (c != at) {
+          if (at >= 0) flush();
+          at = c;
+        }
+        Weight w;
+        if (set.in(l, c, w) && place_of(l, n - logits.skip) >= least && above_floor(l)) sum += set.scaled(c, w.fixed());
+      });
+      if (at >= 0) flush();
     }
   }
   __syncthreads();
@@ -604,18 +647,16 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   const double u = u0 > 0.0f ? fminf(u0, 1.0f) : 0.0;
   const uint64_t want = min((uint64_t)(u * (double)total), total - 1);  // (the first sum above it is wanted)
   int c = 0;
-  {
-    int lo = 0, hi = a.C - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (sh.kept[mid] > want) hi = mid;
-      else lo = mid + 1;
+  for (int c0 = 0; c0 < a.C; c0 += 64) {
+    const uint64_t m = __ballot(c0 + lane < a.C && sh.kept[min(c0 + lane, a.C - 1)] > want);
+    if (m) {
+      c = c0 + (int)__builtin_ctzll(m);
+      break;
     }
-    c = lo;
   }
   // in the chunk, in its own weights
-  const int shift = whole ? 0 : sh.shift[c];
-  const double from = whole ? anchor : sh.anchor[c];
+  const int shift = sh.shift[c];
+  const double from = sh.anchor[c];
   uint64_t target = (want - (c > 0 ? sh.kept[c - 1] : 0)) << shift;
   constexpr int kHave = kChunk / L::kVec;  // threads with logits
   float l[L::kVec];
@@ -628,9 +669,8 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
     mine = 0;
 #pragma unroll
     for (int e = 0; e < L::kVec; ++e) {
-      const double y = exponent_of(l[e], row.c);
-      const bool keep = l[e] > -INFINITY && place_of(l[e], n + e - logits.skip) >= least && y >= floor;
-      w[e] = keep ? fixed_of(weight_of(y - from, a.bits, sh.pow)) : 0;
+      const bool keep = l[e] > -INFINITY && place_of(l[e], n + e - logits.skip) >= least && above_floor(l[e]);
+      w[e] = keep ? weight_of(l[e], row.c, from, sh.pow).fixed() : 0;
       mine += w[e];
     }
     upto = wave_scan_u64(mine);
@@ -656,8 +696,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
     for (int e = 0; e < L::kVec; ++e) {
       if (target >= sum && target < sum + w[e]) {
         a.token[r] = n + e - logits.skip;
-        if (a.prob)
-          a.prob[r] = (float)(__builtin_ldexp(weight_of(exponent_of(l[e], row.c) - from, a.bits, sh.pow), -shift) / (double)total);
+        if (a.prob) a.prob[r] = (float)(__builtin_amdgcn_ldexp(weight_of(l[e], row.c, from, sh.pow).w, -shift) / (double)total);
       }
       sum += w[e];
     }
@@ -667,7 +706,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
 template <int TYPE>
 hipError_t launch(const SampleArgs &a, hipStream_t s) {
   static std::atomic<uint64_t> done{0};
-  constexpr int lds = 2 * kList * 8;
+  constexpr int lds = kList * 8;
   const hipError_t e = allow_lds(k_sample_pick<TYPE>, lds, done);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_sample_chunks<TYPE>), dim3(a.C, a.R), dim3(kThreads), 0, s, a);
