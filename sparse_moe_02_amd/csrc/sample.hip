@@ -27,7 +27,7 @@ namespace {
 constexpr int kChunk = kSampleChunk, kBins = kSampleBins, kPerOctave = 4;
 constexpr int kThreads = 256;       // of k_sample_chunks
 constexpr int kPick = 1024;         // of k_sample_pick
-constexpr int kList = 8192;         // tokens that are selected among in LDS
+constexpr int kList = 16384;        // tokens that are selected among in LDS
 constexpr int kMaxChunks = (1 << 20) / kChunk + 1;
 constexpr int kCopies = 4;          // of a chunk's bins, by lane, against conflicts
 
@@ -129,25 +129,34 @@ struct Logits {
     base = p - skip * kSize;
     V = a.V;
   }
-  __device__ __forceinline__ float one(uint32_t w) const {
-    const float l = TYPE == 0 ? __uint_as_float(w) : TYPE == 1 ? bf16_to_f32((uint16_t)w) : fp16_to_f32((uint16_t)w);
-    return l == l ? fminf(l, 3.4028234664e38f) : -INFINITY;
+  // of a block, element e
+  __device__ __forceinline__ float raw(u32x4 w, int e) const {
+    const uint32_t v = TYPE == 0 ? w[e % 4] : e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
+    return TYPE == 0 ? __uint_as_float(v) : TYPE == 1 ? bf16_to_f32((uint16_t)v) : fp16_to_f32((uint16_t)v);
   }
   // numbers n .. n + kVec - 1 (n a multiple of kVec); -infinity outside the row
-  __device__ __forceinline__ void load(int n, float (&o)[kVec]) const {
-    if (n >= skip && n + kVec <= skip + V) {
-      const u32x4 w = *(const u32x4 *)(base + (int64_t)n * kSize);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) o[e] = one(TYPE == 0 ? w[e % 4] : e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu);
-      return;
-    }
+  __device__ __forceinline__ u32x4 block(int n) const {
+    if (n >= skip && n + kVec <= skip + V) return *(const u32x4 *)(base + (int64_t)n * kSize);
+    constexpr uint32_t kOut = TYPE == 0 ? 0xff800000u : TYPE == 1 ? 0xff80ff80u : 0xfc00fc00u;
+    u32x4 w = {kOut, kOut, kOut, kOut};
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
-      o[e] = -INFINITY;
       if (n + e < skip || n + e >= skip + V) continue;
-      if constexpr (TYPE == 0) o[e] = one(*(const uint32_t *)(base + (int64_t)(n + e) * 4));
-      else o[e] = one(*(const uint16_t *)(base + (int64_t)(n + e) * 2));
+      if constexpr (TYPE == 0) {
+        w[e % 4] = *(const uint32_t *)(base + (int64_t)(n + e) * 4);
+      } else {
+        const uint32_t v = *(const uint16_t *)(base + (int64_t)(n + e) * 2);
+        w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | v << 16 : (w[e / 2] & 0xffff0000u) | v;
+      }
     }
+    return w;
+  }
+  // as a number; -infinity where it is none
+  __device__ __forceinline__ float clean(float l) const { return l == l ? fminf(l, 3.4028234664e38f) : -INFINITY; }
+  __device__ __forceinline__ void load(int n, float (&o)[kVec]) const {
+    const u32x4 w = block(n);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) o[e] = clean(raw(w, e));
   }
 };
 
@@ -295,30 +304,36 @@ struct Set {
   }
   __device__ __forceinline__ uint64_t scaled(int c, uint64_t m) const { return sh.shift[c] < 64 ? m >> sh.shift[c] : 0; }
 
-  // f(logit, number, chunk, in the bins) for the logits of all active chunks, in whole waves; a wave's
-  // logits are of one chunk
+  // f(blocks, numbers of their first elements, chunks) for the logits of all active chunks, kAhead blocks a
+  // thread at a time, by whole waves: a wave's block is of one chunk (-1: none)
+  static constexpr int kPer = kPick * L::kVec / kChunk, kAhead = 4 / kPer;  // chunks of a step, steps in flight
   template <class F>
   __device__ __forceinline__ void scan(F f) const {
-    constexpr int kPer = kPick * L::kVec / kChunk, kAhead = 4 / kPer;  // chunks of a step, steps in flight
     const int tid = threadIdx.x, sub = tid / (kPick / kPer), off = tid % (kPick / kPer) * L::kVec;
     for (int i = 0; i < sh.n_active; i += kPer * kAhead) {
-      float l[kAhead][L::kVec];
-      int c[kAhead];
+      u32x4 w[kAhead];
+      int n[kAhead], c[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const int at = i + j * kPer + sub;
-        c[j] = at < sh.n_active ? sh.active[at] : -1;
-#pragma unroll
-        for (int e = 0; e < L::kVec; ++e) l[j][e] = -INFINITY;
-        if (c[j] >= 0) logits.load(c[j] * kChunk + off, l[j]);
+        c[j] = __builtin_amdgcn_readfirstlane(at < sh.n_active ? sh.active[at] : -1);
+        n[j] = c[j] * kChunk + off;
+        if (c[j] >= 0) w[j] = logits.block(n[j]);
       }
+      f(w, n, c);
+    }
+  }
+  // f(logit, number, chunk) for all of them
+  template <class F>
+  __device__ __forceinline__ void scan_each(F f) const {
+    scan([&](const u32x4 (&w)[kAhead], const int (&n)[kAhead], const int (&c)[kAhead]) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         if (c[j] < 0) continue;
 #pragma unroll
-        for (int e = 0; e < L::kVec; ++e) f(l[j][e], c[j] * kChunk + off + e, c[j]);
+        for (int e = 0; e < L::kVec; ++e) f(logits.clean(logits.raw(w[j], e)), n[j] + e, c[j]);
       }
-    }
+    });
   }
   // whether a logit is in the bins, and its weight
   __device__ __forceinline__ bool in(float l, int c, Weight &w) const {
@@ -331,11 +346,13 @@ struct Set {
   __device__ __forceinline__ void each(F f) const {
     if (listed) {
       for (int i = threadIdx.x; i < sh.n; i += kPick) {
-        const int c = (index_of(places[i]) + logits.skip) / kChunk;
-        f(places[i], scaled(c, weight_of(logit_of(places[i]), row.c, sh.anchor[c], sh.pow).fixed()), c);
+        const uint64_t place = places[i];
+        if (place == 0) continue;
+        const int c = (index_of(place) + logits.skip) / kChunk;
+        f(place, scaled(c, weight_of(logit_of(place), row.c, sh.anchor[c], sh.pow).fixed()), c);
       }
     } else {
-      scan([&](float l, int n, int c) {
+      scan_each([&](float l, int n, int c) {
         Weight w;
         if (in(l, c, w)) f(place_of(l, n - logits.skip), scaled(c, w.fixed()), c);
       });
@@ -373,16 +390,49 @@ struct Set {
     }
     __syncthreads();
     if (!listed) return;
-    scan([&](float l, int n, int c) {
-      Weight w;
-      const bool hit = in(l, c, w);
-      const uint64_t m = __ballot(hit);
-      if (!m) return;
+    // what lies between the bounds, by a comparison of logits; then those that are in the bins stay: a
+    // weight takes 40 instructions, which whole waves would spend on each of their logits
+    const float top = most_l < 3.4028234664e38f ? most_l : INFINITY;
+    scan([&](const u32x4 (&w)[kAhead], const int (&n)[kAhead], const int (&c)[kAhead]) {
+      int hits = 0;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (c[j] < 0) continue;
+#pragma unroll
+        for (int e = 0; e < L::kVec; ++e) {
+          const float l = logits.raw(w[j], e);
+          hits += l >= least_l && l <= top && l > -INFINITY;
+        }
+      }
+      const int upto = wave_incl_scan(hits), all = __builtin_amdgcn_readlane(upto, 63);
+      if (all == 0) return;
       int at = 0;
-      if (lane == __builtin_ctzll(m)) at = atomicAdd(&sh.n, (int)__popcll(m));
-      at = __shfl(at, __builtin_ctzll(m), 64);
-      if (hit) places[at + __popcll(m & ((uint64_t(1) << lane) - 1))] = place_of(l, n - logits.skip);
+      if (lane == 0) at = atomicAdd(&sh.n, all);
+      at = __builtin_amdgcn_readfirstlane(at) + upto - hits;
+      if (hits == 0) return;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (c[j] < 0) continue;
+#pragma unroll
+        for (int e = 0; e < L::kVec; ++e) {
+          const float l = logits.raw(w[j], e);
+          if (l >= least_l && l <= top && l > -INFINITY) {
+            if (at < kList) places[at] = place_of(logits.clean(l), n[j] + e - logits.skip);
+            ++at;
+          }
+        }
+      }
     });
+    __syncthreads();
+    const int n = sh.n;
+    listed = n <= kList;  // (the bounds may let some more in)
+    if (!listed) return;
+    for (int i = tid; i < n; i += kPick) {
+      const uint64_t place = places[i];
+      const int c = (index_of(place) + logits.skip) / kChunk;
+      Weight w;
+      if (!in(logit_of(place), c, w)) places[i] = 0;
+    }
     __syncthreads();
   }
 };
@@ -542,14 +592,31 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
     const uint64_t *mass = a.mass + (int64_t)r * a.C * kBins;
     const uint32_t *count = a.count + (int64_t)r * a.C * kBins;
     Set<TYPE> set(logits, row, sh, (uint64_t *)lds_raw);
-    for (int i = tid; i < a.C * kBins; i += kPick) {
-      const uint32_t n = count[i];
-      const uint64_t m = mass[i];
-      if (n == 0) continue;
-      const int c = i / kBins, b = set.row_bin(c, i % kBins);
+    // f(chunk, bin of the chunk, count, weights), of those that hold tokens
+    auto bins = [&](auto f) {
+      constexpr int kAhead = 5;
+      for (int i0 = tid; i0 < a.C * kBins; i0 += kAhead * kPick) {
+        uint32_t n[kAhead];
+        uint64_t m[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int i = i0 + j * kPick;
+          n[j] = 0;
+          if (i < a.C * kBins) {
+            n[j] = count[i];
+            m[j] = mass[i];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (n[j] > 0) f((i0 + j * kPick) / kBins, (i0 + j * kPick) % kBins, n[j], m[j]);
+      }
+    };
+    bins([&](int c, int b, uint32_t n, uint64_t m) {
+      b = set.row_bin(c, b);
       atomicAdd(&sh.count[b], n);
       lds_add(&sh.mass[b], set.scaled(c, m));
-    }
+    });
     __syncthreads();
     if (wave == 0) {  // sums down to each bin
       constexpr int kOwn = kBins / 64;
@@ -602,10 +669,10 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
       if (b <= cut && !has(b)) set.take(b, b, anchor, a.C);
     }
     const bool none = set.hi < 0;  // no cut: all bins
-    for (int i = tid; i < a.C * kBins; i += kPick) {
-      const int c = i / kBins;
-      if ((none || set.row_bin(c, i % kBins) < set.lo) && count[i] > 0) lds_add(&sh.kept[c], set.scaled(c, mass[i]));
-    }
+    if (none || set.lo > 0)
+      bins([&](int c, int b, uint32_t, uint64_t m) {
+        if (none || set.row_bin(c, b) < set.lo) lds_add(&sh.kept[c], set.scaled(c, m));
+      });
     if (!none && set.listed) {
       set.each([&](uint64_t place, uint64_t w, int c) {
         if (place >= least && above_floor(logit_of(place))) lds_add(&sh.kept[c], w);
@@ -618,7 +685,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
         if (lane == 0 && v > 0) lds_add(&sh.kept[at], v);
         sum = 0;
       };
-      set.scan([&](float l, int n, int c) {
+      set.scan_each([&](float l, int n, int c) {
         if (c != at) {
           if (at >= 0) flush();
           at = c;
