@@ -2,11 +2,11 @@
 //
 // Weights w = 2^(y - y_max), y = l log2(e) / temperature in binary64, are held as 64-bit fixed point,
 // so that sums are the same in any order.  What is kept is a prefix of the tokens sorted by logit
-// (descending) and index, and a token's place in that order is one 64-bit number (the logit's bits, ordered,
+// (descending) and index, and a token's place in that order is one number (the logit's bits, ordered,
 // over the inverted index), so every cut is one such number, and nothing is sorted.
 //
 //   k_sample_chunks  a workgroup for each 4096 logits: their maximum, and, relative to the power of two
-//                    above it, the count and the sum of weights of each quarter of an octave.  Reads
+//                    above it, the count and the sum of weights of each eighth of an octave.  Reads
 //                    every logit once.  Without filters only the sum.
 //   k_sample_pick    a workgroup a row: adds the chunks' bins up, which gives the bin that each cut
 //                    lies in; collects the tokens of that bin (for top-k, of all bins down to it) and selects
@@ -24,7 +24,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kChunk = kSampleChunk, kBins = kSampleBins, kPerOctave = 4;
+constexpr int kChunk = kSampleChunk, kBins = kSampleBins, kPerOctave = 8;
 constexpr int kThreads = 256;       // of k_sample_chunks
 constexpr int kPick = 1024;         // of k_sample_pick
 constexpr int kList = 16384;        // tokens that are selected among in LDS
@@ -77,10 +77,10 @@ struct Weight {
   int n;
   // whole part (the sum with 2^52 rounds; w < 2^52)
   __device__ __forceinline__ uint64_t fixed() const { return (uint64_t)__double_as_longlong(w + 0x1p52) & 0xfffffffffffffull; }
-  // number of quarter octaves below the anchor
-  __device__ __forceinline__ int bin() const { return min(kBins - 1, -n >> 4); }
+  // number of eighths of an octave below the anchor
+  __device__ __forceinline__ int bin() const { return min(kBins - 1, -n >> 3); }
 };
-static_assert(64 / kPerOctave == 16, "as Weight::bin has it");
+static_assert(64 / kPerOctave == 8, "as Weight::bin has it");
 __device__ __forceinline__ Weight weight_of(double t, const double *pow) {
   t = fmax(t, -2048.0);
   const double n = __builtin_floor(t * 64.0);
@@ -107,13 +107,16 @@ __device__ __forceinline__ uint32_t key_of(float l) {
   const uint32_t b = __float_as_uint(l + 0.0f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+// A token's place in the descending order: the key over the inverted index, 52 bits.
+constexpr int kIndexBits = 20;
+constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1;
+__device__ __forceinline__ uint64_t place_of(float l, int i) { return (uint64_t)key_of(l) << kIndexBits | (kIndexMask - (uint32_t)i); }
+__device__ __forceinline__ int index_of(uint64_t place) { return (int)(kIndexMask - ((uint32_t)place & kIndexMask)); }
+
 __device__ __forceinline__ float logit_of(uint64_t place) {
-  const uint32_t key = (uint32_t)(place >> 32);
+  const uint32_t key = (uint32_t)(place >> kIndexBits);
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
-// A token's place in the descending order.
-__device__ __forceinline__ uint64_t place_of(float l, int i) { return (uint64_t)key_of(l) << 32 | (0xffffffffu - (uint32_t)i); }
-__device__ __forceinline__ int index_of(uint64_t place) { return (int)(0xffffffffu - (uint32_t)place); }
 
 // A row of logits.  Rows may start anywhere; they are read in 16-byte blocks of kVec elements, counted from
 // the block that holds the first one (element i is number i + skip), and one by one where a block is
@@ -280,6 +283,8 @@ struct Shared {
   uint32_t sel_count[256];
   uint64_t red[kPick / 64];
   uint64_t found[3];
+  uint64_t left_place[64], left_weight[64];  // the last tokens of a selection
+  int left_n;
   int n, n_active;             // tokens in the list, chunks that are read
 };
 
@@ -310,16 +315,26 @@ struct Set {
   template <class F>
   __device__ __forceinline__ void scan(F f) const {
     const int tid = threadIdx.x, sub = tid / (kPick / kPer), off = tid % (kPick / kPer) * L::kVec;
-    for (int i = 0; i < sh.n_active; i += kPer * kAhead) {
-      u32x4 w[kAhead];
-      int n[kAhead], c[kAhead];
+    // (the next step's blocks are on their way while f works on this one's)
+    u32x4 w[kAhead], next[kAhead];
+    int n[kAhead], c[kAhead], cn[kAhead];
+    auto ask = [&](int i) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const int at = i + j * kPer + sub;
-        c[j] = __builtin_amdgcn_readfirstlane(at < sh.n_active ? sh.active[at] : -1);
-        n[j] = c[j] * kChunk + off;
-        if (c[j] >= 0) w[j] = logits.block(n[j]);
+        cn[j] = __builtin_amdgcn_readfirstlane(at < sh.n_active ? sh.active[at] : -1);
+        if (cn[j] >= 0) next[j] = logits.block(cn[j] * kChunk + off);
       }
+    };
+    ask(0);
+    for (int i = 0; i < sh.n_active; i += kPer * kAhead) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        w[j] = next[j];
+        c[j] = cn[j];
+        n[j] = c[j] * kChunk + off;
+      }
+      ask(i + kPer * kAhead);
       f(w, n, c);
     }
   }
@@ -363,7 +378,7 @@ struct Set {
     const int tid = threadIdx.x, lane = tid & 63;
     lo = b0;
     hi = b1;
-    // bin b holds 2^t for t from (1 - 16 (b + 1)) / 64 up to (1 - 16 b) / 64 (bounds that are safe against every rounding)
+    // bin b holds 2^t for t from (1 - 8 (b + 1)) / 64 up to (1 - 8 b) / 64 (bounds that are safe against every rounding)
     constexpr double kStep = 1.0 / kPerOctave, kUp = 1.0 / 64;
     auto bound = [&](double y, double way) {
       const double x = (y + way * 1e-3) / row.c;
@@ -371,8 +386,8 @@ struct Set {
     };
     most_l = fminf(bound(anchor - b0 * kStep + kUp, 1.0), 3.4028234664e38f);
     least_l = b1 == kBins - 1 ? -INFINITY : bound(anchor - (b1 + 1) * kStep + kUp, -1.0);
-    first = (uint64_t)key_of(least_l) << 32;
-    last = (uint64_t)key_of(most_l) << 32 | 0xffffffffu;
+    first = (uint64_t)key_of(least_l) << kIndexBits;
+    last = (uint64_t)key_of(most_l) << kIndexBits | kIndexMask;
     listed = sh.count[b1] - (b0 > 0 ? sh.count[b0 - 1] : 0) <= (uint32_t)kList;
     __syncthreads();
     if (tid < 64) {  // chunks that reach the bins
@@ -449,27 +464,17 @@ __device__ __forceinline__ uint64_t block_max(uint64_t v, Shared &sh) {
 
 // The least place `at` such that the set's tokens from it on (of those from `least` on) are at least `want` in
 // number, or weigh that much, and their weight; all of them where they do not reach that.  8 bits of the places at
-// a time, from the first one in which they differ.
+// a time, from the first one in which they differ, until at most 64 tokens are left, one a lane.
 struct Cut {
   uint64_t at, weight;
 };
 template <class S>
-__device__ __forceinline__ Cut select_from(const S &set, bool by_weight, uint64_t want, uint64_t least, Shared &sh) {
+__device__ __forceinline__ Cut select_from(const S &set, bool by_weight, uint64_t want, uint64_t least, uint32_t tokens, Shared &sh) {
   const int tid = threadIdx.x, lane = tid & 63;
   const uint64_t first = max(set.first, least), differ = first ^ set.last;
   int bits = 64 - __builtin_clzll(differ | 1);  // bits that are not known yet
-  uint64_t prefix = bits < 64 ? set.last >> bits : 0, above = 0;
-  // the least place of the set that begins with the prefix (there are tokens outside the set between it and
-  // the prefix followed by zeros)
-  auto least_of = [&](int rest) {
-    uint64_t v = ~uint64_t(0);
-    set.each([&](uint64_t place, uint64_t, int) {
-      if (place >= least && (rest > 63 || place >> rest == prefix)) v = min(v, place);
-    });
-    return ~block_max(~v, sh);
-  };
-  bool started = false;
-  while (true) {
+  uint64_t prefix = set.last >> bits, above = 0;
+  while (tokens > 64 && bits > 0) {
     const int rest = max(bits - 8, 0);  // bits below this step's
     for (int i = tid; i < 256; i += kPick) {
       sh.sel_mass[i] = 0;
@@ -477,7 +482,7 @@ __device__ __forceinline__ Cut select_from(const S &set, bool by_weight, uint64_
     }
     __syncthreads();
     set.each([&](uint64_t place, uint64_t w, int) {
-      if (place < least || (bits < 64 && place >> bits != prefix)) return;
+      if (place < least || place >> bits != prefix) return;
       const int b = (int)(place >> rest & ((1u << (bits - rest)) - 1));
       lds_add(&sh.sel_mass[b], w);
       atomicAdd(&sh.sel_count[b], 1u);
@@ -486,14 +491,16 @@ __device__ __forceinline__ Cut select_from(const S &set, bool by_weight, uint64_
     if (tid < 64) {
       // lane i has bins 255 - 4 i down to 252 - 4 i
       uint64_t own[4], sum = 0;
+      int low = 256;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int b = 255 - 4 * lane - i;
         own[i] = by_weight ? sh.sel_mass[b] : sh.sel_count[b];
         sum += own[i];
+        if (sh.sel_count[b] > 0) low = b;
       }
       const uint64_t upto = wave_scan_u64(sum);
-      const uint64_t hit = __ballot(upto >= want);
+      const uint64_t hit = __ballot(upto >= want), some = __ballot(low < 256);
       uint64_t before = upto - sum;
       int bin = -1;
 #pragma unroll
@@ -501,33 +508,64 @@ __device__ __forceinline__ Cut select_from(const S &set, bool by_weight, uint64_
         if (bin < 0 && before + own[i] >= want) bin = 255 - 4 * lane - i;
         if (bin < 0) before += own[i];
       }
-      const int cut = hit == 0 ? -1 : __shfl(bin, __builtin_ctzll(hit), 64);
-      if (hit == 0 ? lane == 0 : lane == __builtin_ctzll(hit)) {
-        sh.found[0] = (uint64_t)(cut < 0 ? 256 : cut);
-        sh.found[1] = before;
+      // (not reached: the lowest bin that holds anything)
+      if (!hit && some) bin = __shfl(low, 63 - __builtin_clzll(some), 64);
+      const int cut = hit ? __shfl(bin, __builtin_ctzll(hit), 64) : some ? bin : 0;
+      if (hit ? lane == __builtin_ctzll(hit) : lane == 0) {
+        sh.found[0] = (uint64_t)cut;
+        sh.found[1] = hit ? before : 0;
       }
       uint64_t w = 0;  // weight above the bin
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (255 - 4 * lane - i > cut) w += sh.sel_mass[255 - 4 * lane - i];
       w = wave_sum_u64(w);
-      if (lane == 0) sh.found[2] = w;
+      if (lane == 0) {
+        sh.found[2] = w;
+        if (!hit) sh.found[1] = ~uint64_t(0);
+      }
     }
     __syncthreads();
-    const int bin = (int)sh.found[0];
-    const uint64_t before = sh.found[1];
+    const uint64_t bin = sh.found[0], before = sh.found[1];
     above += sh.found[2];
-    const uint32_t n = bin < 256 ? sh.sel_count[bin] : 0;
-    const uint64_t m = bin < 256 ? sh.sel_mass[bin] : 0;
+    tokens = sh.sel_count[bin];
     __syncthreads();
-    if (bin > 255) return Cut{started ? least : least_of(64), above};  // (in the first step only)
-    started = true;
-    prefix = prefix << (bits - rest) | (uint64_t)bin;
-    want -= before;
-    if (rest == 0) return Cut{prefix, above + m};
-    if (n == 1 || (!by_weight && n == want)) return Cut{least_of(rest), above + m};  // the whole bin
+    prefix = prefix << (bits - rest) | bin;
     bits = rest;
+    want = before == ~uint64_t(0) ? before : want - before;  // (not reached: never)
   }
+  // the tokens that are left, one a lane
+  if (tid == 0) sh.left_n = 0;
+  __syncthreads();
+  set.each([&](uint64_t place, uint64_t w, int) {
+    if (place < least || place >> bits != prefix) return;
+    const int at = atomicAdd(&sh.left_n, 1);
+    if (at < 64) {
+      sh.left_place[at] = place;
+      sh.left_weight[at] = w;
+    }
+  });
+  __syncthreads();
+  const int n = min(sh.left_n, 64);
+  const uint64_t place = lane < n ? sh.left_place[lane] : 0, w = lane < n ? sh.left_weight[lane] : 0;
+  uint64_t before = 0, weight = above + w;
+  for (int j = 0; j < n; ++j) {
+    const uint64_t p = sh.left_place[j], v = sh.left_weight[j];
+    if (p > place) {
+      before += by_weight ? v : 1;
+      weight += v;
+    }
+  }
+  const uint64_t own = by_weight ? w : 1;
+  uint64_t hit = __ballot(lane < n && before < want && before + own >= want);
+  if (!hit) {  // the lowest of them
+    uint64_t low = ~wave_max_u64(lane < n ? ~place : 0);
+    hit = __ballot(lane < n && place == low);
+  }
+  __syncthreads();
+  if (!hit) return Cut{least, above};
+  const int l = __builtin_ctzll(hit);
+  return Cut{(uint64_t)__shfl((unsigned long long)place, l, 64), (uint64_t)__shfl((unsigned long long)weight, l, 64)};
 }
 
 template <int TYPE>
@@ -643,6 +681,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
       }
       return kBins - 1;
     };
+    auto held = [&] { return sh.count[set.hi] - count_above(set.lo); };  // tokens of the set
     auto has = [&](int b) { return set.lo <= b && b <= set.hi; };
 
     int cut = kBins;  // the bin of the cut
@@ -650,7 +689,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
     if (row.k > 0 && (uint32_t)row.k < sh.count[kBins - 1]) {
       cut = first_bin([&](int b) { return sh.count[b] >= (uint32_t)row.k; });
       set.take(sh.count[cut] <= (uint32_t)kList ? 0 : cut, cut, anchor, a.C);
-      const Cut o = select_from(set, false, (uint64_t)row.k - count_above(set.lo), 0, sh);
+      const Cut o = select_from(set, false, (uint64_t)row.k - count_above(set.lo), 0, held(), sh);
       least = o.at;
       total = mass_above(set.lo) + o.weight;
     }
@@ -660,7 +699,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
       const int b = min(cut, first_bin([&](int i) { return sh.mass[i] >= want; }));
       if (!has(b)) set.take(b, b, anchor, a.C);
       const uint64_t over = mass_above(set.lo);
-      least = max(least, select_from(set, true, want > over ? want - over : 1, least, sh).at);
+      least = max(least, select_from(set, true, want > over ? want - over : 1, least, held(), sh).at);
       cut = b;
     }
     if (row.m > 0.0) {

@@ -181,7 +181,7 @@ hipError_t launch_linear(const LinArgs &a, hipStream_t s);
 
 // Choice of tokens from logits (sample.hip).
 constexpr int kSampleChunk = 4096;  // logits of one workgroup of the first kernel
-constexpr int kSampleBins = 128;    // bins of a chunk's weights, a quarter of an octave each
+constexpr int kSampleBins = 192;    // bins of a chunk's weights, an eighth of an octave each
 // Of a chunk: its largest logit (times log2(e) / temperature) and the sum of its weights; for a
 // temperature of 0 the largest logit's sort key and index.
 struct SampleChunk {
