@@ -8,11 +8,13 @@
 //   k_sample_chunks  a workgroup for each 4096 logits: their maximum, and, relative to the power of two
 //                    above it, the count and the sum of weights of each eighth of an octave.  Reads
 //                    every logit once.  Without filters only the sum.
-//   k_sample_pick    a workgroup a row: adds the chunks' bins up, which gives the bin that each cut
-//                    lies in; collects the tokens of that bin (for top-k, of all bins down to it) and selects
-//                    among them, 8 bits of their places at a time; the kept weight of each chunk gives the
-//                    chunk that u falls into, which is read once more.  Where a cut's bins hold more than
-//                    kList tokens, each step of the selection reads them from the row.
+//   k_sample_cut     a workgroup a row: adds the chunks' bins up, which gives the bin of the first cut
+//                    (for top-k, all bins down to it).
+//   k_sample_gather  a workgroup a chunk: lists the tokens of that bin, and adds the weights above it.
+//   k_sample_pick    a workgroup a row: selects among the listed tokens, 8 bits of their places at a time;
+//                    the kept weight of each chunk gives the chunk that u falls into, which is read once
+//                    more.  A further cut in another bin is collected here, from the row; where a cut's
+//                    bins hold more than kList tokens, each step of the selection reads them from the row.
 //
 // Bound: memory for many rows, latency for few.
 #include "common.hpp"
@@ -27,7 +29,7 @@ namespace {
 constexpr int kChunk = kSampleChunk, kBins = kSampleBins, kPerOctave = 8;
 constexpr int kThreads = 256;       // of k_sample_chunks
 constexpr int kPick = 1024;         // of k_sample_pick
-constexpr int kList = 16384;        // tokens that are selected among in LDS
+constexpr int kList = kSampleList;  // tokens that are selected among in LDS
 constexpr int kMaxChunks = (1 << 20) / kChunk + 1;
 constexpr int kCopies = 4;          // of a chunk's bins, by lane, against conflicts
 
@@ -270,7 +272,34 @@ __global__ void __launch_bounds__(kThreads) k_sample_chunks(SampleArgs a) {
   }
 }
 
-// What the threads of k_sample_pick share.
+// Logits outside these are in none of the row's bins b0 .. b1 (whatever is rounded how).
+struct Bounds {
+  float least, most;
+  __device__ __forceinline__ bool hold(float l) const {
+    return l >= least && l <= (most < 3.4028234664e38f ? most : INFINITY) && l > -INFINITY;
+  }
+};
+__device__ __forceinline__ Bounds bounds_of(int b0, int b1, double anchor, double c) {
+  // bin b holds 2^t for t from (1 - 8 (b + 1)) / 64 up to (1 - 8 b) / 64
+  constexpr double kStep = 1.0 / kPerOctave, kUp = 1.0 / 64;
+  auto bound = [&](double y, double way) {
+    const double x = (y + way * 1e-3) / c;
+    return (float)(x + way * 1e-6 * fabs(x));
+  };
+  Bounds o;
+  o.most = fminf(bound(anchor - b0 * kStep + kUp, 1.0), 3.4028234664e38f);
+  o.least = b1 == kBins - 1 ? -INFINITY : bound(anchor - (b1 + 1) * kStep + kUp, -1.0);
+  return o;
+}
+
+// A chunk's bin among the row's, `shift` octaves above.
+__device__ __forceinline__ int row_bin_of(int b, int shift) { return b == kBins - 1 ? b : min(kBins - 1, b + kPerOctave * shift); }
+__device__ __forceinline__ int shift_of(double anchor, double chunk) {
+  const double d = anchor - chunk;
+  return d < 64.0 ? (int)d : 64;
+}
+
+// What the threads of k_sample_cut and k_sample_pick share.
 struct Shared {
   double pow[64];
   double anchor[kMaxChunks];
@@ -305,7 +334,7 @@ struct Set {
 
   // a chunk's bin among the row's
   __device__ __forceinline__ int row_bin(int c, int b) const {
-    return b == kBins - 1 ? b : min(kBins - 1, b + kPerOctave * sh.shift[c]);
+    return row_bin_of(b, sh.shift[c]);
   }
   __device__ __forceinline__ uint64_t scaled(int c, uint64_t m) const { return sh.shift[c] < 64 ? m >> sh.shift[c] : 0; }
 
@@ -373,19 +402,14 @@ struct Set {
       });
     }
   }
-  // takes bins b0 .. b1
-  __device__ __forceinline__ void take(int b0, int b1, double anchor, int chunks) {
+  // bins b0 .. b1, and the chunks that reach them
+  __device__ __forceinline__ void range(int b0, int b1, double anchor, int chunks) {
     const int tid = threadIdx.x, lane = tid & 63;
     lo = b0;
     hi = b1;
-    // bin b holds 2^t for t from (1 - 8 (b + 1)) / 64 up to (1 - 8 b) / 64 (bounds that are safe against every rounding)
-    constexpr double kStep = 1.0 / kPerOctave, kUp = 1.0 / 64;
-    auto bound = [&](double y, double way) {
-      const double x = (y + way * 1e-3) / row.c;
-      return (float)(x + way * 1e-6 * fabs(x));
-    };
-    most_l = fminf(bound(anchor - b0 * kStep + kUp, 1.0), 3.4028234664e38f);
-    least_l = b1 == kBins - 1 ? -INFINITY : bound(anchor - (b1 + 1) * kStep + kUp, -1.0);
+    const Bounds o = bounds_of(b0, b1, anchor, row.c);
+    least_l = o.least;
+    most_l = o.most;
     first = (uint64_t)key_of(least_l) << kIndexBits;
     last = (uint64_t)key_of(most_l) << kIndexBits | kIndexMask;
     listed = sh.count[b1] - (b0 > 0 ? sh.count[b0 - 1] : 0) <= (uint32_t)kList;
@@ -404,10 +428,15 @@ struct Set {
       }
     }
     __syncthreads();
+  }
+  // takes bins b0 .. b1 from the row
+  __device__ __forceinline__ void take(int b0, int b1, double anchor, int chunks) {
+    const int lane = threadIdx.x & 63;
+    range(b0, b1, anchor, chunks);
     if (!listed) return;
     // what lies between the bounds, by a comparison of logits; then those that are in the bins stay: a
     // weight takes 40 instructions, which whole waves would spend on each of their logits
-    const float top = most_l < 3.4028234664e38f ? most_l : INFINITY;
+    const Bounds bounds{least_l, most_l};
     scan([&](const u32x4 (&w)[kAhead], const int (&n)[kAhead], const int (&c)[kAhead]) {
       int hits = 0;
 #pragma unroll
@@ -415,8 +444,7 @@ struct Set {
         if (c[j] < 0) continue;
 #pragma unroll
         for (int e = 0; e < L::kVec; ++e) {
-          const float l = logits.raw(w[j], e);
-          hits += l >= least_l && l <= top && l > -INFINITY;
+          hits += bounds.hold(logits.raw(w[j], e));
         }
       }
       const int upto = wave_incl_scan(hits), all = __builtin_amdgcn_readlane(upto, 63);
@@ -431,7 +459,7 @@ struct Set {
 #pragma unroll
         for (int e = 0; e < L::kVec; ++e) {
           const float l = logits.raw(w[j], e);
-          if (l >= least_l && l <= top && l > -INFINITY) {
+          if (bounds.hold(l)) {
             if (at < kList) places[at] = place_of(logits.clean(l), n[j] + e - logits.skip);
             ++at;
           }
@@ -439,14 +467,26 @@ struct Set {
       }
     });
     __syncthreads();
-    const int n = sh.n;
-    listed = n <= kList;  // (the bounds may let some more in)
+    listed = sh.n <= kList;  // (the bounds may let some more in)
+    if (listed) keep_in([&](int i) { return places[i]; });
+  }
+  // takes bins b0 .. b1, whose tokens and some more are listed
+  __device__ __forceinline__ void take_listed(int b0, int b1, double anchor, int chunks, const uint64_t *list, int n) {
+    range(b0, b1, anchor, chunks);
+    listed = n <= kList;
     if (!listed) return;
-    for (int i = tid; i < n; i += kPick) {
-      const uint64_t place = places[i];
+    if (threadIdx.x == 0) sh.n = n;
+    __syncthreads();
+    keep_in([&](int i) { return list[i]; });
+  }
+  // keeps those of the sh.n tokens that are in the bins
+  template <class F>
+  __device__ __forceinline__ void keep_in(F from) {
+    for (int i = threadIdx.x; i < sh.n; i += kPick) {
+      const uint64_t place = from(i);
       const int c = (index_of(place) + logits.skip) / kChunk;
       Weight w;
-      if (!in(logit_of(place), c, w)) places[i] = 0;
+      places[i] = in(logit_of(place), c, w) ? place : 0;
     }
     __syncthreads();
   }
@@ -568,6 +608,199 @@ __device__ __forceinline__ Cut select_from(const S &set, bool by_weight, uint64_
   return Cut{(uint64_t)__shfl((unsigned long long)place, l, 64), (uint64_t)__shfl((unsigned long long)weight, l, 64)};
 }
 
+// The row's largest exponent (-infinity: no tokens); its chunks' anchors and distances.
+__device__ __forceinline__ double read_chunks(const SampleArgs &a, int r, Shared &sh) {
+  const int tid = threadIdx.x;
+  const SampleChunk *chunk = a.chunk + (int64_t)r * a.C;
+  auto ordered = [](double y) {  // binary64 numbers as ordered bits
+    const uint64_t b = (uint64_t)__double_as_longlong(y + 0.0);
+    return b >> 63 ? ~b : b | uint64_t(1) << 63;
+  };
+  uint64_t most = 0;
+  for (int c = tid; c < a.C; c += kPick) {
+    const double y = chunk[c].top;
+    sh.anchor[c] = __builtin_ceil(y);
+    most = max(most, ordered(y));
+  }
+  most = block_max(most, sh);
+  const double y0 = __longlong_as_double((long long)(most >> 63 ? most & ~(uint64_t(1) << 63) : ~most));
+  const double anchor = __builtin_ceil(y0);
+  for (int c = tid; c < a.C; c += kPick) sh.shift[c] = shift_of(anchor, sh.anchor[c]);
+  __syncthreads();
+  return y0;
+}
+// f(chunk, bin of the chunk, count, weights), of those that hold tokens
+template <class F>
+__device__ __forceinline__ void each_bin(const SampleArgs &a, int r, F f) {
+  const uint64_t *mass = a.mass + (int64_t)r * a.C * kBins;
+  const uint32_t *count = a.count + (int64_t)r * a.C * kBins;
+  constexpr int kAhead = 7;
+  for (int i0 = threadIdx.x; i0 < a.C * kBins; i0 += kAhead * kPick) {
+    uint32_t n[kAhead];
+    uint64_t m[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = i0 + j * kPick;
+      n[j] = 0;
+      if (i < a.C * kBins) {
+        n[j] = count[i];
+        m[j] = mass[i];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (n[j] > 0) f((i0 + j * kPick) / kBins, (i0 + j * kPick) % kBins, n[j], m[j]);
+  }
+}
+// the first bin down to which `enough` holds
+template <class F>
+__device__ __forceinline__ int first_bin(F enough) {
+  const int lane = threadIdx.x & 63;
+  for (int b = 0; b < kBins; b += 64) {
+    const uint64_t yes = __ballot(enough(b + lane));
+    if (yes) return b + (int)__builtin_ctzll(yes);
+  }
+  return kBins - 1;
+}
+static_assert(kBins % 64 == 0, "bins are read by whole waves");
+// A share of a total as a whole number, at least 1.
+__device__ __forceinline__ uint64_t share_of(double p, uint64_t total) {
+  return max(min((uint64_t)__builtin_ceil(p * (double)total), total), uint64_t(1));
+}
+// The bins of the top-k cut: from the first one on where they hold few tokens, so that a top-p cut among them
+// needs no others.
+__device__ __forceinline__ void top_k_bins(const Shared &sh, int k, int &lo, int &hi) {
+  hi = first_bin([&](int b) { return sh.count[b] >= (uint32_t)k; });
+  lo = sh.count[hi] <= (uint32_t)kList ? 0 : hi;
+}
+__device__ __forceinline__ double floor_of(const Row &row, double y0) { return row.m > 0.0 ? y0 + log2(row.m) : -INFINITY; }
+
+__global__ void __launch_bounds__(kPick) k_sample_cut(SampleArgs a) {
+  __shared__ Shared sh;
+  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  const Row row = read_row(a, r);
+  if (row.greedy || !row.filtered) return;
+  fill_pow(sh.pow, a.bits);
+  for (int i = tid; i < kBins; i += kPick) {
+    sh.mass[i] = 0;
+    sh.count[i] = 0;
+  }
+  const double y0 = read_chunks(a, r, sh), anchor = __builtin_ceil(y0);
+  SampleRow *out = a.row + r;
+  if (y0 == -INFINITY) {
+    if (tid == 0) {
+      out->lo = 0;
+      out->hi = -1;
+    }
+    return;
+  }
+  each_bin(a, r, [&](int c, int b, uint32_t n, uint64_t m) {
+    const int s = sh.shift[c];
+    b = row_bin_of(b, s);
+    atomicAdd(&sh.count[b], n);
+    lds_add(&sh.mass[b], s < 64 ? m >> s : 0);
+  });
+  __syncthreads();
+  if (tid < 64) {  // sums down to each bin
+    constexpr int kOwn = kBins / 64;
+    uint64_t m[kOwn], n[kOwn], ms = 0, ns = 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      m[i] = ms += sh.mass[lane * kOwn + i];
+      n[i] = ns += sh.count[lane * kOwn + i];
+    }
+    const uint64_t mb = wave_scan_u64(ms) - ms, nb = wave_scan_u64(ns) - ns;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      out->mass[lane * kOwn + i] = sh.mass[lane * kOwn + i] = mb + m[i];
+      out->count[lane * kOwn + i] = sh.count[lane * kOwn + i] = (uint32_t)(nb + n[i]);
+    }
+  }
+  __syncthreads();
+  int lo = 0, hi = -1;
+  const uint64_t total = sh.mass[kBins - 1];
+  if (row.k > 0 && (uint32_t)row.k < sh.count[kBins - 1]) {
+    top_k_bins(sh, row.k, lo, hi);
+  } else if (row.p < 1.0) {
+    lo = hi = first_bin([&](int i) { return sh.mass[i] >= share_of(row.p, total); });
+  } else if (row.m > 0.0) {
+    lo = hi = weight_of(floor_of(row, y0) - anchor, sh.pow).bin();
+  }
+  if (tid == 0) {
+    out->lo = lo;
+    out->hi = hi;
+    out->n = 0;
+  }
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads) k_sample_gather(SampleArgs a) {
+  using L = Logits<TYPE>;
+  constexpr int kVecs = kChunk / kThreads / L::kVec;
+  __shared__ uint64_t sums[kThreads / 64];
+  __shared__ double tops[kThreads / 64];
+  __shared__ int hits[kThreads / 64], base;
+  const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Row row = read_row(a, r);
+  if (row.greedy || !row.filtered) return;
+  SampleRow *out = a.row + r;
+  const int lo = out->lo, hi = out->hi;
+  const L logits(a, r);
+  u32x4 w[kVecs];
+#pragma unroll
+  for (int q = 0; q < kVecs; ++q) w[q] = logits.block(c * kChunk + (q * kThreads + tid) * L::kVec);
+  const SampleChunk *chunk = a.chunk + (int64_t)r * a.C;
+  double y0 = -INFINITY;
+  for (int i = tid; i < a.C; i += kThreads) y0 = fmax(y0, chunk[i].top);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) y0 = fmax(y0, __shfl_xor(y0, d, 64));
+  const double mine = chunk[c].top;
+  const int64_t at = ((int64_t)r * a.C + c) * kBins;
+  const uint32_t n = tid < kBins ? a.count[at + tid] : 0;
+  const uint64_t m = tid < kBins ? a.mass[at + tid] : 0;
+  if (lane == 0) tops[wave] = y0;
+  if (hi < lo) return;
+  __syncthreads();
+  y0 = fmax(fmax(tops[0], tops[1]), fmax(tops[2], tops[3]));
+  const double anchor = __builtin_ceil(y0);
+  const int shift = mine == -INFINITY ? 64 : shift_of(anchor, __builtin_ceil(mine));
+  const uint64_t sum = wave_sum_u64(n > 0 && shift < 64 && row_bin_of(tid, shift) < lo ? m >> shift : 0);
+  const Bounds bounds = bounds_of(lo, hi, anchor, row.c);
+  const bool reaches = mine > -INFINITY && kPerOctave * shift <= hi;
+  int some = 0;
+  if (reaches) {
+#pragma unroll
+    for (int q = 0; q < kVecs; ++q)
+#pragma unroll
+      for (int e = 0; e < L::kVec; ++e) some += bounds.hold(logits.raw(w[q], e));
+  }
+  const int upto = wave_incl_scan(some);
+  if (lane == 63) hits[wave] = upto;
+  if (lane == 0) sums[wave] = sum;
+  __syncthreads();
+  const int all = hits[0] + hits[1] + hits[2] + hits[3];
+  if (tid == 0) {
+    a.kept[(int64_t)r * a.C + c] = sums[0] + sums[1] + sums[2] + sums[3];
+    if (all > 0) base = atomicAdd(&out->n, all);
+  }
+  if (all == 0) return;
+  __syncthreads();
+  int to = base + upto - some;
+  for (int i = 0; i < wave; ++i) to += hits[i];
+  if (some == 0) return;
+  uint64_t *list = a.list + (int64_t)r * a.room;
+#pragma unroll
+  for (int q = 0; q < kVecs; ++q)
+#pragma unroll
+    for (int e = 0; e < L::kVec; ++e) {
+      const float l = logits.raw(w[q], e);
+      if (bounds.hold(l)) {
+        if (to < a.room) list[to] = place_of(logits.clean(l), c * kChunk + (q * kThreads + tid) * L::kVec + e - logits.skip);
+        ++to;
+      }
+    }
+}
+
 template <int TYPE>
 __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   using L = Logits<TYPE>;
@@ -589,24 +822,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
     }
     return;
   }
-  // the largest exponent: binary64 numbers as ordered bits
-  auto ordered = [](double y) {
-    const uint64_t b = (uint64_t)__double_as_longlong(y + 0.0);
-    return b >> 63 ? ~b : b | uint64_t(1) << 63;
-  };
-  uint64_t most = 0;
-  for (int c = tid; c < a.C; c += kPick) {
-    const double y = chunk[c].top;
-    sh.anchor[c] = __builtin_ceil(y);
-    sh.kept[c] = 0;
-    most = max(most, ordered(y));
-  }
-  for (int i = tid; i < kBins; i += kPick) {
-    sh.mass[i] = 0;
-    sh.count[i] = 0;
-  }
-  most = block_max(most, sh);
-  const double y0 = __longlong_as_double((long long)(most >> 63 ? most & ~(uint64_t(1) << 63) : ~most));
+  const double y0 = read_chunks(a, r, sh), anchor = __builtin_ceil(y0);
   if (y0 == -INFINITY) {
     if (tid == 0) {
       a.token[r] = -1;
@@ -614,88 +830,38 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
     }
     return;
   }
-  const double anchor = __builtin_ceil(y0);
-  for (int c = tid; c < a.C; c += kPick) {
-    const double d = anchor - sh.anchor[c];
-    sh.shift[c] = d < 64.0 ? (int)d : 64;
-  }
-  __syncthreads();
 
   uint64_t least = 0;          // places that are kept are at least this
+  const double least_y = floor_of(row, y0);
   double floor = -INFINITY;    // and exponents this
   auto above_floor = [&](float l) { return (double)l * row.c >= floor; };
   if (!row.filtered) {
     for (int c = tid; c < a.C; c += kPick) sh.kept[c] = sh.shift[c] < 64 ? chunk[c].total >> sh.shift[c] : 0;
   } else {
-    const uint64_t *mass = a.mass + (int64_t)r * a.C * kBins;
-    const uint32_t *count = a.count + (int64_t)r * a.C * kBins;
-    Set<TYPE> set(logits, row, sh, (uint64_t *)lds_raw);
-    // f(chunk, bin of the chunk, count, weights), of those that hold tokens
-    auto bins = [&](auto f) {
-      constexpr int kAhead = 5;
-      for (int i0 = tid; i0 < a.C * kBins; i0 += kAhead * kPick) {
-        uint32_t n[kAhead];
-        uint64_t m[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const int i = i0 + j * kPick;
-          n[j] = 0;
-          if (i < a.C * kBins) {
-            n[j] = count[i];
-            m[j] = mass[i];
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-          if (n[j] > 0) f((i0 + j * kPick) / kBins, (i0 + j * kPick) % kBins, n[j], m[j]);
-      }
-    };
-    bins([&](int c, int b, uint32_t n, uint64_t m) {
-      b = set.row_bin(c, b);
-      atomicAdd(&sh.count[b], n);
-      lds_add(&sh.mass[b], set.scaled(c, m));
-    });
-    __syncthreads();
-    if (wave == 0) {  // sums down to each bin
-      constexpr int kOwn = kBins / 64;
-      uint64_t m[kOwn], n[kOwn], ms = 0, ns = 0;
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        m[i] = ms += sh.mass[lane * kOwn + i];
-        n[i] = ns += sh.count[lane * kOwn + i];
-      }
-      const uint64_t mb = wave_scan_u64(ms) - ms, nb = wave_scan_u64(ns) - ns;
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        sh.mass[lane * kOwn + i] = mb + m[i];
-        sh.count[lane * kOwn + i] = (uint32_t)(nb + n[i]);
-      }
+    const SampleRow *in = a.row + r;
+    for (int i = tid; i < kBins; i += kPick) {
+      sh.mass[i] = in->mass[i];
+      sh.count[i] = in->count[i];
     }
+    Set<TYPE> set(logits, row, sh, (uint64_t *)lds_raw);
+    const int lo = in->lo, hi = in->hi;
     __syncthreads();
+    if (hi >= lo) set.take_listed(lo, hi, anchor, a.C, a.list + (int64_t)r * a.room, in->n);
     auto mass_above = [&](int b) { return b > 0 ? sh.mass[b - 1] : 0; };
     auto count_above = [&](int b) { return b > 0 ? sh.count[b - 1] : 0u; };
-    auto first_bin = [&](auto enough) {  // the first bin down to which `enough` holds
-      for (int b = 0; b < kBins; b += 64) {
-        const uint64_t yes = __ballot(enough(b + lane));
-        if (yes) return b + (int)__builtin_ctzll(yes);
-      }
-      return kBins - 1;
-    };
     auto held = [&] { return sh.count[set.hi] - count_above(set.lo); };  // tokens of the set
     auto has = [&](int b) { return set.lo <= b && b <= set.hi; };
 
     int cut = kBins;  // the bin of the cut
     uint64_t total = sh.mass[kBins - 1];
-    if (row.k > 0 && (uint32_t)row.k < sh.count[kBins - 1]) {
-      cut = first_bin([&](int b) { return sh.count[b] >= (uint32_t)row.k; });
-      set.take(sh.count[cut] <= (uint32_t)kList ? 0 : cut, cut, anchor, a.C);
+    if (row.k > 0 && (uint32_t)row.k < sh.count[kBins - 1]) {  // (k_sample_cut has taken its bins)
+      cut = set.hi;
       const Cut o = select_from(set, false, (uint64_t)row.k - count_above(set.lo), 0, held(), sh);
       least = o.at;
       total = mass_above(set.lo) + o.weight;
     }
     if (row.p < 1.0) {
-      // the share as a whole number, at least 1
-      const uint64_t want = max(min((uint64_t)__builtin_ceil(row.p * (double)total), total), uint64_t(1));
+      const uint64_t want = share_of(row.p, total);
       const int b = min(cut, first_bin([&](int i) { return sh.mass[i] >= want; }));
       if (!has(b)) set.take(b, b, anchor, a.C);
       const uint64_t over = mass_above(set.lo);
@@ -703,15 +869,21 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
       cut = b;
     }
     if (row.m > 0.0) {
-      floor = y0 + log2(row.m);
+      floor = least_y;
       const int b = weight_of(floor - anchor, sh.pow).bin();
       if (b <= cut && !has(b)) set.take(b, b, anchor, a.C);
     }
     const bool none = set.hi < 0;  // no cut: all bins
-    if (none || set.lo > 0)
-      bins([&](int c, int b, uint32_t, uint64_t m) {
+    if (!none && set.lo == lo) {
+      for (int c = tid; c < a.C; c += kPick) sh.kept[c] = a.kept[(int64_t)r * a.C + c];
+      __syncthreads();
+    } else {
+      for (int c = tid; c < a.C; c += kPick) sh.kept[c] = 0;
+      __syncthreads();
+      each_bin(a, r, [&](int c, int b, uint32_t, uint64_t m) {
         if (none || set.row_bin(c, b) < set.lo) lds_add(&sh.kept[c], set.scaled(c, m));
       });
+    }
     if (!none && set.listed) {
       set.each([&](uint64_t place, uint64_t w, int c) {
         if (place >= least && above_floor(logit_of(place))) lds_add(&sh.kept[c], w);
@@ -816,6 +988,10 @@ hipError_t launch(const SampleArgs &a, hipStream_t s) {
   const hipError_t e = allow_lds(k_sample_pick<TYPE>, lds, done);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_sample_chunks<TYPE>), dim3(a.C, a.R), dim3(kThreads), 0, s, a);
+  if (a.top_k || a.top_p || a.min_p) {  // (otherwise no row has filters)
+    hipLaunchKernelGGL(k_sample_cut, dim3(a.R), dim3(kPick), 0, s, a);
+    hipLaunchKernelGGL((k_sample_gather<TYPE>), dim3(a.C, a.R), dim3(kThreads), 0, s, a);
+  }
   hipLaunchKernelGGL((k_sample_pick<TYPE>), dim3(a.R), dim3(kPick), lds, s, a);
   return hipGetLastError();
 }

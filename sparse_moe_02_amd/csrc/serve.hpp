@@ -188,6 +188,15 @@ struct SampleChunk {
   double top;
   uint64_t total, best;
 };
+// Of a row with filters: its bins, summed down to each, the bins of the first cut, and the tokens listed.
+constexpr int kSampleList = 16384;
+struct SampleRow {
+  uint64_t mass[kSampleBins];
+  uint32_t count[kSampleBins];
+  int lo, hi;  // hi < lo: no cut
+  int n;       // tokens that lie between the bins' bounds, of which the first kSampleList are listed
+  int pad;
+};
 struct SampleArgs {
   const void *logits;
   int64_t ld;
@@ -200,6 +209,10 @@ struct SampleArgs {
   SampleChunk *chunk;  // [R][C]
   uint64_t *mass;      // [R][C][bins]
   uint32_t *count;     // [R][C][bins]
+  SampleRow *row;      // [R]
+  uint64_t *kept;      // [R][C] weight of a chunk's bins above the cut's
+  uint64_t *list;      // [R][room]
+  int room;            // min(V, kSampleList)
 };
 hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
 

@@ -35,17 +35,21 @@ Rows dev_rows(const moe_heads *x) {
 
 // Places of moe_sample's arrays in its workspace.
 struct SampleWs {
-  int chunks;
-  size_t mass, count, total;
+  int chunks, room;
+  size_t mass, count, row, kept, list, total;
 };
 SampleWs sample_ws(int64_t R, int32_t V) {
   auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
   SampleWs w;
   w.chunks = (V + 7 + kSampleChunk - 1) / kSampleChunk;  // (a row may start up to 7 elements behind a 16-byte block)
+  w.room = V < kSampleList ? V : kSampleList;
   const size_t n = (size_t)R * w.chunks;
   w.mass = up(n * sizeof(SampleChunk));
   w.count = w.mass + up(n * kSampleBins * 8);
-  w.total = w.count + up(n * kSampleBins * 4);
+  w.row = w.count + up(n * kSampleBins * 4);
+  w.kept = w.row + up((size_t)R * sizeof(SampleRow));
+  w.list = w.kept + up(n * 8);
+  w.total = w.list + (size_t)R * w.room * 8;
   return w;
 }
 
@@ -212,6 +216,10 @@ moe_status moe_sample(int64_t R, int32_t V, const void *logits, int64_t row_stri
   a.chunk = reinterpret_cast<SampleChunk *>(base);
   a.mass = reinterpret_cast<uint64_t *>(base + ws.mass);
   a.count = reinterpret_cast<uint32_t *>(base + ws.count);
+  a.row = reinterpret_cast<SampleRow *>(base + ws.row);
+  a.kept = reinterpret_cast<uint64_t *>(base + ws.kept);
+  a.list = reinterpret_cast<uint64_t *>(base + ws.list);
+  a.room = ws.room;
   return launch_sample(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
