@@ -33,24 +33,41 @@ constexpr int kList = kSampleList;  // tokens that are selected among in LDS
 constexpr int kMaxChunks = (1 << 20) / kChunk + 1;
 constexpr int kCopies = 4;          // of a chunk's bins, by lane, against conflicts
 
-// 2^(j / 64)
-__constant__ const double kPow[64] = {
-    0x1.0000000000000p+0, 0x1.02c9a3e778061p+0, 0x1.059b0d3158574p+0, 0x1.0874518759bc8p+0,
-    0x1.0b5586cf9890fp+0, 0x1.0e3ec32d3d1a2p+0, 0x1.11301d0125b51p+0, 0x1.1429aaea92de0p+0,
-    0x1.172b83c7d517bp+0, 0x1.1a35beb6fcb75p+0, 0x1.1d4873168b9aap+0, 0x1.2063b88628cd6p+0,
-    0x1.2387a6e756238p+0, 0x1.26b4565e27cddp+0, 0x1.29e9df51fdee1p+0, 0x1.2d285a6e4030bp+0,
-    0x1.306fe0a31b715p+0, 0x1.33c08b26416ffp+0, 0x1.371a7373aa9cbp+0, 0x1.3a7db34e59ff7p+0,
-    0x1.3dea64c123422p+0, 0x1.4160a21f72e2ap+0, 0x1.44e086061892dp+0, 0x1.486a2b5c13cd0p+0,
-    0x1.4bfdad5362a27p+0, 0x1.4f9b2769d2ca7p+0, 0x1.5342b569d4f82p+0, 0x1.56f4736b527dap+0,
-    0x1.5ab07dd485429p+0, 0x1.5e76f15ad2148p+0, 0x1.6247eb03a5585p+0, 0x1.6623882552225p+0,
-    0x1.6a09e667f3bcdp+0, 0x1.6dfb23c651a2fp+0, 0x1.71f75e8ec5f74p+0, 0x1.75feb564267c9p+0,
-    0x1.7a11473eb0187p+0, 0x1.7e2f336cf4e62p+0, 0x1.82589994cce13p+0, 0x1.868d99b4492edp+0,
-    0x1.8ace5422aa0dbp+0, 0x1.8f1ae99157736p+0, 0x1.93737b0cdc5e5p+0, 0x1.97d829fde4e50p+0,
-    0x1.9c49182a3f090p+0, 0x1.a0c667b5de565p+0, 0x1.a5503b23e255dp+0, 0x1.a9e6b5579fdbfp+0,
-    0x1.ae89f995ad3adp+0, 0x1.b33a2b84f15fbp+0, 0x1.b7f76f2fb5e47p+0, 0x1.bcc1e904bc1d2p+0,
-    0x1.c199bdd85529cp+0, 0x1.c67f12e57d14bp+0, 0x1.cb720dcef9069p+0, 0x1.d072d4a07897cp+0,
-    0x1.d5818dcfba487p+0, 0x1.da9e603db3285p+0, 0x1.dfc97337b9b5fp+0, 0x1.e502ee78b3ff6p+0,
-    0x1.ea4afa2a490dap+0, 0x1.efa1bee615a27p+0, 0x1.f50765b6e4540p+0, 0x1.fa7c1819e90d8p+0};
+// 2^(j / 128)
+constexpr int kSteps = 128;
+__constant__ const double kPow[kSteps] = {
+    0x1.0000000000000p+0, 0x1.0163da9fb3335p+0, 0x1.02c9a3e778061p+0, 0x1.04315e86e7f85p+0,
+    0x1.059b0d3158574p+0, 0x1.0706b29ddf6dep+0, 0x1.0874518759bc8p+0, 0x1.09e3ecac6f383p+0,
+    0x1.0b5586cf9890fp+0, 0x1.0cc922b7247f7p+0, 0x1.0e3ec32d3d1a2p+0, 0x1.0fb66affed31bp+0,
+    0x1.11301d0125b51p+0, 0x1.12abdc06c31ccp+0, 0x1.1429aaea92de0p+0, 0x1.15a98c8a58e51p+0,
+    0x1.172b83c7d517bp+0, 0x1.18af9388c8deap+0, 0x1.1a35beb6fcb75p+0, 0x1.1bbe084045cd4p+0,
+    0x1.1d4873168b9aap+0, 0x1.1ed5022fcd91dp+0, 0x1.2063b88628cd6p+0, 0x1.21f49917ddc96p+0,
+    0x1.2387a6e756238p+0, 0x1.251ce4fb2a63fp+0, 0x1.26b4565e27cddp+0, 0x1.284dfe1f56381p+0,
+    0x1.29e9df51fdee1p+0, 0x1.2b87fd0dad990p+0, 0x1.2d285a6e4030bp+0, 0x1.2ecafa93e2f56p+0,
+    0x1.306fe0a31b715p+0, 0x1.32170fc4cd831p+0, 0x1.33c08b26416ffp+0, 0x1.356c55f929ff1p+0,
+    0x1.371a7373aa9cbp+0, 0x1.38cae6d05d866p+0, 0x1.3a7db34e59ff7p+0, 0x1.3c32dc313a8e5p+0,
+    0x1.3dea64c123422p+0, 0x1.3fa4504ac801cp+0, 0x1.4160a21f72e2ap+0, 0x1.431f5d950a897p+0,
+    0x1.44e086061892dp+0, 0x1.46a41ed1d0057p+0, 0x1.486a2b5c13cd0p+0, 0x1.4a32af0d7d3dep+0,
+    0x1.4bfdad5362a27p+0, 0x1.4dcb299fddd0dp+0, 0x1.4f9b2769d2ca7p+0, 0x1.516daa2cf6642p+0,
+    0x1.5342b569d4f82p+0, 0x1.551a4ca5d920fp+0, 0x1.56f4736b527dap+0, 0x1.58d12d497c7fdp+0,
+    0x1.5ab07dd485429p+0, 0x1.5c9268a5946b7p+0, 0x1.5e76f15ad2148p+0, 0x1.605e1b976dc09p+0,
+    0x1.6247eb03a5585p+0, 0x1.6434634ccc320p+0, 0x1.6623882552225p+0, 0x1.68155d44ca973p+0,
+    0x1.6a09e667f3bcdp+0, 0x1.6c012750bdabfp+0, 0x1.6dfb23c651a2fp+0, 0x1.6ff7df9519484p+0,
+    0x1.71f75e8ec5f74p+0, 0x1.73f9a48a58174p+0, 0x1.75feb564267c9p+0, 0x1.780694fde5d3fp+0,
+    0x1.7a11473eb0187p+0, 0x1.7c1ed0130c132p+0, 0x1.7e2f336cf4e62p+0, 0x1.80427543e1a12p+0,
+    0x1.82589994cce13p+0, 0x1.8471a4623c7adp+0, 0x1.868d99b4492edp+0, 0x1.88ac7d98a6699p+0,
+    0x1.8ace5422aa0dbp+0, 0x1.8cf3216b5448cp+0, 0x1.8f1ae99157736p+0, 0x1.9145b0b91ffc6p+0,
+    0x1.93737b0cdc5e5p+0, 0x1.95a44cbc8520fp+0, 0x1.97d829fde4e50p+0, 0x1.9a0f170ca07bap+0,
+    0x1.9c49182a3f090p+0, 0x1.9e86319e32323p+0, 0x1.a0c667b5de565p+0, 0x1.a309bec4a2d33p+0,
+    0x1.a5503b23e255dp+0, 0x1.a799e1330b358p+0, 0x1.a9e6b5579fdbfp+0, 0x1.ac36bbfd3f37ap+0,
+    0x1.ae89f995ad3adp+0, 0x1.b0e07298db666p+0, 0x1.b33a2b84f15fbp+0, 0x1.b59728de5593ap+0,
+    0x1.b7f76f2fb5e47p+0, 0x1.ba5b030a1064ap+0, 0x1.bcc1e904bc1d2p+0, 0x1.bf2c25bd71e09p+0,
+    0x1.c199bdd85529cp+0, 0x1.c40ab5fffd07ap+0, 0x1.c67f12e57d14bp+0, 0x1.c8f6d9406e7b5p+0,
+    0x1.cb720dcef9069p+0, 0x1.cdf0b555dc3fap+0, 0x1.d072d4a07897cp+0, 0x1.d2f87080d89f2p+0,
+    0x1.d5818dcfba487p+0, 0x1.d80e316c98398p+0, 0x1.da9e603db3285p+0, 0x1.dd321f301b460p+0,
+    0x1.dfc97337b9b5fp+0, 0x1.e264614f5a129p+0, 0x1.e502ee78b3ff6p+0, 0x1.e7a51fbc74c83p+0,
+    0x1.ea4afa2a490dap+0, 0x1.ecf482d8e67f1p+0, 0x1.efa1bee615a27p+0, 0x1.f252b376bba97p+0,
+    0x1.f50765b6e4540p+0, 0x1.f7bfdad9cbe14p+0, 0x1.fa7c1819e90d8p+0, 0x1.fd3c22b8f71f1p+0};
 
 struct Row {
   double c;          // log2(e) / temperature
@@ -72,36 +89,38 @@ __device__ __forceinline__ Row read_row(const SampleArgs &a, int r) {
   return o;
 }
 
-// 2^t times 2^bits, t = l c - anchor <= 0, and floor(64 t): 2^x, 0 <= x < 1/64, by its series (off by less
-// than 2^-48), times the table's 2^(j / 64 + bits).  (Of l = -infinity: 0.)
+// 2^(t / 128) times 2^bits, t = 128 (l c - anchor) <= 0, and n = t rounded: 2^x, |x| <= 1/256, by its series
+// (off by less than 2^-49), times the table's 2^(j / 128 + bits).  What is below 2^-64 is taken as that (and so is l =
+// -infinity), so exponents stay in range and are added as they are; it is 0 as a whole number.
 struct Weight {
   double w;
   int n;
   // whole part (the sum with 2^52 rounds; w < 2^52)
   __device__ __forceinline__ uint64_t fixed() const { return (uint64_t)__double_as_longlong(w + 0x1p52) & 0xfffffffffffffull; }
   // number of eighths of an octave below the anchor
-  __device__ __forceinline__ int bin() const { return min(kBins - 1, -n >> 3); }
+  __device__ __forceinline__ int bin() const { return min(kBins - 1, -n >> 4); }
 };
-static_assert(64 / kPerOctave == 8, "as Weight::bin has it");
-__device__ __forceinline__ Weight weight_of(double t, const double *pow) {
-  t = fmax(t, -2048.0);
-  const double n = __builtin_floor(t * 64.0);
-  const int i = (int)n;
-  const double x = __builtin_fma(n, -0.015625, t);
-  constexpr double k1 = 0.69314718055994531, k2 = k1 * k1 / 2, k3 = k2 * k1 / 3, k4 = k3 * k1 / 4, k5 = k4 * k1 / 5;
-  double s = __builtin_fma(x, k5, k4);
-  s = __builtin_fma(x, s, k3);
+static_assert(kSteps / kPerOctave == 16 && kBins <= 64 * kPerOctave, "as Weight::bin has it");
+__device__ __forceinline__ Weight weight_at(double t, const double *pow) {
+  t = fmax(t, -64.0 * kSteps);
+  const double r = t + 0x1.8p52;  // the sum's low bits are t rounded
+  const int n = (int)(uint32_t)__double_as_longlong(r);
+  const double x = t - (r - 0x1.8p52);
+  constexpr double k1 = 0.69314718055994531 / kSteps, k2 = k1 * k1 / 2, k3 = k2 * k1 / 3, k4 = k3 * k1 / 4;
+  double s = __builtin_fma(x, k4, k3);
   s = __builtin_fma(x, s, k2);
   s = __builtin_fma(x, s, k1);
   s = __builtin_fma(x, s, 1.0);
-  return Weight{__builtin_amdgcn_ldexp(s * pow[i & 63], i >> 6), i};
+  const uint64_t w = (uint64_t)__double_as_longlong(s * pow[n & (kSteps - 1)]);
+  return Weight{__longlong_as_double((long long)(w + ((uint64_t)(uint32_t)(n >> 7) << 52))), n};
 }
+// c: of Row; anchor: in octaves
 __device__ __forceinline__ Weight weight_of(float l, double c, double anchor, const double *pow) {
   // (not fused: the anchor is above the rounded product, and far out that is off by whole octaves)
-  return weight_of((double)l * c - anchor, pow);
+  return weight_at(((double)l * c - anchor) * kSteps, pow);
 }
 __device__ __forceinline__ void fill_pow(double *pow, int bits) {
-  if (threadIdx.x < 64) pow[threadIdx.x] = __builtin_amdgcn_ldexp(kPow[threadIdx.x], bits);
+  if (threadIdx.x < kSteps) pow[threadIdx.x] = __builtin_amdgcn_ldexp(kPow[threadIdx.x], bits);
 }
 
 // Order-preserving bits of a logit (both zeros alike).
@@ -191,9 +210,9 @@ template <int TYPE>
 __global__ void __launch_bounds__(kThreads) k_sample_chunks(SampleArgs a) {
   using L = Logits<TYPE>;
   constexpr int kVecs = kChunk / kThreads / L::kVec;  // blocks of a thread
-  __shared__ double pow[64];
-  __shared__ uint64_t mass[kBins][kCopies];
-  __shared__ uint32_t count[kBins][kCopies];
+  __shared__ double pow[kSteps];
+  __shared__ uint64_t mass[kBins + 1][kCopies];
+  __shared__ uint32_t count[kBins + 1][kCopies];
   __shared__ float tops[kThreads / 64];
   __shared__ uint64_t sums[kThreads / 64];
   const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
@@ -237,18 +256,27 @@ __global__ void __launch_bounds__(kThreads) k_sample_chunks(SampleArgs a) {
   uint64_t sum = 0;
   const int copy = tid % kCopies;
   if (top > -INFINITY) {
+    // (without a branch a logit, so that several are on their way at once: those that are out go to a bin behind
+    // the last)
 #pragma unroll
-    for (int q = 0; q < kVecs; ++q)
+    for (int q = 0; q < kVecs; ++q) {
+      uint64_t w[L::kVec];
+      int b[L::kVec];
 #pragma unroll
       for (int e = 0; e < L::kVec; ++e) {
-        const Weight w = weight_of(l[q][e], row.c, anchor, pow);
-        sum += w.fixed();
-        if (row.filtered && l[q][e] > -INFINITY) {
-          const int b = w.bin();
-          lds_add(&mass[b][copy], w.fixed());
-          atomicAdd(&count[b][copy], 1u);
+        const Weight o = weight_of(l[q][e], row.c, anchor, pow);
+        w[e] = o.fixed();
+        b[e] = l[q][e] == -INFINITY ? kBins : o.bin();
+        sum += w[e];
+      }
+      if (row.filtered) {
+#pragma unroll
+        for (int e = 0; e < L::kVec; ++e) {
+          lds_add(&mass[b[e]][copy], w[e]);
+          atomicAdd(&count[b[e]][copy], 1u);
         }
       }
+    }
   }
   sum = wave_sum_u64(sum);
   if ((tid & 63) == 0) sums[tid >> 6] = sum;
@@ -280,8 +308,8 @@ struct Bounds {
   }
 };
 __device__ __forceinline__ Bounds bounds_of(int b0, int b1, double anchor, double c) {
-  // bin b holds 2^t for t from (1 - 8 (b + 1)) / 64 up to (1 - 8 b) / 64
-  constexpr double kStep = 1.0 / kPerOctave, kUp = 1.0 / 64;
+  // bin b holds 2^t for t from (1/2 - 16 (b + 1)) / 128 up to (1/2 - 16 b) / 128
+  constexpr double kStep = 1.0 / kPerOctave, kUp = 0.5 / kSteps;
   auto bound = [&](double y, double way) {
     const double x = (y + way * 1e-3) / c;
     return (float)(x + way * 1e-6 * fabs(x));
@@ -301,7 +329,7 @@ __device__ __forceinline__ int shift_of(double anchor, double chunk) {
 
 // What the threads of k_sample_cut and k_sample_pick share.
 struct Shared {
-  double pow[64];
+  double pow[kSteps];
   double anchor[kMaxChunks];
   int shift[kMaxChunks];       // octaves of a chunk's anchor below the row's (64: out of reach)
   uint64_t kept[kMaxChunks];   // kept weight of the chunks, then the sums up to each
@@ -724,7 +752,7 @@ __global__ void __launch_bounds__(kPick) k_sample_cut(SampleArgs a) {
   } else if (row.p < 1.0) {
     lo = hi = first_bin([&](int i) { return sh.mass[i] >= share_of(row.p, total); });
   } else if (row.m > 0.0) {
-    lo = hi = weight_of(floor_of(row, y0) - anchor, sh.pow).bin();
+    lo = hi = weight_at((floor_of(row, y0) - anchor) * kSteps, sh.pow).bin();
   }
   if (tid == 0) {
     out->lo = lo;
@@ -870,7 +898,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
     }
     if (row.m > 0.0) {
       floor = least_y;
-      const int b = weight_of(floor - anchor, sh.pow).bin();
+      const int b = weight_at((floor - anchor) * kSteps, sh.pow).bin();
       if (b <= cut && !has(b)) set.take(b, b, anchor, a.C);
     }
     const bool none = set.hi < 0;  // no cut: all bins
