@@ -171,7 +171,7 @@ struct LinArgs {
   void *out;
   int64_t xld, old;     // strides of x's and out's rows in elements
   int64_t T;
-  int n, k;
+  int n, k, cols;  // cols: workgroups that share a run of weights
   int xs_cols, xs_shift;  // a group of 64 has scale (group >> xs_shift), 31: the row's
   bool qbf16;
   LinX x_type;
