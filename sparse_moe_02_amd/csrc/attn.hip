@@ -894,6 +894,25 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
   const int all_hi_t = (int)(full ? (int64_t)t.len : max(min(tf + 1, (int64_t)t.len), (int64_t)0));
   const int all_lo_t = PREFIX ? t.lo : a.window ? (int)max(tl - a.window + 1, (int64_t)0) : 0;
 
+  const int blk0 = t.lo / kAttnKeys, nblk = (t.hi + kAttnKeys - 1) / kAttnKeys - blk0;
+  const int b0 = blk0 + min(nblk, split * work.per);
+  const int b1 = blk0 + (split + 1 == splits ? nblk : min(nblk, (split + 1) * work.per));
+
+  // the rows that this wave loads lie in one 16-key half of a block
+  const int my_r0 = wave * kInstr * kRowsPer, upper = my_r0 >> 4;
+  // Pages are looked up 64 halves at a time, one a lane, and a block's read from the lanes (numbers
+  // fetched and checked block by block take twice the scalar instructions: 4096 tokens at 32K 1898 us,
+  // 1849 this way; one token at 500 11.6 and 11.2).
+  constexpr int kPageStep = 16;  // blocks after which the next 64 halves are taken, which half overlap
+  const int32_t *table = a.b.table + (int64_t)max(t.row, 0) * a.b.cols;
+  auto pages_from = [&](int blk) {  // lane i: page of half i of the blocks from blk on, or -1
+    const int col = (blk * kAttnKeys + lane * 16) >> a.kv.page_shift;
+    const int page = table[min(col, a.b.cols - 1)];
+    return col < a.b.cols && (unsigned)page < (unsigned)a.kv.n_pages ? page : -1;
+  };
+  // (asked for before the queries, whose arrival they need not wait for: one token at 4096 keys, 2 heads of 256,
+  // 12.0 us and 12.6 otherwise; 24 ragged chunks, heads of 128, 125 and 129)
+  int pages = pages_from(b0), more = b0 + kPageStep < b1 ? pages_from(b0 + kPageStep) : -1, from = b0;
   // a negative scale is taken as a positive one on negated queries, so that the largest score
   // is the largest product
   const float scale = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);  // 0: of queries of zeros
@@ -913,22 +932,6 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
     qf[c] ^= flip;
   }
 
-  const int blk0 = t.lo / kAttnKeys, nblk = (t.hi + kAttnKeys - 1) / kAttnKeys - blk0;
-  const int b0 = blk0 + min(nblk, split * work.per);
-  const int b1 = blk0 + (split + 1 == splits ? nblk : min(nblk, (split + 1) * work.per));
-
-  // the rows that this wave loads lie in one 16-key half of a block
-  const int my_r0 = wave * kInstr * kRowsPer, upper = my_r0 >> 4;
-  // Pages are looked up 64 halves at a time, one a lane, and a block's read from the lanes (numbers
-  // fetched and checked block by block take twice the scalar instructions: 4096 tokens at 32K 1898 us,
-  // 1849 this way; one token at 500 11.6 and 11.2).
-  constexpr int kPageStep = 16;  // blocks after which the next 64 halves are taken, which half overlap
-  const int32_t *table = a.b.table + (int64_t)max(t.row, 0) * a.b.cols;
-  auto pages_from = [&](int blk) {  // lane i: page of half i of the blocks from blk on, or -1
-    const int col = (blk * kAttnKeys + lane * 16) >> a.kv.page_shift;
-    const int page = table[min(col, a.b.cols - 1)];
-    return col < a.b.cols && (unsigned)page < (unsigned)a.kv.n_pages ? page : -1;
-  };
   uint32_t voff[kInstr];
 #pragma unroll
   for (int i = 0; i < kInstr; ++i) {
@@ -955,7 +958,6 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : D == 128 ? 3 : 4) k_a
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
   float m = -INFINITY, l = 0.0f, es = 0.0f;  // m: of the unscaled products
 
-  int pages = pages_from(b0), more = b0 + kPageStep < b1 ? pages_from(b0 + kPageStep) : -1, from = b0;
   uint64_t absent = __ballot(pages < 0);
   auto page_of = [&](int blk) { return __builtin_amdgcn_readlane(pages, 2 * (blk - from) + upper); };
   pages = max(pages, 0);
@@ -1446,20 +1448,37 @@ AttnShape prefix_shape(int64_t T, int n_seqs, int n_groups, int64_t max_q, int64
   s.p_tiles = (int)(T * G / kAttnTile + n_groups);
   s.tiles = (int)(T * G / kAttnTile + n_seqs);
   if (T == 0) return s;
-  // Splits of one length for both, of a length that makes them fill the chip.
   const int64_t p_blocks = (max_prefix + kAttnKeys - 1) / kAttnKeys, s_blocks = (max_suffix + kAttnKeys - 1) / kAttnKeys + 1;
-  int64_t busy = (max_q * G + kAttnTile - 1) / kAttnTile;
-  busy = (busy < 1 ? 1 : busy) * n_seqs;
-  if (busy < T * G / kAttnTile) busy = T * G / kAttnTile;
-  if (busy > s.tiles) busy = s.tiles;
+  // tiles that can hold rows
+  int64_t s_busy = (max_q * G + kAttnTile - 1) / kAttnTile;
+  s_busy = (s_busy < 1 ? 1 : s_busy) * n_seqs;
+  if (s_busy < T * G / kAttnTile) s_busy = T * G / kAttnTile;  // (whatever max_q says)
+  if (s_busy > s.tiles) s_busy = s.tiles;
   const int64_t p_busy = (T * G + kAttnTile - 1) / kAttnTile;
-  const int64_t total = n_kv * (p_busy * p_blocks + busy * s_blocks);
-  int64_t per = (total + tile_slots(dim) - 1) / tile_slots(dim);
-  if (per < 2) per = 2;
-  auto splits = [&](int64_t blocks) { return (blocks + per - 1) / per; };
-  while (splits(p_blocks) + splits(s_blocks) > kMaxSplits) ++per;
-  s.p_splits = (int)(p_blocks > 0 ? splits(p_blocks) : 1);
-  s.splits = s.p_splits + (int)splits(s_blocks);
+  // Blocks of a split, the same for both: of some lengths the one of least estimated time, in blocks: of the longest
+  // workgroup, whose start and end take as long as kFixed blocks, or of all of them over the chip's slots and half of
+  // the longest where these are not enough for all at once, and of the join, which reads each split's results.
+  // (Just as many splits as fill the slots: 64 sequences of up to 512 keys behind 16384, 2 heads of 256, had 576
+  // workgroups for 512 slots and took 58.6 us.)
+  constexpr double kFixed = 8.0;
+  const double slots = (dim == 256 ? 512.0 : 768.0) / n_kv, join = 1.2e-6 * (double)(T * H) * dim;
+  auto splits = [](int64_t blocks, int64_t per) { return blocks > 0 ? (blocks + per - 1) / per : 1; };
+  const int64_t most = p_blocks > s_blocks ? p_blocks : s_blocks;
+  double best = 0.0;
+  int64_t per = 2;
+  for (int64_t l = 2; l <= most + l / 3; l += 1 + l / 4) {
+    const int64_t ps = splits(p_blocks, l), ss = splits(s_blocks, l);
+    if (ps + ss > kMaxSplits) continue;
+    const double all = (double)(p_busy * ps + s_busy * ss), work = (double)(p_busy * p_blocks + s_busy * s_blocks) + kFixed * all;
+    const double longest = kFixed + (double)(l < most ? l : most);
+    double time = work / slots + (all > slots ? 0.5 * longest : 0.0);
+    if (time < longest) time = longest;
+    time += join * (double)(ps + ss);
+    if (best == 0.0 || time < best) best = time, per = l;
+  }
+  while (splits(p_blocks, per) + splits(s_blocks, per) > kMaxSplits) per += 1 + per / 4;
+  s.p_splits = (int)splits(p_blocks, per);
+  s.splits = s.p_splits + (int)splits(s_blocks, per);
   s.p_blocks = s.split_blocks = (int)per;
   const size_t rows = (size_t)T * H * s.splits;
   s.off_stats = (rows * dim * 4 + 255) & ~(size_t)255;
