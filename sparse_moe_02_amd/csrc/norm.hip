@@ -4,7 +4,16 @@
 // (448), code = y / s rounded.  Every element is read once, held in registers as binary32 while
 // the row's sum goes round, and written once.
 //
-// Bound: memory.
+// A row of more than 1024 elements lies over a workgroup, 8 elements a lane at 2048: 4 rows of
+// 2048 2.45 us (a row on one wave: 3.9) and 8192 of them 24 us (29).  Shorter rows take the lanes
+// they fill, down to 8.
+//
+// Bound: the launch for few rows (2.5 us), memory for many: 8192 rows of 2048 bf16, residual and
+// both outputs 24 us (5.6 TB/s), with int8 in groups of 128 24.5 us (4.8 TB/s); 24496 heads of 256
+// fp16 out of rows of 20 7.7 us (3.3 TB/s: 1/5 of each row is passed over).  Stores that go round
+// the caches take 10% off a large norm alone and cost the product that reads it next more
+// (8192 rows, norm, product and norm 260 -> 263 us), so they are ordinary ones.  Weights loaded
+// ahead of the row's sum changed nothing for few rows and cost many 1.5 us.
 #include "common.hpp"
 #include "serve.hpp"
 
@@ -334,20 +343,22 @@ hipError_t go(const NormArgs &a, hipStream_t s) {
 
 template <bool F16, int KIND>
 hipError_t launch(const NormArgs &a, hipStream_t s) {
-  if (a.W > 8192) {
+  if (a.W > (a.vec ? 16384 : 8192)) {
     if (a.vec) hipLaunchKernelGGL((k_norm_long<F16, KIND, 8>), dim3((unsigned)a.rows), dim3(kThreads), 0, s, a);
     else hipLaunchKernelGGL((k_norm_long<F16, KIND, 1>), dim3((unsigned)a.rows), dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
-  if (!a.vec) return go<F16, KIND, 1, 256, 32>(a, s);
+  if (!a.vec) return a.W <= 2048 ? go<F16, KIND, 1, 256, 8>(a, s) : go<F16, KIND, 1, 256, 32>(a, s);
   // (groups of 128 elements lie over 16 lanes)
   if (a.W <= 64 && (KIND == 0 || a.group <= 64)) return go<F16, KIND, 8, 8, 1>(a, s);
   if (a.W <= 128) return go<F16, KIND, 8, 16, 1>(a, s);
   if (a.W <= 256) return go<F16, KIND, 8, 32, 1>(a, s);
   if (a.W <= 512) return go<F16, KIND, 8, 64, 1>(a, s);
   if (a.W <= 1024) return go<F16, KIND, 8, 64, 2>(a, s);
-  if (a.W <= 2048) return go<F16, KIND, 8, 64, 4>(a, s);
-  return go<F16, KIND, 8, 256, 4>(a, s);
+  if (a.W <= 2048) return go<F16, KIND, 8, 256, 1>(a, s);
+  if (a.W <= 4096) return go<F16, KIND, 8, 256, 2>(a, s);
+  if (a.W <= 8192) return go<F16, KIND, 8, 256, 4>(a, s);
+  return go<F16, KIND, 8, 256, 8>(a, s);
 }
 
 }  // namespace

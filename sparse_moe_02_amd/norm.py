@@ -41,9 +41,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, *,
     if codes and out_dtype not in (torch.int8, torch.float8_e4m3fn):
         raise ValueError("out_dtype: x's type, torch.int8 or torch.float8_e4m3fn required")
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+        out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
     if sum is None and residual is not None:
-        sum = torch.empty(x.shape, dtype=type_, device=x.device)
+        sum = torch.empty_like(x, memory_format=torch.contiguous_format)
     if codes:
         groups = D // group if group > 0 and D > 0 else 1
         if scale is None:

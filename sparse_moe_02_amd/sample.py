@@ -37,9 +37,9 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | No
     pp = None if top_p is None else at("top_p", top_p, f32, index, R)
     mp = None if min_p is None else at("min_p", min_p, f32, index, R)
     if out is None:
-        out = torch.empty(R, dtype=torch.int32, device=logits.device)
+        out = torch.empty_like(u, dtype=torch.int32)
     if prob is None and return_prob:
-        prob = torch.empty(R, dtype=torch.float32, device=logits.device)
+        prob = torch.empty_like(u)
     op = at("out", out, N.INT32, index, R)
     qp = None if prob is None else at("prob", prob, f32, index, R)
     if R:

@@ -1,7 +1,7 @@
 """The norm (moe_rms_norm) against its binary64 form.
 
 Tolerances, u = 2^-24: the sum of squares adds, on a lane's path, at most 128 terms one by one (rows of
-32768 elements over 256 lanes; 32 in rows of up to 8192) and joins lanes in 8 more steps; all terms are
+32768 elements over 256 lanes; 64 in rows of up to 16384) and joins lanes in 8 more steps; all terms are
 positive, so it is off by less than 137 u relative, its root by half of that, and the root, quotient and
 two products by 5 u more: y is off by less than 74 u < 2^-17 relative before it is rounded once, by 2^-8
 (bf16) or 2^-11 (fp16) relative, 2^-25 absolute among fp16's small numbers.  h = x + r is rounded in
@@ -77,7 +77,7 @@ def _check(x, r, w, kind, group=0, offset=0.0, eps=1e-6, what="", **kw):
 
 
 WIDTHS = [1, 7, 8, 63, 64, 65, 120, 128, 136, 248, 256, 264, 511, 512, 520, 1000, 1024, 1032, 2047, 2048, 2056, 4096, 8191, 8192,
-          8200, 8201, 32768]
+          8200, 8201, 16384, 16392, 32768]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
