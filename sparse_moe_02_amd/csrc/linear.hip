@@ -261,8 +261,8 @@ hipError_t go(LinArgs a, int per_cu, hipStream_t s) {
   static std::atomic<uint64_t> done{0};
   const hipError_t e = allow_lds(k_linear<X, CT, KS, R, MAX_WAVES>, kWaveLds * MAX_WAVES, done);
   if (e != hipSuccess) return e;
-  // runs of tiles that fill the chip once, or of R tiles
-  int64_t runs = R == 1 ? tiles : 256 * (per_cu / waves) / cols;
+  // runs of tiles that fill the chip once, or of R tiles; of one tile (a launch holds less than 2^32 work-items)
+  int64_t runs = R == 1 ? (1 << 21) / cols : 256 * (per_cu / waves) / cols;
   if (runs > (tiles + R - 1) / R) runs = (tiles + R - 1) / R;
   if (runs < 1) runs = 1;
   if (cols > 1 && R > 1) runs = (runs + 7) / 8 * 8;

@@ -171,6 +171,13 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v, int group) {
   return group == 8 * VEC ? lanes_max<8>(v) : group == 4 * VEC ? lanes_max<4>(v) : lanes_max<16>(v);
 }
 
+// A launch holds less than 2^32 work-items along x, so the workgroups of many rows lie over y as well.
+constexpr int64_t kGridX = 1 << 20;
+__device__ __forceinline__ int64_t block_of() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+dim3 grid_of(int64_t blocks) {
+  return blocks <= kGridX ? dim3((unsigned)blocks) : dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
+}
+
 // A row over LANES lanes (256: a whole workgroup), NV * VEC elements each: LANES * VEC * NV >= W.
 template <bool F16, int KIND, int VEC, int LANES, int NV>
 __global__ void __launch_bounds__(kThreads) k_norm(NormArgs a) {
@@ -178,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) k_norm(NormArgs a) {
   __shared__ uint32_t redm[4];
   constexpr int kRows = kThreads / LANES;
   const int tid = threadIdx.x, lane = tid % LANES;
-  const int64_t row = (int64_t)blockIdx.x * kRows + tid / LANES;
+  const int64_t row = block_of() * kRows + tid / LANES;
   const bool live = row < a.rows;
   const int64_t rr = live ? row : a.rows - 1;
   const int64_t t = a.n == 1 ? rr : rr / a.n;
@@ -269,7 +276,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_long(NormArgs a) {
   __shared__ float red[4];
   __shared__ uint32_t redm[4];
   const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x, t = row / a.n;
+  const int64_t row = block_of(), t = row / a.n;
+  if (row >= a.rows) return;
   const int hd = (int)(row - t * a.n);
   const uint16_t *x = (const uint16_t *)a.x.p + place(a.x, t, hd);
   const uint16_t *r = a.r.p ? (const uint16_t *)a.r.p + place(a.r, t, hd) : nullptr;
@@ -337,15 +345,15 @@ __global__ void __launch_bounds__(kThreads) k_norm_long(NormArgs a) {
 template <bool F16, int KIND, int VEC, int LANES, int NV>
 hipError_t go(const NormArgs &a, hipStream_t s) {
   constexpr int kRows = kThreads / LANES;
-  hipLaunchKernelGGL((k_norm<F16, KIND, VEC, LANES, NV>), dim3((unsigned)((a.rows + kRows - 1) / kRows)), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((k_norm<F16, KIND, VEC, LANES, NV>), grid_of((a.rows + kRows - 1) / kRows), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
 template <bool F16, int KIND>
 hipError_t launch(const NormArgs &a, hipStream_t s) {
   if (a.W > (a.vec ? 16384 : 8192)) {
-    if (a.vec) hipLaunchKernelGGL((k_norm_long<F16, KIND, 8>), dim3((unsigned)a.rows), dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_norm_long<F16, KIND, 1>), dim3((unsigned)a.rows), dim3(kThreads), 0, s, a);
+    if (a.vec) hipLaunchKernelGGL((k_norm_long<F16, KIND, 8>), grid_of(a.rows), dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((k_norm_long<F16, KIND, 1>), grid_of(a.rows), dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
   if (!a.vec) return a.W <= 2048 ? go<F16, KIND, 1, 256, 8>(a, s) : go<F16, KIND, 1, 256, 32>(a, s);
