@@ -16,7 +16,7 @@ _TYPES = {torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_FP16, torch.float32: 
 
 class QLinear:
     """Weights [n][k] of 4 bits: code * scale + bias, one scale and one bias for each group of 64
-    along k, in the library's tiles.
+    along k, in the library's tiles, which are whole when this returns.
 
     codes: int32 [n][k / 8], element k in bits 4 (k % 8) of word k / 8; scale, bias: float16 or
     bfloat16 [n][k / 64]; all row-major, on any device.  They are laid out once, here; the tensors
@@ -51,6 +51,7 @@ class QLinear:
         with on(self.device.index):
             self.codes = tiled(codes, k // 8, B.moe_pack_codes)
             self.scale, self.bias = (tiled(t, k // 64, B.moe_pack_qparams) for t in (scale, bias))
+            torch.cuda.current_stream().synchronize()  # (calls may come on any stream)
         self._index = self.device.index
         self._w = B.moe_linear_weights(self.codes.data_ptr(), self.scale.data_ptr(), self.bias.data_ptr(), self.n, self.k,
                                        _TYPES[scale.dtype])
@@ -70,7 +71,7 @@ class QLinear:
                 out_dtype = torch.bfloat16 if t == B.MOE_INT8 else x.dtype
             if out_dtype not in (torch.bfloat16, torch.float16, torch.float32):
                 raise ValueError("out_dtype: bfloat16, float16 or float32 required")
-            out = torch.empty((T, self.n), dtype=out_dtype, device=x.device)
+            out = x.new_empty((T, self.n), dtype=out_dtype)
         o = _TYPES.get(out.dtype, B.MOE_INT8)
         if o == B.MOE_INT8:
             raise ValueError("out: bfloat16, float16 or float32 required")
