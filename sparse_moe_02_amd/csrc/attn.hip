@@ -1445,8 +1445,9 @@ AttnShape prefix_shape(int64_t T, int n_seqs, int n_groups, int64_t max_q, int64
   AttnShape s{};
   const int64_t G = H / n_kv;
   s.rows = kAttnTile;
-  s.p_tiles = (int)(T * G / kAttnTile + n_groups);
-  s.tiles = (int)(T * G / kAttnTile + n_seqs);
+  // (as find_prefix_tile and find_tile lay them out)
+  s.p_tiles = (int)((T * G + kAttnTile - 1) / kAttnTile + n_groups - 1);
+  s.tiles = (int)((T * G + kAttnTile - 1) / kAttnTile + n_seqs - 1);
   if (T == 0) return s;
   const int64_t p_blocks = (max_prefix + kAttnKeys - 1) / kAttnKeys, s_blocks = (max_suffix + kAttnKeys - 1) / kAttnKeys + 1;
   // tiles that can hold rows
@@ -1454,32 +1455,67 @@ AttnShape prefix_shape(int64_t T, int n_seqs, int n_groups, int64_t max_q, int64
   s_busy = (s_busy < 1 ? 1 : s_busy) * n_seqs;
   if (s_busy < T * G / kAttnTile) s_busy = T * G / kAttnTile;  // (whatever max_q says)
   if (s_busy > s.tiles) s_busy = s.tiles;
-  const int64_t p_busy = (T * G + kAttnTile - 1) / kAttnTile;
-  // Blocks of a split, the same for both: of some lengths the one of least estimated time, in blocks: of the longest
-  // workgroup, whose start and end take as long as kFixed blocks, or of all of them over the chip's slots and half of
-  // the longest where these are not enough for all at once, and of the join, which reads each split's results.
-  // (Just as many splits as fill the slots: 64 sequences of up to 512 keys behind 16384, 2 heads of 256, had 576
-  // workgroups for 512 slots and took 58.6 us.)
-  constexpr double kFixed = 8.0;
-  const double slots = (dim == 256 ? 512.0 : 768.0) / n_kv, join = 1.2e-6 * (double)(T * H) * dim;
+  int64_t p_busy = (T * G + kAttnTile - 1) / kAttnTile;
+  if (p_busy < n_groups) p_busy = n_groups;
+  // Blocks of a split, for prefixes and for suffixes: of some lengths those of least estimated time, in blocks (about
+  // 0.95 us, heads of 256).  It is kFixed for the first workgroups' start, and the most of: the longest workgroup's, where
+  // one whose rows are all there needs the matrix units of its compute unit to itself, so that of two there one
+  // waits; the matrix units' work over all of them; and that of the workgroups in the order in which they find
+  // place.  Then the join, which reads each split's results.  us so, and with the best pair of all lengths: 64
+  // sequences of up to 512 keys behind 16384, 2 heads of 256, 41.7 and 40.3 (58.6 where splits just filled the chip);
+  // 128 of them 59.6 both; 23 of 5 prefixes of up to 5000, drafts of up to 4 tokens, 32/8 heads of 128, 28.8 and 27.9; 64
+  // of 64 prefixes of up to 2000 40 and 39; 64 of 2048, 32/8 heads of 128, 21.6 and 21.0; 64 of up to 512 behind 512
+  // 25 and 22.
+  constexpr double kFixed = 6.0, kNext = 1.5;  // (kNext: a further workgroup's start, while others run)
+  constexpr int kUnits = 256;
+  const double slots = (dim == 256 ? 2 : 3) * kUnits, join = 2e-6 * (double)(T * H) * dim;
+  auto full = [&](int64_t busy) { return fmin(fmax((double)(T * G) / (double)(busy * kAttnTile), 0.25), 1.0); };
+  const double p_full = full(p_busy), s_full = full(s_busy);
   auto splits = [](int64_t blocks, int64_t per) { return blocks > 0 ? (blocks + per - 1) / per : 1; };
+  auto time = [&](int64_t p_per, int64_t s_per) {
+    const int64_t ps = splits(p_blocks, p_per), ss = splits(s_blocks, s_per);
+    if (ps + ss > kMaxSplits) return 1e300;
+    const double p_len = (double)(p_per < p_blocks ? p_per : p_blocks), s_len = (double)(s_per < s_blocks ? s_per : s_blocks);
+    const double p_all = (double)(p_busy * ps * n_kv), s_all = (double)(s_busy * ss * n_kv);
+    const double longest = fmax(p_len * fmax(1.0, 1.2 * p_full * ceil(p_all / kUnits)), s_len);
+    const double work = (p_all * p_len * p_full + s_all * s_len * s_full) / kUnits;
+    // rounds of prefixes, suffixes in the places that the last of these leaves, and those that find none
+    const double p_one = p_len + kNext, s_one = s_len + kNext, p_rounds = ceil(p_all / slots);
+    const double beside = (p_rounds * slots - p_all) * floor(p_one / s_one);
+    const double ends = p_rounds * p_one - kNext + fmax(ceil((s_all - beside) / slots), 0.0) * s_one;
+    const double even = (p_all * p_one + s_all * s_one) / slots;  // (at least this, and not much more)
+    return kFixed + fmax(fmax(longest, work), fmax(even, fmin(ends, even + fmax(p_len, s_len)))) + join * (double)(ps + ss);
+  };
+  // lengths: geometric ones, those that give each compute unit the same number of prefixes' workgroups, and the one that
+  // leaves each suffix a place beside them
   const int64_t most = p_blocks > s_blocks ? p_blocks : s_blocks;
-  double best = 0.0;
-  int64_t per = 2;
-  for (int64_t l = 2; l <= most + l / 3; l += 1 + l / 4) {
-    const int64_t ps = splits(p_blocks, l), ss = splits(s_blocks, l);
-    if (ps + ss > kMaxSplits) continue;
-    const double all = (double)(p_busy * ps + s_busy * ss), work = (double)(p_busy * p_blocks + s_busy * s_blocks) + kFixed * all;
-    const double longest = kFixed + (double)(l < most ? l : most);
-    double time = work / slots + (all > slots ? 0.5 * longest : 0.0);
-    if (time < longest) time = longest;
-    time += join * (double)(ps + ss);
-    if (best == 0.0 || time < best) best = time, per = l;
+  auto best_of = [&](auto t) {
+    int64_t best = 2;
+    double least = 1e300;
+    auto take = [&](int64_t l) {
+      const double v = t(l);
+      if (v < least) least = v, best = l;
+    };
+    for (int64_t l = 2; l <= most + l / 3; l += 1 + l / 4) take(l);
+    for (int r = 0; r <= 3; ++r) {
+      const int64_t ps = (r > 0 ? r * kUnits : (int64_t)slots - s_busy * n_kv) / (p_busy * n_kv);
+      if (ps > 0 && p_blocks > 2 * ps) take((p_blocks + ps - 1) / ps);
+    }
+    return best;
+  };
+  int64_t p_per = best_of([&](int64_t l) { return time(l, l); });
+  int64_t s_per = best_of([&](int64_t l) { return time(p_per, l); });
+  p_per = best_of([&](int64_t l) { return time(l, s_per); });
+  // (a launch holds less than 2^32 work-items; groups and sequences without tokens count)
+  auto many = [&] { return n_kv * (s.p_tiles * splits(p_blocks, p_per) + s.tiles * splits(s_blocks, s_per)) >= int64_t(1) << 24; };
+  while (splits(p_blocks, p_per) + splits(s_blocks, s_per) > kMaxSplits || many()) {
+    p_per += 1 + p_per / 4;
+    s_per += 1 + s_per / 4;
   }
-  while (splits(p_blocks, per) + splits(s_blocks, per) > kMaxSplits) per += 1 + per / 4;
-  s.p_splits = (int)splits(p_blocks, per);
-  s.splits = s.p_splits + (int)splits(s_blocks, per);
-  s.p_blocks = s.split_blocks = (int)per;
+  s.p_splits = (int)splits(p_blocks, p_per);
+  s.splits = s.p_splits + (int)splits(s_blocks, s_per);
+  s.p_blocks = (int)p_per;
+  s.split_blocks = (int)s_per;
   const size_t rows = (size_t)T * H * s.splits;
   s.off_stats = (rows * dim * 4 + 255) & ~(size_t)255;
   s.ws_bytes = s.off_stats + rows * sizeof(AttnStats);

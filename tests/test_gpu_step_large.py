@@ -106,3 +106,30 @@ def test_prefix_in_far_pages(new):
     b, lb = prefix_attn(q, big[0], big[1], i32(table) + at, *args, return_lse=True)
     assert torch.equal(a, b) and torch.equal(la, lb)
     say(f"pages from {at} of {pages}")
+
+
+def test_prefixes_of_many_sequences_without_tokens():
+    """65535 sequences, each a group, 3 of them with a token: groups times splits of their bounds pass 2^24
+    workgroups."""
+    import torch
+
+    from sparse_moe_02_amd.attn import prefix_attn
+
+    n, page, hk, D, H = 65535, 16, 4, 64, 4
+    g = torch.Generator(device="cuda").manual_seed(4)
+    kc, vc = (torch.randn((8, page, hk, D), generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn((3, H, D), generator=g, device="cuda").bfloat16()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    has = [0, 33333, n - 1]
+    start = torch.zeros(n + 1, **i32)
+    for b in has:
+        start[b + 1:] += 1
+    table = torch.zeros((n, 2), **i32)
+    lens, prefix = torch.zeros(n, **i32), torch.zeros(n, **i32)
+    small = torch.tensor([[0, 1], [2, 3], [4, 5]], **i32)
+    table[has], lens[has], prefix[has] = small, torch.tensor([20, 32, 5], **i32), torch.tensor([16, 9, 0], **i32)
+    most = 1, 1 << 20, 1 << 20
+    a, la = prefix_attn(q, kc, vc, table, start, lens, torch.arange(n + 1, **i32), prefix, *most, return_lse=True)
+    b, lb = prefix_attn(q, kc, vc, small, start[[0, *(x + 1 for x in has)]], lens[has], torch.arange(4, **i32), prefix[has], 1, 16, 32,
+                        return_lse=True)
+    assert (a.double() - b.double()).abs().max() <= 2.0 ** -7 * vc.abs().max() and (la - lb).abs().max() <= 2.0 ** -18 * (1 + lb.abs().max())
