@@ -105,70 +105,79 @@ __device__ __forceinline__ uint32_t codes4(const float *y, const Step &s) {
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(code_of(y[2], s, 448.0f), code_of(y[3], s, 448.0f), w, true);
   }
 }
-template <int KIND>
-__device__ __forceinline__ uint8_t code1(float y, const Step &s) {
-  const float four[4] = {y, y, y, y};
-  return (uint8_t)(codes4<KIND>(four, s) & 0xffu);
-}
-
 // Element offset of row `row` of an array.
 __device__ __forceinline__ int64_t place(const Rows &a, int64_t t, int h) { return t * a.ts + h * a.hs; }
 
-// VEC consecutive elements as binary32: x + r.
-template <bool F16, int VEC>
-__device__ __forceinline__ void load_h(const uint16_t *x, const uint16_t *r, int at, float *h) {
-  if constexpr (VEC == 8) {
-    const u32x4 a = *(const u32x4 *)(x + at);
-    u32x4 b = {0, 0, 0, 0};
-    if (r) b = *(const u32x4 *)(r + at);
+// Elements are handled eight at a time.  WIDE: all arrays and rows are aligned for that and rows hold whole
+// eights.  Otherwise the same accesses are made at addresses aligned to an element (4271 rows of 3326 bf16,
+// residual and both outputs, 28 us; one element at a time 82), and a row's last elements one by one.
+typedef u32x4 __attribute__((aligned(2))) u32x4_2;
+typedef uint32_t __attribute__((__vector_size__(2 * sizeof(uint32_t)), aligned(1))) u32x2_1;
+template <bool WIDE, class F>
+__device__ __forceinline__ void last_ones(int at, int W, F f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[2 * i] = value<F16>(a[i] & 0xffffu);
-      h[2 * i + 1] = value<F16>(a[i] >> 16);
-      if (r) {
-        h[2 * i] += value<F16>(b[i] & 0xffffu);
-        h[2 * i + 1] += value<F16>(b[i] >> 16);
-      }
+  for (int i = 0; i < 8; ++i)
+    if (at + i < W) f(i);
+}
+template <bool F16, bool WIDE>
+__device__ __forceinline__ u32x4 load8(const uint16_t *p, int at, int W) {
+  if constexpr (WIDE) return *(const u32x4 *)(p + at);
+  if (at + 8 <= W) return *(const u32x4_2 *)(p + at);
+  u32x4 v = {0, 0, 0, 0};
+  last_ones<WIDE>(at, W, [&](int i) { v[i / 2] |= (uint32_t)p[at + i] << (16 * (i % 2)); });
+  return v;
+}
+// x + r, 0 behind the row's end
+template <bool F16, bool WIDE>
+__device__ __forceinline__ void load_h(const uint16_t *x, const uint16_t *r, int at, int W, float *h) {
+  const u32x4 a = load8<F16, WIDE>(x, at, W);
+  u32x4 b = {0, 0, 0, 0};
+  if (r) b = load8<F16, WIDE>(r, at, W);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[2 * i] = value<F16>(a[i] & 0xffffu);
+    h[2 * i + 1] = value<F16>(a[i] >> 16);
+    if (r) {
+      h[2 * i] += value<F16>(b[i] & 0xffffu);
+      h[2 * i + 1] += value<F16>(b[i] >> 16);
     }
-  } else {
-    h[0] = value<F16>(x[at]);
-    if (r) h[0] += value<F16>(r[at]);
   }
 }
-template <bool F16, int VEC>
-__device__ __forceinline__ void store_h(uint16_t *o, int at, const float *h) {
-  if constexpr (VEC == 8)
-    *(u32x4 *)(o + at) = u32x4{pair_of<F16>(h[0], h[1]), pair_of<F16>(h[2], h[3]), pair_of<F16>(h[4], h[5]), pair_of<F16>(h[6], h[7])};
-  else
-    o[at] = (uint16_t)pair_of<F16>(h[0], 0.0f);
+template <bool F16, bool WIDE>
+__device__ __forceinline__ void store_h(uint16_t *o, int at, int W, const float *h) {
+  const u32x4 v = {pair_of<F16>(h[0], h[1]), pair_of<F16>(h[2], h[3]), pair_of<F16>(h[4], h[5]), pair_of<F16>(h[6], h[7])};
+  if constexpr (WIDE) {
+    *(u32x4 *)(o + at) = v;
+  } else {
+    if (at + 8 <= W) *(u32x4_2 *)(o + at) = v;
+    else last_ones<WIDE>(at, W, [&](int i) { o[at + i] = (uint16_t)(v[i / 2] >> (16 * (i % 2))); });
+  }
 }
-template <bool F16, int VEC>
-__device__ __forceinline__ void load_w(const uint16_t *w, float offset, int at, float *o) {
+template <bool F16, bool WIDE>
+__device__ __forceinline__ void load_w(const uint16_t *w, float offset, int at, int W, float *o) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) o[i] = offset;
+  for (int i = 0; i < 8; ++i) o[i] = offset;
   if (!w) return;
-  if constexpr (VEC == 8) {
-    const u32x4 a = *(const u32x4 *)(w + at);
+  const u32x4 a = load8<F16, WIDE>(w, at, W);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] += value<F16>(i & 1 ? a[i / 2] >> 16 : a[i / 2] & 0xffffu);
-  } else {
-    o[0] += value<F16>(w[at]);
-  }
+  for (int i = 0; i < 8; ++i) o[i] += value<F16>(i & 1 ? a[i / 2] >> 16 : a[i / 2] & 0xffffu);
 }
-template <int KIND, int VEC>
-__device__ __forceinline__ void store_codes(uint8_t *o, int at, const float *y, const Step &s) {
-  if constexpr (VEC == 8)
-    *(uint2 *)(o + at) = make_uint2(codes4<KIND>(y, s), codes4<KIND>(y + 4, s));
-  else
-    o[at] = code1<KIND>(y[0], s);
+template <int KIND, bool WIDE>
+__device__ __forceinline__ void store_codes(uint8_t *o, int at, int W, const float *y, const Step &s) {
+  const uint32_t lo = codes4<KIND>(y, s), hi = codes4<KIND>(y + 4, s);
+  if constexpr (WIDE) {
+    *(uint2 *)(o + at) = make_uint2(lo, hi);
+  } else {
+    if (at + 8 <= W) *(u32x2_1 *)(o + at) = u32x2_1{lo, hi};
+    else last_ones<WIDE>(at, W, [&](int i) { o[at + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i % 4))); });
+  }
 }
 
 __device__ __forceinline__ uint32_t bits_of(float y) { return __float_as_uint(y) & 0x7fffffffu; }
 
-// Of a group of `group` elements that lies over consecutive lanes, VEC elements each.
-template <int VEC>
+// Of a group of `group` elements that lies over consecutive lanes, 8 elements each.
 __device__ __forceinline__ uint32_t group_max(uint32_t v, int group) {
-  return group == 8 * VEC ? lanes_max<8>(v) : group == 4 * VEC ? lanes_max<4>(v) : lanes_max<16>(v);
+  return group == 64 ? lanes_max<8>(v) : group == 32 ? lanes_max<4>(v) : lanes_max<16>(v);
 }
 
 // A launch holds less than 2^32 work-items along x, so the workgroups of many rows lie over y as well.
@@ -178,8 +187,8 @@ dim3 grid_of(int64_t blocks) {
   return blocks <= kGridX ? dim3((unsigned)blocks) : dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
 }
 
-// A row over LANES lanes (256: a whole workgroup), NV * VEC elements each: LANES * VEC * NV >= W.
-template <bool F16, int KIND, int VEC, int LANES, int NV>
+// A row over LANES lanes (256: a whole workgroup), 8 NV elements each: LANES * 8 NV >= W.
+template <bool F16, int KIND, bool WIDE, int LANES, int NV>
 __global__ void __launch_bounds__(kThreads) k_norm(NormArgs a) {
   __shared__ float red[4];
   __shared__ uint32_t redm[4];
@@ -192,22 +201,22 @@ __global__ void __launch_bounds__(kThreads) k_norm(NormArgs a) {
   const int hd = a.n == 1 ? 0 : (int)(rr - t * a.n);
   const uint16_t *x = (const uint16_t *)a.x.p + place(a.x, t, hd);
   const uint16_t *r = a.r.p ? (const uint16_t *)a.r.p + place(a.r, t, hd) : nullptr;
-  float h[NV][VEC];
+  float h[NV][8];
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int at = (i * LANES + lane) * VEC;
+    const int at = (i * LANES + lane) * 8;
     if (at < a.W) {
-      load_h<F16, VEC>(x, r, at, h[i]);
+      load_h<F16, WIDE>(x, r, at, a.W, h[i]);
     } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) h[i][e] = 0.0f;
+      for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) ss = __builtin_fmaf(h[i][e], h[i][e], ss);
+    for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[i][e], h[i][e], ss);
   ss = lanes_sum<LANES>(ss);
   if constexpr (LANES == kThreads) {
     if ((tid & 63) == 0) red[tid >> 6] = ss;
@@ -220,18 +229,18 @@ __global__ void __launch_bounds__(kThreads) k_norm(NormArgs a) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int at = (i * LANES + lane) * VEC;
+    const int at = (i * LANES + lane) * 8;
     if (at >= a.W) continue;
-    if (sum && live) store_h<F16, VEC>(sum, at, h[i]);
-    float w[VEC];
-    load_w<F16, VEC>(a.w, a.offset, at, w);
+    if (sum && live) store_h<F16, WIDE>(sum, at, a.W, h[i]);
+    float w[8];
+    load_w<F16, WIDE>(a.w, a.offset, at, a.W, w);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) h[i][e] = h[i][e] * f * w[e];
+    for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * f * w[e];
     if constexpr (KIND == 0) {
-      if (live) store_h<F16, VEC>((uint16_t *)a.out.p + out, at, h[i]);
+      if (live) store_h<F16, WIDE>((uint16_t *)a.out.p + out, at, a.W, h[i]);
     } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) top = max(top, bits_of(h[i][e]));
+      for (int e = 0; e < 8; ++e) top = max(top, bits_of(h[i][e]));
     }
   }
   if constexpr (KIND > 0) {
@@ -247,23 +256,23 @@ __global__ void __launch_bounds__(kThreads) k_norm(NormArgs a) {
       if (live && lane == 0) a.scale[rr] = s.scale;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int at = (i * LANES + lane) * VEC;
-        if (at < a.W && live) store_codes<KIND, VEC>(o, at, h[i], s);
+        const int at = (i * LANES + lane) * 8;
+        if (at < a.W && live) store_codes<KIND, WIDE>(o, at, a.W, h[i], s);
       }
-    } else if constexpr (VEC == 8) {
+    } else if constexpr (WIDE) {
       const int groups = a.W / a.group;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int at = (i * LANES + lane) * VEC;
+        const int at = (i * LANES + lane) * 8;
         uint32_t m = 0;  // (a lane behind the row's end is in no group of one before it)
         if (at < a.W) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) m = max(m, bits_of(h[i][e]));
+          for (int e = 0; e < 8; ++e) m = max(m, bits_of(h[i][e]));
         }
-        const Step s = step_of<KIND>(group_max<VEC>(m, a.group));
+        const Step s = step_of<KIND>(group_max(m, a.group));
         if (at >= a.W || !live) continue;
         if (at % a.group == 0) a.scale[rr * groups + at / a.group] = s.scale;
-        store_codes<KIND, VEC>(o, at, h[i], s);
+        store_codes<KIND, WIDE>(o, at, a.W, h[i], s);
       }
     }
   }
@@ -271,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) k_norm(NormArgs a) {
 
 // Rows too long for registers, one a workgroup: h is formed anew in each pass and written in the
 // last, so that it may be written over what it comes from.
-template <bool F16, int KIND, int VEC>
+template <bool F16, int KIND, bool WIDE>
 __global__ void __launch_bounds__(kThreads) k_norm_long(NormArgs a) {
   __shared__ float red[4];
   __shared__ uint32_t redm[4];
@@ -282,11 +291,11 @@ __global__ void __launch_bounds__(kThreads) k_norm_long(NormArgs a) {
   const uint16_t *x = (const uint16_t *)a.x.p + place(a.x, t, hd);
   const uint16_t *r = a.r.p ? (const uint16_t *)a.r.p + place(a.r, t, hd) : nullptr;
   float ss = 0.0f;
-  for (int at = tid * VEC; at < a.W; at += kThreads * VEC) {
-    float h[VEC];
-    load_h<F16, VEC>(x, r, at, h);
+  for (int at = tid * 8; at < a.W; at += kThreads * 8) {
+    float h[8];
+    load_h<F16, WIDE>(x, r, at, a.W, h);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) ss = __builtin_fmaf(h[e], h[e], ss);
+    for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[e], h[e], ss);
   }
   ss = wave_sum(ss);
   if ((tid & 63) == 0) red[tid >> 6] = ss;
@@ -294,20 +303,20 @@ __global__ void __launch_bounds__(kThreads) k_norm_long(NormArgs a) {
   ss = (red[0] + red[1]) + (red[2] + red[3]);
   const float f = 1.0f / __builtin_sqrtf(ss / (float)a.W + a.eps);
   auto normed = [&](int at, float *h, float *y) {
-    float w[VEC];
-    load_h<F16, VEC>(x, r, at, h);
-    load_w<F16, VEC>(a.w, a.offset, at, w);
+    float w[8];
+    load_h<F16, WIDE>(x, r, at, a.W, h);
+    load_w<F16, WIDE>(a.w, a.offset, at, a.W, w);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) y[e] = h[e] * f * w[e];
+    for (int e = 0; e < 8; ++e) y[e] = h[e] * f * w[e];
   };
   Step s{};
   if (KIND > 0 && a.group == a.W) {
     uint32_t top = 0;
-    for (int at = tid * VEC; at < a.W; at += kThreads * VEC) {
-      float h[VEC], y[VEC];
+    for (int at = tid * 8; at < a.W; at += kThreads * 8) {
+      float h[8], y[8];
       normed(at, h, y);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) top = max(top, bits_of(y[e]));
+      for (int e = 0; e < 8; ++e) top = max(top, bits_of(y[e]));
     }
     top = wave_max_u32(top);
     if ((tid & 63) == 0) redm[tid >> 6] = top;
@@ -317,56 +326,58 @@ __global__ void __launch_bounds__(kThreads) k_norm_long(NormArgs a) {
   }
   uint16_t *sum = a.sum.p ? (uint16_t *)a.sum.p + place(a.sum, t, hd) : nullptr;
   const int64_t out = place(a.out, t, hd);
-  for (int b = 0; b < a.W; b += kThreads * VEC) {
-    const int at = b + tid * VEC;
+  for (int b = 0; b < a.W; b += kThreads * 8) {
+    const int at = b + tid * 8;
     const bool in = at < a.W;
-    float h[VEC], y[VEC];
+    float h[8], y[8];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) y[e] = 0.0f;
+    for (int e = 0; e < 8; ++e) y[e] = 0.0f;
     if (in) normed(at, h, y);
-    if constexpr (KIND > 0 && VEC == 8) {
+    if constexpr (KIND > 0 && WIDE) {
       if (a.group != a.W) {
         uint32_t m = 0;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) m = max(m, bits_of(y[e]));
-        s = step_of<KIND>(group_max<VEC>(m, a.group));
+        for (int e = 0; e < 8; ++e) m = max(m, bits_of(y[e]));
+        s = step_of<KIND>(group_max(m, a.group));
         if (in && at % a.group == 0) a.scale[row * (a.W / a.group) + at / a.group] = s.scale;
       }
     }
     if (!in) continue;
-    if (sum) store_h<F16, VEC>(sum, at, h);
+    if (sum) store_h<F16, WIDE>(sum, at, a.W, h);
     if constexpr (KIND == 0)
-      store_h<F16, VEC>((uint16_t *)a.out.p + out, at, y);
+      store_h<F16, WIDE>((uint16_t *)a.out.p + out, at, a.W, y);
     else
-      store_codes<KIND, VEC>((uint8_t *)a.out.p + out, at, y, s);
+      store_codes<KIND, WIDE>((uint8_t *)a.out.p + out, at, a.W, y, s);
   }
 }
 
-template <bool F16, int KIND, int VEC, int LANES, int NV>
+template <bool F16, int KIND, bool WIDE, int LANES, int NV>
 hipError_t go(const NormArgs &a, hipStream_t s) {
   constexpr int kRows = kThreads / LANES;
-  hipLaunchKernelGGL((k_norm<F16, KIND, VEC, LANES, NV>), grid_of((a.rows + kRows - 1) / kRows), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((k_norm<F16, KIND, WIDE, LANES, NV>), grid_of((a.rows + kRows - 1) / kRows), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
-template <bool F16, int KIND>
+template <bool F16, int KIND, bool WIDE>
 hipError_t launch(const NormArgs &a, hipStream_t s) {
-  if (a.W > (a.vec ? 16384 : 8192)) {
-    if (a.vec) hipLaunchKernelGGL((k_norm_long<F16, KIND, 8>), grid_of(a.rows), dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_norm_long<F16, KIND, 1>), grid_of(a.rows), dim3(kThreads), 0, s, a);
+  if (a.W > 16384) {
+    hipLaunchKernelGGL((k_norm_long<F16, KIND, WIDE>), grid_of(a.rows), dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
-  if (!a.vec) return a.W <= 2048 ? go<F16, KIND, 1, 256, 8>(a, s) : go<F16, KIND, 1, 256, 32>(a, s);
   // (groups of 128 elements lie over 16 lanes)
-  if (a.W <= 64 && (KIND == 0 || a.group <= 64)) return go<F16, KIND, 8, 8, 1>(a, s);
-  if (a.W <= 128) return go<F16, KIND, 8, 16, 1>(a, s);
-  if (a.W <= 256) return go<F16, KIND, 8, 32, 1>(a, s);
-  if (a.W <= 512) return go<F16, KIND, 8, 64, 1>(a, s);
-  if (a.W <= 1024) return go<F16, KIND, 8, 64, 2>(a, s);
-  if (a.W <= 2048) return go<F16, KIND, 8, 256, 1>(a, s);
-  if (a.W <= 4096) return go<F16, KIND, 8, 256, 2>(a, s);
-  if (a.W <= 8192) return go<F16, KIND, 8, 256, 4>(a, s);
-  return go<F16, KIND, 8, 256, 8>(a, s);
+  if (a.W <= 64 && (KIND == 0 || a.group <= 64)) return go<F16, KIND, WIDE, 8, 1>(a, s);
+  if (a.W <= 128) return go<F16, KIND, WIDE, 16, 1>(a, s);
+  if (a.W <= 256) return go<F16, KIND, WIDE, 32, 1>(a, s);
+  if (a.W <= 512) return go<F16, KIND, WIDE, 64, 1>(a, s);
+  if (a.W <= 1024) return go<F16, KIND, WIDE, 64, 2>(a, s);
+  if (a.W <= 2048) return go<F16, KIND, WIDE, 256, 1>(a, s);
+  if (a.W <= 4096) return go<F16, KIND, WIDE, 256, 2>(a, s);
+  if (a.W <= 8192) return go<F16, KIND, WIDE, 256, 4>(a, s);
+  return go<F16, KIND, WIDE, 256, 8>(a, s);
+}
+template <bool F16, int KIND>
+hipError_t launch(const NormArgs &a, hipStream_t s) {
+  return a.vec ? launch<F16, KIND, true>(a, s) : launch<F16, KIND, false>(a, s);
 }
 
 }  // namespace

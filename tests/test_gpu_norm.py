@@ -229,3 +229,29 @@ def test_refusals():
     with pytest.raises(B.MoeError) as e:
         rms_norm(odd, w, out_dtype=torch.int8, group=64)
     assert e.value.status == B.MOE_ERR_ALIGN
+
+
+@pytest.mark.parametrize("width", [1, 6, 8, 17, 120, 256, 771, 2048, 3326, 8195, 20003])
+@pytest.mark.parametrize("start", [1, 2, 5])
+def test_rows_that_start_anywhere(width, start):
+    """Every array aligned to its elements only, rows an odd distance apart, between elements that stay as they were."""
+    import torch
+
+    def place(t):
+        buf = torch.full((t.shape[0], t.shape[1] + 3), 7, dtype=torch.float32, device="cuda").to(t.dtype).flatten()
+        buf = torch.cat([buf, buf[:start]])
+        v = buf[start:].view(t.shape[0], -1)[:, :width]
+        v.copy_(t)
+        return buf, v
+
+    for kind in (None, torch.int8):
+        x, r, w = _make((11, width), "bf16", width + start)
+        (_, x), (_, r), (_, w) = place(x), place(r), place(w[None])
+        w = w[0]
+        ob, o = place(torch.zeros((11, width), dtype=torch.bfloat16 if kind is None else kind, device="cuda"))
+        sb, s = place(torch.zeros((11, width), dtype=torch.bfloat16, device="cuda"))
+        _check(x, r, w, kind, out=o, sum=s, what=f"{width} from {start}")
+        for b in (ob, sb):
+            inside = torch.zeros(b.shape, dtype=torch.bool, device="cuda")
+            inside[start:].view(11, -1)[:, :width] = True
+            assert (b[~inside].float() == 7).all()
