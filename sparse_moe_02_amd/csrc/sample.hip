@@ -341,6 +341,7 @@ struct Shared {
   uint64_t red[kPick / 64];
   uint64_t found[3];
   uint64_t left_place[64], left_weight[64];  // the last tokens of a selection
+  uint64_t left_before[64], left_above[64];  // what stands above each of them
   int left_n;
   int n, n_active;             // tokens in the list, chunks that are read
 };
@@ -417,11 +418,17 @@ struct Set {
   template <class F>
   __device__ __forceinline__ void each(F f) const {
     if (listed) {
-      for (int i = threadIdx.x; i < sh.n; i += kPick) {
-        const uint64_t place = places[i];
-        if (place == 0) continue;
-        const int c = (index_of(place) + logits.skip) / kChunk;
-        f(place, scaled(c, weight_of(logit_of(place), row.c, sh.anchor[c], sh.pow).fixed()), c);
+      constexpr int kAhead = 4;
+      for (int i0 = threadIdx.x; i0 < sh.n; i0 += kAhead * kPick) {
+        uint64_t place[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) place[j] = i0 + j * kPick < sh.n ? places[i0 + j * kPick] : 0;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          if (place[j] == 0) continue;
+          const int c = (index_of(place[j]) + logits.skip) / kChunk;
+          f(place[j], scaled(c, weight_of(logit_of(place[j]), row.c, sh.anchor[c], sh.pow).fixed()), c);
+        }
       }
     } else {
       scan_each([&](float l, int n, int c) {
@@ -510,11 +517,23 @@ struct Set {
   // keeps those of the sh.n tokens that are in the bins
   template <class F>
   __device__ __forceinline__ void keep_in(F from) {
-    for (int i = threadIdx.x; i < sh.n; i += kPick) {
-      const uint64_t place = from(i);
-      const int c = (index_of(place) + logits.skip) / kChunk;
-      Weight w;
-      places[i] = in(logit_of(place), c, w) ? place : 0;
+    // (several on their way at once)
+    constexpr int kAhead = 8;
+    for (int i0 = threadIdx.x; i0 < sh.n; i0 += kAhead * kPick) {
+      uint64_t place[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j * kPick;
+        place[j] = i < sh.n ? from(i) : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j * kPick;
+        if (i >= sh.n) break;
+        const int c = (index_of(place[j]) + logits.skip) / kChunk;
+        Weight w;
+        places[i] = in(logit_of(place[j]), c, w) ? place[j] : 0;
+      }
     }
     __syncthreads();
   }
@@ -614,16 +633,30 @@ __device__ __forceinline__ Cut select_from(const S &set, bool by_weight, uint64_
     }
   });
   __syncthreads();
+  // (each wave compares with its share of them)
   const int n = min(sh.left_n, 64);
   const uint64_t place = lane < n ? sh.left_place[lane] : 0, w = lane < n ? sh.left_weight[lane] : 0;
-  uint64_t before = 0, weight = above + w;
-  for (int j = 0; j < n; ++j) {
+  if (tid < 64) sh.left_before[tid] = sh.left_above[tid] = 0;
+  __syncthreads();
+  constexpr int kOwn = 64 / (kPick / 64);
+  uint64_t before = 0, weight = 0;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int j = (tid >> 6) * kOwn + i;
+    if (j >= n) break;
     const uint64_t p = sh.left_place[j], v = sh.left_weight[j];
     if (p > place) {
       before += by_weight ? v : 1;
       weight += v;
     }
   }
+  if (weight > 0 || before > 0) {
+    lds_add(&sh.left_before[lane], before);
+    lds_add(&sh.left_above[lane], weight);
+  }
+  __syncthreads();
+  before = sh.left_before[lane];
+  weight = sh.left_above[lane] + above + w;
   const uint64_t own = by_weight ? w : 1;
   uint64_t hit = __ballot(lane < n && before < want && before + own >= want);
   if (!hit) {  // the lowest of them
@@ -657,15 +690,14 @@ __device__ __forceinline__ double read_chunks(const SampleArgs &a, int r, Shared
   __syncthreads();
   return y0;
 }
-// f(chunk, bin of the chunk, count, weights), of those that hold tokens
-template <class F>
-__device__ __forceinline__ void each_bin(const SampleArgs &a, int r, F f) {
-  const uint64_t *mass = a.mass + (int64_t)r * a.C * kBins;
-  const uint32_t *count = a.count + (int64_t)r * a.C * kBins;
-  constexpr int kAhead = 7;
-  for (int i0 = threadIdx.x; i0 < a.C * kBins; i0 += kAhead * kPick) {
-    uint32_t n[kAhead];
-    uint64_t m[kAhead];
+// The chunks' bins, kAhead a thread at a time from number i0 on.
+struct Bins {
+  static constexpr int kAhead = 7;
+  uint32_t n[kAhead];
+  uint64_t m[kAhead];
+  __device__ __forceinline__ void load(const SampleArgs &a, int r, int i0) {
+    const uint64_t *mass = a.mass + (int64_t)r * a.C * kBins;
+    const uint32_t *count = a.count + (int64_t)r * a.C * kBins;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int i = i0 + j * kPick;
@@ -675,9 +707,16 @@ __device__ __forceinline__ void each_bin(const SampleArgs &a, int r, F f) {
         m[j] = mass[i];
       }
     }
+  }
+};
+// f(chunk, bin of the chunk, count, weights), of those that hold tokens; b: the first ones
+template <class F>
+__device__ __forceinline__ void each_bin(const SampleArgs &a, int r, Bins &b, F f) {
+  for (int i0 = threadIdx.x; i0 < a.C * kBins; i0 += Bins::kAhead * kPick) {
+    if (i0 >= Bins::kAhead * kPick) b.load(a, r, i0);
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (n[j] > 0) f((i0 + j * kPick) / kBins, (i0 + j * kPick) % kBins, n[j], m[j]);
+    for (int j = 0; j < Bins::kAhead; ++j)
+      if (b.n[j] > 0) f((i0 + j * kPick) / kBins, (i0 + j * kPick) % kBins, b.n[j], b.m[j]);
   }
 }
 // the first bin down to which `enough` holds
@@ -708,6 +747,8 @@ __global__ void __launch_bounds__(kPick) k_sample_cut(SampleArgs a) {
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
   const Row row = read_row(a, r);
   if (row.greedy || !row.filtered) return;
+  Bins bins;  // (asked for before the chunks' maxima are waited for)
+  bins.load(a, r, tid);
   fill_pow(sh.pow, a.bits);
   for (int i = tid; i < kBins; i += kPick) {
     sh.mass[i] = 0;
@@ -722,7 +763,7 @@ __global__ void __launch_bounds__(kPick) k_sample_cut(SampleArgs a) {
     }
     return;
   }
-  each_bin(a, r, [&](int c, int b, uint32_t n, uint64_t m) {
+  each_bin(a, r, bins, [&](int c, int b, uint32_t n, uint64_t m) {
     const int s = sh.shift[c];
     b = row_bin_of(b, s);
     atomicAdd(&sh.count[b], n);
@@ -839,6 +880,23 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   const L logits(a, r);
   const SampleChunk *chunk = a.chunk + (int64_t)r * a.C;
   fill_pow(sh.pow, a.bits);
+  // asked for here, so that these are not waited for one after the other
+  const float u0 = a.u[r];
+  const SampleRow *in = a.row + r;
+  int lo = 0, hi = -1, listed = 0;
+  uint64_t mass = 0, kept = 0;
+  uint32_t count = 0;
+  if (row.filtered && !row.greedy) {
+    lo = in->lo;
+    hi = in->hi;
+    listed = in->n;
+    if (tid < kBins) {
+      mass = in->mass[tid];
+      count = in->count[tid];
+    }
+    if (tid < a.C) kept = a.kept[(int64_t)r * a.C + tid];
+  }
+  static_assert(kBins <= kPick && kMaxChunks <= kPick, "one a thread");
 
   if (row.greedy) {
     uint64_t best = 0;
@@ -866,15 +924,13 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   if (!row.filtered) {
     for (int c = tid; c < a.C; c += kPick) sh.kept[c] = sh.shift[c] < 64 ? chunk[c].total >> sh.shift[c] : 0;
   } else {
-    const SampleRow *in = a.row + r;
-    for (int i = tid; i < kBins; i += kPick) {
-      sh.mass[i] = in->mass[i];
-      sh.count[i] = in->count[i];
+    if (tid < kBins) {
+      sh.mass[tid] = mass;
+      sh.count[tid] = count;
     }
     Set<TYPE> set(logits, row, sh, (uint64_t *)lds_raw);
-    const int lo = in->lo, hi = in->hi;
     __syncthreads();
-    if (hi >= lo) set.take_listed(lo, hi, anchor, a.C, a.list + (int64_t)r * a.room, in->n);
+    if (hi >= lo) set.take_listed(lo, hi, anchor, a.C, a.list + (int64_t)r * a.room, listed);
     auto mass_above = [&](int b) { return b > 0 ? sh.mass[b - 1] : 0; };
     auto count_above = [&](int b) { return b > 0 ? sh.count[b - 1] : 0u; };
     auto held = [&] { return sh.count[set.hi] - count_above(set.lo); };  // tokens of the set
@@ -903,12 +959,14 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
     }
     const bool none = set.hi < 0;  // no cut: all bins
     if (!none && set.lo == lo) {
-      for (int c = tid; c < a.C; c += kPick) sh.kept[c] = a.kept[(int64_t)r * a.C + c];
+      if (tid < a.C) sh.kept[tid] = kept;
       __syncthreads();
     } else {
       for (int c = tid; c < a.C; c += kPick) sh.kept[c] = 0;
       __syncthreads();
-      each_bin(a, r, [&](int c, int b, uint32_t, uint64_t m) {
+      Bins bins;
+      bins.load(a, r, tid);
+      each_bin(a, r, bins, [&](int c, int b, uint32_t, uint64_t m) {
         if (none || set.row_bin(c, b) < set.lo) lds_add(&sh.kept[c], set.scaled(c, m));
       });
     }
@@ -949,7 +1007,6 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   }
   __syncthreads();
   const uint64_t total = sh.kept[a.C - 1];
-  const float u0 = a.u[r];
   const double u = u0 > 0.0f ? fminf(u0, 1.0f) : 0.0;
   const uint64_t want = min((uint64_t)(u * (double)total), total - 1);  // (the first sum above it is wanted)
   int c = 0;
