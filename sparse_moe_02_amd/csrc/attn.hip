@@ -27,6 +27,8 @@
 //                171 us, 5.0 TB/s (a copy reaches 5.2).
 //
 // Results of splits and runs are joined by their references, in fixed order.
+#include <algorithm>
+
 #include "paged.hpp"
 
 #pragma clang fp contract(off)
@@ -1449,7 +1451,7 @@ AttnShape prefix_shape(int64_t T, int n_seqs, int n_groups, int64_t max_q, int64
   s.p_tiles = (int)((T * G + kAttnTile - 1) / kAttnTile + n_groups - 1);
   s.tiles = (int)((T * G + kAttnTile - 1) / kAttnTile + n_seqs - 1);
   if (T == 0) return s;
-  const int64_t p_blocks = (max_prefix + kAttnKeys - 1) / kAttnKeys, s_blocks = (max_suffix + kAttnKeys - 1) / kAttnKeys + 1;
+  const int p_blocks = (int)((max_prefix + kAttnKeys - 1) / kAttnKeys), s_blocks = (int)((max_suffix + kAttnKeys - 1) / kAttnKeys) + 1;
   // tiles that can hold rows
   int64_t s_busy = (max_q * G + kAttnTile - 1) / kAttnTile;
   s_busy = (s_busy < 1 ? 1 : s_busy) * n_seqs;
@@ -1468,54 +1470,54 @@ AttnShape prefix_shape(int64_t T, int n_seqs, int n_groups, int64_t max_q, int64
   // 25 and 22.
   constexpr double kFixed = 6.0, kNext = 1.5;  // (kNext: a further workgroup's start, while others run)
   constexpr int kUnits = 256;
-  const double slots = (dim == 256 ? 2 : 3) * kUnits, join = 2e-6 * (double)(T * H) * dim;
-  auto full = [&](int64_t busy) { return fmin(fmax((double)(T * G) / (double)(busy * kAttnTile), 0.25), 1.0); };
+  const int slots = (dim == 256 ? 2 : 3) * kUnits;
+  const double join = 2e-6 * (double)(T * H) * dim;
+  auto full = [&](int64_t busy) { return std::min(std::max((double)(T * G) / (double)(busy * kAttnTile), 0.25), 1.0); };
   const double p_full = full(p_busy), s_full = full(s_busy);
-  auto splits = [](int64_t blocks, int64_t per) { return blocks > 0 ? (blocks + per - 1) / per : 1; };
-  auto time = [&](int64_t p_per, int64_t s_per) {
-    const int64_t ps = splits(p_blocks, p_per), ss = splits(s_blocks, s_per);
+  auto splits = [](int blocks, int per) { return blocks > 0 ? (blocks + per - 1) / per : 1; };
+  auto time = [&](int p_per, int s_per) {
+    const int ps = splits(p_blocks, p_per), ss = splits(s_blocks, s_per);
     if (ps + ss > kMaxSplits) return 1e300;
-    const double p_len = (double)(p_per < p_blocks ? p_per : p_blocks), s_len = (double)(s_per < s_blocks ? s_per : s_blocks);
-    const double p_all = (double)(p_busy * ps * n_kv), s_all = (double)(s_busy * ss * n_kv);
-    const double longest = fmax(p_len * fmax(1.0, 1.2 * p_full * ceil(p_all / kUnits)), s_len);
-    const double work = (p_all * p_len * p_full + s_all * s_len * s_full) / kUnits;
+    const int p_len = std::min(p_per, p_blocks), s_len = std::min(s_per, s_blocks);
+    const int64_t p_all = p_busy * ps * n_kv, s_all = s_busy * ss * n_kv;
+    const double longest = std::max(p_len * std::max(1.0, 1.2 * p_full * (double)((p_all + kUnits - 1) / kUnits)), (double)s_len);
+    const double work = ((double)p_all * p_len * p_full + (double)s_all * s_len * s_full) * (1.0 / kUnits);
     // rounds of prefixes, suffixes in the places that the last of these leaves, and those that find none
-    const double p_one = p_len + kNext, s_one = s_len + kNext, p_rounds = ceil(p_all / slots);
-    const double beside = (p_rounds * slots - p_all) * floor(p_one / s_one);
-    const double ends = p_rounds * p_one - kNext + fmax(ceil((s_all - beside) / slots), 0.0) * s_one;
-    const double even = (p_all * p_one + s_all * s_one) / slots;  // (at least this, and not much more)
-    return kFixed + fmax(fmax(longest, work), fmax(even, fmin(ends, even + fmax(p_len, s_len)))) + join * (double)(ps + ss);
+    const double p_one = p_len + kNext, s_one = s_len + kNext;
+    const int64_t p_rounds = (p_all + slots - 1) / slots, beside = (p_rounds * slots - p_all) * (int)(p_one / s_one);
+    const double ends = (double)p_rounds * p_one - kNext + (s_all > beside ? (double)((s_all - beside + slots - 1) / slots) * s_one : 0.0);
+    const double even = ((double)p_all * p_one + (double)s_all * s_one) / slots;  // (at least this, and not much more)
+    const double places = std::max(even, std::min(ends, even + std::max(p_len, s_len)));
+    return kFixed + std::max(std::max(longest, work), places) + join * (ps + ss);
   };
   // lengths: geometric ones, those that give each compute unit the same number of prefixes' workgroups, and the one that
   // leaves each suffix a place beside them
-  const int64_t most = p_blocks > s_blocks ? p_blocks : s_blocks;
+  const int most = p_blocks > s_blocks ? p_blocks : s_blocks;
   auto best_of = [&](auto t) {
-    int64_t best = 2;
+    int best = 2;
     double least = 1e300;
-    auto take = [&](int64_t l) {
+    auto take = [&](int l) {
       const double v = t(l);
       if (v < least) least = v, best = l;
     };
-    for (int64_t l = 2; l <= most + l / 3; l += 1 + l / 4) take(l);
+    for (int l = 2; l <= most + l / 3; l += 1 + l / 4) take(l);
     for (int r = 0; r <= 3; ++r) {
-      const int64_t ps = (r > 0 ? r * kUnits : (int64_t)slots - s_busy * n_kv) / (p_busy * n_kv);
-      if (ps > 0 && p_blocks > 2 * ps) take((p_blocks + ps - 1) / ps);
+      const int64_t ps = (r > 0 ? r * kUnits : slots - s_busy * n_kv) / (p_busy * n_kv);
+      if (ps > 0 && p_blocks > 2 * ps) take((int)((p_blocks + ps - 1) / ps));
     }
     return best;
   };
-  int64_t p_per = best_of([&](int64_t l) { return time(l, l); });
-  int64_t s_per = best_of([&](int64_t l) { return time(p_per, l); });
-  p_per = best_of([&](int64_t l) { return time(l, s_per); });
+  int p_per = best_of([&](int l) { return time(l, l); }), s_per = best_of([&](int l) { return time(p_per, l); });
   // (a launch holds less than 2^32 work-items; groups and sequences without tokens count)
-  auto many = [&] { return n_kv * (s.p_tiles * splits(p_blocks, p_per) + s.tiles * splits(s_blocks, s_per)) >= int64_t(1) << 24; };
+  auto many = [&] { return n_kv * ((int64_t)s.p_tiles * splits(p_blocks, p_per) + (int64_t)s.tiles * splits(s_blocks, s_per)) >= int64_t(1) << 24; };
   while (splits(p_blocks, p_per) + splits(s_blocks, s_per) > kMaxSplits || many()) {
     p_per += 1 + p_per / 4;
     s_per += 1 + s_per / 4;
   }
-  s.p_splits = (int)splits(p_blocks, p_per);
-  s.splits = s.p_splits + (int)splits(s_blocks, s_per);
-  s.p_blocks = (int)p_per;
-  s.split_blocks = (int)s_per;
+  s.p_splits = splits(p_blocks, p_per);
+  s.splits = s.p_splits + splits(s_blocks, s_per);
+  s.p_blocks = p_per;
+  s.split_blocks = s_per;
   const size_t rows = (size_t)T * H * s.splits;
   s.off_stats = (rows * dim * 4 + 255) & ~(size_t)255;
   s.ws_bytes = s.off_stats + rows * sizeof(AttnStats);
