@@ -46,7 +46,8 @@ typedef struct {
  *              aligned to its elements
  * What is written may overlap nothing that is read (MOE_ERR_ALIAS; weights included).
  * MOE_ERR_TOKENS, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN, MOE_ERR_ALIAS,
- * MOE_ERR_DEVICE, MOE_ERR_HIP.  Results are bitwise repeatable. */
+ * MOE_ERR_DEVICE, MOE_ERR_HIP.  Results are bitwise repeatable.
+ * A row of x that holds an infinity or NaN has no finite results; other rows are not touched by it. */
 moe_status moe_linear(const moe_linear_weights *w, int64_t T, const void *x, int64_t x_stride, moe_dtype x_dtype,
                       const float *x_scale, int32_t x_group, void *out, int64_t out_stride, moe_dtype out_dtype,
                       hipStream_t stream);

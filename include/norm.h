@@ -27,7 +27,7 @@ extern "C" {
  *   width      1 .. 2^20; n_heads 1 .. 4096; T 0 .. 2^20 (0: nothing is enqueued), T * n_heads <= 2^28
  *   dtype      MOE_BF16 or MOE_FP16: of x, residual, sum, weight
  *   x          [T][n_heads][width]; any strides >= 0, 2-byte aligned (16-byte aligned rows of a multiple
- *              of 8 elements are read 16 bytes a lane)
+ *              of 8 elements are a little faster)
  *   residual   the same, or NULL: nothing is added
  *   sum        h, or NULL (needs no residual).  May be x or residual itself (same address and
  *              strides).

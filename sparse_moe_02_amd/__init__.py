@@ -3,8 +3,9 @@
 The layer runs in hand-written HIP kernels behind the C ABI of ``include/moe.h``;
 ``binding`` marshals arguments to it and ``layer.MoeLayer`` keeps one layer's device
 tensors, plan and workspace.  ``gdn`` has the Gated DeltaNet scan and its single-token step,
-``attn`` rotary positions with the append to a paged cache and attention over it, ``pages``
-the cache's bookkeeping.  Importing this package does not load the library;
+``attn`` rotary positions with the append to a paged cache and attention over it, also of sequences that
+share prefixes, ``pages`` the cache's bookkeeping, ``norm`` the norm with the residual's addition, ``linear``
+products with 4-bit weights, ``sample`` the choice of tokens.  Importing this package does not load the library;
 the first call does, and fails loudly if it has not been built.
 """
 

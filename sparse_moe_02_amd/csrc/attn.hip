@@ -19,8 +19,15 @@
 //                128, 1.04 ms (floor 0.79), and at 8K, 16/16 of 64, 0.186 ms (0.084): matrix units
 //                busy for 69, 48 and 23 % of the cycles, vector units 44, 55 and 48.  24 chunks of 0 to
 //                509 tokens, window 1024, 32/8 heads of 128, fp16: 0.127 ms, 0.64 PFLOP/s (masked
-//                parts of blocks, an uneven last round).  One token at 4K: 12.6 us, a chain of
-//                dependent loads and a second launch.
+//                parts of blocks, an uneven last round).  One token at 4K: 12.0 us, a chain of
+//                dependent loads and a second launch.  With PREFIX, rows of many sequences against
+//                a prefix that they share, and each sequence's against the keys behind it, all in one
+//                launch: 64 tokens, 16/2 heads of 256, up to 512 keys behind a prefix of 16384, 41.8 us
+//                (38 and the join's 7 under the profiler), 17 GFLOP of the prefix's and 9 of short tiles.
+//                0.95 us a block where a compute unit has one such tile, half of it the matrix units' (a ring of
+//                three blocks, and so one workgroup a compute unit, takes as long a block and 50 us in all);
+//                the rest is the start, a chain of loads (groups, batch, table, pages, keys), and 33 MB of partial
+//                results.
 //   k_attn_rows  16 rows, four waves sharing the keys out (v_mfma_f32_16x16x32); the keys of all
 //                sequences cut into equal runs, joined by k_attn_join_runs.  For few rows over
 //                many long sequences.  Bound: memory.  One token of 64 sequences up to 16K:
@@ -1461,8 +1468,8 @@ AttnShape prefix_shape(int64_t T, int n_seqs, int n_groups, int64_t max_q, int64
   if (p_busy < n_groups) p_busy = n_groups;
   // Blocks of a split, for prefixes and for suffixes: of some lengths those of least estimated time, in blocks (about
   // 0.95 us, heads of 256).  It is kFixed for the first workgroups' start, and the most of: the longest workgroup's, where
-  // one whose rows are all there needs the matrix units of its compute unit to itself, so that of two there one
-  // waits; the matrix units' work over all of them; and that of the workgroups in the order in which they find
+  // two whose rows are all there gain little from a compute unit in common; the work of all of them over
+  // the compute units; and that of the workgroups in the order in which they find
   // place.  Then the join, which reads each split's results.  us so, and with the best pair of all lengths: 64
   // sequences of up to 512 keys behind 16384, 2 heads of 256, 41.7 and 40.3 (58.6 where splits just filled the chip);
   // 128 of them 59.6 both; 23 of 5 prefixes of up to 5000, drafts of up to 4 tokens, 32/8 heads of 128, 28.8 and 27.9; 64

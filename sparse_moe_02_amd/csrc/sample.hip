@@ -16,7 +16,11 @@
 //                    more.  A further cut in another bin is collected here, from the row; where a cut's
 //                    bins hold more than kList tokens, each step of the selection reads them from the row.
 //
-// Bound: memory for many rows, latency for few.
+// Bound: memory and vector units for many rows, latency for few.  256 rows of 131072 fp32: 96 us; chunks 45 (28
+// without weights, whose 40 instructions a logit are not hidden behind the 134 MB; 39 without the bins' atomics, with a
+// copy of the bins for each 4th lane), cut 12, gather 23 (the logits again, a quarter of them from the last-level cache),
+// pick 21.  One row: 26 to 36 us by what its cut's bins hold, of which 5, 6, 5 to 8 and 10 to 18 are the four launches: a chain
+// of loads and barriers in each.
 #include "common.hpp"
 #include "serve.hpp"
 

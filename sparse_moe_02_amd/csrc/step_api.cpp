@@ -1,5 +1,5 @@
-// Host side of the C ABI declared in include/norm.h and include/linear.h: argument checks and launches.  Every check
-// precedes every launch.
+// Host side of the C ABI declared in include/norm.h, include/linear.h and include/sample.h: argument checks and
+// launches.  Every check precedes every launch.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
