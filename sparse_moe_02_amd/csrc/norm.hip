@@ -113,26 +113,26 @@ __device__ __forceinline__ int64_t place(const Rows &a, int64_t t, int h) { retu
 // residual and both outputs, 28 us; one element at a time 82), and a row's last elements one by one.
 typedef u32x4 __attribute__((aligned(2))) u32x4_2;
 typedef uint32_t __attribute__((__vector_size__(2 * sizeof(uint32_t)), aligned(1))) u32x2_1;
-template <bool WIDE, class F>
+template <class F>
 __device__ __forceinline__ void last_ones(int at, int W, F f) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (at + i < W) f(i);
 }
-template <bool F16, bool WIDE>
+template <bool WIDE>
 __device__ __forceinline__ u32x4 load8(const uint16_t *p, int at, int W) {
   if constexpr (WIDE) return *(const u32x4 *)(p + at);
   if (at + 8 <= W) return *(const u32x4_2 *)(p + at);
   u32x4 v = {0, 0, 0, 0};
-  last_ones<WIDE>(at, W, [&](int i) { v[i / 2] |= (uint32_t)p[at + i] << (16 * (i % 2)); });
+  last_ones(at, W, [&](int i) { v[i / 2] |= (uint32_t)p[at + i] << (16 * (i % 2)); });
   return v;
 }
 // x + r, 0 behind the row's end
 template <bool F16, bool WIDE>
 __device__ __forceinline__ void load_h(const uint16_t *x, const uint16_t *r, int at, int W, float *h) {
-  const u32x4 a = load8<F16, WIDE>(x, at, W);
+  const u32x4 a = load8<WIDE>(x, at, W);
   u32x4 b = {0, 0, 0, 0};
-  if (r) b = load8<F16, WIDE>(r, at, W);
+  if (r) b = load8<WIDE>(r, at, W);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     h[2 * i] = value<F16>(a[i] & 0xffffu);
@@ -150,7 +150,7 @@ __device__ __forceinline__ void store_h(uint16_t *o, int at, int W, const float 
     *(u32x4 *)(o + at) = v;
   } else {
     if (at + 8 <= W) *(u32x4_2 *)(o + at) = v;
-    else last_ones<WIDE>(at, W, [&](int i) { o[at + i] = (uint16_t)(v[i / 2] >> (16 * (i % 2))); });
+    else last_ones(at, W, [&](int i) { o[at + i] = (uint16_t)(v[i / 2] >> (16 * (i % 2))); });
   }
 }
 template <bool F16, bool WIDE>
@@ -158,7 +158,7 @@ __device__ __forceinline__ void load_w(const uint16_t *w, float offset, int at, 
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = offset;
   if (!w) return;
-  const u32x4 a = load8<F16, WIDE>(w, at, W);
+  const u32x4 a = load8<WIDE>(w, at, W);
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] += value<F16>(i & 1 ? a[i / 2] >> 16 : a[i / 2] & 0xffffu);
 }
@@ -169,7 +169,7 @@ __device__ __forceinline__ void store_codes(uint8_t *o, int at, int W, const flo
     *(uint2 *)(o + at) = make_uint2(lo, hi);
   } else {
     if (at + 8 <= W) *(u32x2_1 *)(o + at) = u32x2_1{lo, hi};
-    else last_ones<WIDE>(at, W, [&](int i) { o[at + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i % 4))); });
+    else last_ones(at, W, [&](int i) { o[at + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i % 4))); });
   }
 }
 
