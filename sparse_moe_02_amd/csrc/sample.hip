@@ -16,11 +16,13 @@
 //                    more.  A further cut in another bin is collected here, from the row; where a cut's
 //                    bins hold more than kList tokens, each step of the selection reads them from the row.
 //
-// Bound: memory and vector units for many rows, latency for few.  256 rows of 131072 fp32: 96 us; chunks 45 (28
-// without weights, whose 40 instructions a logit are not hidden behind the 134 MB; 39 without the bins' atomics, with a
-// copy of the bins for each 4th lane), cut 12, gather 23 (the logits again, a quarter of them from the last-level cache),
-// pick 21.  One row: 26 to 36 us by what its cut's bins hold, of which 5, 6, 5 to 8 and 10 to 18 are the four launches: a chain
-// of loads and barriers in each.
+// Short rows and many rows go without the two launches in the middle (`alone`).
+//
+// Bound: memory and vector units for many rows, latency for few.  256 rows of 131072 fp32: 92 us, of which the chunks
+// take 45 (28 without weights, whose 40 instructions a logit are not hidden behind the 134 MB; 39 without the bins'
+// atomics); in four launches 96, of which cut 12, gather 23 (the logits again, a quarter of them from the last-level
+// cache), pick 21.  One row: 26 to 36 us by what its cut's bins hold, of which 5, 6, 5 to 8 and 10 to 18 are the four
+// launches: a chain of loads and barriers in each.
 #include "common.hpp"
 #include "serve.hpp"
 
@@ -694,9 +696,10 @@ __device__ __forceinline__ double read_chunks(const SampleArgs &a, int r, Shared
   __syncthreads();
   return y0;
 }
-// The chunks' bins, kAhead a thread at a time from number i0 on.
+// The chunks' bins, N a thread at a time from number i0 on.
+template <int N>
 struct Bins {
-  static constexpr int kAhead = 7;
+  static constexpr int kAhead = N;
   uint32_t n[kAhead];
   uint64_t m[kAhead];
   __device__ __forceinline__ void load(const SampleArgs &a, int r, int i0) {
@@ -714,12 +717,12 @@ struct Bins {
   }
 };
 // f(chunk, bin of the chunk, count, weights), of those that hold tokens; b: the first ones
-template <class F>
-__device__ __forceinline__ void each_bin(const SampleArgs &a, int r, Bins &b, F f) {
-  for (int i0 = threadIdx.x; i0 < a.C * kBins; i0 += Bins::kAhead * kPick) {
-    if (i0 >= Bins::kAhead * kPick) b.load(a, r, i0);
+template <int N, class F>
+__device__ __forceinline__ void each_bin(const SampleArgs &a, int r, Bins<N> &b, F f) {
+  for (int i0 = threadIdx.x; i0 < a.C * kBins; i0 += N * kPick) {
+    if (i0 >= N * kPick) b.load(a, r, i0);
 #pragma unroll
-    for (int j = 0; j < Bins::kAhead; ++j)
+    for (int j = 0; j < N; ++j)
       if (b.n[j] > 0) f((i0 + j * kPick) / kBins, (i0 + j * kPick) % kBins, b.n[j], b.m[j]);
   }
 }
@@ -746,27 +749,11 @@ __device__ __forceinline__ void top_k_bins(const Shared &sh, int k, int &lo, int
 }
 __device__ __forceinline__ double floor_of(const Row &row, double y0) { return row.m > 0.0 ? y0 + log2(row.m) : -INFINITY; }
 
-__global__ void __launch_bounds__(kPick) k_sample_cut(SampleArgs a) {
-  __shared__ Shared sh;
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
-  const Row row = read_row(a, r);
-  if (row.greedy || !row.filtered) return;
-  Bins bins;  // (asked for before the chunks' maxima are waited for)
-  bins.load(a, r, tid);
-  fill_pow(sh.pow, a.bits);
-  for (int i = tid; i < kBins; i += kPick) {
-    sh.mass[i] = 0;
-    sh.count[i] = 0;
-  }
-  const double y0 = read_chunks(a, r, sh), anchor = __builtin_ceil(y0);
-  SampleRow *out = a.row + r;
-  if (y0 == -INFINITY) {
-    if (tid == 0) {
-      out->lo = 0;
-      out->hi = -1;
-    }
-    return;
-  }
+// Adds the chunks' bins up (into sh.mass and sh.count, which are 0 before) down to each; the bins of the first
+// cut (hi < lo: none).
+template <int N>
+__device__ __forceinline__ void cut_bins(const SampleArgs &a, int r, const Row &row, Shared &sh, Bins<N> &bins, double y0, int &lo, int &hi) {
+  const int tid = threadIdx.x, lane = tid & 63;
   each_bin(a, r, bins, [&](int c, int b, uint32_t n, uint64_t m) {
     const int s = sh.shift[c];
     b = row_bin_of(b, s);
@@ -785,19 +772,49 @@ __global__ void __launch_bounds__(kPick) k_sample_cut(SampleArgs a) {
     const uint64_t mb = wave_scan_u64(ms) - ms, nb = wave_scan_u64(ns) - ns;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-      out->mass[lane * kOwn + i] = sh.mass[lane * kOwn + i] = mb + m[i];
-      out->count[lane * kOwn + i] = sh.count[lane * kOwn + i] = (uint32_t)(nb + n[i]);
+      sh.mass[lane * kOwn + i] = mb + m[i];
+      sh.count[lane * kOwn + i] = (uint32_t)(nb + n[i]);
     }
   }
   __syncthreads();
-  int lo = 0, hi = -1;
+  lo = 0;
+  hi = -1;
   const uint64_t total = sh.mass[kBins - 1];
   if (row.k > 0 && (uint32_t)row.k < sh.count[kBins - 1]) {
     top_k_bins(sh, row.k, lo, hi);
   } else if (row.p < 1.0) {
     lo = hi = first_bin([&](int i) { return sh.mass[i] >= share_of(row.p, total); });
   } else if (row.m > 0.0) {
-    lo = hi = weight_at((floor_of(row, y0) - anchor) * kSteps, sh.pow).bin();
+    lo = hi = weight_at((floor_of(row, y0) - __builtin_ceil(y0)) * kSteps, sh.pow).bin();
+  }
+}
+
+__global__ void __launch_bounds__(kPick) k_sample_cut(SampleArgs a) {
+  __shared__ Shared sh;
+  const int r = blockIdx.x, tid = threadIdx.x;
+  const Row row = read_row(a, r);
+  if (row.greedy || !row.filtered) return;
+  Bins<7> bins;  // (asked for before the chunks' maxima are waited for)
+  bins.load(a, r, tid);
+  fill_pow(sh.pow, a.bits);
+  for (int i = tid; i < kBins; i += kPick) {
+    sh.mass[i] = 0;
+    sh.count[i] = 0;
+  }
+  const double y0 = read_chunks(a, r, sh);
+  SampleRow *out = a.row + r;
+  if (y0 == -INFINITY) {
+    if (tid == 0) {
+      out->lo = 0;
+      out->hi = -1;
+    }
+    return;
+  }
+  int lo, hi;
+  cut_bins(a, r, row, sh, bins, y0, lo, hi);
+  if (tid < kBins) {
+    out->mass[tid] = sh.mass[tid];
+    out->count[tid] = sh.count[tid];
   }
   if (tid == 0) {
     out->lo = lo;
@@ -874,7 +891,8 @@ __global__ void __launch_bounds__(kThreads) k_sample_gather(SampleArgs a) {
     }
 }
 
-template <int TYPE>
+// ALONE: without k_sample_cut and k_sample_gather before it, whose work it does itself.
+template <int TYPE, bool ALONE>
 __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   using L = Logits<TYPE>;
   extern __shared__ __align__(16) uint8_t lds_raw[];
@@ -890,7 +908,14 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   int lo = 0, hi = -1, listed = 0;
   uint64_t mass = 0, kept = 0;
   uint32_t count = 0;
-  if (row.filtered && !row.greedy) {
+  Bins<4> bins;
+  if (row.filtered && !row.greedy && ALONE) {
+    bins.load(a, r, tid);
+    if (tid < kBins) {
+      sh.mass[tid] = 0;
+      sh.count[tid] = 0;
+    }
+  } else if (row.filtered && !row.greedy) {
     lo = in->lo;
     hi = in->hi;
     listed = in->n;
@@ -928,13 +953,16 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   if (!row.filtered) {
     for (int c = tid; c < a.C; c += kPick) sh.kept[c] = sh.shift[c] < 64 ? chunk[c].total >> sh.shift[c] : 0;
   } else {
-    if (tid < kBins) {
+    if constexpr (ALONE) {
+      cut_bins(a, r, row, sh, bins, y0, lo, hi);
+    } else if (tid < kBins) {
       sh.mass[tid] = mass;
       sh.count[tid] = count;
     }
     Set<TYPE> set(logits, row, sh, (uint64_t *)lds_raw);
     __syncthreads();
-    if (hi >= lo) set.take_listed(lo, hi, anchor, a.C, a.list + (int64_t)r * a.room, listed);
+    if (hi >= lo && ALONE) set.take(lo, hi, anchor, a.C);
+    else if (hi >= lo) set.take_listed(lo, hi, anchor, a.C, a.list + (int64_t)r * a.room, listed);
     auto mass_above = [&](int b) { return b > 0 ? sh.mass[b - 1] : 0; };
     auto count_above = [&](int b) { return b > 0 ? sh.count[b - 1] : 0u; };
     auto held = [&] { return sh.count[set.hi] - count_above(set.lo); };  // tokens of the set
@@ -962,13 +990,12 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
       if (b <= cut && !has(b)) set.take(b, b, anchor, a.C);
     }
     const bool none = set.hi < 0;  // no cut: all bins
-    if (!none && set.lo == lo) {
+    if (!none && set.lo == lo && !ALONE) {
       if (tid < a.C) sh.kept[tid] = kept;
       __syncthreads();
     } else {
       for (int c = tid; c < a.C; c += kPick) sh.kept[c] = 0;
       __syncthreads();
-      Bins bins;
       bins.load(a, r, tid);
       each_bin(a, r, bins, [&](int c, int b, uint32_t, uint64_t m) {
         if (none || set.row_bin(c, b) < set.lo) lds_add(&sh.kept[c], set.scaled(c, m));
@@ -1070,19 +1097,31 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   }
 }
 
-template <int TYPE>
-hipError_t launch(const SampleArgs &a, hipStream_t s) {
+template <int TYPE, bool ALONE>
+hipError_t pick(const SampleArgs &a, hipStream_t s) {
   static std::atomic<uint64_t> done{0};
   constexpr int lds = kList * 8;
-  const hipError_t e = allow_lds(k_sample_pick<TYPE>, lds, done);
+  const hipError_t e = allow_lds(k_sample_pick<TYPE, ALONE>, lds, done);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_sample_chunks<TYPE>), dim3(a.C, a.R), dim3(kThreads), 0, s, a);
-  if (a.top_k || a.top_p || a.min_p) {  // (otherwise no row has filters)
-    hipLaunchKernelGGL(k_sample_cut, dim3(a.R), dim3(kPick), 0, s, a);
-    hipLaunchKernelGGL((k_sample_gather<TYPE>), dim3(a.C, a.R), dim3(kThreads), 0, s, a);
-  }
-  hipLaunchKernelGGL((k_sample_pick<TYPE>), dim3(a.R), dim3(kPick), lds, s, a);
+  hipLaunchKernelGGL((k_sample_pick<TYPE, ALONE>), dim3(a.R), dim3(kPick), lds, s, a);
   return hipGetLastError();
+}
+
+// Whether k_sample_pick goes alone behind the first launch: for short rows, whose two launches in between take longer
+// than reading them once more with one workgroup, and for many, which fill the chip by themselves.  us alone and not, rows
+// with top-p: 1 of 1000 17.8 and 23.2, 1 of 32000 21.4 and 24.2, but 1 of 131072 31.5 and 26.3; 48 of 64000 40 and 37, of
+// 131072 64 and 53; 96 of 64000 46.1 and 46.8, of 131072 74 and 69; 192 of 64000 60 and 68, of 131072 92 and 100; 256 of
+// 131072 101 and 112.
+bool alone(const SampleArgs &a) { return a.C <= 8 || 5 * a.C <= a.R; }
+
+template <int TYPE>
+hipError_t launch(const SampleArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL((k_sample_chunks<TYPE>), dim3(a.C, a.R), dim3(kThreads), 0, s, a);
+  const bool filters = a.top_k || a.top_p || a.min_p;  // (otherwise no row has any)
+  if (!filters || alone(a)) return pick<TYPE, true>(a, s);
+  hipLaunchKernelGGL(k_sample_cut, dim3(a.R), dim3(kPick), 0, s, a);
+  hipLaunchKernelGGL((k_sample_gather<TYPE>), dim3(a.C, a.R), dim3(kThreads), 0, s, a);
+  return pick<TYPE, false>(a, s);
 }
 
 }  // namespace

@@ -279,3 +279,19 @@ def test_refusals():
         with pytest.raises(B.MoeError) as e:
             sample(*args, **kw)
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("R, V, part, dtype", [(200, 40000, 7, "bf16"), (180, 131072, 60, "fp32"), (45, 33000, 1, "fp16"), (64, 300, 3, "fp32")])
+def test_rows_do_not_depend_on_others(R, V, part, dtype):
+    """Many rows at once, few at a time: the same tokens and probabilities, bit for bit, whatever launches do it."""
+    import torch
+
+    rng = np.random.default_rng(R)
+    g = torch.Generator(device="cuda").manual_seed(V)
+    logits = (torch.randn((R, V), generator=g, device="cuda") * torch.linspace(0.01, 6, R, device="cuda")[:, None]).to(_dt(dtype))
+    p, u = _params(R, rng, "mixed"), rng.random(R)
+    token, prob = _run(logits, u, p)
+    for i in range(0, R, part):
+        t, q = _run(logits[i:i + part], u[i:i + part], {k: v[i:i + part] for k, v in p.items()})
+        assert torch.equal(t, token[i:i + part]) and torch.equal(q, prob[i:i + part]), i
+    _check(logits[::max(1, R // 12)], u[::max(1, R // 12)], {k: v[::max(1, R // 12)] for k, v in p.items()}, f"{R} x {V}", undecided=2)
