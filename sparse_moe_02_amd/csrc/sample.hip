@@ -332,12 +332,16 @@ __device__ __forceinline__ int shift_of(double anchor, double chunk) {
   const double d = anchor - chunk;
   return d < 64.0 ? (int)d : 64;
 }
+// Whether a chunk `shift` octaves below the row, if it has tokens, may have some in the row's bins down to `hi`.  The last
+// bin holds what lies anywhere below the others, and such tokens are many: 131071 logits of 0 beside one of 18 have
+// 0.2% of the weight.
+__device__ __forceinline__ bool reaches_bin(int shift, int hi) { return row_bin_of(0, shift) <= hi; }
 
 // What the threads of k_sample_cut and k_sample_pick share.
 struct Shared {
   double pow[kSteps];
   double anchor[kMaxChunks];
-  int shift[kMaxChunks];       // octaves of a chunk's anchor below the row's (64: out of reach)
+  int shift[kMaxChunks];       // octaves of a chunk's anchor below the row's (64: as many or more, weights of 0)
   uint64_t kept[kMaxChunks];   // kept weight of the chunks, then the sums up to each
   int active[kMaxChunks];      // chunks that are read
   uint64_t mass[kBins];        // of the row; then the sums down to each bin
@@ -458,7 +462,7 @@ struct Set {
     if (tid < 64) {  // chunks that reach the bins
       int n = 0;
       for (int c0 = 0; c0 < chunks; c0 += 64) {
-        const bool some = c0 + lane < chunks && kPerOctave * sh.shift[c0 + lane] <= b1 && sh.anchor[c0 + lane] > -INFINITY;
+        const bool some = c0 + lane < chunks && reaches_bin(sh.shift[c0 + lane], b1) && sh.anchor[c0 + lane] > -INFINITY;
         const uint64_t m = __ballot(some);
         if (some) sh.active[n + __popcll(m & ((uint64_t(1) << lane) - 1))] = c0 + lane;
         n += __popcll(m);
@@ -856,7 +860,7 @@ __global__ void __launch_bounds__(kThreads) k_sample_gather(SampleArgs a) {
   const int shift = mine == -INFINITY ? 64 : shift_of(anchor, __builtin_ceil(mine));
   const uint64_t sum = wave_sum_u64(n > 0 && shift < 64 && row_bin_of(tid, shift) < lo ? m >> shift : 0);
   const Bounds bounds = bounds_of(lo, hi, anchor, row.c);
-  const bool reaches = mine > -INFINITY && kPerOctave * shift <= hi;
+  const bool reaches = mine > -INFINITY && reaches_bin(shift, hi);
   int some = 0;
   if (reaches) {
 #pragma unroll

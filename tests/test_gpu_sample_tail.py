@@ -1,0 +1,174 @@
+"""Choice of tokens (moe_sample) from rows of a few likely tokens far above all others, whose chunks lie 24 and more
+octaves below the row's largest logit, with cuts that fall there.
+
+The limit of ``test_gpu_sample.py``: a share of a sum of weights is off by less than 2 (2^-46 + V 2^-(bits + 1)), bits =
+min(51, 62 - ceil(log2 V)).  Tokens out there are hardly wider than that, so beside the rows that are decided every
+row's token is held to this: it is kept (by the definition in binary64), u lies in its interval of the running sum of the
+kept weights, give or take the limit twice (the interval's borders and the total), and its probability is off by no
+more than 2^-24 relative and the limit."""
+
+import numpy as np
+import pytest
+
+from gpu_helpers import ensure_lib, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ensure_lib()
+
+
+def _limit(V):
+    bits = min(51, 62 - int(np.ceil(np.log2(V))) if V > 1 else 51)
+    return 2 * (2.0 ** -46 + V * 2.0 ** -(bits + 1))
+
+
+def _kept(l, temperature, top_k, top_p, min_p):
+    """Kept tokens, by index, and their weights."""
+    far = (l - l.max()) / temperature
+    order = np.argsort(-l, kind="stable")
+    order = order[l[order] > -np.inf]
+    if top_k > 0:
+        order = order[:top_k]
+    w = np.exp(far[order])
+    if top_p < 1:
+        upto = np.cumsum(w)
+        order = order[:max(1, int((upto < top_p * upto[-1]).sum()) + 1)]
+    if min_p > 0:
+        order = order[np.exp(far[order]) >= min_p]
+    order = np.sort(order)
+    return order, np.exp(far[order])
+
+
+def _check(logits, u, temperature, top_k, top_p, min_p, what):
+    import torch
+
+    from oracle import step
+    from sparse_moe_02_amd.sample import sample
+
+    f = lambda x: torch.tensor(np.asarray(x), dtype=torch.float32, device="cuda")
+    u, temperature, top_p, min_p = f(u), f(temperature), f(top_p), f(min_p)
+    k = torch.tensor(np.asarray(top_k), dtype=torch.int32, device="cuda")
+    token, prob = (x.cpu().numpy() for x in sample(logits, u, temperature, k, top_p, min_p, return_prob=True))
+    l = logits.double().cpu().numpy()
+    limit = _limit(l.shape[1])
+    u, temperature, top_p, min_p = (x.double().cpu().numpy() for x in (u, temperature, top_p, min_p))
+    decided = 0
+    for r in range(len(l)):
+        told = (what, r, int(token[r]), float(u[r]), float(temperature[r]), int(top_k[r]), float(top_p[r]), float(min_p[r]))
+        kept, w = _kept(l[r], temperature[r], int(top_k[r]), top_p[r], min_p[r])
+        t, q, slack = step.sample_row(l[r], float(u[r]), float(temperature[r]), int(top_k[r]), float(top_p[r]), float(min_p[r]))
+        if slack >= limit:
+            decided += 1
+            assert token[r] == t and abs(prob[r] - q) <= (2.0 ** -24 + limit) * q, (told, t, q, float(prob[r]))
+        i = int(np.searchsorted(kept, token[r]))
+        assert i < len(kept) and kept[i] == token[r], told
+        upto = np.cumsum(w)
+        lo, hi = (upto[i] - w[i]) / upto[-1], upto[i] / upto[-1]
+        assert lo - 2 * limit <= u[r] <= hi + 2 * limit, (told, lo, hi)
+        assert abs(prob[r] - w[i] / upto[-1]) <= (2.0 ** -24 + limit) * w[i] / upto[-1], (told, float(prob[r]), w[i] / upto[-1])
+    say(f"{what}: {decided} of {len(l)} rows decided")
+    return token
+
+
+def _rows(V, dtype, gaps, finite, seed):
+    """A row for each gap: likely tokens that far (in nats) above the others, of which `finite` are there at all."""
+    import torch
+
+    rng = np.random.default_rng(seed)
+    l = 0.5 * rng.standard_normal((len(gaps), V))
+    likely = []
+    for r, gap in enumerate(gaps):
+        if finite < V:
+            l[r, rng.choice(V, V - finite, replace=False)] = -np.inf
+        at = rng.choice(V, 1 + r % 2, replace=False) if r % 3 else np.array([(0, V - 1)[r % 2]])
+        l[r, at] = gap + 0.25 * np.arange(len(at))
+        likely.append(at)
+    t = torch.from_numpy(l).to(dtype={"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}[dtype]).cuda()
+    return t, likely
+
+
+# 23, 24, 25 octaves, and further: behind 64 of them a weight is 0
+GAPS = [15.9, 16.7, 17.0, 17.4, 18.0, 19.0, 21.0, 25.0]
+
+
+@pytest.mark.parametrize("how", ["top_k", "top_p", "min_p", "all"])
+@pytest.mark.parametrize("V, copies, finite, dtype", [
+    (30000, 1, 30000, "fp32"), (30000, 1, 9000, "bf16"),        # two launches: short rows
+    (40009, 1, 40009, "fp32"), (40009, 2, 12000, "fp16"),       # four launches
+    (131072, 1, 131072, "fp32"), (131072, 1, 131072, "bf16"),
+    (40009, 7, 40009, "fp32"), (40009, 7, 12000, "bf16")])      # two launches: many rows
+def test_cuts_far_below_the_likely_tokens(V, copies, finite, dtype, how):
+    gaps = GAPS * copies
+    R = len(gaps)
+    rng = np.random.default_rng(V + copies + finite)
+    logits, likely = _rows(V, dtype, gaps, finite, V + finite)
+    l = logits.double().cpu().numpy()
+    temperature, top_k, top_p, min_p = np.ones(R), np.zeros(R, int), np.ones(R), np.zeros(R)
+    u = np.empty(R)
+    for r in range(R):
+        w = np.exp(l[r] - l[r].max())
+        rest = w.copy()
+        rest[likely[r]] = 0
+        share = rest.sum() / w.sum()
+        if how in ("top_k", "all"):
+            top_k[r] = int(rng.uniform(0.2, 0.9) * finite)
+        if how in ("top_p", "all"):
+            top_p[r] = 1 - share * rng.uniform(0.1, 0.6)
+        if how in ("min_p", "all"):
+            min_p[r] = np.quantile(rest[rest > 0], rng.uniform(0.1, 0.6))
+        # the middle of some token's share of those that are kept, and some anywhere
+        kept, w = _kept(l[r], 1.0, top_k[r], float(np.float32(top_p[r])), float(np.float32(min_p[r])))
+        upto = np.cumsum(w)
+        i = rng.integers(len(kept))
+        u[r] = (upto[i] - w[i] / 2) / upto[-1] if r % 4 else rng.random()
+    token = _check(logits, u, temperature, top_k, top_p, min_p, f"{V} {dtype} {how}")
+    assert sum(int(t) not in at for t, at in zip(token, likely)) > R // 3  # (most u are in the tail)
+
+
+def test_one_token_above_a_flat_row():
+    """Weights that are whole powers of two: V - 1 tokens of weight 2^-32 beside one of 1 have 2^-32 (V - 1) in all."""
+    import torch
+
+    from sparse_moe_02_amd.sample import sample
+
+    for V, R in ((20000, 3), (70000, 3), (70000, 100)):
+        l = torch.zeros((R, V), device="cuda")
+        l[:, -1] = 32.0
+        t = torch.full((R,), 1.4426950408889634, device="cuda")  # (base 2, but for its rounding)
+        n = V // 2
+        k = torch.full((R,), n + 1, dtype=torch.int32, device="cuda")
+        w = 2.0 ** -32
+        u = (torch.arange(R, device="cuda").double() + 0.5) * (n / R) * w
+        token, prob = sample(l, u.float(), t, k, return_prob=True)
+        want = (u.float().double() * (1 + n * w) / w).floor()
+        # (the temperature's rounding moves the tail's whole weight by 32 ln 2 2^-25 relative)
+        assert ((token - want).abs() <= 1 + 2e-6 * n).all() and (prob.double() / w - 1).abs().max() <= 1e-5
+        token, prob = sample(l, torch.ones(R, device="cuda"), t, k, return_prob=True)
+        assert (token == V - 1).all()
+
+
+def test_weights_of_nothing_count_for_top_k():
+    """More than 64 octaves below the largest logit: such tokens are kept or not, and never chosen."""
+    import torch
+
+    from sparse_moe_02_amd.sample import sample
+
+    for V, R in ((30000, 2), (70000, 2), (70000, 100)):
+        l = torch.full((R, V), -100.0, device="cuda")
+        l[:, V // 2] = 0.0
+        l[:, V // 2 + 5] = 1.0
+        for top_k in (1, 2, 3, V // 3, V - 1):
+            k = torch.full((R,), top_k, dtype=torch.int32, device="cuda")
+            u = torch.linspace(0, 1, R, device="cuda")
+            token, prob = sample(l, u, None, k, torch.full((R,), 0.9999, device="cuda"), return_prob=True)
+            p = [1.0] if top_k == 1 else [1 / (1 + np.e), np.e / (1 + np.e)]
+            at = [V // 2 + 5] if top_k == 1 else [V // 2, V // 2 + 5]
+            i = (u.double().cpu().numpy()[:, None] >= np.cumsum(p)[:-1]).sum(1)
+            assert token.tolist() == [at[x] for x in i], (V, top_k)
+            assert np.abs(prob.double().cpu().numpy() - np.array(p)[i]).max() <= 2.0 ** -24
