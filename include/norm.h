@@ -9,7 +9,7 @@
  * y is rounded once, to dtype, or to 8 bits with scales: of each `group` elements of a row
  * (whole rows: group 0) s = max|y| / 127 and code = y / s rounded to the nearest integer (ties to
  * even), or s = max|y| / 448 and code = y / s rounded to the nearest e4m3 number (without infinities).
- * A group of zeros (or of nothing above 2^-120) has scale and codes 0; one with an infinity or NaN has
+ * A group of zeros (or of nothing that reaches 2^-120) has scale and codes 0; one with an infinity or NaN has
  * scale infinity or NaN and codes 0.  The sum of squares is binary32.
  *
  * Conventions are those of attn.h.

@@ -76,21 +76,24 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
 }
 
 // Scale of a group whose largest magnitude has these bits, and what its elements are multiplied by
-// to get codes.
+// to get codes (e4m3: to get half of them, for 448 / 2^-120 would overflow).
 struct Step {
   float scale, inv;
 };
 template <int KIND>
 __device__ __forceinline__ Step step_of(uint32_t top) {
-  constexpr float kMost = KIND == 1 ? 127.0f : 448.0f;
+  constexpr float kMost = KIND == 1 ? 127.0f : 448.0f, kInv = KIND == 1 ? 127.0f : 224.0f;
   const float t = __uint_as_float(top);
   if (!(t < INFINITY)) return Step{t, 0.0f};
-  if (t < 0x1p-120f) return Step{0.0f, 0.0f};  // (127 / t would overflow)
-  return Step{t / kMost, kMost / t};
+  if (t < 0x1p-120f) return Step{0.0f, 0.0f};  // (127 / t and 224 / t would overflow)
+  return Step{t / kMost, kInv / t};
 }
-__device__ __forceinline__ float code_of(float y, const Step &s, float most) {
-  const float c = s.inv == 0.0f ? 0.0f : y * s.inv;
-  return fminf(fmaxf(c, -most), most);
+template <int KIND>
+__device__ __forceinline__ float code_of(float y, const Step &s) {
+  constexpr float kMost = KIND == 1 ? 127.0f : 448.0f;
+  float c = s.inv == 0.0f ? 0.0f : y * s.inv;
+  if constexpr (KIND == 2) c += c;
+  return fminf(fmaxf(c, -kMost), kMost);
 }
 // Four codes packed into a word.
 template <int KIND>
@@ -98,11 +101,11 @@ __device__ __forceinline__ uint32_t codes4(const float *y, const Step &s) {
   if constexpr (KIND == 1) {
     uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)__builtin_rintf(code_of(y[i], s, 127.0f)) & 0xffu) << (8 * i);
+    for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)__builtin_rintf(code_of<KIND>(y[i], s)) & 0xffu) << (8 * i);
     return w;
   } else {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(code_of(y[0], s, 448.0f), code_of(y[1], s, 448.0f), 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(code_of(y[2], s, 448.0f), code_of(y[3], s, 448.0f), w, true);
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(code_of<KIND>(y[0], s), code_of<KIND>(y[1], s), 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(code_of<KIND>(y[2], s), code_of<KIND>(y[3], s), w, true);
   }
 }
 // Element offset of row `row` of an array.
