@@ -11,7 +11,8 @@
  *
  * x is bfloat16 or float16, or the int8 codes and scales that moe_rms_norm gives, in which case
  * sums of products are exact integers within a group of 64.  Codes enter the matrix units as they are (x is
- * not rounded, nor is a dequantised weight); sums are binary32; the result is rounded once.
+ * not rounded, nor is a dequantised weight); sums are binary32; the result is rounded once.  A group's
+ * sum is formed of x (16 + code), which numbers of x up to 2^117 cannot overflow (bfloat16 has larger ones).
  *
  * Conventions are those of attn.h.
  */

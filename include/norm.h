@@ -39,7 +39,7 @@ extern "C" {
  *              and weight 16-byte and out 8-byte aligned, strides multiples of 8, MOE_ERR_ALIGN);
  *              otherwise 0
  *   scale      8-bit outputs: float32 [T][n_heads][width / group, or 1]; otherwise NULL
- *   eps        >= 0, finite; offset finite
+ *   eps        >= 0, finite (0: a row whose squares vanish in binary32 has no number: zeros give NaN); offset finite
  * What is written may otherwise overlap nothing that is read or written (MOE_ERR_ALIAS).
  * MOE_ERR_TOKENS, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN, MOE_ERR_ALIAS,
  * MOE_ERR_DEVICE, MOE_ERR_HIP. */

@@ -59,7 +59,7 @@ class QLinear:
 
     def __call__(self, x: torch.Tensor, x_scale: torch.Tensor | None = None, *, out: torch.Tensor | None = None,
                  out_dtype: torch.dtype | None = None) -> torch.Tensor:
-        """x W^T (see ``moe_linear``).  x: [T][k], rows any distance apart, bfloat16 or float16, or int8 with
+        """x W^T (see ``moe_linear``).  x: [T][k], 16-byte aligned rows any distance apart, bfloat16 or float16, or int8 with
         x_scale float32 [T][1, k / 64 or k / 128], as ``rms_norm`` gives them.  out: [T][n] of bfloat16, float16 or
         float32, by default a new tensor of out_dtype (x's type, or bfloat16)."""
         t = _TYPES.get(x.dtype)
