@@ -99,7 +99,7 @@ typedef enum {
                             calls since then are not valid */
 } moe_status;
 
-/* (MOE_INT8 and MOE_FP8, e4m3 without infinities: norm.h and linear.h only) */
+/* (MOE_INT8: norm.h and linear.h only; MOE_FP8, e4m3 without infinities: norm.h only) */
 typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2, MOE_INT8 = 3, MOE_FP8 = 4 } moe_dtype;
 
 /* Flags (moe_config.flags).  Section "Optimization strategy" of the pages measures each

@@ -12,6 +12,9 @@
  * A group of zeros (or of nothing that reaches 2^-120) has scale and codes 0; one with an infinity or NaN has
  * scale infinity or NaN and codes 0.  The sum of squares is binary32.
  *
+ * linear.h takes int8 with a scale for each row or for each 64 or 128 elements; int8 by 32 and e4m3 are for
+ * products outside this library.
+ *
  * Conventions are those of attn.h.
  */
 #ifndef MOE_NORM_MI355X_H
