@@ -54,7 +54,7 @@ def _check(logits, u, temperature, top_k, top_p, min_p, what):
     f = lambda x: torch.tensor(np.asarray(x), dtype=torch.float32, device="cuda")
     u, temperature, top_p, min_p = f(u), f(temperature), f(top_p), f(min_p)
     k = torch.tensor(np.asarray(top_k), dtype=torch.int32, device="cuda")
-    token, prob = (x.cpu().numpy() for x in sample(logits, u, temperature, k, top_p, min_p, return_prob=True))
+    token, prob = (x.cpu().numpy().astype(t) for x, t in zip(sample(logits, u, temperature, k, top_p, min_p, return_prob=True), (int, float)))
     l = logits.double().cpu().numpy()
     limit = _limit(l.shape[1])
     u, temperature, top_p, min_p = (x.double().cpu().numpy() for x in (u, temperature, top_p, min_p))
