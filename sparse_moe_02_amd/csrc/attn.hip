@@ -1474,7 +1474,8 @@ AttnShape prefix_shape(int64_t T, int n_seqs, int n_groups, int64_t max_q, int64
   // sequences of up to 512 keys behind 16384, 2 heads of 256, 41.7 and 40.3 (58.6 where splits just filled the chip);
   // 128 of them 59.6 both; 23 of 5 prefixes of up to 5000, drafts of up to 4 tokens, 32/8 heads of 128, 28.8 and 27.9; 64
   // of 64 prefixes of up to 2000 40 and 39; 64 of 2048, 32/8 heads of 128, 21.6 and 21.0; 64 of up to 512 behind 512
-  // 25 and 22.
+  // 25 and 22.  (Heads of 64, whose blocks are shorter while starts are not: 64 sequences of up to 512 keys behind 16384, 2
+  // heads, 24.4; other lengths were not tried there.)
   constexpr double kFixed = 6.0, kNext = 1.5;  // (kNext: a further workgroup's start, while others run)
   constexpr int kUnits = 256;
   const int slots = (dim == 256 ? 2 : 3) * kUnits;

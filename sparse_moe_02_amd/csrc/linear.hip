@@ -19,6 +19,7 @@
 // Measured: 8 rows of 2048 -> 131072, fp32 out, 34 to 37.5 us, 155 MB at 4.1 to 4.6 TB/s, vector units busy for three
 // quarters of the cycles (they turn codes into operands); one row of 2048 -> 5120 5.5 (launch, a chain of two loads, a
 // barrier); 37 int8 rows of 4096 -> 2047 11 (three 16-row tiles of x to each tile of weights, their sums through LDS).
+// bfloat16 scales and biases take the same time as float16 ones (33 and 34 us, 6.3 and 6.4, 13.3 and 13.5 for bf16 rows).
 //
 // A workgroup's waves share K out (256 of it, a span, at a time) and keep their part of x in registers, so
 // that x is read once a workgroup whatever the number of weight rows; their sums of some tiles of 16 weight

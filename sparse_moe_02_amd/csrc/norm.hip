@@ -9,7 +9,7 @@
 // they fill, down to 8.
 //
 // Bound: the launch for few rows (2.5 us), memory for many: 8192 rows of 2048 bf16, residual and
-// both outputs 24 us (5.6 TB/s), with int8 in groups of 128 24.5 us (4.8 TB/s); 24496 heads of 256
+// both outputs 24 us (5.6 TB/s), with int8 or e4m3 in groups of 128 22.5 to 24.5 us (4.8 TB/s); 24496 heads of 256
 // fp16 out of rows of 20 7.7 us (3.3 TB/s: 1/5 of each row is passed over).  Stores that go round
 // the caches take 10% off a large norm alone and cost the product that reads it next more
 // (8192 rows, norm, product and norm 260 -> 263 us), so they are ordinary ones.  Weights loaded
@@ -282,7 +282,9 @@ __global__ void __launch_bounds__(kThreads) k_norm(NormArgs a) {
 }
 
 // Rows too long for registers, one a workgroup: h is formed anew in each pass and written in the
-// last, so that it may be written over what it comes from.
+// last, so that it may be written over what it comes from.  Bound: memory for many rows (1000 of 32768
+// bf16, no residual, 31.5 us, 131 MB; int8 with one scale a row, a third pass, 44.5), a workgroup's own reads for few (64
+// of 65536 27 us, 8 of 2^20 486: the other compute units have nothing to do).
 template <bool F16, int KIND, bool WIDE>
 __global__ void __launch_bounds__(kThreads) k_norm_long(NormArgs a) {
   __shared__ float red[4];
